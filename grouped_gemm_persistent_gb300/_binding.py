@@ -11,6 +11,7 @@ import ctypes
 import os
 import re
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -24,8 +25,10 @@ STATUS_NAMES = {0: "TG_OK", 1: "TG_ERR_INVALID_ARG", 2: "TG_ERR_UNSUPPORTED", 3:
                 4: "TG_ERR_TIMEOUT", 5: "TG_ERR_NO_DEVICE"}
 EPILOGUES = {"none": 0, "bias": 1, "bias_gelu": 2}
 ROW_MAJOR, COL_MAJOR = 0, 1
-BF16, F32, F16 = 0, 1, 2
+BF16, F32, F16, E4M3, E5M2 = 0, 1, 2, 3, 4
 _DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
+_FP8_CODE = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+FP8_BLOCK = 128     # values that share a scale
 
 _lib = None
 _lock = threading.Lock()
@@ -50,11 +53,20 @@ class GroupProblem(ctypes.Structure):
     ]
 
 
+class Fp8Operand(ctypes.Structure):
+    """Mirror of tg_fp8_operand."""
+    _fields_ = [
+        ("data", ctypes.c_void_p), ("ld", ctypes.c_int64),
+        ("scale", ctypes.c_void_p), ("scale_stride", ctypes.c_int64), ("scale_k_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int), ("layout", ctypes.c_int), ("block", ctypes.c_int),
+    ]
+
+
 def header_functions() -> list[str]:
     """Names of the functions include/tg.h declares."""
     text = open(HEADER).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(tg_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(tg_[a-z0-9_]+)\s*\(", text)))
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
@@ -85,6 +97,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_grouped_gemm.argtypes = [ctypes.POINTER(GroupProblem), ci, vp]
         lib.tg_grouped_gemm_noalloc.restype = ci
         lib.tg_grouped_gemm_noalloc.argtypes = [ctypes.POINTER(GroupProblem), ci, vp]
+        lib.tg_quantize_fp8.restype = ci
+        lib.tg_quantize_fp8.argtypes = [vp, ci, i64, i64, i64, ci, ci, vp, ci, i64, vp, i64, vp]
+        op8 = ctypes.POINTER(Fp8Operand)
+        lib.tg_gemm_fp8.restype = ci
+        lib.tg_gemm_fp8.argtypes = [op8, op8, vp, ci, i64, i64, i64, i64, ci, vp, vp]
+        lib.tg_moe_gemm_fp8.restype = ci
+        lib.tg_moe_gemm_fp8.argtypes = [op8, i64, i64, op8, i64, i64, i64, i64, vp, ci, i64, vp, ci, vp, vp]
+        lib.tg_moe_router.restype = ci
+        lib.tg_moe_router.argtypes = [vp, ci, i64, i64, i64, i64, ci, vp, vp, vp, vp, vp, vp]
+        lib.tg_moe_router_backward.restype = ci
+        lib.tg_moe_router_backward.argtypes = [vp, ci, i64, i64, i64, i64, ci, vp, vp, vp, vp, vp, vp, i64, vp]
         lib.tg_status_string.restype = ctypes.c_char_p
         lib.tg_status_string.argtypes = [ci]
         lib.tg_last_error_message.restype = ctypes.c_char_p
@@ -305,6 +328,268 @@ def moe_gemm_device(a: torch.Tensor, b: torch.Tensor, counts: torch.Tensor, out:
     _check(load().tg_moe_gemm(_ptr(a), lda, T, K, _ptr(b), lb, ldb, b.stride(0), G, N, _ptr(out),
                               _DTYPE_CODE[out.dtype], ldc, counts.data_ptr(), epi, _ptr(bias) if epi else None,
                               _stream_handle(stream)))
+    return out
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """torch.empty in the allocator's order of ``stream``, so that a block freed on another stream is not
+    handed out while that stream still uses it."""
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows_of_16_bytes(rows: int, cols: int, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An uninitialised [rows, cols] tensor whose rows start on 16-byte boundaries."""
+    step = 16 // dtype.itemsize
+    ld = -(-cols // step) * step
+    t = _empty((rows, ld), dtype, device, stream)
+    return t if ld == cols else t[:, :cols]
+
+
+def _on_one_gpu(**tensors) -> None:
+    """The tensors (None is left out) are on one CUDA device, the current one."""
+    where = {name: t.device for name, t in tensors.items() if t is not None}
+    for name, dev in where.items():
+        if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must be on the current CUDA device, got {dev}")
+
+
+def quantize_fp8(x: torch.Tensor, block: tuple[int, int] = (1, 128), q: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None, *, dtype: torch.dtype = torch.float8_e4m3fn,
+                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(q, scale): ``x`` [M, K] in 8 bits with one power-of-two scale for each ``block`` of values (tg_quantize_fp8).
+
+    ``block`` is (1, 128), (128, 1) or (128, 128); ``scale`` (fp32) is [M, ceil(K / 128)] (a transposed view:
+    a block column's scales lie side by side), [ceil(M / 128), K] or [ceil(M / 128), ceil(K / 128)].  ``x`` is
+    row-major bf16, fp16 or fp32; ``q`` (allocated with rows of a multiple of 16 bytes if not given) has
+    ``dtype`` torch.float8_e4m3fn or torch.float8_e5m2, and ``x`` is ``q * scale`` up to its rounding.
+    """
+    if x.dtype not in _DTYPE_CODE:
+        raise TypeError("x must be bf16, fp16 or fp32")
+    lx, ldx = _matrix(x, "x")
+    if lx != ROW_MAJOR:
+        raise ValueError("x must be row-major")
+    M, K = x.shape
+    block = tuple(block)
+    shape = {(1, 128): (M, _blocks(K)), (128, 1): (_blocks(M), K), (128, 128): (_blocks(M), _blocks(K))}.get(block)
+    if shape is None:
+        raise ValueError(f"block must be (1, 128), (128, 1) or (128, 128), got {block}")
+    if q is None:
+        if dtype not in _FP8_CODE:
+            raise TypeError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
+        q = _rows_of_16_bytes(M, K, dtype, x.device, stream)
+    if q.dtype not in _FP8_CODE or tuple(q.shape) != (M, K):
+        raise ValueError("q must be [M, K] float8_e4m3fn or float8_e5m2")
+    lq, ldq = _matrix(q, "q")
+    if lq != ROW_MAJOR:
+        raise ValueError("q must be row-major")
+    if scale is None:
+        scale = (_empty(shape[::-1], torch.float32, x.device, stream).t() if block == (1, 128)
+                 else _empty(shape, torch.float32, x.device, stream))
+    if scale.dtype != torch.float32 or tuple(scale.shape) != shape:
+        raise ValueError(f"scale must be fp32 {list(shape)}")
+    stored = scale.t() if block == (1, 128) else scale
+    if stored.shape[1] > 1 and stored.stride(1) != 1:
+        raise ValueError("scale must have " + ("contiguous columns" if block == (1, 128) else "contiguous rows"))
+    scale_ld = stored.stride(0) if stored.shape[0] > 1 else max(stored.shape[1], 1)
+    _on_one_gpu(x=x, q=q, scale=scale)
+    _check(load().tg_quantize_fp8(_ptr(x), _DTYPE_CODE[x.dtype], ldx, M, K, block[0], block[1], _ptr(q),
+                                  _FP8_CODE[q.dtype], ldq, _ptr(scale), scale_ld, _stream_handle(stream)))
+    return q, scale
+
+
+def _fp8_matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """(layout, ld) of a 2-D 8-bit tensor view.  A single row or column is never stepped past: its leading
+    dimension is reported as its extent rounded up to 16 elements."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    r, c = t.shape
+    s0, s1 = t.stride()
+    if s1 == 1 and (c > 1 or r <= 1):
+        return ROW_MAJOR, (s0 if r > 1 else -(-max(c, 1) // 16) * 16)
+    if s0 == 1:
+        return COL_MAJOR, (s1 if c > 1 else -(-max(r, 1) // 16) * 16)
+    if c == 1:
+        return ROW_MAJOR, s0
+    if r == 1:
+        return COL_MAJOR, s1
+    raise ValueError(f"{name}: neither rows nor columns are contiguous (strides {t.stride()})")
+
+
+def _fp8_scale(s: torch.Tensor, name: str, rows: int, kb: int, dim: int) -> tuple[int, int, int]:
+    """(block, stride, k stride) of an operand's scales; ``dim`` is the operand's row (A) or column (B) dimension."""
+    if s.dtype != torch.float32 or s.dim() != 2 or s.shape[1 - dim] != kb or s.shape[dim] not in (rows, _blocks(rows)):
+        raise ValueError(f"{name} must be fp32 with {kb} blocks of K and {rows} or {_blocks(rows)} entries, "
+                         f"got {tuple(s.shape)} {s.dtype}")
+    return (1 if s.shape[dim] == rows else FP8_BLOCK), s.stride(dim), s.stride(1 - dim)
+
+
+def gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: torch.Tensor,
+             out: torch.Tensor | None = None, *, bias: torch.Tensor | None = None, epilogue: str = "none",
+             out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """out[M,N] = epilogue((a * scale_a) @ (b * scale_b)) for 8-bit operands with a scale per block of 128 (tg_gemm_fp8).
+
+    ``a`` [M, K] and ``b`` [K, N] are float8_e4m3fn or float8_e5m2, each a row-major or column-major view.
+    ``scale_a`` is fp32 [M, ceil(K / 128)] (or [ceil(M / 128), ...]), ``scale_b`` [ceil(K / 128), N] or
+    [ceil(K / 128), ceil(N / 128)], with any strides; scales of which neighbouring rows lie side by side
+    (quantize_fp8's) load fastest.  ``bias`` is bf16 [N]; ``out`` (allocated if not given) bf16, fp16 or fp32.
+    """
+    if a.dtype not in _FP8_CODE or b.dtype not in _FP8_CODE:
+        raise TypeError("a and b must be float8_e4m3fn or float8_e5m2")
+    M, K = a.shape
+    K2, N = b.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if out is None:
+        if out_dtype not in _DTYPE_CODE:
+            raise TypeError("out_dtype must be bf16, fp16 or fp32")
+        out = _rows_of_16_bytes(M, N, out_dtype, a.device, stream)
+    if out.dtype not in _DTYPE_CODE or tuple(out.shape) != (M, N):
+        raise ValueError("out must be [M, N] bf16, fp16 or fp32")
+    la, lda = _fp8_matrix(a, "a")
+    lb, ldb = _fp8_matrix(b, "b")
+    lc, ldc = _matrix(out, "out")
+    if lc != ROW_MAJOR:
+        raise ValueError("out must be row-major")
+    ba, sa, sak = _fp8_scale(scale_a, "scale_a", M, _blocks(K), 0)
+    bb, sb, sbk = _fp8_scale(scale_b, "scale_b", N, _blocks(K), 1)
+    epi = EPILOGUES[epilogue]
+    if epi and (bias is None or bias.dtype != torch.bfloat16 or bias.numel() != N or not bias.is_contiguous()):
+        raise ValueError("this epilogue needs a contiguous bf16 bias of length N")
+    _on_one_gpu(a=a, scale_a=scale_a, b=b, scale_b=scale_b, out=out, bias=bias if epi else None)
+    oa = Fp8Operand(_ptr(a), lda, _ptr(scale_a), sa, sak, _FP8_CODE[a.dtype], la, ba)
+    ob = Fp8Operand(_ptr(b), ldb, _ptr(scale_b), sb, sbk, _FP8_CODE[b.dtype], lb, bb)
+    _check(load().tg_gemm_fp8(ctypes.byref(oa), ctypes.byref(ob), _ptr(out), _DTYPE_CODE[out.dtype], ldc, M, N, K, epi,
+                              _ptr(bias) if epi else None, _stream_handle(stream)))
+    return out
+
+
+def moe_gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: torch.Tensor, counts: torch.Tensor,
+                 out: torch.Tensor | None = None, *, bias: torch.Tensor | None = None, epilogue: str = "none",
+                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """moe_gemm_device with 8-bit operands (tg_moe_gemm_fp8): the token counts stay on the GPU.
+
+    ``a`` [T, K] row-major, rows grouped by expert, ``scale_a`` [T, ceil(K / 128)]; ``b`` [G, K, N], each expert
+    row- or column-major, ``scale_b`` [G, ceil(K / 128), ceil(N / 128)]; ``counts`` int32 CUDA tensor [G];
+    ``out`` [T, N], rows past sum(counts) not written; ``bias`` bf16 [G, N].
+    """
+    if a.dtype not in _FP8_CODE or b.dtype not in _FP8_CODE:
+        raise TypeError("a and b must be float8_e4m3fn or float8_e5m2")
+    if counts.dtype != torch.int32 or counts.dim() != 1 or not counts.is_contiguous():
+        raise TypeError("counts must be a contiguous int32 tensor [G]")
+    T, K = a.shape
+    if b.dim() != 3 or b.shape[1] != K or counts.shape[0] != b.shape[0]:
+        raise ValueError("shapes: a [T, K], b [G, K, N], counts [G]")
+    G, _, N = b.shape
+    la, lda = _fp8_matrix(a, "a")
+    if la != ROW_MAJOR:
+        raise ValueError("a must be row-major")
+    if out is None:
+        if out_dtype not in _DTYPE_CODE:
+            raise TypeError("out_dtype must be bf16, fp16 or fp32")
+        out = _rows_of_16_bytes(T, N, out_dtype, a.device, stream)
+    if out.dtype not in _DTYPE_CODE or tuple(out.shape) != (T, N):
+        raise ValueError("out must be [T, N] bf16, fp16 or fp32")
+    lc, ldc = _matrix(out, "out")
+    if lc != ROW_MAJOR:
+        raise ValueError("out must be row-major")
+    ba, sa, sak = _fp8_scale(scale_a, "scale_a", T, _blocks(K), 0)
+    if ba != 1:
+        raise ValueError("scale_a must have a scale per row")
+    shape = (G, _blocks(K), _blocks(N))
+    if scale_b.dtype != torch.float32 or tuple(scale_b.shape) != shape:
+        raise ValueError(f"scale_b must be fp32 {list(shape)}")
+    epi = EPILOGUES[epilogue]
+    if epi and (bias is None or bias.dtype != torch.bfloat16 or tuple(bias.shape) != (G, N) or not bias.is_contiguous()):
+        raise ValueError("this epilogue needs a contiguous bf16 bias [G, N]")
+    _on_one_gpu(a=a, scale_a=scale_a, b=b, scale_b=scale_b, counts=counts, out=out, bias=bias if epi else None)
+    if G == 0:
+        return out
+    lb, ldb = _fp8_matrix(b[0], "b")
+    per = (K if lb == ROW_MAJOR else N) * ldb
+    oa = Fp8Operand(_ptr(a), lda, _ptr(scale_a), sa, sak, _FP8_CODE[a.dtype], la, 1)
+    ob = Fp8Operand(_ptr(b), ldb, _ptr(scale_b), scale_b.stride(2), scale_b.stride(1), _FP8_CODE[b.dtype], lb, FP8_BLOCK)
+    _check(load().tg_moe_gemm_fp8(ctypes.byref(oa), T, K, ctypes.byref(ob), b.stride(0) if G > 1 else per,
+                                  scale_b.stride(0), G, N, _ptr(out), _DTYPE_CODE[out.dtype], ldc, counts.data_ptr(), epi,
+                                  _ptr(bias) if epi else None, _stream_handle(stream)))
+    return out
+
+
+class Routing(NamedTuple):
+    """What moe_router returns, and moe_router_backward needs again."""
+    experts: torch.Tensor    # int32 [T, k], -1 where a row has no further expert
+    weights: torch.Tensor    # fp32 [T, k]
+    counts: torch.Tensor     # int32 [G]
+    loss: torch.Tensor       # fp32, balance loss
+    slope: torch.Tensor      # fp32 [G], d loss / d probability
+    renormalize: bool
+
+
+def moe_router(logits: torch.Tensor, top_k: int, *, renormalize: bool = False, stream=None) -> Routing:
+    """Top-k experts of each token, their softmax weights, per-expert counts and balance loss (tg_moe_router).
+
+    ``logits`` is row-major [T, G] bf16, fp16 or fp32; -infinity forbids an expert, a row of it is padding.
+    ``counts`` is what moe_gemm_device and moe_gemm_fp8 read; the loss is G * sum(f * P), 1 when all is even.
+    """
+    if logits.dtype not in _DTYPE_CODE:
+        raise TypeError("logits must be bf16, fp16 or fp32")
+    layout, ld = _matrix(logits, "logits")
+    if layout != ROW_MAJOR:
+        raise ValueError("logits must be row-major")
+    T, G = logits.shape
+    if not isinstance(top_k, int) or top_k < 1:
+        raise ValueError("top_k must be a positive integer")
+    _on_one_gpu(logits=logits)
+
+    def new(shape, dtype):
+        return _empty(shape, dtype, logits.device, stream)
+
+    r = Routing(new((T, top_k), torch.int32), new((T, top_k), torch.float32), new((G,), torch.int32),
+                new((), torch.float32), new((G,), torch.float32), bool(renormalize))
+    _check(load().tg_moe_router(_ptr(logits), _DTYPE_CODE[logits.dtype], ld, T, G, top_k, int(renormalize), _ptr(r.experts),
+                                _ptr(r.weights), _ptr(r.counts), _ptr(r.loss), _ptr(r.slope), _stream_handle(stream)))
+    return r
+
+
+def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch.Tensor | None = None,
+                        d_loss: torch.Tensor | None = None, out: torch.Tensor | None = None, *,
+                        stream=None) -> torch.Tensor:
+    """The gradient of ``logits`` from those of routing.weights (fp32 [T, k]) and routing.loss (fp32, one
+    element, on the GPU); None is zero (tg_moe_router_backward).  ``out`` has the logits' type."""
+    if logits.dtype not in _DTYPE_CODE:
+        raise TypeError("logits must be bf16, fp16 or fp32")
+    layout, ld = _matrix(logits, "logits")
+    if layout != ROW_MAJOR:
+        raise ValueError("logits must be row-major")
+    T, G = logits.shape
+    k = routing.experts.shape[1]
+    for name, t, dt, shape in (("routing.experts", routing.experts, torch.int32, (T, k)),
+                               ("routing.weights", routing.weights, torch.float32, (T, k)),
+                               ("routing.slope", routing.slope, torch.float32, (G,)),
+                               ("d_weights", d_weights, torch.float32, (T, k))):
+        if t is not None and (t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)}")
+    if d_loss is not None and (d_loss.dtype != torch.float32 or d_loss.numel() != 1):
+        raise ValueError("d_loss must be an fp32 tensor of one element")
+    if out is None:
+        out = _empty((T, G), logits.dtype, logits.device, stream)
+    if out.dtype != logits.dtype or tuple(out.shape) != (T, G):
+        raise ValueError("out must be [T, G] of the logits' type")
+    lo, ldd = _matrix(out, "out")
+    if lo != ROW_MAJOR:
+        raise ValueError("out must be row-major")
+    _on_one_gpu(logits=logits, experts=routing.experts, weights=routing.weights, slope=routing.slope,
+                d_weights=d_weights, d_loss=d_loss, out=out)
+    _check(load().tg_moe_router_backward(_ptr(logits), _DTYPE_CODE[logits.dtype], ld, T, G, k, int(routing.renormalize),
+                                         _ptr(routing.experts), _ptr(routing.weights), _ptr(routing.slope),
+                                         _ptr(d_weights) or None, _ptr(d_loss) or None, _ptr(out), ldd,
+                                         _stream_handle(stream)))
     return out
 
 

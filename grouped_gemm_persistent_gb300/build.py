@@ -29,7 +29,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
                 "--expt-relaxed-constexpr"]
 
-UNITS = [("tg_api", "tg_api.cu", []), ("tg_aux", "tg_aux.cu", [])] + [
+UNITS = [("tg_api", "tg_api.cu", []), ("tg_aux", "tg_aux.cu", []), ("tg_fp8", "tg_fp8.cu", []),
+         ("tg_quant", "tg_quant.cu", []), ("tg_router", "tg_router.cu", [])] + [
     (f"tg_inst_f{f}_m{m}", "tg_inst.cu", [f"-DTG_INST_F32={f}", f"-DTG_INST_MODE={m}"])
     for f in (0, 1) for m in (0, 1, 2)
 ]

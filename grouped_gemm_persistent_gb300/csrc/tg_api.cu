@@ -25,6 +25,7 @@
 #include <vector>
 
 #include "tg.h"
+#include "tg_host.cuh"
 #include "tg_launch.cuh"
 
 // Per-device record of the first in-kernel wait that ran out (zero at module load).
@@ -1101,3 +1102,72 @@ uint32_t tg_version(void) { return (0u << 16) | 2u; }
 uint64_t tg_launch_count(void) { return t_launches; }
 
 }  // extern "C"
+
+// ========================================================================================
+// What the other host translation units use (tg_host.cuh)
+
+namespace tg {
+namespace host {
+
+tg_status fail(tg_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return ::fail(s, "%s", buf);
+}
+
+tg_status cuda_fail(cudaError_t e, const char* what) { return ::cuda_fail(e, what); }
+
+tg_status device(Device* out) {
+    DeviceState* d = nullptr;
+    const tg_status s = device_state(&d);
+    if (s != TG_OK) return s;
+    out->id = d->dev;
+    out->sms = d->sms;
+    out->err = d->err;
+    return TG_OK;
+}
+
+tg_status workspace(size_t bytes, cudaStream_t stream, const char* what, void** out) {
+    DeviceState* d = nullptr;
+    tg_status s = device_state(&d);
+    if (s != TG_OK) return s;
+    cudaMemPool_t pool = nullptr;
+    if ((s = device_pool(d, &pool)) != TG_OK) return s;
+    const cudaError_t e = cudaMallocFromPoolAsync(out, bytes, pool, stream);
+    return e == cudaSuccess ? TG_OK : ::cuda_fail(e, what);
+}
+
+tg_status encoder() { return ::encoder(); }
+
+tg_status encode_bytes(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box, const char* what) {
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank), const_cast<void*>(ptr),
+                                d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return ::fail(TG_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what, int(r));
+    return TG_OK;
+}
+
+void launch_params(Params* p, ErrorRecord* err) {
+    const TraceArm trace = t_trace;
+    t_trace = TraceArm{};
+    base_params(p, err);
+    t_trace = trace;
+}
+
+void count_launches(int n) { t_launches += static_cast<uint64_t>(n); }
+
+}  // namespace host
+}  // namespace tg

@@ -1,0 +1,607 @@
+// tg_fp8.cuh - the 8-bit GEMM with a scale for each block of 128 along K.
+//
+//   C[m, n] = epilogue( sum_kb sa[m, kb] * sb[kb, n] * ( sum_{k in block kb} A[m, k] B[k, n] ) )
+//
+// The inner sum runs on the tensor cores (tcgen05.mma kind::f8f6f4, fp32 accumulator);
+// the scales are fp32 of any value, so the outer sum cannot stay in tensor memory: each
+// k-block's partial product is read back, scaled and added to fp32 registers.  One ring
+// stage is one scale block (128 bytes of K per row, four MMAs of K = 32).
+//
+//   warp 0       TMA producer: A and B k-blocks into a STAGES-deep ring.
+//   warp 1       MMA issuer: per k-block, four MMAs into one of two TMEM buffers, then a
+//                commit that frees the ring stage and one that hands the buffer over.
+//                It also allocates and frees tensor memory.
+//   warps 4-11   accumulation and epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and
+//                half the tile's columns: acc += scale * partial while the MMAs of the next
+//                k-block run; after the last k-block bias, GELU, rounding and the store.
+//
+// 256 x 256 tiles of a CTA pair: per k-block and SM the tensor cores need 512 cycles
+// (128 x 256 x 128 at 8192 MAC/cycle), reading back 128 x 256 fp32 takes 256 (one column
+// of 32 lanes a cycle and quarter) and the packed fma.rn.f32x2 additions 128 issue slots a
+// quarter, so the accumulation hides behind the MMAs; 128 accumulator registers a thread
+// for eight warps need the registers of the first four (setmaxnreg).
+//
+// Waits, aborts and draining are those of tg_kernel.cuh.
+#pragma once
+
+#include "tg_kernel.cuh"
+
+namespace tg {
+
+constexpr int F8_BK = 128;                 // K per stage: one scale block
+constexpr int F8_THREADS = 384;
+constexpr int F8_EPI_WARP0 = 4;
+constexpr int F8_EPI_WARPS = 8;
+
+// What the 8-bit form needs besides Params (whose `dense` problem holds the maps, sizes,
+// bias and epilogue; tma_c is unused).
+struct Fp8Params {
+    const float* sa;           // sa[(m >> sa_shift) * sa_mn + kb * sa_k]
+    const float* sb;           // sb[expert * sb_g + (n >> sb_shift) * sb_mn + kb * sb_k]
+    int64_t sa_mn, sa_k;
+    int64_t sb_mn, sb_k, sb_g;
+    int32_t sa_shift;          // 0: a scale per row, 7: per 128 rows
+    uint32_t a_mn, b_mn;       // A stored M-contiguous, B stored N-contiguous
+    uint32_t vec_c;            // rows of C are 16-byte aligned
+    void* c;
+    int64_t ldc;
+};
+
+template <int CTA_GROUP_, bool SB_COL_, bool MOE_>
+struct Fp8Config {
+    static constexpr int CTA_GROUP = CTA_GROUP_;
+    static constexpr bool SB_COL = SB_COL_;          // B has a scale per column (else per 128 columns)
+    static constexpr bool GROUPED = false;
+    static constexpr bool MOE = MOE_;
+    static constexpr int BN = 128 * CTA_GROUP;
+    static constexpr int BN_CTA = 128;
+    static constexpr int TILE_M = BM * CTA_GROUP;
+    static constexpr int COLS = BN / 2;              // columns one epilogue warp accumulates
+    static constexpr int A_BYTES = BM * F8_BK;
+    static constexpr int B_BYTES = BN_CTA * F8_BK;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int C_BYTES = F8_EPI_WARPS * C_STAGE_BYTES;
+    static constexpr int TABLE_BYTES = MOE ? 8 * (MOE_MAX_G + 1) : 0;
+    static constexpr int FIXED = C_BYTES + TABLE_BYTES + 512 + 1024;
+    static constexpr int STAGES = (SMEM_LIMIT - FIXED) / (A_BYTES + B_BYTES);
+    static constexpr int OFF_A = 0;
+    static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
+    static constexpr int OFF_C = OFF_B + STAGES * B_BYTES;
+    static constexpr int OFF_TABLE = OFF_C + C_BYTES;
+    static constexpr int OFF_BAR = OFF_TABLE + TABLE_BYTES;
+    static constexpr int NUM_BARS = 2 * STAGES + 5;
+    static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NUM_BARS;
+    static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
+    static constexpr int OFF_MOE_TOTAL = OFF_ABORT + 4;
+    static constexpr int OFF_DRAIN_FLAG = OFF_MOE_TOTAL + 4;
+    static constexpr int OFF_DRAIN_POS = OFF_DRAIN_FLAG + 4;
+    static constexpr int OFF_DRAIN_LAST = OFF_DRAIN_POS + 4;
+    static constexpr int OFF_DRAIN_BYTES = OFF_DRAIN_LAST + 4 * MAX_STAGES;
+    static constexpr int SMEM_BYTES = OFF_DRAIN_BYTES + 4 * MAX_STAGES + 1024;
+    static_assert(STAGES >= 2 && STAGES <= MAX_STAGES, "ring depth");
+    static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
+    static_assert(OFF_BAR % 8 == 0, "barrier alignment");
+};
+
+namespace f8 {
+
+// Prefix tables of a device-counts launch (one warp): rows and tiles before each expert, and the
+// number of tiles; 0 tiles and an error record when the counts are negative or exceed the rows.
+__device__ __forceinline__ int32_t build_moe_table(const Params& p, int tile_m, int64_t tiles_n, int32_t* tile_pref,
+                                                   int32_t* row_off, int lane) {
+    long long rows = 0, tiles = 0;
+    bool bad = false;
+    if (lane == 0) { tile_pref[0] = 0; row_off[0] = 0; }
+    for (int g0 = 0; g0 < p.moe_groups; g0 += 32) {
+        const int i = g0 + lane;
+        long long c = i < p.moe_groups ? static_cast<long long>(__ldg(p.moe_counts + i)) : 0ll;
+        bad |= c < 0;
+        c = c < 0 ? 0 : c;
+        long long t = (c + tile_m - 1) / tile_m * tiles_n;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long xc = __shfl_up_sync(0xffffffffu, c, d);
+            const long long xt = __shfl_up_sync(0xffffffffu, t, d);
+            if (lane >= d) { c += xc; t += xt; }
+        }
+        if (i < p.moe_groups) {
+            row_off[i + 1] = static_cast<int32_t>(min(rows + c, 0x7fffffffll));
+            tile_pref[i + 1] = static_cast<int32_t>(min(tiles + t, 0x7fffffffll));
+        }
+        rows += __shfl_sync(0xffffffffu, c, 31);
+        tiles += __shfl_sync(0xffffffffu, t, 31);
+    }
+    bad = __any_sync(0xffffffffu, bad) || rows > p.moe_rows || tiles > 0x7fffffffll;
+    if (bad && lane == 0 && blockIdx.x == 0 && atomicCAS(&p.err->code, ERR_NONE, ERR_COUNTS) == ERR_NONE) {
+        p.err->role = 0;
+        p.err->block = 0;
+        p.err->stage = 0;
+        p.err->tile = rows;
+        p.err->waited_ns = 0;
+    }
+    return bad ? 0 : static_cast<int32_t>(tiles);
+}
+
+// Wait for all tcgen05.ld of this thread; the registers they fill are operands, so no use of
+// them can be scheduled before the wait.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :: "memory");
+}
+
+// One k-block: four MMAs of K = 32 that start a new accumulator, the commit that frees the ring
+// stage (`empty`) and the one that hands the accumulator over (`tfull`).  Executed by a
+// converged warp; one elected lane issues.
+template <int CTA_GROUP>
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint64_t a_step, uint64_t b_step,
+                                          uint32_t idesc, uint32_t empty, uint32_t tfull) {
+    if constexpr (CTA_GROUP == 2)
+        asm volatile(
+            "{\n\t.reg .pred g, f, t;\n\t"
+            "elect.sync _|g, 0xffffffff;\n\t"
+            "setp.ne.u32 f, 0, 0;\n\t"
+            "setp.eq.u32 t, 0, 0;\n\t"
+            "@g tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %5, %9, f;\n\t"
+            "@g tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %2, %6, %9, t;\n\t"
+            "@g tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %3, %7, %9, t;\n\t"
+            "@g tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %4, %8, %9, t;\n\t"
+            "@g tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%10], %12;\n\t"
+            "@g tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%11], %12;\n\t"
+            "}"
+            :: "r"(d), "l"(a), "l"(a + a_step), "l"(a + 2 * a_step), "l"(a + 3 * a_step), "l"(b), "l"(b + b_step),
+               "l"(b + 2 * b_step), "l"(b + 3 * b_step), "r"(idesc), "r"(empty), "r"(tfull),
+               "h"(static_cast<uint16_t>(0x3)) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred g, f, t;\n\t"
+            "elect.sync _|g, 0xffffffff;\n\t"
+            "setp.ne.u32 f, 0, 0;\n\t"
+            "setp.eq.u32 t, 0, 0;\n\t"
+            "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %5, %9, f;\n\t"
+            "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %2, %6, %9, t;\n\t"
+            "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %3, %7, %9, t;\n\t"
+            "@g tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %4, %8, %9, t;\n\t"
+            "@g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t"
+            "@g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n\t"
+            "}"
+            :: "r"(d), "l"(a), "l"(a + a_step), "l"(a + 2 * a_step), "l"(a + 3 * a_step), "l"(b), "l"(b + b_step),
+               "l"(b + 2 * b_step), "l"(b + 3 * b_step), "r"(idesc), "r"(empty), "r"(tfull) : "memory");
+}
+
+// Eight bf16 values from column `col` of a bias of N values (zeros past its end) as fp32.
+__device__ __forceinline__ void load_bias8(const uint16_t* bias, int col, int N, float (&b)[8]) {
+    const uint16_t* p = bias + col;
+    if (col + 8 <= N && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[2 * i] = __uint_as_float(ws[i] << 16);
+            b[2 * i + 1] = __uint_as_float(ws[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            b[i] = col + i < N ? __uint_as_float(static_cast<uint32_t>(__ldg(p + i)) << 16) : 0.0f;
+    }
+}
+
+template <int REGS>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(REGS)); }
+template <int REGS>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REGS)); }
+
+// Columns [n, n + 128 / esize) of 32 rows, one row a lane: rounded, staged in 4 KiB of shared
+// memory (16-byte chunks swizzled by the row, so that neither side has bank conflicts), read back
+// eight lanes to a row and stored as 128-byte row pieces.  v holds the fp32 values.
+template <bool F32, int CW>
+__device__ __forceinline__ void store_rows(const float (&v)[CW], uint32_t stage, const Fp8Params& x, bool c_f16,
+                                           int row0, int row_limit, int n, int N, int lane) {
+    constexpr int PER = F32 ? 4 : 8;      // columns in 16 bytes
+    __syncwarp();                         // the previous chunk has been read back
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) w[i] = __float_as_uint(v[4 * j + i]);
+            else w[i] = c_f16 ? pack_f16x2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1])
+                              : pack_bf16x2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(stage + lane * 128 + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4)), "r"(w[0]), "r"(w[1]),
+                        "r"(w[2]), "r"(w[3]) : "memory");
+    }
+    __syncwarp();
+    const int j = lane % 8, col = n + j * PER;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + lane / 8;
+        const float4 w = ptx::ld_shared_f4(stage + r * 128 + ((static_cast<uint32_t>(j) ^ (r & 7u)) << 4));
+        if (row0 + r >= row_limit || col >= N) continue;
+        const int64_t at = static_cast<int64_t>(row0 + r) * x.ldc + col;
+        const uint32_t ws[4] = {__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w)};
+        if (x.vec_c && col + PER <= N) {
+            if constexpr (F32) __stcs(reinterpret_cast<float4*>(static_cast<float*>(x.c) + at), w);
+            else __stcs(reinterpret_cast<float4*>(static_cast<uint16_t*>(x.c) + at), w);
+        } else if constexpr (F32) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (col + c < N) static_cast<uint32_t*>(x.c)[at + c] = ws[c];
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (col + c < N) static_cast<uint16_t*>(x.c)[at + c] = static_cast<uint16_t>(ws[c / 2] >> ((c & 1) * 16));
+        }
+    }
+}
+
+}  // namespace f8
+
+// ----------------------------------------------------------------------------------------
+
+template <class Cfg>
+__global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constant__ Params p,
+                                                            const __grid_constant__ Fp8Params x) {
+    constexpr int STAGES = Cfg::STAGES;
+    constexpr int CG = Cfg::CTA_GROUP;
+    constexpr int BN = Cfg::BN;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const uint32_t sA = base + Cfg::OFF_A, sB = base + Cfg::OFF_B, sC = base + Cfg::OFF_C;
+    const uint32_t bar0 = base + Cfg::OFF_BAR;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+    const uint32_t abort_addr = base + Cfg::OFF_ABORT;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int64_t unit = blockIdx.x / CG, num_units = gridDim.x / CG;
+
+    // ---- set-up
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(tfull_bar(b), 1);
+            ptx::mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        st_shared_u32(abort_addr, 0u);
+        st_shared_u32(base + Cfg::OFF_DRAIN_FLAG, 0u);
+        st_shared_u32(base + Cfg::OFF_DRAIN_POS, 0u);
+        for (int s = 0; s < MAX_STAGES; ++s) {
+            st_shared_u32(base + Cfg::OFF_DRAIN_LAST + 4 * s, 0xffffffffu);
+            st_shared_u32(base + Cfg::OFF_DRAIN_BYTES + 4 * s, 0u);
+        }
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&p.dense.tma_a);
+        ptx::prefetch_tensormap(&p.dense.tma_b);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<CG>(base + Cfg::OFF_TMEM_SLOT, Cfg::TMEM_COLS);
+        ptx::tmem_relinquish<CG>();
+    }
+    MoeTable mt{};
+    if constexpr (Cfg::MOE) {
+        int32_t* tile_pref = reinterpret_cast<int32_t*>(smem + Cfg::OFF_TABLE);
+        int32_t* row_off = tile_pref + (MOE_MAX_G + 1);
+        if (warp == 2) {
+            const int32_t n = f8::build_moe_table(p, Cfg::TILE_M, p.dense.tiles_n, tile_pref, row_off, lane);
+            if (lane == 0) *reinterpret_cast<volatile int32_t*>(smem + Cfg::OFF_MOE_TOTAL) = n;
+        }
+        mt.tile_pref = tile_pref;
+        mt.row_off = row_off;
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_TMEM_SLOT);
+    int64_t total_tiles = p.total_tiles;
+    if constexpr (Cfg::MOE) total_tiles = *reinterpret_cast<volatile int32_t*>(smem + Cfg::OFF_MOE_TOTAL);
+
+    // Registers: 384 x 168 at launch = 64512 >= 128 x 80 + 256 x 208 = 63488.  Each split stands at
+    // the head of its own branch: after a common one the compiler kept to the smaller count.
+    const Problem& pr = p.dense;
+    if (warp < F8_EPI_WARP0) {
+    f8::regs_dec<80>();
+    if (warp == 0) {
+        // ================================ TMA producer ================================
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, pos = 0;
+            int g = 0;
+            bool aborted = false;
+            bool withhold = p.withhold_kb >= 0 && blockIdx.x == static_cast<uint32_t>(p.withhold_block);
+            constexpr uint32_t TX = Cfg::A_BYTES + Cfg::B_BYTES;
+            Sched sc = sched_begin<Cfg>(p, unit);
+            Work w;
+            while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
+                g = find_problem<Cfg>(p, w.t, g, mt);
+                const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
+                const int nb0 = tc.n0 + static_cast<int>(rank) * Cfg::BN_CTA;
+                for (int kb = 0; kb < pr.k_blocks; ++kb) {
+                    if (!ptx::mbar_test_wait(empty_bar(stage), phase ^ 1u) &&
+                        !wait_bounded<CG>(empty_bar(stage), phase ^ 1u, p, abort_addr, ROLE_PRODUCER, w.slot, stage)) {
+                        aborted = true;
+                        break;
+                    }
+                    if (!(withhold && kb == p.withhold_kb)) {
+                        const uint32_t fb = CG == 2 ? ptx::mapa(full_bar(stage), 0) : full_bar(stage);
+                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), TX * CG);
+                        const int k0 = kb * F8_BK;
+                        const uint32_t a_dst = sA + stage * Cfg::A_BYTES, b_dst = sB + stage * Cfg::B_BYTES;
+                        const int ax = x.a_mn ? tc.m0 : k0, ay = x.a_mn ? k0 : tc.m0;
+                        const int bx = x.b_mn ? nb0 : k0, by = x.b_mn ? k0 : nb0;
+                        if constexpr (CG == 2) ptx::tma_load_2d_pair(a_dst, &pr.tma_a, ax, ay, fb);
+                        else ptx::tma_load_2d(a_dst, &pr.tma_a, ax, ay, fb);
+                        if constexpr (Cfg::MOE) {
+                            if constexpr (CG == 2) ptx::tma_load_3d_pair(b_dst, &pr.tma_b, bx, by, g, fb);
+                            else ptx::tma_load_3d(b_dst, &pr.tma_b, bx, by, g, fb);
+                        } else {
+                            if constexpr (CG == 2) ptx::tma_load_2d_pair(b_dst, &pr.tma_b, bx, by, fb);
+                            else ptx::tma_load_2d(b_dst, &pr.tma_b, bx, by, fb);
+                        }
+                        st_shared_u32(base + Cfg::OFF_DRAIN_LAST + 4 * stage, pos);
+                        st_shared_u32(base + Cfg::OFF_DRAIN_BYTES + 4 * stage, TX);
+                    }
+                    ++pos;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                withhold = false;
+            }
+            if (!aborted) {
+                // Tail: every slot released, so no commit arrives here after this CTA leaves.
+                for (int i = 0; i < STAGES; ++i) {
+                    if (!wait_bounded<CG>(empty_bar(stage), phase ^ 1u, p, abort_addr, ROLE_PRODUCER, -1, stage)) {
+                        aborted = true;
+                        break;
+                    }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            st_shared_u32(base + Cfg::OFF_DRAIN_POS, pos);
+            ptx::st_release_cluster_u32(base + Cfg::OFF_DRAIN_FLAG, 1u);
+            if (aborted && leader) drain_issued_loads<Cfg>(p, base);
+        }
+    } else if (warp == 1) {
+        // ================================ MMA issuer ================================
+        if (leader) {
+            int stage = 0, acc = 0, g = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool aborted = false, any_mma = false;
+            // 8-row (K-major) or 8-k (MN-major) groups are 1024 bytes apart; the next 32 k of a
+            // stage are 32 bytes along the row, or 32 rows of 128 bytes down
+            const uint64_t a_desc0 = ptx::smem_desc_sw128(sA, 16, 1024), b_desc0 = ptx::smem_desc_sw128(sB, 16, 1024);
+            const uint64_t a_step = x.a_mn ? 4096u >> 4 : 32u >> 4, b_step = x.b_mn ? 4096u >> 4 : 32u >> 4;
+            auto warp_wait = [&](uint32_t bar, uint32_t par, int64_t tile, uint32_t st) -> bool {
+                if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, par))) return true;
+                uint32_t ok = 1;
+                if (lane == 0) ok = wait_bounded<CG, false>(bar, par, p, abort_addr, ROLE_MMA, tile, st) ? 1u : 0u;
+                return __shfl_sync(0xffffffffu, ok, 0) != 0;
+            };
+            Sched sc = sched_begin<Cfg>(p, unit);
+            Work w;
+            while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
+                g = find_problem<Cfg>(p, w.t, g, mt);
+                uint32_t idesc = pr.idesc;
+                if (tile_coord<Cfg>(p, w.t, g, rank, mt).half) idesc = (idesc & ~(0x1Fu << 24)) | ((128u >> 4) << 24);
+                for (int kb = 0; kb < pr.k_blocks; ++kb) {
+                    if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, w.slot, 16 + acc) ||
+                        !warp_wait(full_bar(stage), phase, w.slot, stage)) {
+                        aborted = true;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    f8::mma_block<CG>(tmem_base + static_cast<uint32_t>(acc * BN),
+                                      a_desc0 + static_cast<uint64_t>((stage * Cfg::A_BYTES) >> 4),
+                                      b_desc0 + static_cast<uint64_t>((stage * Cfg::B_BYTES) >> 4), a_step, b_step, idesc,
+                                      empty_bar(stage), tfull_bar(acc));
+                    any_mma = true;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                }
+            }
+            if (aborted && any_mma && lane == 0) {
+                if constexpr (CG == 2) ptx::mma_commit_pair(drain_bar, 0x1);
+                else ptx::mma_commit(drain_bar);
+                if (!wait_quiet(drain_bar, 0, p.wait_budget_ns)) report_timeout(p, ROLE_DRAIN, -1, 0, p.wait_budget_ns);
+            }
+            __syncwarp();
+        }
+    }
+    } else {
+        f8::regs_inc<208>();
+        // ================================ accumulation and epilogue ================================
+        constexpr int COLS = Cfg::COLS;
+        const int q = warp % 4, h = (warp - F8_EPI_WARP0) / 4;
+        const uint32_t stage_c = sC + (warp - F8_EPI_WARP0) * C_STAGE_BYTES;
+        int buf = 0, g = 0;
+        uint32_t buf_phase = 0;
+        bool aborted = false;
+        Sched sc = sched_begin<Cfg>(p, unit);
+        Work w;
+        while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
+            g = find_problem<Cfg>(p, w.t, g, mt);
+            const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
+            // a half tile keeps 64 rows in lanes 0-63 (columns [0, BN/2)) and again in lanes 64-127
+            // (columns [BN/2, BN)), in BN/2 TMEM columns: the two warps of a quarter split those
+            const int row0 = tc.m0 + (tc.half ? (q % 2) * 32 : q * 32);
+            const int n0 = tc.n0 + (tc.half ? (q / 2) * (BN / 2) + h * (BN / 4) : h * COLS);
+            const int n_cols = tc.half ? COLS / 2 : COLS;
+            const uint32_t t_col = static_cast<uint32_t>(tc.half ? h * (BN / 4) : h * COLS);
+            int row_limit = pr.M;
+            if constexpr (Cfg::MOE) row_limit = static_cast<int>(min(static_cast<int64_t>(tc.row_end), p.moe_rows));
+            const bool active = row0 < row_limit && n0 < pr.N;
+
+            // scales: this lane's row, and one value (or, per column, COLS / 32 of this lane) of B;
+            // fetched PF k-blocks ahead of their use
+            constexpr int PF = 4;
+            constexpr int NB = Cfg::SB_COL ? COLS / 32 : 1;
+            const int row = min(row0 + lane, row_limit - 1);
+            const float* pa = x.sa + static_cast<int64_t>(row >> x.sa_shift) * x.sa_mn;
+            const float* pb[NB];
+            bool col_ok[NB];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int n = Cfg::SB_COL ? n0 + j * 32 + lane : n0;
+                col_ok[j] = active && n < pr.N;
+                pb[j] = x.sb + static_cast<int64_t>(Cfg::SB_COL ? n : n >> 7) * x.sb_mn +
+                        (Cfg::MOE ? static_cast<int64_t>(g) * x.sb_g : 0);
+            }
+            float fa[PF], fb[PF][NB];
+            auto fetch = [&](int kb, float& a, float (&b)[NB]) {
+                const bool ok = active && kb < pr.k_blocks;
+                a = ok ? __ldg(pa + kb * x.sa_k) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) b[j] = ok && col_ok[j] ? __ldg(pb[j] + kb * x.sb_k) : 0.0f;
+            };
+#pragma unroll
+            for (int i = 0; i < PF; ++i) fetch(i, fa[i], fb[i]);
+
+            uint64_t acc[COLS / 2];
+#pragma unroll
+            for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+#pragma unroll 1
+            for (int kb = 0; kb < pr.k_blocks; ++kb) {
+                const float sa = fa[0];
+                float sb[NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) sb[j] = fb[0][j];
+#pragma unroll
+                for (int i = 0; i + 1 < PF; ++i) {
+                    fa[i] = fa[i + 1];
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) fb[i][j] = fb[i + 1][j];
+                }
+                fetch(kb + PF, fa[PF - 1], fb[PF - 1]);
+                uint32_t sb_smem = stage_c + static_cast<uint32_t>(kb & 1) * (COLS * 4);
+                if constexpr (Cfg::SB_COL) {
+                    if (kb == 0) __syncwarp();     // the previous tile's staging has been read back
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) st_shared_u32(sb_smem + (j * 32 + lane) * 4, __float_as_uint(sb[j]));
+                    __syncwarp();
+                }
+                uint32_t ok = 1;
+                if (lane == 0)
+                    ok = wait_bounded<CG>(tfull_bar(buf), buf_phase, p, abort_addr, ROLE_EPILOGUE, w.slot, 16 + buf) ? 1u : 0u;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) { aborted = true; break; }
+                ptx::tc_fence_after_sync();
+                const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN) + t_col;
+                const uint64_t s2 = Cfg::SB_COL ? ptx::f32x2_pack(sa, sa) : ptx::f32x2_pack(sa * sb[0], sa * sb[0]);
+                uint32_t r[2][32];
+                if (active) ptx::tmem_ld_32x32b_x32(t, r[0]);
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    const bool mine = active && c * 32 < n_cols;
+                    if (mine) {
+                        f8::tmem_ld_wait32(r[c & 1]);
+                        if (c + 1 < COLS / 32 && (c + 1) * 32 < n_cols) ptx::tmem_ld_32x32b_x32(t + (c + 1) * 32, r[(c + 1) & 1]);
+                    }
+                    if (c + 1 == COLS / 32) {
+                        // everything is in registers: the buffer goes back to the MMA issuer
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (CG == 2 && !leader) ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(buf), 0));
+                            else ptx::mbar_arrive(tempty_bar(buf));
+                        }
+                    }
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            uint64_t v = ptx::f32x2_pack(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1]));
+                            if constexpr (Cfg::SB_COL) {
+                                if (i % 2 == 0) {
+                                    const float4 f = ptx::ld_shared_f4(sb_smem + (c * 32 + 2 * i) * 4);
+                                    const uint64_t v1 = ptx::f32x2_pack(__uint_as_float(r[c & 1][2 * i + 2]),
+                                                                        __uint_as_float(r[c & 1][2 * i + 3]));
+                                    acc[c * 16 + i] = ptx::f32x2_fma(ptx::f32x2_mul(v, ptx::f32x2_pack(f.x, f.y)), s2,
+                                                                     acc[c * 16 + i]);
+                                    acc[c * 16 + i + 1] = ptx::f32x2_fma(ptx::f32x2_mul(v1, ptx::f32x2_pack(f.z, f.w)), s2,
+                                                                         acc[c * 16 + i + 1]);
+                                }
+                            } else {
+                                acc[c * 16 + i] = ptx::f32x2_fma(v, s2, acc[c * 16 + i]);
+                            }
+                        }
+                    }
+                }
+                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            }
+            if (aborted) break;
+            if (!active) continue;
+
+            // epilogue: 32 columns at a time into values, bias, GELU; 64 (16-bit) or 32 (fp32) to a store
+            const uint16_t* bias = static_cast<const uint16_t*>(pr.bias);
+            if constexpr (Cfg::MOE) { if (bias) bias += static_cast<int64_t>(g) * pr.N; }
+            const int epi = pr.epi;
+            // columns [C0, C0 + CW) of this warp's
+            auto finish = [&](auto first, auto& v) {
+                constexpr int C0 = decltype(first)::value;
+                constexpr int CW = static_cast<int>(sizeof(v) / sizeof(float));
+#pragma unroll
+                for (int j = 0; j < CW / 8; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        ptx::f32x2_unpack(acc[C0 / 2 + 4 * j + i], v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+                    if (epi != EPI_NONE) {
+                        float b[8];
+                        f8::load_bias8(bias, n0 + C0 + 8 * j, pr.N, b);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
+                        if (epi == EPI_BIAS_GELU) {
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) gelu_tanh_f32x2(v[8 * j + i], v[8 * j + i + 1]);
+                        }
+                    }
+                }
+            };
+            const bool f32 = (pr.flags & FLAG_C_F32) != 0, f16 = (pr.flags & FLAG_C_F16) != 0;
+            auto chunk = [&](auto first, auto f32_tag) {
+                constexpr int C0 = decltype(first)::value;
+                constexpr bool F32 = decltype(f32_tag)::value;
+                if (C0 < n_cols && n0 + C0 < pr.N) {
+                    float v[F32 ? 32 : 64];
+                    finish(first, v);
+                    f8::store_rows<F32>(v, stage_c, x, f16, row0, row_limit, n0 + C0, pr.N, lane);
+                }
+            };
+            using std::integral_constant;
+            if (f32) {
+                chunk(integral_constant<int, 0>{}, std::true_type{});
+                chunk(integral_constant<int, 32>{}, std::true_type{});
+                if constexpr (COLS > 64) {
+                    chunk(integral_constant<int, 64>{}, std::true_type{});
+                    chunk(integral_constant<int, 96>{}, std::true_type{});
+                }
+            } else {
+                chunk(integral_constant<int, 0>{}, std::false_type{});
+                if constexpr (COLS > 64) chunk(integral_constant<int, 64>{}, std::false_type{});
+            }
+            __syncwarp();
+        }
+    }
+
+    // ---- teardown
+    __syncwarp();
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    ptx::tc_fence_after_sync();
+    if (warp == 1) ptx::tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
+}
+
+}  // namespace tg

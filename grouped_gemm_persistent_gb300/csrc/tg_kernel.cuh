@@ -114,6 +114,7 @@ enum : uint32_t {
     // Each TMA instruction costs the producer about as much as a quarter of an MMA
     // k-block, so one box instead of BN_CTA / 64 keeps the ring ahead of the MMA.
     FLAG_B_WIDE = 4u,
+    FLAG_C_F32 = 8u,      // fp32 output (the 8-bit kernels, whose output type is not a template argument)
 };
 
 struct Params {

@@ -417,6 +417,15 @@ __host__ __device__ constexpr uint32_t idesc_f32_acc(uint32_t M, uint32_t N, boo
            ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// Instruction descriptor for tcgen05.mma.kind::f8f6f4 with an fp32 accumulator: as above with
+// 8-bit operand formats (0 = e4m3, 1 = e5m2), which may differ.
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, bool a_mn_major, bool b_mn_major, bool a_e5m2,
+                                                bool b_e5m2) {
+    return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(b_e5m2) << 10) |
+           (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(b_mn_major) << 16) |
+           ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
 // cp.async: 16-byte asynchronous copies global -> shared (L2 only), per-thread groups
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");

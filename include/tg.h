@@ -88,7 +88,9 @@ typedef enum {
 typedef enum {
     TG_BF16 = 0,  /* bfloat16; as output, rounded once to nearest even from the fp32 epilogue value */
     TG_F32 = 1,   /* output only: the fp32 epilogue value itself */
-    TG_F16 = 2    /* IEEE binary16 (the TLX listing's type); as output, rounded once to nearest even */
+    TG_F16 = 2,   /* IEEE binary16 (the TLX listing's type); as output, rounded once to nearest even */
+    TG_E4M3 = 3,  /* 8-bit float, 4 exponent and 3 mantissa bits, no infinity, largest 448: operands of the 8-bit products */
+    TG_E5M2 = 4   /* 8-bit float, 5 exponent and 2 mantissa bits, largest finite 57344: operands of the 8-bit products */
 } tg_dtype;
 
 /*
@@ -265,6 +267,132 @@ tg_status tg_moe_gemm(const void *A, int64_t lda, int64_t T, int64_t K,
                       void *C, tg_dtype c_dtype, int64_t ldc,
                       const int32_t *counts, tg_epilogue epi, const void *bias,
                       tg_stream_t stream);
+
+/*
+ * tg_quantize_fp8 - Q, an 8-bit copy of X with one scale for each block of 128 values:
+ * X[m][k] = scale(block of (m, k)) * Q[m][k], up to Q's rounding.
+ *
+ * For a block with largest magnitude a and the type's largest finite value t (448 or
+ * 57344), scale is the smallest power of two s >= 2^-126 with a <= t * s, and
+ * Q = X / s rounded once to nearest even.  A block of zeros has scale 1.  A block with
+ * an infinity or a NaN has scale NaN and zeros in Q: products with it are NaN.
+ *
+ *   X, x_dtype, ldx  : M x K row-major bf16, fp16 or fp32, any alignment (16-byte
+ *                      aligned rows are read with wide loads).
+ *   block_rows x block_cols, scale, scale_ld :
+ *       1 x 128   blocks along a row:    scale[(k / 128) * scale_ld + m], scale_ld >= M
+ *       128 x 1   blocks along a column: scale[(m / 128) * scale_ld + k], scale_ld >= K
+ *       128 x 128                        scale[(m / 128) * scale_ld + k / 128],
+ *                                        scale_ld >= ceil(K / 128)
+ *     The last block of a row or column may be shorter.
+ *   Q, q_dtype, ldq  : M x K row-major TG_E4M3 or TG_E5M2.  The 8-bit products need
+ *                      16-byte aligned Q with ldq a multiple of 16; this call does not.
+ * M == 0 or K == 0 is a no-op.
+ */
+tg_status tg_quantize_fp8(const void *X, tg_dtype x_dtype, int64_t ldx, int64_t M, int64_t K,
+                          int block_rows, int block_cols,
+                          void *Q, tg_dtype q_dtype, int64_t ldq, float *scale, int64_t scale_ld,
+                          tg_stream_t stream);
+
+/*
+ * An operand of an 8-bit product: A (M x K) or B (K x N) with its scales.  K is cut into
+ * blocks of 128; the scale of element (i, k), i being A's row or B's column, is
+ *     scale[(i / block) * scale_stride + (k / 128) * scale_k_stride]
+ * with block = 1 (a scale per row of A or column of B) or 128.  Scales are any fp32
+ * values (not only powers of two); strides are non-negative, in elements.
+ */
+typedef struct tg_fp8_operand {
+    const void *data;          /* DEVICE, 16-byte aligned */
+    int64_t ld;                /* as lda / ldb of tg_gemm, a multiple of 16 */
+    const float *scale;        /* DEVICE */
+    int64_t scale_stride;
+    int64_t scale_k_stride;
+    tg_dtype dtype;            /* TG_E4M3 or TG_E5M2; A's and B's may differ */
+    tg_layout layout;
+    int block;                 /* 1 or 128 */
+} tg_fp8_operand;
+
+/*
+ * tg_gemm_fp8 - C[M,N] = epilogue( sum over k of A[m][k] scale_A[m][k/128] B[k][n] scale_B[k/128][n] ).
+ *
+ * The products of one block of 128 k are summed by the tensor cores in fp32; the
+ * blocks' sums are scaled and added in fp32 registers, in an order fixed by the sizes
+ * (two identical calls write identical C), and the epilogue rounds once.  C, epi and
+ * bias (bf16[N]) are as in tg_gemm, except that C needs only the alignment of its
+ * elements.  K == 0 gives epilogue(0); M == 0 or N == 0 is a no-op.
+ *
+ * The three products of a linear layer Y = X W with X [T, in], W [in, out]:
+ *   Y  = X . W          X in 1 x 128 blocks, W in 128 x 128 blocks
+ *   dX = dY . W^T       dY in 1 x 128 blocks, the same W with the other layout
+ *   dW = X^T . dY       X and dY in 128 x 1 blocks: column-major A, row-major B, block 1
+ */
+tg_status tg_gemm_fp8(const tg_fp8_operand *A, const tg_fp8_operand *B, void *C, tg_dtype c_dtype, int64_t ldc,
+                      int64_t M, int64_t N, int64_t K, tg_epilogue epi, const void *bias, tg_stream_t stream);
+
+/*
+ * tg_moe_gemm_fp8 - tg_moe_gemm with 8-bit operands: expert g multiplies rows
+ * [off_g, off_g + counts[g]) of A by its own B, the counts staying in device memory.
+ *
+ *   A, T, K          : row-major, a scale per row (block 1).
+ *   B, expert_stride, scale_stride, G, N :
+ *                      expert g's B starts at data + g * expert_stride (a multiple of 16
+ *                      elements), its scales at scale + g * scale_stride; block 128.
+ *   C, counts, epi, bias ([G, N]) and the treatment of bad counts: as tg_moe_gemm
+ *                      (C as in tg_gemm_fp8); G <= TG_MOE_MAX_EXPERTS.
+ * An expert's gradient by its weights is the tg_gemm_fp8 of its rows' slices, quantised
+ * in 128 x 1 blocks that start at the expert's first row.
+ */
+tg_status tg_moe_gemm_fp8(const tg_fp8_operand *A, int64_t T, int64_t K, const tg_fp8_operand *B,
+                          int64_t expert_stride, int64_t scale_stride, int64_t G, int64_t N,
+                          void *C, tg_dtype c_dtype, int64_t ldc, const int32_t *counts,
+                          tg_epilogue epi, const void *bias, tg_stream_t stream);
+
+/* Largest number of experts and of choices per token tg_moe_router accepts. */
+#define TG_MOE_ROUTER_MAX_EXPERTS 1024
+#define TG_MOE_ROUTER_MAX_TOP_K 32
+
+/*
+ * tg_moe_router - the gate of a mixture-of-experts layer: each token's k experts, their
+ * weights, the tokens of each expert (the counts that tg_moe_gemm and tg_moe_gemm_fp8
+ * read) and the balance loss.
+ *
+ * With p[t] = softmax(logits[t]) and n = the number of rows with a logit above -infinity:
+ *   experts[t * k + j]  the expert of the j-th largest logit, ties to the lowest index;
+ *                       -1 where the row has no further logit above -infinity
+ *   weights[t * k + j]  its p (0 where experts is -1), divided by the sum of the row's
+ *                       chosen p when renormalize is not 0
+ *   counts[g]           the number of (t, j) with experts[t][j] == g
+ *   loss                G * sum_g f_g P_g, f_g = counts[g] / (n k), P_g = sum_t p[t][g] / n
+ *                       (0 when n == 0); 1 when both are uniform
+ *   slope[g]            d loss / d p[t][g] = G f_g / n, kept for tg_moe_router_backward
+ * A row of -infinity (a padding token) chooses nothing and counts nowhere.  NaN counts as
+ * above every number; a row with a NaN or a +infinity has NaN probabilities.
+ *
+ *   logits, dtype, ld : T x G row-major bf16, fp16 or fp32, any alignment.
+ *   experts, weights  : DEVICE int32 and fp32 [T, k]; counts DEVICE int32 [G]; loss DEVICE
+ *                       fp32; slope DEVICE fp32 [G].
+ * 1 <= k <= min(G, TG_MOE_ROUTER_MAX_TOP_K), G <= TG_MOE_ROUTER_MAX_EXPERTS, T * k below
+ * 2^31.  T == 0 writes zeros to counts, loss and slope.  Deterministic.
+ */
+tg_status tg_moe_router(const void *logits, tg_dtype dtype, int64_t ld, int64_t T, int64_t G, int64_t k,
+                        int renormalize, int32_t *experts, float *weights, int32_t *counts, float *loss,
+                        float *slope, tg_stream_t stream);
+
+/*
+ * tg_moe_router_backward - the gradient of the logits.
+ *
+ *   logits .. weights, slope : what tg_moe_router was given and wrote (renormalize the same).
+ *   d_weights : DEVICE fp32 [T, k], the gradient of weights; entries of experts == -1 are
+ *               not used.  NULL: zero (experts and weights may then be NULL).
+ *   d_loss    : DEVICE fp32, the gradient of loss.  NULL: zero (slope may then be NULL).
+ *   d_logits, ldd : T x G of the logits' type, rounded once.  Zero where the logit is
+ *               -infinity.
+ * The counts are constant in the logits: the loss's gradient goes through p alone.
+ */
+tg_status tg_moe_router_backward(const void *logits, tg_dtype dtype, int64_t ld, int64_t T, int64_t G, int64_t k,
+                                 int renormalize, const int32_t *experts, const float *weights, const float *slope,
+                                 const float *d_weights, const float *d_loss, void *d_logits, int64_t ldd,
+                                 tg_stream_t stream);
 
 /*
  * Largest number of non-empty problems tg_grouped_gemm_noalloc accepts in one
