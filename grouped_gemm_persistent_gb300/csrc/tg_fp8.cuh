@@ -11,6 +11,10 @@
 //   warp 1       MMA issuer: per k-block, four MMAs into one of two TMEM buffers, then a
 //                commit that frees the ring stage and one that hands the buffer over.
 //                It also allocates and frees tensor memory.
+//   warps 2, 3   scale loaders: A's and B's scales of the k-blocks ahead, by cp.async into a
+//                ring of their own.  (Loaded by the accumulating warps into registers, four
+//                k-blocks ahead, they made every tcgen05.wait::ld wait for global loads:
+//                8192^3 took 1340 us.)
 //   warps 4-11   accumulation and epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and
 //                half the tile's columns: acc += scale * partial while the MMAs of the next
 //                k-block run; after the last k-block bias, GELU, rounding and the store.
@@ -32,6 +36,8 @@ constexpr int F8_BK = 128;                 // K per stage: one scale block
 constexpr int F8_THREADS = 384;
 constexpr int F8_EPI_WARP0 = 4;
 constexpr int F8_EPI_WARPS = 8;
+constexpr int F8_SLOTS = 8;                // k-blocks of scales in flight
+constexpr int F8_C_STAGE = 32 * 64;        // per-warp store staging: 32 rows of 64 bytes
 
 // What the 8-bit form needs besides Params (whose `dense` problem holds the maps, sizes,
 // bias and epilogue; tma_c is unused).
@@ -60,16 +66,20 @@ struct Fp8Config {
     static constexpr int A_BYTES = BM * F8_BK;
     static constexpr int B_BYTES = BN_CTA * F8_BK;
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int C_BYTES = F8_EPI_WARPS * C_STAGE_BYTES;
+    static constexpr int C_BYTES = F8_EPI_WARPS * F8_C_STAGE;
+    static constexpr int SB_COUNT = SB_COL ? BN : BN / 128;      // B scales of a tile and k-block
+    static constexpr int SLOT_BYTES = (BM + (SB_COL ? BN : 4)) * 4;
+    static constexpr int SCALE_BYTES = F8_SLOTS * SLOT_BYTES;
     static constexpr int TABLE_BYTES = MOE ? 8 * (MOE_MAX_G + 1) : 0;
-    static constexpr int FIXED = C_BYTES + TABLE_BYTES + 512 + 1024;
+    static constexpr int FIXED = C_BYTES + SCALE_BYTES + TABLE_BYTES + 512 + 1024;
     static constexpr int STAGES = (SMEM_LIMIT - FIXED) / (A_BYTES + B_BYTES);
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_C = OFF_B + STAGES * B_BYTES;
-    static constexpr int OFF_TABLE = OFF_C + C_BYTES;
+    static constexpr int OFF_SCALE = OFF_C + C_BYTES;
+    static constexpr int OFF_TABLE = OFF_SCALE + SCALE_BYTES;
     static constexpr int OFF_BAR = OFF_TABLE + TABLE_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 5;
+    static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * F8_SLOTS;
     static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NUM_BARS;
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
     static constexpr int OFF_MOE_TOTAL = OFF_ABORT + 4;
@@ -189,21 +199,49 @@ __device__ __forceinline__ void load_bias8(const uint16_t* bias, int col, int N,
     }
 }
 
+// f(integral_constant 0), ..., f(integral_constant N - 1)
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_each(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        for_each<N, I + 1>(f);
+    }
+}
+
 template <int REGS>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(REGS)); }
 template <int REGS>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REGS)); }
 
-// Columns [n, n + 128 / esize) of 32 rows, one row a lane: rounded, staged in 4 KiB of shared
+// A 4-byte asynchronous copy global -> shared, zero-filled when !ok (src is then not read), and
+// an arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+
+// Arrive on a barrier of the pair's other CTA.  The release is of CTA scope: what it orders are
+// this thread's tensor-memory loads, complete by tcgen05.wait::ld; with cluster scope every
+// arrival waited for the warp's outstanding global and local accesses.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+}
+
+// Columns [n, n + 64 / esize) of 32 rows, one row a lane: rounded, staged in 2 KiB of shared
 // memory (16-byte chunks swizzled by the row, so that neither side has bank conflicts), read back
-// eight lanes to a row and stored as 128-byte row pieces.  v holds the fp32 values.
+// four lanes to a row and stored as 64-byte row pieces.  v holds the fp32 values.
 template <bool F32, int CW>
 __device__ __forceinline__ void store_rows(const float (&v)[CW], uint32_t stage, const Fp8Params& x, bool c_f16,
                                            int row0, int row_limit, int n, int N, int lane) {
     constexpr int PER = F32 ? 4 : 8;      // columns in 16 bytes
+    static_assert(CW == 4 * PER, "64 bytes a row");
     __syncwarp();                         // the previous chunk has been read back
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -212,15 +250,15 @@ __device__ __forceinline__ void store_rows(const float (&v)[CW], uint32_t stage,
                               : pack_bf16x2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
         }
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(stage + lane * 128 + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4)), "r"(w[0]), "r"(w[1]),
-                        "r"(w[2]), "r"(w[3]) : "memory");
+                     :: "r"(stage + lane * 64 + ((static_cast<uint32_t>(j) ^ (lane >> 1 & 3u)) << 4)), "r"(w[0]),
+                        "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
     }
     __syncwarp();
-    const int j = lane % 8, col = n + j * PER;
+    const int j = lane % 4, col = n + j * PER;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + lane / 8;
-        const float4 w = ptx::ld_shared_f4(stage + r * 128 + ((static_cast<uint32_t>(j) ^ (r & 7u)) << 4));
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4;
+        const float4 w = ptx::ld_shared_f4(stage + r * 64 + ((static_cast<uint32_t>(j) ^ (r >> 1 & 3u)) << 4));
         if (row0 + r >= row_limit || col >= N) continue;
         const int64_t at = static_cast<int64_t>(row0 + r) * x.ldc + col;
         const uint32_t ws[4] = {__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w)};
@@ -261,6 +299,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+    auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
+    auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + F8_SLOTS + s); };
+    const uint32_t sS = base + Cfg::OFF_SCALE;
     const uint32_t abort_addr = base + Cfg::OFF_ABORT;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -277,6 +318,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(tfull_bar(b), 1);
             ptx::mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
+        }
+        for (int s = 0; s < F8_SLOTS; ++s) {
+            ptx::mbar_init(sfull_bar(s), 64);                 // every lane of both loaders
+            ptx::mbar_init(sempty_bar(s), F8_EPI_WARPS);
         }
         ptx::mbar_init(drain_bar, 1);
         st_shared_u32(abort_addr, 0u);
@@ -312,11 +357,19 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     int64_t total_tiles = p.total_tiles;
     if constexpr (Cfg::MOE) total_tiles = *reinterpret_cast<volatile int32_t*>(smem + Cfg::OFF_MOE_TOTAL);
 
-    // Registers: 384 x 168 at launch = 64512 >= 128 x 80 + 256 x 208 = 63488.  Each split stands at
+    // Registers: 384 x 168 at launch = 64512 = 128 x 72 + 256 x 216.  Each split stands at
     // the head of its own branch: after a common one the compiler kept to the smaller count.
     const Problem& pr = p.dense;
+    // Warp-uniform bounded wait: every lane polls once; if the phase is not yet complete, lane 0
+    // runs the bounded wait and tells the others how it ended.
+    auto warp_wait = [&](uint32_t bar, uint32_t par, uint32_t role, int64_t slot, uint32_t st) -> bool {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, par))) return true;
+        uint32_t ok = 1;
+        if (lane == 0) ok = wait_bounded<CG, false>(bar, par, p, abort_addr, role, slot, st) ? 1u : 0u;
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
     if (warp < F8_EPI_WARP0) {
-    f8::regs_dec<80>();
+    f8::regs_dec<72>();
     if (warp == 0) {
         // ================================ TMA producer ================================
         if (lane == 0) {
@@ -386,12 +439,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             // stage are 32 bytes along the row, or 32 rows of 128 bytes down
             const uint64_t a_desc0 = ptx::smem_desc_sw128(sA, 16, 1024), b_desc0 = ptx::smem_desc_sw128(sB, 16, 1024);
             const uint64_t a_step = x.a_mn ? 4096u >> 4 : 32u >> 4, b_step = x.b_mn ? 4096u >> 4 : 32u >> 4;
-            auto warp_wait = [&](uint32_t bar, uint32_t par, int64_t tile, uint32_t st) -> bool {
-                if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, par))) return true;
-                uint32_t ok = 1;
-                if (lane == 0) ok = wait_bounded<CG, false>(bar, par, p, abort_addr, ROLE_MMA, tile, st) ? 1u : 0u;
-                return __shfl_sync(0xffffffffu, ok, 0) != 0;
-            };
             Sched sc = sched_begin<Cfg>(p, unit);
             Work w;
             while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
@@ -399,8 +446,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 uint32_t idesc = pr.idesc;
                 if (tile_coord<Cfg>(p, w.t, g, rank, mt).half) idesc = (idesc & ~(0x1Fu << 24)) | ((128u >> 4) << 24);
                 for (int kb = 0; kb < pr.k_blocks; ++kb) {
-                    if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, w.slot, 16 + acc) ||
-                        !warp_wait(full_bar(stage), phase, w.slot, stage)) {
+                    if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, ROLE_MMA, w.slot, 16 + acc) ||
+                        !warp_wait(full_bar(stage), phase, ROLE_MMA, w.slot, stage)) {
                         aborted = true;
                         break;
                     }
@@ -421,131 +468,144 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             }
             __syncwarp();
         }
-    }
     } else {
-        f8::regs_inc<208>();
-        // ================================ accumulation and epilogue ================================
-        constexpr int COLS = Cfg::COLS;
-        const int q = warp % 4, h = (warp - F8_EPI_WARP0) / 4;
-        const uint32_t stage_c = sC + (warp - F8_EPI_WARP0) * C_STAGE_BYTES;
-        int buf = 0, g = 0;
-        uint32_t buf_phase = 0;
+        // ================================ scale loaders ================================
+        // A slot: the scales of the CTA's 128 rows, then those of the tile's columns (or of its
+        // blocks of 128 columns), of one k-block.
+        const bool for_a = warp == 2;
+        int slot = 0, g = 0;
+        uint32_t phase = 0;
         bool aborted = false;
         Sched sc = sched_begin<Cfg>(p, unit);
         Work w;
         while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
             g = find_problem<Cfg>(p, w.t, g, mt);
             const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
+            constexpr int N_A = BM / 32, N_B = Cfg::SB_COL ? BN / 32 : 1, N_MAX = N_A > N_B ? N_A : N_B;
+            const float* src[N_MAX];
+            uint32_t ok = 0;
+#pragma unroll
+            for (int j = 0; j < N_MAX; ++j) {
+                if (for_a) {
+                    const int64_t row = tc.m0 + j * 32 + lane;
+                    if (j < N_A && row < pr.M) ok |= 1u << j;
+                    src[j] = x.sa + (row >> x.sa_shift) * x.sa_mn;
+                } else {
+                    const int64_t i = j * 32 + lane, n = tc.n0 + (Cfg::SB_COL ? i : i * 128);
+                    if (j < N_B && i < Cfg::SB_COUNT && n < pr.N) ok |= 1u << j;
+                    src[j] = x.sb + (Cfg::SB_COL ? n : n >> 7) * x.sb_mn + (Cfg::MOE ? g * x.sb_g : 0);
+                }
+            }
+            const int64_t step = for_a ? x.sa_k : x.sb_k;
+            for (int kb = 0; kb < pr.k_blocks; ++kb) {
+                if (!warp_wait(sempty_bar(slot), phase ^ 1u, ROLE_PRODUCER, w.slot, 32 + slot)) {
+                    aborted = true;
+                    break;
+                }
+                const uint32_t dst = sS + slot * Cfg::SLOT_BYTES + (for_a ? 0 : BM * 4) + lane * 4;
+#pragma unroll
+                for (int j = 0; j < N_MAX; ++j) {
+                    const int n = for_a ? N_A : N_B;
+                    if (j < n && (Cfg::SB_COL || for_a || lane < Cfg::SB_COUNT)) {
+                        const bool in = ok >> j & 1u;
+                        f8::cp_async_4(dst + j * 128, in ? static_cast<const void*>(src[j] + kb * step) : x.sa, in);
+                    }
+                }
+                f8::cp_async_arrive(sfull_bar(slot));
+                if (++slot == F8_SLOTS) { slot = 0; phase ^= 1u; }
+            }
+        }
+        ptx::cp_async_commit();
+        ptx::cp_async_wait<0>();              // nothing lands after this warp has left
+    }
+    } else {
+        f8::regs_inc<216>();
+        // ================================ accumulation and epilogue ================================
+        constexpr int COLS = Cfg::COLS;
+        const int q = warp % 4, h = (warp - F8_EPI_WARP0) / 4;
+        const uint32_t stage_c = sC + (warp - F8_EPI_WARP0) * F8_C_STAGE;
+        int buf = 0, slot = 0, g = 0;
+        uint32_t buf_phase = 0, slot_phase = 0;
+        bool aborted = false;
+        Sched sc = sched_begin<Cfg>(p, unit);
+        Work w;
+        while (sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
+            g = find_problem<Cfg>(p, w.t, g, mt);
+            const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
             // a half tile keeps 64 rows in lanes 0-63 (columns [0, BN/2)) and again in lanes 64-127
             // (columns [BN/2, BN)), in BN/2 TMEM columns: the two warps of a quarter split those
-            const int row0 = tc.m0 + (tc.half ? (q % 2) * 32 : q * 32);
-            const int n0 = tc.n0 + (tc.half ? (q / 2) * (BN / 2) + h * (BN / 4) : h * COLS);
-            const int n_cols = tc.half ? COLS / 2 : COLS;
+            const int local_row = tc.half ? (q % 2) * 32 : q * 32;
+            const int local_col = tc.half ? (q / 2) * (BN / 2) + h * (BN / 4) : h * COLS;
+            const int row0 = tc.m0 + local_row, n0 = tc.n0 + local_col;
             const uint32_t t_col = static_cast<uint32_t>(tc.half ? h * (BN / 4) : h * COLS);
+            const int n_cols = tc.half ? COLS / 2 : COLS;
             int row_limit = pr.M;
             if constexpr (Cfg::MOE) row_limit = static_cast<int>(min(static_cast<int64_t>(tc.row_end), p.moe_rows));
             const bool active = row0 < row_limit && n0 < pr.N;
-
-            // scales: this lane's row, and one value (or, per column, COLS / 32 of this lane) of B;
-            // fetched PF k-blocks ahead of their use
-            constexpr int PF = 4;
-            constexpr int NB = Cfg::SB_COL ? COLS / 32 : 1;
-            const int row = min(row0 + lane, row_limit - 1);
-            const float* pa = x.sa + static_cast<int64_t>(row >> x.sa_shift) * x.sa_mn;
-            const float* pb[NB];
-            bool col_ok[NB];
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int n = Cfg::SB_COL ? n0 + j * 32 + lane : n0;
-                col_ok[j] = active && n < pr.N;
-                pb[j] = x.sb + static_cast<int64_t>(Cfg::SB_COL ? n : n >> 7) * x.sb_mn +
-                        (Cfg::MOE ? static_cast<int64_t>(g) * x.sb_g : 0);
-            }
-            float fa[PF], fb[PF][NB];
-            auto fetch = [&](int kb, float& a, float (&b)[NB]) {
-                const bool ok = active && kb < pr.k_blocks;
-                a = ok ? __ldg(pa + kb * x.sa_k) : 0.0f;
-#pragma unroll
-                for (int j = 0; j < NB; ++j) b[j] = ok && col_ok[j] ? __ldg(pb[j] + kb * x.sb_k) : 0.0f;
-            };
-#pragma unroll
-            for (int i = 0; i < PF; ++i) fetch(i, fa[i], fb[i]);
+            const uint32_t sa_at = sS + (local_row + lane) * 4;
+            const uint32_t sb_at = sS + BM * 4 + (Cfg::SB_COL ? local_col : local_col >> 7) * 4;
 
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
 #pragma unroll 1
             for (int kb = 0; kb < pr.k_blocks; ++kb) {
-                const float sa = fa[0];
-                float sb[NB];
-#pragma unroll
-                for (int j = 0; j < NB; ++j) sb[j] = fb[0][j];
-#pragma unroll
-                for (int i = 0; i + 1 < PF; ++i) {
-                    fa[i] = fa[i + 1];
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) fb[i][j] = fb[i + 1][j];
-                }
-                fetch(kb + PF, fa[PF - 1], fb[PF - 1]);
-                uint32_t sb_smem = stage_c + static_cast<uint32_t>(kb & 1) * (COLS * 4);
-                if constexpr (Cfg::SB_COL) {
-                    if (kb == 0) __syncwarp();     // the previous tile's staging has been read back
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) st_shared_u32(sb_smem + (j * 32 + lane) * 4, __float_as_uint(sb[j]));
-                    __syncwarp();
-                }
-                uint32_t ok = 1;
-                if (lane == 0)
-                    ok = wait_bounded<CG>(tfull_bar(buf), buf_phase, p, abort_addr, ROLE_EPILOGUE, w.slot, 16 + buf) ? 1u : 0u;
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) { aborted = true; break; }
+                if (!warp_wait(sfull_bar(slot), slot_phase, ROLE_EPILOGUE, w.slot, 32 + slot)) { aborted = true; break; }
+                const uint32_t off = slot * Cfg::SLOT_BYTES;
+                float s = f8::ld_shared_f32(sa_at + off);
+                if constexpr (!Cfg::SB_COL) s *= f8::ld_shared_f32(sb_at + off);
+                const uint64_t s2 = ptx::f32x2_pack(s, s);
+                if (!warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, w.slot, 16 + buf)) { aborted = true; break; }
                 ptx::tc_fence_after_sync();
-                const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN) + t_col;
-                const uint64_t s2 = Cfg::SB_COL ? ptx::f32x2_pack(sa, sa) : ptx::f32x2_pack(sa * sb[0], sa * sb[0]);
+                const uint32_t tm = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN) + t_col;
                 uint32_t r[2][32];
-                if (active) ptx::tmem_ld_32x32b_x32(t, r[0]);
+                if (active) ptx::tmem_ld_32x32b_x32(tm, r[0]);
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
                     const bool mine = active && c * 32 < n_cols;
                     if (mine) {
                         f8::tmem_ld_wait32(r[c & 1]);
-                        if (c + 1 < COLS / 32 && (c + 1) * 32 < n_cols) ptx::tmem_ld_32x32b_x32(t + (c + 1) * 32, r[(c + 1) & 1]);
+                        if (c + 1 < COLS / 32 && (c + 1) * 32 < n_cols)
+                            ptx::tmem_ld_32x32b_x32(tm + (c + 1) * 32, r[(c + 1) & 1]);
                     }
                     if (c + 1 == COLS / 32) {
-                        // everything is in registers: the buffer goes back to the MMA issuer
+                        // everything is in registers: the buffer goes back to the MMA issuer, and (unless
+                        // the columns' scales are still read) the scale slot to the loaders
                         ptx::tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) {
-                            if (CG == 2 && !leader) ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(buf), 0));
+                            if (CG == 2 && !leader) f8::mbar_arrive_peer(ptx::mapa(tempty_bar(buf), 0));
                             else ptx::mbar_arrive(tempty_bar(buf));
+                            if constexpr (!Cfg::SB_COL) ptx::mbar_arrive(sempty_bar(slot));
                         }
                     }
                     if (mine) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            uint64_t v = ptx::f32x2_pack(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1]));
+                        for (int i = 0; i < 16; i += 2) {
+                            const uint32_t* v = r[c & 1] + 2 * i;
+                            uint64_t v0 = ptx::f32x2_pack(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                            uint64_t v1 = ptx::f32x2_pack(__uint_as_float(v[2]), __uint_as_float(v[3]));
                             if constexpr (Cfg::SB_COL) {
-                                if (i % 2 == 0) {
-                                    const float4 f = ptx::ld_shared_f4(sb_smem + (c * 32 + 2 * i) * 4);
-                                    const uint64_t v1 = ptx::f32x2_pack(__uint_as_float(r[c & 1][2 * i + 2]),
-                                                                        __uint_as_float(r[c & 1][2 * i + 3]));
-                                    acc[c * 16 + i] = ptx::f32x2_fma(ptx::f32x2_mul(v, ptx::f32x2_pack(f.x, f.y)), s2,
-                                                                     acc[c * 16 + i]);
-                                    acc[c * 16 + i + 1] = ptx::f32x2_fma(ptx::f32x2_mul(v1, ptx::f32x2_pack(f.z, f.w)), s2,
-                                                                         acc[c * 16 + i + 1]);
-                                }
-                            } else {
-                                acc[c * 16 + i] = ptx::f32x2_fma(v, s2, acc[c * 16 + i]);
+                                const float4 f = ptx::ld_shared_f4(sb_at + off + (c * 32 + 2 * i) * 4);
+                                v0 = ptx::f32x2_mul(v0, ptx::f32x2_pack(f.x, f.y));
+                                v1 = ptx::f32x2_mul(v1, ptx::f32x2_pack(f.z, f.w));
                             }
+                            acc[c * 16 + i] = ptx::f32x2_fma(v0, s2, acc[c * 16 + i]);
+                            acc[c * 16 + i + 1] = ptx::f32x2_fma(v1, s2, acc[c * 16 + i + 1]);
                         }
                     }
                 }
+                if constexpr (Cfg::SB_COL) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sempty_bar(slot));
+                }
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+                if (++slot == F8_SLOTS) { slot = 0; slot_phase ^= 1u; }
             }
             if (aborted) break;
             if (!active) continue;
 
-            // epilogue: 32 columns at a time into values, bias, GELU; 64 (16-bit) or 32 (fp32) to a store
+            // epilogue: 32 (16-bit output) or 16 (fp32) columns at a time: bias, GELU, rounding, store
             const uint16_t* bias = static_cast<const uint16_t*>(pr.bias);
             if constexpr (Cfg::MOE) { if (bias) bias += static_cast<int64_t>(g) * pr.N; }
             const int epi = pr.epi;
@@ -575,23 +635,19 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 constexpr int C0 = decltype(first)::value;
                 constexpr bool F32 = decltype(f32_tag)::value;
                 if (C0 < n_cols && n0 + C0 < pr.N) {
-                    float v[F32 ? 32 : 64];
+                    float v[F32 ? 16 : 32];
                     finish(first, v);
                     f8::store_rows<F32>(v, stage_c, x, f16, row0, row_limit, n0 + C0, pr.N, lane);
                 }
             };
-            using std::integral_constant;
-            if (f32) {
-                chunk(integral_constant<int, 0>{}, std::true_type{});
-                chunk(integral_constant<int, 32>{}, std::true_type{});
-                if constexpr (COLS > 64) {
-                    chunk(integral_constant<int, 64>{}, std::true_type{});
-                    chunk(integral_constant<int, 96>{}, std::true_type{});
-                }
-            } else {
-                chunk(integral_constant<int, 0>{}, std::false_type{});
-                if constexpr (COLS > 64) chunk(integral_constant<int, 64>{}, std::false_type{});
-            }
+            auto chunks = [&](auto f32_tag) {
+                constexpr int CW = decltype(f32_tag)::value ? 16 : 32;
+                f8::for_each<COLS / CW>([&](auto i) {
+                    chunk(std::integral_constant<int, decltype(i)::value * CW>{}, f32_tag);
+                });
+            };
+            if (f32) chunks(std::true_type{});
+            else chunks(std::false_type{});
             __syncwarp();
         }
     }
