@@ -36,7 +36,7 @@ constexpr int F8_BK = 128;                 // K per stage: one scale block
 constexpr int F8_THREADS = 384;
 constexpr int F8_EPI_WARP0 = 4;
 constexpr int F8_EPI_WARPS = 8;
-constexpr int F8_SLOTS = 8;                // k-blocks of scales in flight
+constexpr int F8_GROUP = 4;                // k-blocks whose scales share a slot
 constexpr int F8_C_STAGE = 32 * 64;        // per-warp store staging: 32 rows of 64 bytes
 
 // What the 8-bit form needs besides Params (whose `dense` problem holds the maps, sizes,
@@ -68,8 +68,9 @@ struct Fp8Config {
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int C_BYTES = F8_EPI_WARPS * F8_C_STAGE;
     static constexpr int SB_COUNT = SB_COL ? BN : BN / 128;      // B scales of a tile and k-block
-    static constexpr int SLOT_BYTES = (BM + (SB_COL ? BN : 4)) * 4;
-    static constexpr int SCALE_BYTES = F8_SLOTS * SLOT_BYTES;
+    static constexpr int SLOTS = SB_COL ? 2 : 4;                 // groups of scales in flight
+    static constexpr int SLOT_BYTES = (BM + SB_COUNT) * F8_GROUP * 4;
+    static constexpr int SCALE_BYTES = SLOTS * SLOT_BYTES;
     static constexpr int TABLE_BYTES = MOE ? 8 * (MOE_MAX_G + 1) : 0;
     static constexpr int FIXED = C_BYTES + SCALE_BYTES + TABLE_BYTES + 512 + 1024;
     static constexpr int STAGES = (SMEM_LIMIT - FIXED) / (A_BYTES + B_BYTES);
@@ -79,7 +80,7 @@ struct Fp8Config {
     static constexpr int OFF_SCALE = OFF_C + C_BYTES;
     static constexpr int OFF_TABLE = OFF_SCALE + SCALE_BYTES;
     static constexpr int OFF_BAR = OFF_TABLE + TABLE_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * F8_SLOTS;
+    static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * SLOTS;
     static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NUM_BARS;
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
     static constexpr int OFF_MOE_TOTAL = OFF_ABORT + 4;
@@ -224,11 +225,13 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
 
-// Arrive on a barrier of the pair's other CTA.  The release is of CTA scope: what it orders are
-// this thread's tensor-memory loads, complete by tcgen05.wait::ld; with cluster scope every
-// arrival waited for the warp's outstanding global and local accesses.
-__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+// Lane 0 arrives on a barrier of the cluster (address from mapa), predicated rather than
+// branched to.  The release is of CTA scope: what it orders are the warp's tensor-memory loads,
+// complete by tcgen05.wait::ld; with cluster scope every arrival waited for the warp's
+// outstanding global and local accesses.
+__device__ __forceinline__ void arrive_lane0(uint32_t cluster_bar, int lane) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" :: "r"(cluster_bar), "r"(lane) : "memory");
 }
 
 // Columns [n, n + 64 / esize) of 32 rows, one row a lane: rounded, staged in 2 KiB of shared
@@ -300,11 +303,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
     auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
-    auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + F8_SLOTS + s); };
+    auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + Cfg::SLOTS + s); };
     const uint32_t sS = base + Cfg::OFF_SCALE;
     const uint32_t abort_addr = base + Cfg::OFF_ABORT;
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // broadcast, so that the compiler knows the warp's index and what follows from it as uniform
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
     const bool leader = rank == 0;
     const int64_t unit = blockIdx.x / CG, num_units = gridDim.x / CG;
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             ptx::mbar_init(tfull_bar(b), 1);
             ptx::mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
         }
-        for (int s = 0; s < F8_SLOTS; ++s) {
+        for (int s = 0; s < Cfg::SLOTS; ++s) {
             ptx::mbar_init(sfull_bar(s), 64);                 // every lane of both loaders
             ptx::mbar_init(sempty_bar(s), F8_EPI_WARPS);
         }
@@ -366,6 +370,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, par))) return true;
         uint32_t ok = 1;
         if (lane == 0) ok = wait_bounded<CG, false>(bar, par, p, abort_addr, role, slot, st) ? 1u : 0u;
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
+    // The same for warps that run ahead: lane 0 is suspended between its polls.
+    auto warp_wait_sleep = [&](uint32_t bar, uint32_t par, uint32_t role, int64_t slot, uint32_t st) -> bool {
+        uint32_t ok = 1;
+        if (lane == 0) ok = wait_bounded<CG, true>(bar, par, p, abort_addr, role, slot, st) ? 1u : 0u;
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
     if (warp < F8_EPI_WARP0) {
@@ -470,8 +480,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         }
     } else {
         // ================================ scale loaders ================================
-        // A slot: the scales of the CTA's 128 rows, then those of the tile's columns (or of its
-        // blocks of 128 columns), of one k-block.
+        // A slot: the scales of F8_GROUP k-blocks: [128 rows][k-block] of A, then of B
+        // [k-block][columns], or [block of 128 columns][k-block].
         const bool for_a = warp == 2;
         int slot = 0, g = 0;
         uint32_t phase = 0;
@@ -497,22 +507,26 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 }
             }
             const int64_t step = for_a ? x.sa_k : x.sb_k;
-            for (int kb = 0; kb < pr.k_blocks; ++kb) {
+            for (int kb = 0; kb < pr.k_blocks; kb += F8_GROUP) {
                 if (!warp_wait(sempty_bar(slot), phase ^ 1u, ROLE_PRODUCER, w.slot, 32 + slot)) {
                     aborted = true;
                     break;
                 }
-                const uint32_t dst = sS + slot * Cfg::SLOT_BYTES + (for_a ? 0 : BM * 4) + lane * 4;
+                const uint32_t dst = sS + slot * Cfg::SLOT_BYTES + (for_a ? 0 : BM * F8_GROUP * 4);
+                const int n = for_a ? N_A : N_B;
 #pragma unroll
-                for (int j = 0; j < N_MAX; ++j) {
-                    const int n = for_a ? N_A : N_B;
-                    if (j < n && (Cfg::SB_COL || for_a || lane < Cfg::SB_COUNT)) {
-                        const bool in = ok >> j & 1u;
-                        f8::cp_async_4(dst + j * 128, in ? static_cast<const void*>(src[j] + kb * step) : x.sa, in);
+                for (int i = 0; i < F8_GROUP; ++i) {
+#pragma unroll
+                    for (int j = 0; j < N_MAX; ++j) {
+                        if (j < n && kb + i < pr.k_blocks && (Cfg::SB_COL || for_a || lane < Cfg::SB_COUNT)) {
+                            const bool in = ok >> j & 1u;
+                            const int at = for_a || !Cfg::SB_COL ? (j * 32 + lane) * F8_GROUP + i : i * BN + j * 32 + lane;
+                            f8::cp_async_4(dst + at * 4, in ? static_cast<const void*>(src[j] + (kb + i) * step) : x.sa, in);
+                        }
                     }
                 }
                 f8::cp_async_arrive(sfull_bar(slot));
-                if (++slot == F8_SLOTS) { slot = 0; phase ^= 1u; }
+                if (++slot == Cfg::SLOTS) { slot = 0; phase ^= 1u; }
             }
         }
         ptx::cp_async_commit();
@@ -526,7 +540,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         const uint32_t stage_c = sC + (warp - F8_EPI_WARP0) * F8_C_STAGE;
         int buf = 0, slot = 0, g = 0;
         uint32_t buf_phase = 0, slot_phase = 0;
-        bool aborted = false;
+        const uint32_t lead_tempty = ptx::mapa(tempty_bar(0), 0), own_sempty = ptx::mapa(sempty_bar(0), rank);
+        constexpr bool MAY_HALVE = CG == 2 && Cfg::MOE;
         Sched sc = sched_begin<Cfg>(p, unit);
         Work w;
         while (sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
@@ -542,67 +557,104 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             int row_limit = pr.M;
             if constexpr (Cfg::MOE) row_limit = static_cast<int>(min(static_cast<int64_t>(tc.row_end), p.moe_rows));
             const bool active = row0 < row_limit && n0 < pr.N;
-            const uint32_t sa_at = sS + (local_row + lane) * 4;
-            const uint32_t sb_at = sS + BM * 4 + (Cfg::SB_COL ? local_col : local_col >> 7) * 4;
+            const uint32_t tm0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + t_col;
+            const uint32_t sa_at = sS + (local_row + lane) * F8_GROUP * 4;
+            const uint32_t sb_at = sS + BM * F8_GROUP * 4 + (Cfg::SB_COL ? local_col : (local_col >> 7) * F8_GROUP) * 4;
 
-            uint64_t acc[COLS / 2];
+            float acc[COLS];
 #pragma unroll
-            for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
-#pragma unroll 1
-            for (int kb = 0; kb < pr.k_blocks; ++kb) {
-                if (!warp_wait(sfull_bar(slot), slot_phase, ROLE_EPILOGUE, w.slot, 32 + slot)) { aborted = true; break; }
-                const uint32_t off = slot * Cfg::SLOT_BYTES;
-                float s = f8::ld_shared_f32(sa_at + off);
-                if constexpr (!Cfg::SB_COL) s *= f8::ld_shared_f32(sb_at + off);
-                const uint64_t s2 = ptx::f32x2_pack(s, s);
-                if (!warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, w.slot, 16 + buf)) { aborted = true; break; }
-                ptx::tc_fence_after_sync();
-                const uint32_t tm = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * BN) + t_col;
-                uint32_t r[2][32];
-                if (active) ptx::tmem_ld_32x32b_x32(tm, r[0]);
-#pragma unroll
-                for (int c = 0; c < COLS / 32; ++c) {
-                    const bool mine = active && c * 32 < n_cols;
-                    if (mine) {
-                        f8::tmem_ld_wait32(r[c & 1]);
-                        if (c + 1 < COLS / 32 && (c + 1) * 32 < n_cols)
-                            ptx::tmem_ld_32x32b_x32(tm + (c + 1) * 32, r[(c + 1) & 1]);
-                    }
-                    if (c + 1 == COLS / 32) {
-                        // everything is in registers: the buffer goes back to the MMA issuer, and (unless
-                        // the columns' scales are still read) the scale slot to the loaders
-                        ptx::tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (CG == 2 && !leader) f8::mbar_arrive_peer(ptx::mapa(tempty_bar(buf), 0));
-                            else ptx::mbar_arrive(tempty_bar(buf));
-                            if constexpr (!Cfg::SB_COL) ptx::mbar_arrive(sempty_bar(slot));
-                        }
-                    }
-                    if (mine) {
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const uint32_t* v = r[c & 1] + 2 * i;
-                            uint64_t v0 = ptx::f32x2_pack(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                            uint64_t v1 = ptx::f32x2_pack(__uint_as_float(v[2]), __uint_as_float(v[3]));
-                            if constexpr (Cfg::SB_COL) {
-                                const float4 f = ptx::ld_shared_f4(sb_at + off + (c * 32 + 2 * i) * 4);
-                                v0 = ptx::f32x2_mul(v0, ptx::f32x2_pack(f.x, f.y));
-                                v1 = ptx::f32x2_mul(v1, ptx::f32x2_pack(f.z, f.w));
-                            }
-                            acc[c * 16 + i] = ptx::f32x2_fma(v0, s2, acc[c * 16 + i]);
-                            acc[c * 16 + i + 1] = ptx::f32x2_fma(v1, s2, acc[c * 16 + i + 1]);
-                        }
-                    }
-                }
+            for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
+            // acc[32 C ..] += scale * partial columns [32 C, 32 C + 32).  Scalar: a warp's fused
+            // multiply-add measured 1.03 issue cycles, a packed pair of them 2.34.
+            auto add = [&](auto chunk_index, const uint32_t (&r)[32], float s, uint32_t sb) {
+                constexpr int C = decltype(chunk_index)::value;
                 if constexpr (Cfg::SB_COL) {
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(sempty_bar(slot));
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 f = ptx::ld_shared_f4(sb + (C * 32 + i) * 4);
+                        acc[C * 32 + i] = fmaf(__uint_as_float(r[i]) * f.x, s, acc[C * 32 + i]);
+                        acc[C * 32 + i + 1] = fmaf(__uint_as_float(r[i + 1]) * f.y, s, acc[C * 32 + i + 1]);
+                        acc[C * 32 + i + 2] = fmaf(__uint_as_float(r[i + 2]) * f.z, s, acc[C * 32 + i + 2]);
+                        acc[C * 32 + i + 3] = fmaf(__uint_as_float(r[i + 3]) * f.w, s, acc[C * 32 + i + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[C * 32 + i] = fmaf(__uint_as_float(r[i]), s, acc[C * 32 + i]);
                 }
-                if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
-                if (++slot == F8_SLOTS) { slot = 0; slot_phase ^= 1u; }
-            }
-            if (aborted) break;
+            };
+            // This lane's scales of four k-blocks (times B's, one for all the warp's columns), from the
+            // next slot.  Read once per group, a k-block ahead: shared memory answers slowly
+            // while the tensor cores and TMA use it.
+            auto read_scales = [&](float (&f)[F8_GROUP]) -> bool {
+                if (!warp_wait(sfull_bar(slot), slot_phase, ROLE_EPILOGUE, w.slot, 32 + slot)) return false;
+                const uint32_t off = slot * Cfg::SLOT_BYTES;
+                const float4 a = ptx::ld_shared_f4(sa_at + off);
+                f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+                if constexpr (!Cfg::SB_COL) {
+                    const float4 b = ptx::ld_shared_f4(sb_at + off);
+                    f[0] *= b.x; f[1] *= b.y; f[2] *= b.z; f[3] *= b.w;
+                    __syncwarp();
+                    f8::arrive_lane0(own_sempty + 8u * slot, lane);
+                    if (++slot == Cfg::SLOTS) { slot = 0; slot_phase ^= 1u; }
+                }
+                return true;
+            };
+            // All k-blocks over the first 32 * CHUNKS columns of this warp (none: it only keeps the
+            // barriers going).
+            auto accumulate = [&](auto chunk_count) -> bool {
+                constexpr int CHUNKS = decltype(chunk_count)::value;
+                static_assert(F8_GROUP == 4, "a lane's scales of a group are one 16-byte word");
+                float f[F8_GROUP];
+                if (pr.k_blocks == 0) return true;
+                if (!read_scales(f)) return false;
+                bool ready = ptx::mbar_test_wait(tfull_bar(buf), buf_phase);
+#pragma unroll 1
+                for (int kb = 0; kb < pr.k_blocks; ++kb) {
+                    const int u = kb % F8_GROUP;
+                    if (!__all_sync(0xffffffffu, ready) &&
+                        !warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, w.slot, 16 + buf)) return false;
+                    ptx::tc_fence_after_sync();
+                    const uint32_t tm = tm0 + static_cast<uint32_t>(buf * BN);
+                    uint32_t r[2][32];
+                    if constexpr (CHUNKS > 0) ptx::tmem_ld_32x32b_x32(tm, r[0]);
+                    const float s = f[0];
+                    const uint32_t sb = sb_at + slot * Cfg::SLOT_BYTES + u * (BN * 4);      // SB_COL
+                    f[0] = f[1]; f[1] = f[2]; f[2] = f[3];
+                    if constexpr (!Cfg::SB_COL) {
+                        if (u == F8_GROUP - 1 && kb + 1 < pr.k_blocks && !read_scales(f)) return false;
+                    }
+                    f8::for_each<(CHUNKS > 0 ? CHUNKS : 1)>([&](auto ci) {
+                        constexpr int C = decltype(ci)::value;
+                        if constexpr (CHUNKS > 0) f8::tmem_ld_wait32(r[C & 1]);
+                        if constexpr (C + 1 < CHUNKS) {
+                            ptx::tmem_ld_32x32b_x32(tm + (C + 1) * 32, r[(C + 1) & 1]);
+                        } else {
+                            // everything is in registers: the buffer goes back to the MMA issuer; the next
+                            // one is asked for early, so that the answer is there after the additions
+                            ptx::tc_fence_before_sync();
+                            f8::arrive_lane0(lead_tempty + 8u * buf, lane);
+                            if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+                            ready = ptx::mbar_test_wait(tfull_bar(buf), buf_phase);
+                        }
+                        if constexpr (CHUNKS > 0) add(ci, r[C & 1], s, sb);
+                    });
+                    if constexpr (Cfg::SB_COL) {
+                        if (u == F8_GROUP - 1 || kb + 1 == pr.k_blocks) {
+                            // the columns' scales have been read: on to the next group's slot
+                            __syncwarp();
+                            f8::arrive_lane0(own_sempty + 8u * slot, lane);
+                            if (++slot == Cfg::SLOTS) { slot = 0; slot_phase ^= 1u; }
+                            if (kb + 1 < pr.k_blocks && !read_scales(f)) return false;
+                        }
+                    }
+                }
+                return true;
+            };
+            bool ok;
+            if (!active) ok = accumulate(std::integral_constant<int, 0>{});
+            else if (MAY_HALVE && tc.half) ok = accumulate(std::integral_constant<int, COLS / 64>{});
+            else ok = accumulate(std::integral_constant<int, COLS / 32>{});
+            if (!ok) break;
             if (!active) continue;
 
             // epilogue: 32 (16-bit output) or 16 (fp32) columns at a time: bias, GELU, rounding, store
@@ -616,8 +668,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
 #pragma unroll
                 for (int j = 0; j < CW / 8; ++j) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        ptx::f32x2_unpack(acc[C0 / 2 + 4 * j + i], v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+                    for (int i = 0; i < 8; ++i) v[8 * j + i] = acc[C0 + 8 * j + i];
                     if (epi != EPI_NONE) {
                         float b[8];
                         f8::load_bias8(bias, n0 + C0 + 8 * j, pr.N, b);
