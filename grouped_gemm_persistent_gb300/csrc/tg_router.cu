@@ -14,9 +14,12 @@
 //   renormalised:  d x = p (u - sum p u) + [chosen] w (w' - sum w w'),   u = d_loss * slope
 //   otherwise:     d x = p (u - sum p u - sum w w') + [chosen] w w'.
 //
-// One warp holds one row: lane l the experts l, l + 32, ...  Everything is summed in a
-// fixed order - a lane over its rows, the warps of a block, then the blocks in double -
-// so results do not depend on timing.
+// L lanes of a warp hold one row (L = 8, 16 or 32, at least k and G / 8), each V
+// neighbouring experts; a warp works on 32 / L rows at once, with the next rows' logits on
+// their way.  Everything is summed in a fixed order - a lane over its rows, a warp's row
+// slots, the warps of a block, then the blocks in double - so results do not depend on
+// timing.  The kernels are bound by instruction issue (the k selection steps), not by the
+// memory they read once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,268 +34,459 @@ namespace tg {
 
 namespace {
 
-constexpr int R_WARPS = 8;                    // rows in flight per block
+constexpr int R_WARPS = 16;
 constexpr int R_THREADS = 32 * R_WARPS;
 constexpr int R_BLOCKS_PER_SM = 2;
 constexpr int R_MAX_G = TG_MOE_ROUTER_MAX_EXPERTS;
 constexpr int R_MAX_K = TG_MOE_ROUTER_MAX_TOP_K;
+constexpr uint32_t FULL = 0xffffffffu;
 
-template <int DT>
-__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-    if constexpr (DT == TG_F32) return __ldg(static_cast<const float*>(p) + i);
-    const uint16_t h = __ldg(static_cast<const uint16_t*>(p) + i);
-    if constexpr (DT == TG_F16) return __half2float(__ushort_as_half(h));
-    else return __uint_as_float(static_cast<uint32_t>(h) << 16);
-}
+// ----------------------------------------------------------------------------------------
+// a lane's V logits of one row, as they lie in memory
 
-template <int DT>
-__device__ __forceinline__ void store_logit(void* p, int64_t i, float v) {
-    if constexpr (DT == TG_F32) static_cast<float*>(p)[i] = v;
-    else if constexpr (DT == TG_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
+template <int DT, int V>
+struct Logits {
+    static constexpr int ESIZE = DT == TG_F32 ? 4 : 2;
+    static constexpr int WORDS = V * ESIZE / 4;
+    static constexpr uint32_t NEG_INF = DT == TG_F32 ? 0xff800000u : DT == TG_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    uint32_t w[WORDS];
 
-// An unsigned key that orders like the value: -0 equals +0, NaN is above everything, and 0
-// stands for "not to be chosen" (-infinity, or already taken).
-__device__ __forceinline__ uint32_t order_key(float x) {
-    if (x == __int_as_float(0xff800000)) return 0u;
-    if (x != x) return 0xffffffffu;
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-}
-
-__device__ __forceinline__ float warp_max(float v) {
+    // n of the V are inside the row (the others become -infinity); vec: 16-byte loads allowed
+    __device__ __forceinline__ void load(const uint8_t* p, int n, bool vec) {
+        if (n == V && vec) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
+            for (int i = 0; i < WORDS; i += 4) {
+                const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+                w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
+            }
+            return;
+        }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-
-// Softmax of a row held as v[j] = logit of expert lane + 32 j (-infinity past the last).
-// false: the row has no logit above -infinity (p is then 0).
-template <int V>
-__device__ __forceinline__ bool row_softmax(const float (&v)[V], float (&p)[V]) {
-    float m = __int_as_float(0xff800000);
-    bool any = false;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        m = fmaxf(m, v[j]);
-        any |= v[j] != __int_as_float(0xff800000);       // true for NaN, too
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (DT == TG_F32) {
+                w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : NEG_INF;
+            } else {
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+                const uint32_t lo = 2 * i < n ? __ldg(h + 2 * i) : NEG_INF & 0xffffu;
+                const uint32_t hi = 2 * i + 1 < n ? __ldg(h + 2 * i + 1) : NEG_INF & 0xffffu;
+                w[i] = lo | hi << 16;
+            }
+        }
     }
-    m = warp_max(m);
-    any = __any_sync(0xffffffffu, any);
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        p[j] = any ? expf(v[j] - m) : 0.0f;
-        s += p[j];
+    __device__ __forceinline__ uint32_t bits(int j) const {
+        if constexpr (DT == TG_F32) return w[j];
+        else return j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu;
     }
-    s = warp_sum(s);
-    const float inv = any ? 1.0f / s : 0.0f;
+    static __device__ __forceinline__ float widen(uint32_t b) {
+        if constexpr (DT == TG_F32) return __uint_as_float(b);
+        else if constexpr (DT == TG_F16) return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+        else return __uint_as_float(b << 16);
+    }
+    __device__ __forceinline__ float value(int j) const { return widen(bits(j)); }
+};
+
+// An unsigned key that orders like the value: -0 equals +0, NaN is above everything, and 0 stands
+// for "not to be chosen" (-infinity, or taken already).  The 16-bit types' keys carry the expert's
+// index below the value, so that a maximum is unique and goes to the lowest index.
+template <int DT>
+__device__ __forceinline__ uint32_t order_key(uint32_t b, uint32_t expert) {
+    if constexpr (DT == TG_F32) {
+        if (b == 0xff800000u) return 0u;
+        if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
+        if (b == 0x80000000u) b = 0u;
+        return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    } else {
+        constexpr uint32_t INF = DT == TG_F16 ? 0x7c00u : 0x7f80u;
+        if (b == (0x8000u | INF)) return 0u;
+        if (b == 0x8000u) b = 0u;
+        uint32_t s = (b & 0x8000u) ? b ^ 0xffffu : b | 0x8000u;
+        if ((b & 0x7fffu) > INF) s = 0xffffu;
+        return s << 16 | (0xffffu ^ expert);
+    }
+}
+
+// The value a key stands for (NaN for a NaN).
+template <int DT>
+__device__ __forceinline__ float key_value(uint32_t key) {
+    if constexpr (DT == TG_F32) return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+    const uint32_t s = key >> 16;
+    return Logits<DT, 8>::widen((s & 0x8000u) ? s & 0x7fffu : s ^ 0xffffu);
+}
+
+// Over the L lanes of a row
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if constexpr (L == 32) {
+        return __reduce_max_sync(FULL, v);
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) p[j] *= inv;
-    return any;
+        for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(FULL, v, d));
+        return v;
+    }
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(FULL, v, d);
+    return v;
 }
 
 struct RouterArgs {
-    const void* logits;
-    int64_t ld, T;
-    int G, k, renorm;
+    const uint8_t* logits;
+    int64_t ld_bytes, T;
+    int G, k, renorm, vec;
     int32_t* experts;     // [T, k]
     float* weights;       // [T, k]
     int32_t* counts;      // [G]
     float* loss;
     float* slope;         // [G]
-    // per block: probability sums [G], counts [G], then the number of rows
+    // several blocks: each one's probability sums [G], counts [G] and number of rows
     float* part_p;
     int32_t* part_c;
     int32_t* part_n;
 };
 
-template <int DT, int V>
-__global__ void __launch_bounds__(R_THREADS) router_kernel(const RouterArgs a) {
+// counts, slope and this expert's term of the loss
+__device__ __forceinline__ double finish_expert(const RouterArgs& a, int g, double sum, int32_t count, double rows) {
+    a.counts[g] = count;
+    const double slope = a.G * static_cast<double>(count) / (rows * a.k) / rows;
+    a.slope[g] = static_cast<float>(slope);
+    return slope * sum;
+}
+
+template <int DT, int L, int V>
+__global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const RouterArgs a) {
     ptx::grid_launch_dependents();
-    __shared__ int32_t s_count[32 * V];
-    __shared__ float s_sum[R_WARPS][32 * V];
+    constexpr int SPAN = L * V;                   // experts a row's lanes cover
+    constexpr int ROWS = 32 / L;                  // rows of a warp at once
+    extern __shared__ __align__(16) uint8_t dyn[];
+    float* s_sum = reinterpret_cast<float*>(dyn);                              // [warps][SPAN]
+    int32_t* s_count = reinterpret_cast<int32_t*>(s_sum + R_WARPS * SPAN);     // [SPAN]
     __shared__ int32_t s_rows[R_WARPS];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int i = threadIdx.x; i < 32 * V; i += R_THREADS) s_count[i] = 0;
+    __shared__ double s_loss[R_WARPS];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, in = lane % L;
+    for (int i = threadIdx.x; i < SPAN; i += R_THREADS) s_count[i] = 0;
     __syncthreads();
 
+    const int first = in * V;                     // this lane's experts [first, first + V)
+    const int n = a.G - first < 0 ? 0 : a.G - first < V ? a.G - first : V;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R_WARPS * ROWS;
+    // (a warp's rows are neighbours; lanes past the last row keep -infinity and store nothing)
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
+    const int64_t warp_first = t - lane / L;
+    Logits<DT, V> next;
+    auto fetch = [&](int64_t row) {
+        next.load(a.logits + row * a.ld_bytes + first * Logits<DT, V>::ESIZE, row < a.T ? n : 0, a.vec != 0);
+    };
+    fetch(t);
     float sum[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] = 0.0f;
     int rows = 0;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * R_WARPS;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * R_WARPS + warp; t < a.T; t += stride) {
-        float v[V], p[V];
+    for (int64_t base = warp_first; base < a.T; base += step, t += step) {
+        const Logits<DT, V> x = next;
+        if (base + step < a.T) fetch(t + step);
+        uint32_t key[V];
+        uint32_t best = 0u;                       // this lane's largest key, and (fp32) where it is
+        int at = 0;
+        auto rescan = [&]() {
+            best = 0u;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if constexpr (DT == TG_F32) {
+                    if (key[j] > best) { best = key[j]; at = j; }
+                } else {
+                    best = max(best, key[j]);
+                }
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = order_key<DT>(x.bits(j), static_cast<uint32_t>(first + j));
+        rescan();
+        uint32_t top = group_max<L>(best);
+        const bool any = top != 0u;
+        const float m = any ? key_value<DT>(top) : 0.0f;      // the row's largest logit
+        float p[V];
+        float total = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int g = lane + 32 * j;
-            v[j] = g < a.G ? load_logit<DT>(a.logits, t * a.ld + g) : __int_as_float(0xff800000);
+            p[j] = any ? __expf(x.value(j) - m) : 0.0f;
+            total += p[j];
         }
-        rows += row_softmax<V>(v, p) ? 1 : 0;
+        total = group_sum<L>(total);
+        const float inv = any ? 1.0f / total : 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] += p[j];
+        for (int j = 0; j < V; ++j) sum[j] = fmaf(p[j], inv, sum[j]);
+        rows += any && in == 0 ? 1 : 0;
 
-        uint32_t key[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = order_key(v[j]);
+        // the i-th choice ends up with lane i of the row
         int my_e = -1;
-        float my_w = 0.0f, total = 0.0f;
+        float my_w = 0.0f, chosen = 0.0f;
         for (int i = 0; i < a.k; ++i) {
-            uint32_t best = 0u;
-#pragma unroll
-            for (int j = 0; j < V; ++j) best = max(best, key[j]);
-            best = __reduce_max_sync(0xffffffffu, best);
-            if (best == 0u) break;
-            uint32_t at = 0xffffffffu;
-#pragma unroll
-            for (int j = V - 1; j >= 0; --j)
-                if (key[j] == best) at = static_cast<uint32_t>(lane + 32 * j);
-            at = __reduce_min_sync(0xffffffffu, at);
-            float w = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (static_cast<uint32_t>(lane + 32 * j) == at) {
-                    key[j] = 0u;
-                    w = p[j];
-                }
-            w = __shfl_sync(0xffffffffu, w, at % 32);
-            total += w;
-            if (lane == i) {
-                my_e = static_cast<int>(at);
+            if (i > 0) top = group_max<L>(best);
+            if (!__any_sync(FULL, top != 0u)) break;
+            int e;
+            bool mine;
+            if constexpr (DT == TG_F32) {
+                // equal values: the lowest lane holds the lowest indices
+                const uint32_t has = __ballot_sync(FULL, best == top) >> (lane - in) & (L == 32 ? FULL : (1u << L % 32) - 1u);
+                const int who = __ffs(has) - 1;
+                e = __shfl_sync(FULL, first + at, who, L);
+                mine = in == who;
+            } else {
+                e = static_cast<int>(0xffffu ^ (top & 0xffffu));
+                mine = best == top;
+            }
+            if (top == 0u) continue;              // another row of the warp still chooses
+            const float w = __expf(key_value<DT>(top) - m) * inv;
+            chosen += w;
+            if (in == i) {
+                my_e = e;
                 my_w = w;
-                atomicAdd(&s_count[at], 1);
+                atomicAdd(&s_count[e], 1);
+            }
+            if (mine) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (DT == TG_F32 ? j == at : key[j] == top) key[j] = 0u;
+                rescan();
             }
         }
-        if (lane < a.k) {
-            a.experts[t * a.k + lane] = my_e;
-            a.weights[t * a.k + lane] = (a.renorm && my_e >= 0) ? my_w / total : my_w;
+        if (in < a.k && t < a.T) {
+            a.experts[t * a.k + in] = my_e;
+            a.weights[t * a.k + in] = (a.renorm && my_e >= 0) ? my_w / chosen : my_w;
         }
     }
+    // the row slots of a warp, then the warps of the block
 #pragma unroll
-    for (int j = 0; j < V; ++j) s_sum[warp][lane + 32 * j] = sum[j];
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int d = L; d < 32; d <<= 1) sum[j] += __shfl_xor_sync(FULL, sum[j], d);
+        if (lane < L) s_sum[warp * SPAN + first + j] = sum[j];
+    }
+    rows = __reduce_add_sync(FULL, rows);
     if (lane == 0) s_rows[warp] = rows;
     __syncthreads();
+    int block_rows = 0;
+#pragma unroll
+    for (int w = 0; w < R_WARPS; ++w) block_rows += s_rows[w];
+    const double live = block_rows > 0 ? static_cast<double>(block_rows) : 1.0;
+    double loss = 0.0;
     for (int g = threadIdx.x; g < a.G; g += R_THREADS) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < R_WARPS; ++w) s += s_sum[w][g];
-        a.part_p[static_cast<int64_t>(blockIdx.x) * a.G + g] = s;
-        a.part_c[static_cast<int64_t>(blockIdx.x) * a.G + g] = s_count[g];
+        for (int w = 0; w < R_WARPS; ++w) s += s_sum[w * SPAN + g];
+        if (a.part_p) {
+            a.part_p[static_cast<int64_t>(blockIdx.x) * a.G + g] = s;
+            a.part_c[static_cast<int64_t>(blockIdx.x) * a.G + g] = s_count[g];
+        } else {
+            loss += finish_expert(a, g, s, s_count[g], live);
+        }
     }
+    if (a.part_p) {
+        if (threadIdx.x == 0) a.part_n[blockIdx.x] = block_rows;
+        return;
+    }
+    // the only block finishes the loss itself
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) loss += __shfl_xor_sync(FULL, loss, d);
+    if (lane == 0) s_loss[warp] = loss;
+    __syncthreads();
     if (threadIdx.x == 0) {
-        int n = 0;
-        for (int w = 0; w < R_WARPS; ++w) n += s_rows[w];
-        a.part_n[blockIdx.x] = n;
+        for (int w = 1; w < R_WARPS; ++w) loss += s_loss[w];
+        *a.loss = static_cast<float>(loss);
     }
 }
 
-// Join the blocks' partial sums (in block order, probabilities in double): counts, slope, loss.
-constexpr int F_THREADS = 256;
+// Join the blocks' partial sums, probabilities in double: a cluster of JOIN_CTAS blocks, each
+// taking every JOIN_CTAS-th group of 32 experts (a lane each) with its warps spread over the
+// partial sums, and the first block adding the loss's terms.  (One block reading one partial
+// sum after the other took 70 us for 304 of them.)
+constexpr int JOIN_CTAS = 8;
+constexpr int JOIN_WARPS = 32;
 
-__global__ void __launch_bounds__(F_THREADS) router_join_kernel(const RouterArgs a, int blocks) {
-    __shared__ int64_t s_n[F_THREADS];
-    __shared__ double s_loss[F_THREADS];
+__global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(32 * JOIN_WARPS)
+    router_join_kernel(const RouterArgs a, int blocks) {
+    __shared__ double s_p[JOIN_WARPS][32];
+    __shared__ int32_t s_c[JOIN_WARPS][32];
+    __shared__ int32_t s_n[JOIN_WARPS];
+    __shared__ double s_loss[JOIN_CTAS];           // in block 0: every block's share
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = ptx::cluster_ctarank();
     ptx::grid_dependency_wait();
-    int64_t n = 0;
-    for (int b = threadIdx.x; b < blocks; b += F_THREADS) n += a.part_n[b];
-    s_n[threadIdx.x] = n;
+    int n = 0;
+    for (int b = threadIdx.x; b < blocks; b += 32 * JOIN_WARPS) n += a.part_n[b];
+    n = __reduce_add_sync(FULL, n);
+    if (lane == 0) s_n[warp] = n;
     __syncthreads();
-    for (int d = F_THREADS / 2; d > 0; d >>= 1) {
-        if (threadIdx.x < d) s_n[threadIdx.x] += s_n[threadIdx.x + d];
-        __syncthreads();
-    }
-    const double rows = s_n[0] > 0 ? static_cast<double>(s_n[0]) : 1.0;
+    int64_t total = 0;
+    for (int w = 0; w < JOIN_WARPS; ++w) total += s_n[w];
+    const double rows = total > 0 ? static_cast<double>(total) : 1.0;
     double loss = 0.0;
-    for (int g = threadIdx.x; g < a.G; g += F_THREADS) {
+    for (int g0 = static_cast<int>(rank) * 32; g0 < a.G; g0 += 32 * JOIN_CTAS) {
+        const int g = g0 + lane;
         double s = 0.0;
         int32_t c = 0;
-        for (int b = 0; b < blocks; ++b) {
-            s += static_cast<double>(a.part_p[static_cast<int64_t>(b) * a.G + g]);
-            c += a.part_c[static_cast<int64_t>(b) * a.G + g];
+        if (g < a.G) {
+#pragma unroll 4
+            for (int b = warp; b < blocks; b += JOIN_WARPS) {
+                s += static_cast<double>(a.part_p[static_cast<int64_t>(b) * a.G + g]);
+                c += a.part_c[static_cast<int64_t>(b) * a.G + g];
+            }
         }
-        a.counts[g] = c;
-        const double slope = a.G * static_cast<double>(c) / (rows * a.k) / rows;
-        a.slope[g] = static_cast<float>(slope);
-        loss += slope * s;
-    }
-    s_loss[threadIdx.x] = loss;
-    __syncthreads();
-    for (int d = F_THREADS / 2; d > 0; d >>= 1) {
-        if (threadIdx.x < d) s_loss[threadIdx.x] += s_loss[threadIdx.x + d];
+        s_p[warp][lane] = s;
+        s_c[warp][lane] = c;
+        __syncthreads();
+        if (warp == 0 && g < a.G) {
+            for (int w = 1; w < JOIN_WARPS; ++w) {
+                s += s_p[w][lane];
+                c += s_c[w][lane];
+            }
+            loss += finish_expert(a, g, s, c, rows);
+        }
         __syncthreads();
     }
-    if (threadIdx.x == 0) *a.loss = static_cast<float>(s_loss[0]);
+    if (warp == 0) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) loss += __shfl_xor_sync(FULL, loss, d);
+        if (lane == 0) {
+            const uint32_t dst = ptx::mapa(ptx::smem_u32(&s_loss[rank]), 0);
+            asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(dst), "d"(loss) : "memory");
+        }
+    }
+    ptx::cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        double sum = 0.0;
+        for (int r = 0; r < JOIN_CTAS; ++r) sum += s_loss[r];
+        *a.loss = static_cast<float>(sum);
+    }
 }
 
 struct BackArgs {
-    const void* logits;
-    int64_t ld, T;
-    int G, k, renorm;
+    const uint8_t* logits;
+    int64_t ld_bytes, T;
+    int G, k, renorm, vec_in, vec_out;
     const int32_t* experts;
     const float* weights;
     const float* slope;
     const float* d_weights;   // null: zero
     const float* d_loss;      // null: zero
-    void* out;
-    int64_t ldo;
+    uint8_t* out;
+    int64_t ldo_bytes;
 };
 
-template <int DT, int V>
-__global__ void __launch_bounds__(R_THREADS) router_backward_kernel(const BackArgs a) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+template <int DT, int L, int V>
+__global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_backward_kernel(const BackArgs a) {
+    using X = Logits<DT, V>;
+    constexpr int ROWS = 32 / L;
+    // per warp: what the chosen experts of its rows get on top, by expert; zero elsewhere
+    extern __shared__ __align__(16) uint8_t dyn[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, in = lane % L;
+    float* extra = reinterpret_cast<float*>(dyn) + warp * 32 * V + (lane / L) * L * V;
+    const int first = in * V;
+    const int n = a.G - first < 0 ? 0 : a.G - first < V ? a.G - first : V;
     const float dl = a.d_loss ? __ldg(a.d_loss) : 0.0f;
     float u[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int g = lane + 32 * j;
-        u[j] = (a.d_loss && g < a.G) ? dl * __ldg(a.slope + g) : 0.0f;
+        u[j] = (a.d_loss && j < n) ? dl * __ldg(a.slope + first + j) : 0.0f;
+        extra[first + j] = 0.0f;
     }
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * R_WARPS;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * R_WARPS + warp; t < a.T; t += stride) {
-        float v[V], p[V];
+    __syncwarp();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R_WARPS * ROWS;
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
+    const int64_t warp_first = t - lane / L;
+    const bool choice = a.d_weights != nullptr && in < a.k;
+    X next;
+    int e_next = -1;
+    float w_next = 0.0f, dw_next = 0.0f;
+    auto fetch = [&](int64_t row) {
+        next.load(a.logits + row * a.ld_bytes + first * X::ESIZE, row < a.T ? n : 0, a.vec_in != 0);
+        e_next = -1;
+        if (choice && row < a.T) {
+            e_next = __ldg(a.experts + row * a.k + in);
+            w_next = __ldg(a.weights + row * a.k + in);
+            dw_next = __ldg(a.d_weights + row * a.k + in);
+        }
+        if (e_next < 0 || e_next >= a.G) {       // no choice (-1): nothing of it counts
+            e_next = -1;
+            w_next = dw_next = 0.0f;
+        }
+    };
+    fetch(t);
+    for (int64_t base = warp_first; base < a.T; base += step, t += step) {
+        const X x = next;
+        const int e = e_next;
+        const float w = w_next, dw = dw_next;
+        if (base + step < a.T) fetch(t + step);
+        float m = __int_as_float(0xff800000);
+        bool any = false;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int g = lane + 32 * j;
-            v[j] = g < a.G ? load_logit<DT>(a.logits, t * a.ld + g) : __int_as_float(0xff800000);
+            m = fmaxf(m, x.value(j));
+            any |= x.value(j) != __int_as_float(0xff800000);       // true for NaN, too
         }
-        int e = -1;
-        float w = 0.0f, dw = 0.0f;
-        if (a.d_weights && lane < a.k) {
-            e = __ldg(a.experts + t * a.k + lane);
-            w = __ldg(a.weights + t * a.k + lane);
-            dw = __ldg(a.d_weights + t * a.k + lane);
-            if (e < 0) w = dw = 0.0f;
-        }
-        row_softmax<V>(v, p);
-        float cu = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) cu = fmaf(p[j], u[j], cu);
-        cu = warp_sum(cu);
-        const float cw = warp_sum(w * dw);
-        const float c = a.renorm ? cu : cu + cw;
-        const float add = a.renorm ? w * (dw - cw) : w * dw;
+        for (int d = L / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
+        any = (__ballot_sync(FULL, any) >> (lane - in) & (L == 32 ? FULL : (1u << L % 32) - 1u)) != 0u;
+        float p[V];
+        float total = 0.0f, pu = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            p[j] = any ? __expf(x.value(j) - m) : 0.0f;
+            total += p[j];
+            pu = fmaf(p[j], u[j], pu);
+        }
+        total = group_sum<L>(total);
+        const float inv = any ? 1.0f / total : 0.0f;
+        const float cu = group_sum<L>(pu) * inv;
+        float c = cu;
+        if (a.d_weights) {
+            const float cw = group_sum<L>(w * dw);
+            if (!a.renorm) c += cw;
+            if (e >= 0) extra[e] = a.renorm ? w * (dw - cw) : w * dw;
+            __syncwarp();
+        }
         float d[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = p[j] * (u[j] - c);
-        for (int i = 0; i < a.k; ++i) {
-            const int ei = __shfl_sync(0xffffffffu, e, i);
-            const float ai = __shfl_sync(0xffffffffu, add, i);
+        for (int j = 0; j < V; ++j) d[j] = p[j] * inv * (u[j] - c);
+        if (a.d_weights) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (lane + 32 * j == ei) d[j] += ai;
+            for (int j = 0; j < V; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(extra + first + j);
+                d[j] += f.x; d[j + 1] += f.y; d[j + 2] += f.z; d[j + 3] += f.w;
+            }
+            __syncwarp();
+            if (e >= 0) extra[e] = 0.0f;
+            __syncwarp();
         }
+        if (t >= a.T) continue;
+        uint8_t* dst = a.out + t * a.ldo_bytes + first * X::ESIZE;
+        uint32_t o[X::WORDS];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int g = lane + 32 * j;
-            if (g < a.G) store_logit<DT>(a.out, t * a.ldo + g, d[j]);
+        for (int i = 0; i < X::WORDS; ++i) {
+            if constexpr (DT == TG_F32) {
+                o[i] = __float_as_uint(d[i]);
+            } else if constexpr (DT == TG_F16) {
+                const __half2 h = __floats2half2_rn(d[2 * i], d[2 * i + 1]);
+                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
+                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        if (n == V && a.vec_out) {
+#pragma unroll
+            for (int i = 0; i < X::WORDS; i += 4)
+                reinterpret_cast<uint4*>(dst)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (j >= n) continue;
+                if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(dst)[j] = o[j];
+                else reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(o[j / 2] >> ((j & 1) * 16));
+            }
         }
     }
 }
@@ -300,17 +494,25 @@ __global__ void __launch_bounds__(R_THREADS) router_backward_kernel(const BackAr
 using RouterKernel = void (*)(const RouterArgs);
 using BackKernel = void (*)(const BackArgs);
 
-template <int DT>
-RouterKernel router_for(int G) {
-    return G <= 32 ? &router_kernel<DT, 1> : G <= 64 ? &router_kernel<DT, 2> : G <= 128 ? &router_kernel<DT, 4>
-         : G <= 256 ? &router_kernel<DT, 8> : G <= 512 ? &router_kernel<DT, 16> : &router_kernel<DT, 32>;
-}
+// The kernel for G experts and k choices: L lanes a row, V experts a lane.
+struct RouterVariant {
+    RouterKernel forward;
+    BackKernel backward;
+    int lanes, per_lane;
+};
 
 template <int DT>
-BackKernel back_for(int G) {
-    return G <= 32 ? &router_backward_kernel<DT, 1> : G <= 64 ? &router_backward_kernel<DT, 2>
-         : G <= 128 ? &router_backward_kernel<DT, 4> : G <= 256 ? &router_backward_kernel<DT, 8>
-         : G <= 512 ? &router_backward_kernel<DT, 16> : &router_backward_kernel<DT, 32>;
+RouterVariant variant_for(int G, int k) {
+    const int need = (G + 7) / 8 > k ? (G + 7) / 8 : k;
+    if (G > 512) return {&router_kernel<DT, 32, 32>, &router_backward_kernel<DT, 32, 32>, 32, 32};
+    if (G > 256) return {&router_kernel<DT, 32, 16>, &router_backward_kernel<DT, 32, 16>, 32, 16};
+    if (need > 16) return {&router_kernel<DT, 32, 8>, &router_backward_kernel<DT, 32, 8>, 32, 8};
+    if (need > 8) return {&router_kernel<DT, 16, 8>, &router_backward_kernel<DT, 16, 8>, 16, 8};
+    return {&router_kernel<DT, 8, 8>, &router_backward_kernel<DT, 8, 8>, 8, 8};
+}
+
+RouterVariant variant_for(tg_dtype dt, int G, int k) {
+    return dt == TG_F32 ? variant_for<TG_F32>(G, k) : dt == TG_F16 ? variant_for<TG_F16>(G, k) : variant_for<TG_BF16>(G, k);
 }
 
 tg_status check_router(const void* logits, tg_dtype dt, int64_t ld, int64_t T, int64_t G, int64_t k) {
@@ -333,9 +535,11 @@ tg_status check_router(const void* logits, tg_dtype dt, int64_t ld, int64_t T, i
     return TG_OK;
 }
 
-int row_blocks(int64_t T, int sms) {
-    const int64_t want = (T + R_WARPS - 1) / R_WARPS, cap = static_cast<int64_t>(sms) * R_BLOCKS_PER_SM;
-    return static_cast<int>(want < 1 ? 1 : want > cap ? cap : want);
+// Raise a kernel's limit of dynamic shared memory where it needs more than the default.
+template <class K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
 }  // namespace
@@ -358,34 +562,51 @@ extern "C" tg_status tg_moe_router(const void* logits, tg_dtype dtype, int64_t l
     host::Device d;
     if ((s = host::device(&d)) != TG_OK) return s;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int blocks = row_blocks(T, d.sms);
+    const RouterVariant v = variant_for(dtype, static_cast<int>(G), static_cast<int>(k));
+    const int64_t esize = dtype == TG_F32 ? 4 : 2;
+    const int64_t block_rows = R_WARPS * (32 / v.lanes);
+    // One block (which then needs no second kernel and no workspace) while it has at most four rows
+    // a slot; beyond that every SM.
+    const int64_t want = (T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
+    const int blocks = want <= 4 ? 1 : static_cast<int>(want < cap ? want : cap);
     void* ws = nullptr;
-    const size_t words = static_cast<size_t>(blocks) * (2 * G + 1);
-    if ((s = host::workspace(words * 4, st, "cudaMallocFromPoolAsync(router partial sums)", &ws)) != TG_OK) return s;
-    RouterArgs a{logits, ld, T, int(G), int(k), renormalize != 0, experts, weights, counts, loss, slope,
-                 static_cast<float*>(ws), static_cast<int32_t*>(ws) + blocks * G,
-                 static_cast<int32_t*>(ws) + 2 * blocks * G};
-    const RouterKernel kern = dtype == TG_F32 ? router_for<TG_F32>(a.G)
-                            : dtype == TG_F16 ? router_for<TG_F16>(a.G) : router_for<TG_BF16>(a.G);
-    kern<<<blocks, R_THREADS, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    RouterArgs a{static_cast<const uint8_t*>(logits), ld * esize, T, int(G), int(k), renormalize != 0,
+                 host::aligned(logits, 16) && ld * esize % 16 == 0, experts, weights, counts, loss, slope,
+                 nullptr, nullptr, nullptr};
+    if (blocks > 1) {
+        const size_t words = static_cast<size_t>(blocks) * (2 * G + 1);
+        if ((s = host::workspace(words * 4, st, "cudaMallocFromPoolAsync(router partial sums)", &ws)) != TG_OK) return s;
+        a.part_p = static_cast<float*>(ws);
+        a.part_c = static_cast<int32_t*>(ws) + blocks * G;
+        a.part_n = static_cast<int32_t*>(ws) + 2 * blocks * G;
+    }
+    const size_t smem = static_cast<size_t>(R_WARPS + 1) * v.lanes * v.per_lane * 4;
+    cudaError_t e = allow_smem(v.forward, smem);
+    if (e == cudaSuccess) {
+        v.forward<<<blocks, R_THREADS, smem, st>>>(a);
+        e = cudaGetLastError();
+    }
     if (e == cudaSuccess) {
         host::count_launches(1);
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(1, 1, 1);
-        cfg.blockDim = dim3(F_THREADS, 1, 1);
-        cfg.stream = st;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, router_join_kernel, static_cast<const RouterArgs&>(a), blocks);
-        if (e == cudaSuccess) host::count_launches(1);
+        if (blocks > 1) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(JOIN_CTAS, 1, 1);
+            cfg.blockDim = dim3(32 * JOIN_WARPS, 1, 1);
+            cfg.stream = st;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, router_join_kernel, static_cast<const RouterArgs&>(a), blocks);
+            if (e == cudaSuccess) host::count_launches(1);
+        }
     }
     s = e == cudaSuccess ? TG_OK : host::cuda_fail(e, "router launch");
-    e = cudaFreeAsync(ws, st);
-    if (e != cudaSuccess && s == TG_OK) s = host::cuda_fail(e, "cudaFreeAsync(router partial sums)");
+    if (ws) {
+        e = cudaFreeAsync(ws, st);
+        if (e != cudaSuccess && s == TG_OK) s = host::cuda_fail(e, "cudaFreeAsync(router partial sums)");
+    }
     return s;
 }
 
@@ -410,13 +631,20 @@ extern "C" tg_status tg_moe_router_backward(const void* logits, tg_dtype dtype, 
         return fail(TG_ERR_INVALID_ARG, "an input is not 4-byte aligned");
     host::Device d;
     if ((s = host::device(&d)) != TG_OK) return s;
-    const BackArgs a{logits, ld, T, int(G), int(k), renormalize != 0, experts, weights, slope, d_weights, d_loss,
-                     d_logits, ldd};
-    const BackKernel kern = dtype == TG_F32 ? back_for<TG_F32>(a.G)
-                          : dtype == TG_F16 ? back_for<TG_F16>(a.G) : back_for<TG_BF16>(a.G);
-    const int64_t want = (T + R_WARPS - 1) / R_WARPS, cap = static_cast<int64_t>(d.sms) * 8;
-    kern<<<static_cast<unsigned>(want < cap ? want : cap), R_THREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const RouterVariant v = variant_for(dtype, static_cast<int>(G), static_cast<int>(k));
+    const int64_t esize = dtype == TG_F32 ? 4 : 2;
+    const BackArgs a{static_cast<const uint8_t*>(logits), ld * esize, T, int(G), int(k), renormalize != 0,
+                     host::aligned(logits, 16) && ld * esize % 16 == 0,
+                     host::aligned(d_logits, 16) && ldd * esize % 16 == 0, experts, weights, slope, d_weights, d_loss,
+                     static_cast<uint8_t*>(d_logits), ldd * esize};
+    const int64_t block_rows = R_WARPS * (32 / v.lanes);
+    const int64_t want = (T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
+    const size_t smem = static_cast<size_t>(R_WARPS) * 32 * v.per_lane * 4;
+    cudaError_t e = allow_smem(v.backward, smem);
+    if (e == cudaSuccess) {
+        v.backward<<<static_cast<unsigned>(want < cap ? want : cap), R_THREADS, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return host::cuda_fail(e, "router backward launch");
     host::count_launches(1);
     return TG_OK;
