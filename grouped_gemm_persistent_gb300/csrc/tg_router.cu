@@ -17,9 +17,17 @@
 // L lanes of a warp hold one row (L = 8, 16 or 32, at least k and G / 8), each V
 // neighbouring experts; a warp works on 32 / L rows at once, with the next rows' logits on
 // their way.  Everything is summed in a fixed order - a lane over its rows, a warp's row
-// slots, the warps of a block, then the blocks in double - so results do not depend on
-// timing.  The kernels are bound by instruction issue (the k selection steps), not by the
-// memory they read once.
+// slots, the warps of a block, then the blocks - so results do not depend on
+// timing.
+//
+// Selection.  An expert's key is its logit's bits made to order like an unsigned integer, the
+// lowest 8 (9, 10 above 256, 512 experts) replaced by the expert's index counted down, so that
+// keys are unique and equal logits go to the lowest index.  Keys come out in decreasing order,
+// so those still to come are the ones below the last one, t: the largest of (key - t) modulo
+// 2^32, one fused add-and-maximum a key.  For 16-bit logits the replaced bits are zeros anyway;
+// fp32 logits that agree in all the others, at the top of a row, send that row through an exact
+// selection (choose_exactly).  131072 x 256 fp32, k = 8: 152 us with a rescan of (value, index)
+// pairs after every choice, 1018 warp instructions a row, against the read's 20 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -83,34 +91,19 @@ struct Logits {
         else return __uint_as_float(b << 16);
     }
     __device__ __forceinline__ float value(int j) const { return widen(bits(j)); }
+    // logit g of the row at p
+    static __device__ __forceinline__ float one(const uint8_t* p, int g) {
+        if constexpr (DT == TG_F32) return __ldg(reinterpret_cast<const float*>(p) + g);
+        else return widen(__ldg(reinterpret_cast<const uint16_t*>(p) + g));
+    }
 };
 
-// An unsigned key that orders like the value: -0 equals +0, NaN is above everything, and 0 stands
-// for "not to be chosen" (-infinity, or taken already).  The 16-bit types' keys carry the expert's
-// index below the value, so that a maximum is unique and goes to the lowest index.
-template <int DT>
-__device__ __forceinline__ uint32_t order_key(uint32_t b, uint32_t expert) {
-    if constexpr (DT == TG_F32) {
-        if (b == 0xff800000u) return 0u;
-        if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
-        if (b == 0x80000000u) b = 0u;
-        return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    } else {
-        constexpr uint32_t INF = DT == TG_F16 ? 0x7c00u : 0x7f80u;
-        if (b == (0x8000u | INF)) return 0u;
-        if (b == 0x8000u) b = 0u;
-        uint32_t s = (b & 0x8000u) ? b ^ 0xffffu : b | 0x8000u;
-        if ((b & 0x7fffu) > INF) s = 0xffffu;
-        return s << 16 | (0xffffu ^ expert);
-    }
-}
+constexpr uint32_t KEY_MIN = 0x00800000u;      // keys of -infinity lie below it
 
-// The value a key stands for (NaN for a NaN).
-template <int DT>
-__device__ __forceinline__ float key_value(uint32_t key) {
-    if constexpr (DT == TG_F32) return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
-    const uint32_t s = key >> 16;
-    return Logits<DT, 8>::widen((s & 0x8000u) ? s & 0x7fffu : s ^ 0xffffu);
+// The bits of a value that is not NaN, ordered like an unsigned integer; -0 equals +0.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 
 // Over the L lanes of a row
@@ -132,6 +125,50 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
+// NaN if any is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// e^x, zero below fp32's normal values: for probabilities that are summed.
+__device__ __forceinline__ float exp_flush(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+
+// The k choices of a row from its logits alone, in order of value (NaN first) and index: lane i
+// gets the i-th expert, or -1.  Every lane of the warp calls it; a row that need not choose
+// (!wanted) takes part and gets nothing.
+template <int DT, int L, int V>
+__device__ __noinline__ int choose_exactly(const Logits<DT, V>& x, int first, int k, bool wanted) {
+    const int lane = threadIdx.x % 32, in = lane % L;
+    uint32_t taken = wanted ? 0u : (V == 32 ? FULL : (1u << V % 32) - 1u);
+    int my_e = -1;
+    for (int i = 0; i < k; ++i) {
+        // this lane's best: the key of its value (1 and up; NaN on top), then the lowest index
+        uint32_t best = 0u;
+        int at = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float v = x.value(j);
+            const uint32_t key = (taken >> j & 1u) || v == __int_as_float(0xff800000) ? 0u : v != v ? FULL : order_bits(v);
+            if (key > best) { best = key; at = j; }
+        }
+        const uint32_t top = group_max<L>(best);
+        const uint32_t has = __ballot_sync(FULL, best == top) >> (lane - in) & (L == 32 ? FULL : (1u << L % 32) - 1u);
+        const int who = __ffs(has) - 1;          // the lowest lane holds the lowest indices
+        const int e = __shfl_sync(FULL, first + at, who, L);
+        if (top != 0u) {
+            if (in == i) my_e = e;
+            if (in == who) taken |= 1u << at;
+        }
+    }
+    return my_e;
+}
+
 struct RouterArgs {
     const uint8_t* logits;
     int64_t ld_bytes, T;
@@ -147,10 +184,17 @@ struct RouterArgs {
     int32_t* part_n;
 };
 
+// What turns an expert's count into its slope: G / (n k) / n.  Computed once a thread: this GPU's
+// double precision is slow, a division a warp and expert cost the join 7 us.
+__device__ __forceinline__ double slope_per_count(const RouterArgs& a, int64_t rows) {
+    const double n = rows > 0 ? static_cast<double>(rows) : 1.0;
+    return a.G / (n * n * a.k);
+}
+
 // counts, slope and this expert's term of the loss
-__device__ __forceinline__ double finish_expert(const RouterArgs& a, int g, double sum, int32_t count, double rows) {
+__device__ __forceinline__ double finish_expert(const RouterArgs& a, int g, float sum, int32_t count, double per_count) {
     a.counts[g] = count;
-    const double slope = a.G * static_cast<double>(count) / (rows * a.k) / rows;
+    const double slope = per_count * count;
     a.slope[g] = static_cast<float>(slope);
     return slope * sum;
 }
@@ -187,31 +231,17 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const
     for (int64_t base = warp_first; base < a.T; base += step, t += step) {
         const Logits<DT, V> x = next;
         if (base + step < a.T) fetch(t + step);
-        uint32_t key[V];
-        uint32_t best = 0u;                       // this lane's largest key, and (fp32) where it is
-        int at = 0;
-        auto rescan = [&]() {
-            best = 0u;
+        float m = x.value(0);                     // the row's largest logit, NaN if it has one
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if constexpr (DT == TG_F32) {
-                    if (key[j] > best) { best = key[j]; at = j; }
-                } else {
-                    best = max(best, key[j]);
-                }
-            }
-        };
+        for (int j = 1; j < V; ++j) m = max_nan(m, x.value(j));
 #pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = order_key<DT>(x.bits(j), static_cast<uint32_t>(first + j));
-        rescan();
-        uint32_t top = group_max<L>(best);
-        const bool any = top != 0u;
-        const float m = any ? key_value<DT>(top) : 0.0f;      // the row's largest logit
+        for (int d = L / 2; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(FULL, m, d));
+        const bool any = m != __int_as_float(0xff800000);
         float p[V];
         float total = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            p[j] = any ? __expf(x.value(j) - m) : 0.0f;
+            p[j] = any ? exp_flush(x.value(j) - m) : 0.0f;
             total += p[j];
         }
         total = group_sum<L>(total);
@@ -220,42 +250,53 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const
         for (int j = 0; j < V; ++j) sum[j] = fmaf(p[j], inv, sum[j]);
         rows += any && in == 0 ? 1 : 0;
 
-        // the i-th choice ends up with lane i of the row
-        int my_e = -1;
-        float my_w = 0.0f, chosen = 0.0f;
-        for (int i = 0; i < a.k; ++i) {
-            if (i > 0) top = group_max<L>(best);
-            if (!__any_sync(FULL, top != 0u)) break;
-            int e;
-            bool mine;
-            if constexpr (DT == TG_F32) {
-                // equal values: the lowest lane holds the lowest indices
-                const uint32_t has = __ballot_sync(FULL, best == top) >> (lane - in) & (L == 32 ? FULL : (1u << L % 32) - 1u);
-                const int who = __ffs(has) - 1;
-                e = __shfl_sync(FULL, first + at, who, L);
-                mine = in == who;
-            } else {
-                e = static_cast<int>(0xffffu ^ (top & 0xffffu));
-                mine = best == top;
-            }
-            if (top == 0u) continue;              // another row of the warp still chooses
-            const float w = __expf(key_value<DT>(top) - m) * inv;
-            chosen += w;
-            if (in == i) {
-                my_e = e;
-                my_w = w;
-                atomicAdd(&s_count[e], 1);
-            }
-            if (mine) {
+        // the i-th choice ends up with lane i of the row; one more is looked at, to see that the
+        // last one is apart from it
+        constexpr uint32_t LOW = L * V - 1 > 255 ? L * V - 1 : 255;
+        uint32_t key[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (DT == TG_F32 ? j == at : key[j] == top) key[j] = 0u;
-                rescan();
+        for (int j = 0; j < V; ++j)
+            key[j] = (order_bits(x.value(j)) & ~LOW) | (LOW - static_cast<uint32_t>(first + j));
+        uint32_t mine = 0u, top = 0u;
+        for (int i = 0; i <= a.k; ++i) {
+            uint32_t best = 0u;
+#pragma unroll
+            for (int j = 0; j < V; ++j) best = __viaddmax_u32(key[j], 0u - top, best);
+            top += group_max<L>(best);
+            if (in == i) mine = top;
+        }
+        // lane k (or, when there is none, every lane) has the first key left out
+        int my_e = mine >= KEY_MIN ? static_cast<int>(LOW - (mine & LOW)) : -1;
+        bool redo = m != m;
+        if constexpr (DT == TG_F32) {
+            uint32_t after = __shfl_down_sync(FULL, mine, 1, L);
+            if (in == L - 1) after = top;
+            const bool close = in < a.k && after >= KEY_MIN && ((mine ^ after) & ~LOW) == 0u;
+            if (__any_sync(FULL, close)) {
+                // do the row's values differ in the bits that the keys leave out?
+                uint32_t low = 0u;
+#pragma unroll
+                for (int j = 0; j < V; ++j) low |= x.bits(j);
+                const uint32_t group = L == 32 ? FULL : (1u << L % 32) - 1u;
+                const uint32_t c = __ballot_sync(FULL, close) >> (lane - in) & group;
+                const uint32_t o = __ballot_sync(FULL, (low & LOW) != 0u) >> (lane - in) & group;
+                redo |= c != 0u && o != 0u;
             }
         }
+        if (__any_sync(FULL, redo)) {
+            const int e = choose_exactly<DT, L, V>(x, first, a.k, redo);
+            if (redo) my_e = e;
+        }
+        float my_w = 0.0f;
+        if (in >= a.k) my_e = -1;
+        if (my_e >= 0) {
+            my_w = __expf(Logits<DT, V>::one(a.logits + t * a.ld_bytes, my_e) - m) * inv;
+            atomicAdd(&s_count[my_e], 1);
+        }
+        const float chosen = a.renorm ? group_sum<L>(my_w) : 1.0f;
         if (in < a.k && t < a.T) {
             a.experts[t * a.k + in] = my_e;
-            a.weights[t * a.k + in] = (a.renorm && my_e >= 0) ? my_w / chosen : my_w;
+            a.weights[t * a.k + in] = my_e >= 0 ? my_w / chosen : 0.0f;
         }
     }
     // the row slots of a warp, then the warps of the block
@@ -271,8 +312,8 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const
     int block_rows = 0;
 #pragma unroll
     for (int w = 0; w < R_WARPS; ++w) block_rows += s_rows[w];
-    const double live = block_rows > 0 ? static_cast<double>(block_rows) : 1.0;
-    double loss = 0.0;
+    double loss = 0.0, per_count = 0.0;
+    if (!a.part_p && warp * 32 < a.G) per_count = slope_per_count(a, block_rows);
     for (int g = threadIdx.x; g < a.G; g += R_THREADS) {
         float s = 0.0f;
 #pragma unroll
@@ -281,7 +322,7 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const
             a.part_p[static_cast<int64_t>(blockIdx.x) * a.G + g] = s;
             a.part_c[static_cast<int64_t>(blockIdx.x) * a.G + g] = s_count[g];
         } else {
-            loss += finish_expert(a, g, s, s_count[g], live);
+            loss += finish_expert(a, g, s, s_count[g], per_count);
         }
     }
     if (a.part_p) {
@@ -299,17 +340,19 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const
     }
 }
 
-// Join the blocks' partial sums, probabilities in double: a cluster of JOIN_CTAS blocks, each
-// taking every JOIN_CTAS-th group of 32 experts (a lane each) with its warps spread over the
-// partial sums, and the first block adding the loss's terms.  (One block reading one partial
-// sum after the other took 70 us for 304 of them.)
+// Join the blocks' partial sums: a cluster of JOIN_CTAS blocks, each taking every JOIN_CTAS-th
+// group of 32 experts, first with a lane an expert and the warps spread over the partial sums,
+// then with a warp an expert; one warp finishes them, and the first block adds the loss's terms.  (One block reading one
+// partial sum after the other took 70 us for 304 of them.)
 constexpr int JOIN_CTAS = 8;
 constexpr int JOIN_WARPS = 32;
 
 __global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(32 * JOIN_WARPS)
     router_join_kernel(const RouterArgs a, int blocks) {
-    __shared__ double s_p[JOIN_WARPS][32];
-    __shared__ int32_t s_c[JOIN_WARPS][32];
+    __shared__ float s_p[JOIN_WARPS][33];
+    __shared__ int32_t s_c[JOIN_WARPS][33];
+    __shared__ float s_sum[32];
+    __shared__ int32_t s_count[32];
     __shared__ int32_t s_n[JOIN_WARPS];
     __shared__ double s_loss[JOIN_CTAS];           // in block 0: every block's share
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -319,31 +362,30 @@ __global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(32 * JOIN_WA
     for (int b = threadIdx.x; b < blocks; b += 32 * JOIN_WARPS) n += a.part_n[b];
     n = __reduce_add_sync(FULL, n);
     if (lane == 0) s_n[warp] = n;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < JOIN_WARPS; ++w) total += s_n[w];
-    const double rows = total > 0 ? static_cast<double>(total) : 1.0;
-    double loss = 0.0;
+    double loss = 0.0, per_count = -1.0;
     for (int g0 = static_cast<int>(rank) * 32; g0 < a.G; g0 += 32 * JOIN_CTAS) {
-        const int g = g0 + lane;
-        double s = 0.0;
+        float s = 0.0f;
         int32_t c = 0;
-        if (g < a.G) {
-#pragma unroll 4
+        if (g0 + lane < a.G) {
+#pragma unroll 10
             for (int b = warp; b < blocks; b += JOIN_WARPS) {
-                s += static_cast<double>(a.part_p[static_cast<int64_t>(b) * a.G + g]);
-                c += a.part_c[static_cast<int64_t>(b) * a.G + g];
+                s += a.part_p[static_cast<int64_t>(b) * a.G + g0 + lane];
+                c += a.part_c[static_cast<int64_t>(b) * a.G + g0 + lane];
             }
         }
         s_p[warp][lane] = s;
         s_c[warp][lane] = c;
         __syncthreads();
-        if (warp == 0 && g < a.G) {
-            for (int w = 1; w < JOIN_WARPS; ++w) {
-                s += s_p[w][lane];
-                c += s_c[w][lane];
-            }
-            loss += finish_expert(a, g, s, c, rows);
+        s = group_sum<32>(s_p[lane][warp]);
+        c = __reduce_add_sync(FULL, s_c[lane][warp]);
+        if (lane == 0) {
+            s_sum[warp] = s;
+            s_count[warp] = c;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            if (per_count < 0.0) per_count = slope_per_count(a, __reduce_add_sync(FULL, s_n[lane]));
+            if (g0 + lane < a.G) loss += finish_expert(a, g0 + lane, s_sum[lane], s_count[lane], per_count);
         }
         __syncthreads();
     }
@@ -420,21 +462,17 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_backward_ker
         const int e = e_next;
         const float w = w_next, dw = dw_next;
         if (base + step < a.T) fetch(t + step);
-        float m = __int_as_float(0xff800000);
-        bool any = false;
+        float m = x.value(0);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            m = fmaxf(m, x.value(j));
-            any |= x.value(j) != __int_as_float(0xff800000);       // true for NaN, too
-        }
+        for (int j = 1; j < V; ++j) m = max_nan(m, x.value(j));
 #pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, d));
-        any = (__ballot_sync(FULL, any) >> (lane - in) & (L == 32 ? FULL : (1u << L % 32) - 1u)) != 0u;
+        for (int d = L / 2; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(FULL, m, d));
+        const bool any = m != __int_as_float(0xff800000);
         float p[V];
         float total = 0.0f, pu = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            p[j] = any ? __expf(x.value(j) - m) : 0.0f;
+            p[j] = any ? exp_flush(x.value(j) - m) : 0.0f;
             total += p[j];
             pu = fmaf(p[j], u[j], pu);
         }
