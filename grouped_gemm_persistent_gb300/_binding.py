@@ -32,6 +32,7 @@ FP8_BLOCK = 128     # values that share a scale
 
 _lib = None
 _lock = threading.Lock()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class TGError(RuntimeError):
@@ -54,7 +55,7 @@ class GroupProblem(ctypes.Structure):
 
 
 class Fp8Operand(ctypes.Structure):
-    """Mirror of tg_fp8_operand."""
+    """Mirror of tg_scaled_operand."""
     _fields_ = [
         ("data", ctypes.c_void_p), ("ld", ctypes.c_int64),
         ("scale", ctypes.c_void_p), ("scale_stride", ctypes.c_int64), ("scale_k_stride", ctypes.c_int64),
@@ -66,12 +67,14 @@ def header_functions() -> list[str]:
     """Names of the functions include/tg.h declares."""
     text = open(HEADER).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(tg_[a-z0-9_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(tg_[a-z_]+)\s*\(", text)))
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load libtg.so (built by grouped_gemm_persistent_gb300.build); raise if it is missing."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -97,13 +100,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_grouped_gemm.argtypes = [ctypes.POINTER(GroupProblem), ci, vp]
         lib.tg_grouped_gemm_noalloc.restype = ci
         lib.tg_grouped_gemm_noalloc.argtypes = [ctypes.POINTER(GroupProblem), ci, vp]
-        lib.tg_quantize_fp8.restype = ci
-        lib.tg_quantize_fp8.argtypes = [vp, ci, i64, i64, i64, ci, ci, vp, ci, i64, vp, i64, vp]
+        lib.tg_quantize_blocks.restype = ci
+        lib.tg_quantize_blocks.argtypes = [vp, ci, i64, i64, i64, ci, ci, vp, ci, i64, vp, i64, vp]
         op8 = ctypes.POINTER(Fp8Operand)
-        lib.tg_gemm_fp8.restype = ci
-        lib.tg_gemm_fp8.argtypes = [op8, op8, vp, ci, i64, i64, i64, i64, ci, vp, vp]
-        lib.tg_moe_gemm_fp8.restype = ci
-        lib.tg_moe_gemm_fp8.argtypes = [op8, i64, i64, op8, i64, i64, i64, i64, vp, ci, i64, vp, ci, vp, vp]
+        lib.tg_gemm_scaled.restype = ci
+        lib.tg_gemm_scaled.argtypes = [op8, op8, vp, ci, i64, i64, i64, i64, ci, vp, vp]
+        lib.tg_moe_gemm_scaled.restype = ci
+        lib.tg_moe_gemm_scaled.argtypes = [op8, i64, i64, op8, i64, i64, i64, i64, vp, ci, i64, vp, ci, vp, vp]
         lib.tg_moe_router.restype = ci
         lib.tg_moe_router.argtypes = [vp, ci, i64, i64, i64, i64, ci, vp, vp, vp, vp, vp, vp]
         lib.tg_moe_router_backward.restype = ci
@@ -139,6 +142,8 @@ def _check(status: int) -> None:
 
 def _stream_handle(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:      # the handle alone, without the Stream object around it
+            return _raw_stream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -352,18 +357,22 @@ def _rows_of_16_bytes(rows: int, cols: int, dtype: torch.dtype, device, stream) 
     return t if ld == cols else t[:, :cols]
 
 
-def _on_one_gpu(**tensors) -> None:
+def _on_one_gpu(names: str, *tensors) -> None:
     """The tensors (None is left out) are on one CUDA device, the current one."""
-    where = {name: t.device for name, t in tensors.items() if t is not None}
-    for name, dev in where.items():
-        if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-            raise ValueError(f"{name} must be on the current CUDA device, got {dev}")
+    current = None
+    for i, t in enumerate(tensors):
+        if t is not None:
+            dev = t.get_device()
+            if dev >= 0 and current is None:
+                current = torch.cuda.current_device()
+            if dev != current:
+                raise ValueError(f"{names.split()[i]} must be on the current CUDA device, got {t.device}")
 
 
 def quantize_fp8(x: torch.Tensor, block: tuple[int, int] = (1, 128), q: torch.Tensor | None = None,
                  scale: torch.Tensor | None = None, *, dtype: torch.dtype = torch.float8_e4m3fn,
                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-    """(q, scale): ``x`` [M, K] in 8 bits with one power-of-two scale for each ``block`` of values (tg_quantize_fp8).
+    """(q, scale): ``x`` [M, K] in 8 bits with one power-of-two scale for each ``block`` of values (tg_quantize_blocks).
 
     ``block`` is (1, 128), (128, 1) or (128, 128); ``scale`` (fp32) is [M, ceil(K / 128)] (a transposed view:
     a block column's scales lie side by side), [ceil(M / 128), K] or [ceil(M / 128), ceil(K / 128)].  ``x`` is
@@ -398,8 +407,8 @@ def quantize_fp8(x: torch.Tensor, block: tuple[int, int] = (1, 128), q: torch.Te
     if stored.shape[1] > 1 and stored.stride(1) != 1:
         raise ValueError("scale must have " + ("contiguous columns" if block == (1, 128) else "contiguous rows"))
     scale_ld = stored.stride(0) if stored.shape[0] > 1 else max(stored.shape[1], 1)
-    _on_one_gpu(x=x, q=q, scale=scale)
-    _check(load().tg_quantize_fp8(_ptr(x), _DTYPE_CODE[x.dtype], ldx, M, K, block[0], block[1], _ptr(q),
+    _on_one_gpu("x q scale", x, q, scale)
+    _check(load().tg_quantize_blocks(_ptr(x), _DTYPE_CODE[x.dtype], ldx, M, K, block[0], block[1], _ptr(q),
                                   _FP8_CODE[q.dtype], ldq, _ptr(scale), scale_ld, _stream_handle(stream)))
     return q, scale
 
@@ -433,7 +442,7 @@ def _fp8_scale(s: torch.Tensor, name: str, rows: int, kb: int, dim: int) -> tupl
 def gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: torch.Tensor,
              out: torch.Tensor | None = None, *, bias: torch.Tensor | None = None, epilogue: str = "none",
              out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
-    """out[M,N] = epilogue((a * scale_a) @ (b * scale_b)) for 8-bit operands with a scale per block of 128 (tg_gemm_fp8).
+    """out[M,N] = epilogue((a * scale_a) @ (b * scale_b)) for 8-bit operands with a scale per block of 128 (tg_gemm_scaled).
 
     ``a`` [M, K] and ``b`` [K, N] are float8_e4m3fn or float8_e5m2, each a row-major or column-major view.
     ``scale_a`` is fp32 [M, ceil(K / 128)] (or [ceil(M / 128), ...]), ``scale_b`` [ceil(K / 128), N] or
@@ -462,10 +471,10 @@ def gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: t
     epi = EPILOGUES[epilogue]
     if epi and (bias is None or bias.dtype != torch.bfloat16 or bias.numel() != N or not bias.is_contiguous()):
         raise ValueError("this epilogue needs a contiguous bf16 bias of length N")
-    _on_one_gpu(a=a, scale_a=scale_a, b=b, scale_b=scale_b, out=out, bias=bias if epi else None)
+    _on_one_gpu("a scale_a b scale_b out bias", a, scale_a, b, scale_b, out, bias if epi else None)
     oa = Fp8Operand(_ptr(a), lda, _ptr(scale_a), sa, sak, _FP8_CODE[a.dtype], la, ba)
     ob = Fp8Operand(_ptr(b), ldb, _ptr(scale_b), sb, sbk, _FP8_CODE[b.dtype], lb, bb)
-    _check(load().tg_gemm_fp8(ctypes.byref(oa), ctypes.byref(ob), _ptr(out), _DTYPE_CODE[out.dtype], ldc, M, N, K, epi,
+    _check(load().tg_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), _ptr(out), _DTYPE_CODE[out.dtype], ldc, M, N, K, epi,
                               _ptr(bias) if epi else None, _stream_handle(stream)))
     return out
 
@@ -473,7 +482,7 @@ def gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: t
 def moe_gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: torch.Tensor, counts: torch.Tensor,
                  out: torch.Tensor | None = None, *, bias: torch.Tensor | None = None, epilogue: str = "none",
                  out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
-    """moe_gemm_device with 8-bit operands (tg_moe_gemm_fp8): the token counts stay on the GPU.
+    """moe_gemm_device with 8-bit operands (tg_moe_gemm_scaled): the token counts stay on the GPU.
 
     ``a`` [T, K] row-major, rows grouped by expert, ``scale_a`` [T, ceil(K / 128)]; ``b`` [G, K, N], each expert
     row- or column-major, ``scale_b`` [G, ceil(K / 128), ceil(N / 128)]; ``counts`` int32 CUDA tensor [G];
@@ -508,14 +517,14 @@ def moe_gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_
     epi = EPILOGUES[epilogue]
     if epi and (bias is None or bias.dtype != torch.bfloat16 or tuple(bias.shape) != (G, N) or not bias.is_contiguous()):
         raise ValueError("this epilogue needs a contiguous bf16 bias [G, N]")
-    _on_one_gpu(a=a, scale_a=scale_a, b=b, scale_b=scale_b, counts=counts, out=out, bias=bias if epi else None)
+    _on_one_gpu("a scale_a b scale_b counts out bias", a, scale_a, b, scale_b, counts, out, bias if epi else None)
     if G == 0:
         return out
     lb, ldb = _fp8_matrix(b[0], "b")
     per = (K if lb == ROW_MAJOR else N) * ldb
     oa = Fp8Operand(_ptr(a), lda, _ptr(scale_a), sa, sak, _FP8_CODE[a.dtype], la, 1)
     ob = Fp8Operand(_ptr(b), ldb, _ptr(scale_b), scale_b.stride(2), scale_b.stride(1), _FP8_CODE[b.dtype], lb, FP8_BLOCK)
-    _check(load().tg_moe_gemm_fp8(ctypes.byref(oa), T, K, ctypes.byref(ob), b.stride(0) if G > 1 else per,
+    _check(load().tg_moe_gemm_scaled(ctypes.byref(oa), T, K, ctypes.byref(ob), b.stride(0) if G > 1 else per,
                                   scale_b.stride(0), G, N, _ptr(out), _DTYPE_CODE[out.dtype], ldc, counts.data_ptr(), epi,
                                   _ptr(bias) if epi else None, _stream_handle(stream)))
     return out
@@ -545,7 +554,7 @@ def moe_router(logits: torch.Tensor, top_k: int, *, renormalize: bool = False, s
     T, G = logits.shape
     if not isinstance(top_k, int) or top_k < 1:
         raise ValueError("top_k must be a positive integer")
-    _on_one_gpu(logits=logits)
+    _on_one_gpu("logits", logits)
 
     def new(shape, dtype):
         return _empty(shape, dtype, logits.device, stream)
@@ -584,8 +593,8 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
     lo, ldd = _matrix(out, "out")
     if lo != ROW_MAJOR:
         raise ValueError("out must be row-major")
-    _on_one_gpu(logits=logits, experts=routing.experts, weights=routing.weights, slope=routing.slope,
-                d_weights=d_weights, d_loss=d_loss, out=out)
+    _on_one_gpu("logits routing.experts routing.weights routing.slope d_weights d_loss out", logits, routing.experts,
+                routing.weights, routing.slope, d_weights, d_loss, out)
     _check(load().tg_moe_router_backward(_ptr(logits), _DTYPE_CODE[logits.dtype], ld, T, G, k, int(routing.renormalize),
                                          _ptr(routing.experts), _ptr(routing.weights), _ptr(routing.slope),
                                          _ptr(d_weights) or None, _ptr(d_loss) or None, _ptr(out), ldd,

@@ -1,4 +1,4 @@
-// tg_fp8.cu - host side of the 8-bit products (tg_gemm_fp8 and tg_moe_gemm_fp8 in
+// tg_fp8.cu - host side of the 8-bit products (tg_gemm_scaled and tg_moe_gemm_scaled in
 // include/tg.h): argument checks, tensor maps, the choice of tile and the launch.
 #include <cuda_runtime.h>
 
@@ -19,9 +19,6 @@ using host::fail;
 
 template <class Cfg>
 cudaError_t launch_fp8(const Params& p, const Fp8Params& x, int grid, cudaStream_t stream) {
-    auto kern = &fp8_kernel<Cfg>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(F8_THREADS, 1, 1);
@@ -34,10 +31,11 @@ cudaError_t launch_fp8(const Params& p, const Fp8Params& x, int grid, cudaStream
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, x);
+    return cudaLaunchKernelEx(&cfg, &fp8_kernel<Cfg>, p, x);
 }
 
-// CTAs, or CTA pairs, that can be resident at once.
+// CTAs, or CTA pairs, that can be resident at once; asked once per device and kernel, before its
+// first launch there, and sets the kernel's shared memory limit.
 template <class Cfg>
 cudaError_t units_fp8(int* units) {
     auto kern = &fp8_kernel<Cfg>;
@@ -95,7 +93,7 @@ tg_status resident(const host::Device& d, int form, int pair, int* units) {
 }
 
 // One operand: `rows` x K with its scales, rows being A's rows or B's columns.
-tg_status check_operand(const tg_fp8_operand* o, const char* name, int64_t rows, int64_t K, tg_layout k_major) {
+tg_status check_operand(const tg_scaled_operand* o, const char* name, int64_t rows, int64_t K, tg_layout k_major) {
     if (o->dtype != TG_E4M3 && o->dtype != TG_E5M2)
         return fail(TG_ERR_INVALID_ARG, "%s: bad dtype %d (e4m3 or e5m2)", name, int(o->dtype));
     if (o->layout != TG_ROW_MAJOR && o->layout != TG_COL_MAJOR)
@@ -135,7 +133,7 @@ tg_status check_output(const void* C, tg_dtype cd, int64_t ldc, int64_t M, int64
 
 // Everything both forms fill alike.  rows: rows of A; experts: 0 for the dense form.
 struct Fp8Call {
-    const tg_fp8_operand *A, *B;
+    const tg_scaled_operand *A, *B;
     int64_t rows, N, K;
     void* C;
     tg_dtype c_dtype;
@@ -224,7 +222,7 @@ tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
 
 }  // namespace tg
 
-extern "C" tg_status tg_gemm_fp8(const tg_fp8_operand* A, const tg_fp8_operand* B, void* C, tg_dtype c_dtype,
+extern "C" tg_status tg_gemm_scaled(const tg_scaled_operand* A, const tg_scaled_operand* B, void* C, tg_dtype c_dtype,
                                  int64_t ldc, int64_t M, int64_t N, int64_t K, tg_epilogue epi, const void* bias,
                                  tg_stream_t stream) {
     using namespace tg;
@@ -238,7 +236,7 @@ extern "C" tg_status tg_gemm_fp8(const tg_fp8_operand* A, const tg_fp8_operand* 
     return run_fp8(c, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" tg_status tg_moe_gemm_fp8(const tg_fp8_operand* A, int64_t T, int64_t K, const tg_fp8_operand* B,
+extern "C" tg_status tg_moe_gemm_scaled(const tg_scaled_operand* A, int64_t T, int64_t K, const tg_scaled_operand* B,
                                      int64_t expert_stride, int64_t scale_stride, int64_t G, int64_t N, void* C,
                                      tg_dtype c_dtype, int64_t ldc, const int32_t* counts, tg_epilogue epi,
                                      const void* bias, tg_stream_t stream) {

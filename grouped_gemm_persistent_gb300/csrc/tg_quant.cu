@@ -1,5 +1,5 @@
 // tg_quant.cu - 8-bit floating point with one scale for each block of 128 values:
-// the operands of the 8-bit products (tg_quantize_fp8 in include/tg.h).
+// the operands of the 8-bit products (tg_quantize_blocks in include/tg.h).
 //
 // For a block B (128 values along a row, along a column, or a 128 x 128 square) with
 // largest magnitude a and a type whose largest finite value is 1.75 * 2^E (e4m3: E = 8,
@@ -255,7 +255,7 @@ QuantKernel pick_kernel(tg_dtype x, int mode) {
 
 }  // namespace tg
 
-extern "C" tg_status tg_quantize_fp8(const void* X, tg_dtype x_dtype, int64_t ldx, int64_t M, int64_t K,
+extern "C" tg_status tg_quantize_blocks(const void* X, tg_dtype x_dtype, int64_t ldx, int64_t M, int64_t K,
                                      int block_rows, int block_cols, void* Q, tg_dtype q_dtype, int64_t ldq,
                                      float* scale, int64_t scale_ld, tg_stream_t stream) {
     using namespace tg;

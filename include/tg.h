@@ -269,7 +269,7 @@ tg_status tg_moe_gemm(const void *A, int64_t lda, int64_t T, int64_t K,
                       tg_stream_t stream);
 
 /*
- * tg_quantize_fp8 - Q, an 8-bit copy of X with one scale for each block of 128 values:
+ * tg_quantize_blocks - Q, an 8-bit copy of X with one scale for each block of 128 values:
  * X[m][k] = scale(block of (m, k)) * Q[m][k], up to Q's rounding.
  *
  * For a block with largest magnitude a and the type's largest finite value t (448 or
@@ -289,7 +289,7 @@ tg_status tg_moe_gemm(const void *A, int64_t lda, int64_t T, int64_t K,
  *                      16-byte aligned Q with ldq a multiple of 16; this call does not.
  * M == 0 or K == 0 is a no-op.
  */
-tg_status tg_quantize_fp8(const void *X, tg_dtype x_dtype, int64_t ldx, int64_t M, int64_t K,
+tg_status tg_quantize_blocks(const void *X, tg_dtype x_dtype, int64_t ldx, int64_t M, int64_t K,
                           int block_rows, int block_cols,
                           void *Q, tg_dtype q_dtype, int64_t ldq, float *scale, int64_t scale_ld,
                           tg_stream_t stream);
@@ -301,7 +301,7 @@ tg_status tg_quantize_fp8(const void *X, tg_dtype x_dtype, int64_t ldx, int64_t 
  * with block = 1 (a scale per row of A or column of B) or 128.  Scales are any fp32
  * values (not only powers of two); strides are non-negative, in elements.
  */
-typedef struct tg_fp8_operand {
+typedef struct tg_scaled_operand {
     const void *data;          /* DEVICE, 16-byte aligned */
     int64_t ld;                /* as lda / ldb of tg_gemm, a multiple of 16 */
     const float *scale;        /* DEVICE */
@@ -310,10 +310,10 @@ typedef struct tg_fp8_operand {
     tg_dtype dtype;            /* TG_E4M3 or TG_E5M2; A's and B's may differ */
     tg_layout layout;
     int block;                 /* 1 or 128 */
-} tg_fp8_operand;
+} tg_scaled_operand;
 
 /*
- * tg_gemm_fp8 - C[M,N] = epilogue( sum over k of A[m][k] scale_A[m][k/128] B[k][n] scale_B[k/128][n] ).
+ * tg_gemm_scaled - C[M,N] = epilogue( sum over k of A[m][k] scale_A[m][k/128] B[k][n] scale_B[k/128][n] ).
  *
  * The products of one block of 128 k are summed by the tensor cores in fp32; the
  * blocks' sums are scaled and added in fp32 registers, in an order fixed by the sizes
@@ -326,11 +326,11 @@ typedef struct tg_fp8_operand {
  *   dX = dY . W^T       dY in 1 x 128 blocks, the same W with the other layout
  *   dW = X^T . dY       X and dY in 128 x 1 blocks: column-major A, row-major B, block 1
  */
-tg_status tg_gemm_fp8(const tg_fp8_operand *A, const tg_fp8_operand *B, void *C, tg_dtype c_dtype, int64_t ldc,
+tg_status tg_gemm_scaled(const tg_scaled_operand *A, const tg_scaled_operand *B, void *C, tg_dtype c_dtype, int64_t ldc,
                       int64_t M, int64_t N, int64_t K, tg_epilogue epi, const void *bias, tg_stream_t stream);
 
 /*
- * tg_moe_gemm_fp8 - tg_moe_gemm with 8-bit operands: expert g multiplies rows
+ * tg_moe_gemm_scaled - tg_moe_gemm with 8-bit operands: expert g multiplies rows
  * [off_g, off_g + counts[g]) of A by its own B, the counts staying in device memory.
  *
  *   A, T, K          : row-major, a scale per row (block 1).
@@ -338,11 +338,11 @@ tg_status tg_gemm_fp8(const tg_fp8_operand *A, const tg_fp8_operand *B, void *C,
  *                      expert g's B starts at data + g * expert_stride (a multiple of 16
  *                      elements), its scales at scale + g * scale_stride; block 128.
  *   C, counts, epi, bias ([G, N]) and the treatment of bad counts: as tg_moe_gemm
- *                      (C as in tg_gemm_fp8); G <= TG_MOE_MAX_EXPERTS.
- * An expert's gradient by its weights is the tg_gemm_fp8 of its rows' slices, quantised
+ *                      (C as in tg_gemm_scaled); G <= TG_MOE_MAX_EXPERTS.
+ * An expert's gradient by its weights is the tg_gemm_scaled of its rows' slices, quantised
  * in 128 x 1 blocks that start at the expert's first row.
  */
-tg_status tg_moe_gemm_fp8(const tg_fp8_operand *A, int64_t T, int64_t K, const tg_fp8_operand *B,
+tg_status tg_moe_gemm_scaled(const tg_scaled_operand *A, int64_t T, int64_t K, const tg_scaled_operand *B,
                           int64_t expert_stride, int64_t scale_stride, int64_t G, int64_t N,
                           void *C, tg_dtype c_dtype, int64_t ldc, const int32_t *counts,
                           tg_epilogue epi, const void *bias, tg_stream_t stream);
@@ -353,7 +353,7 @@ tg_status tg_moe_gemm_fp8(const tg_fp8_operand *A, int64_t T, int64_t K, const t
 
 /*
  * tg_moe_router - the gate of a mixture-of-experts layer: each token's k experts, their
- * weights, the tokens of each expert (the counts that tg_moe_gemm and tg_moe_gemm_fp8
+ * weights, the tokens of each expert (the counts that tg_moe_gemm and tg_moe_gemm_scaled
  * read) and the balance loss.
  *
  * With p[t] = softmax(logits[t]) and n = the number of rows with a logit above -infinity:

@@ -34,14 +34,14 @@ def operand(**kw):
 def call_gemm(lib, A=None, B=None, C=3 * PTR, cd=0, ldc=128, M=64, N=64, K=128, epi=0, bias=None):
     A = operand() if A is None else A
     B = operand(layout=1) if B is None else B
-    return lib.tg_gemm_fp8(ctypes.byref(A), ctypes.byref(B), C, cd, ldc, M, N, K, epi, bias, None)
+    return lib.tg_gemm_scaled(ctypes.byref(A), ctypes.byref(B), C, cd, ldc, M, N, K, epi, bias, None)
 
 
 def call_moe(lib, A=None, B=None, C=3 * PTR, cd=0, ldc=128, T=64, N=64, K=128, G=2, es=64 * 128, ss=1, counts=4 * PTR,
              epi=0, bias=None):
     A = operand() if A is None else A
     B = operand(layout=1, block=128) if B is None else B
-    return lib.tg_moe_gemm_fp8(ctypes.byref(A), T, K, ctypes.byref(B), es, ss, G, N, C, cd, ldc, counts, epi, bias, None)
+    return lib.tg_moe_gemm_scaled(ctypes.byref(A), T, K, ctypes.byref(B), es, ss, G, N, C, cd, ldc, counts, epi, bias, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -77,8 +77,8 @@ def test_gemm_refusals(lib, kw, code):
 
 def test_gemm_null_operands_and_empty_sizes(lib):
     b = operand(layout=1)
-    assert lib.tg_gemm_fp8(None, ctypes.byref(b), PTR, 0, 64, 64, 64, 128, 0, None, None) == tg.TG_ERR_INVALID_ARG
-    assert lib.tg_gemm_fp8(ctypes.byref(b), None, PTR, 0, 64, 64, 64, 128, 0, None, None) == tg.TG_ERR_INVALID_ARG
+    assert lib.tg_gemm_scaled(None, ctypes.byref(b), PTR, 0, 64, 64, 64, 128, 0, None, None) == tg.TG_ERR_INVALID_ARG
+    assert lib.tg_gemm_scaled(ctypes.byref(b), None, PTR, 0, 64, 64, 64, 128, 0, None, None) == tg.TG_ERR_INVALID_ARG
     assert call_gemm(lib, M=0, A=operand(data=None, scale=None), C=None) == tg.TG_OK
     assert call_gemm(lib, N=0, C=None) == tg.TG_OK
     assert call_moe(lib, T=0, A=operand(data=None), C=None) == tg.TG_OK
@@ -124,14 +124,14 @@ def test_moe_refusals(lib, kw, code):
 def test_quantize_refusals(lib, kw, code):
     a = dict(X=PTR, x_dtype=0, ldx=256, M=10, K=256, br=1, bc=128, Q=2 * PTR, q_dtype=3, ldq=256, scale=3 * PTR, sld=10)
     a.update(kw)
-    assert lib.tg_quantize_fp8(a["X"], a["x_dtype"], a["ldx"], a["M"], a["K"], a["br"], a["bc"], a["Q"], a["q_dtype"],
+    assert lib.tg_quantize_blocks(a["X"], a["x_dtype"], a["ldx"], a["M"], a["K"], a["br"], a["bc"], a["Q"], a["q_dtype"],
                                a["ldq"], a["scale"], a["sld"], None) == code
     assert lib.tg_last_error_message()
 
 
 def test_quantize_empty(lib):
-    assert lib.tg_quantize_fp8(None, 0, 0, 0, 128, 1, 128, None, 3, 0, None, 0, None) == tg.TG_OK
-    assert lib.tg_quantize_fp8(None, 0, 0, 5, 0, 1, 128, None, 3, 0, None, 0, None) == tg.TG_OK
+    assert lib.tg_quantize_blocks(None, 0, 0, 0, 128, 1, 128, None, 3, 0, None, 0, None) == tg.TG_OK
+    assert lib.tg_quantize_blocks(None, 0, 0, 5, 0, 1, 128, None, 3, 0, None, 0, None) == tg.TG_OK
 
 
 def test_binding_refusals():
