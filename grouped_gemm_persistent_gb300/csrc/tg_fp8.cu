@@ -26,7 +26,7 @@ cudaError_t launch_fp8(const Params& p, const Fp8Params& x, int grid, cudaStream
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = Cfg::CTA_GROUP;
+    attr[0].val.clusterDim.x = Cfg::SPLIT ? static_cast<unsigned>(x.splits) : Cfg::CTA_GROUP;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -61,24 +61,26 @@ struct Fp8Variant {
     int cta_group;
 };
 
-template <int CG, bool SBC, bool MOE>
+template <int CG, bool SBC, bool MOE, bool SPLIT = false>
 constexpr Fp8Variant fp8_variant() {
-    using C = Fp8Config<CG, SBC, MOE>;
+    using C = Fp8Config<CG, SBC, MOE, SPLIT>;
     return Fp8Variant{&launch_fp8<C>, &units_fp8<C>, CG};
 }
 
-enum : int { FORM_BLOCK = 0, FORM_COLUMN = 1, FORM_MOE = 2 };
+enum : int { FORM_BLOCK = 0, FORM_COLUMN = 1, FORM_MOE = 2, FORM_BLOCK_SPLIT = 3, FORM_COLUMN_SPLIT = 4, FORMS = 5 };
 
-// [form][CTA pair]
-const Fp8Variant kFp8[3][2] = {
+// [form][CTA pair]; split tiles are single CTAs'
+const Fp8Variant kFp8[FORMS][2] = {
     {fp8_variant<1, false, false>(), fp8_variant<2, false, false>()},
     {fp8_variant<1, true, false>(), fp8_variant<2, true, false>()},
     {fp8_variant<1, false, true>(), fp8_variant<2, false, true>()},
+    {fp8_variant<1, false, false, true>(), {}},
+    {fp8_variant<1, true, false, true>(), {}},
 };
 
 constexpr int kMaxDevices = 64;
 std::mutex g_units_mu;
-int g_units[kMaxDevices][3][2];
+int g_units[kMaxDevices][FORMS][2];
 
 tg_status resident(const host::Device& d, int form, int pair, int* units) {
     std::lock_guard<std::mutex> lock(g_units_mu);
@@ -144,12 +146,24 @@ struct Fp8Call {
     const int32_t* counts;
 };
 
+// CTAs that share each 128 x 128 tile of a dense launch with fewer tiles than SMs: the largest
+// power of two, at most 8, that keeps every CTA resident and gives each at least two k-blocks.
+// 1 x 4096 x 4096: 16.5 us with one CTA a tile (32 of them).  TG_STREAM_K=0 keeps tiles whole.
+int pick_splits(const Fp8Call& c, int sms) {
+    const char* env = std::getenv("TG_STREAM_K");
+    if (env && env[0] == '0') return 1;
+    const int64_t tiles = ((c.rows + 127) / 128) * ((c.N + 127) / 128), kb = (c.K + F8_BK - 1) / F8_BK;
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= sms && kb >= s * 4) s *= 2;
+    return s;
+}
+
 tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
     host::Device d;
     tg_status s = host::device(&d);
     if (s != TG_OK || (s = host::encoder()) != TG_OK) return s;
     const bool moe = c.experts > 0;
-    const int form = moe ? FORM_MOE : c.B->block == 1 ? FORM_COLUMN : FORM_BLOCK;
+    int form = moe ? FORM_MOE : c.B->block == 1 ? FORM_COLUMN : FORM_BLOCK;
 
     // CTA pairs where their 256 x 256 tiles give every pair work, single CTAs (128 x 128) below
     const int64_t pair_tiles = ((c.rows + 255) / 256) * ((c.N + 255) / 256);
@@ -158,6 +172,8 @@ tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
         int cg = 0, bn = 0;
         if (std::sscanf(env, "%dx%d", &cg, &bn) == 2 && (cg == 1 || cg == 2)) pair = cg - 1;
     }
+    const int splits = moe || pair ? 1 : pick_splits(c, d.sms);
+    if (splits > 1) form = form == FORM_COLUMN ? FORM_COLUMN_SPLIT : FORM_BLOCK_SPLIT;
     const Fp8Variant& v = kFp8[form][pair];
     int units = 0;
     if ((s = resident(d, form, pair, &units)) != TG_OK) return s;
@@ -207,11 +223,12 @@ tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
     x.sb_g = c.scale_stride;
     x.a_mn = a_mn;
     x.b_mn = b_mn;
+    x.splits = splits;
     x.c = c.C;
     x.ldc = c.ldc;
     x.vec_c = host::aligned(c.C, 16) && (c.ldc * (c.c_dtype == TG_F32 ? 4 : 2)) % 16 == 0;
     host::launch_params(&p, d.err);
-    const int64_t want = moe || p.total_tiles > units ? units : p.total_tiles;
+    const int64_t want = splits > 1 ? p.total_tiles * splits : moe || p.total_tiles > units ? units : p.total_tiles;
     const cudaError_t e = v.launch(p, x, static_cast<int>(want) * v.cta_group, stream);
     if (e != cudaSuccess) return host::cuda_fail(e, "8-bit kernel launch");
     host::count_launches(1);

@@ -49,12 +49,16 @@ struct Fp8Params {
     int32_t sa_shift;          // 0: a scale per row, 7: per 128 rows
     uint32_t a_mn, b_mn;       // A stored M-contiguous, B stored N-contiguous
     uint32_t vec_c;            // rows of C are 16-byte aligned
+    int32_t splits;            // SPLIT: CTAs that share a tile (the cluster's size)
     void* c;
     int64_t ldc;
 };
 
-template <int CTA_GROUP_, bool SB_COL_, bool MOE_>
+// SPLIT (single CTAs, dense): the CTAs of a cluster share one tile, each summing its own range of
+// k-blocks, and join their sums through distributed shared memory.
+template <int CTA_GROUP_, bool SB_COL_, bool MOE_, bool SPLIT_ = false>
 struct Fp8Config {
+    static constexpr bool SPLIT = SPLIT_;
     static constexpr int CTA_GROUP = CTA_GROUP_;
     static constexpr bool SB_COL = SB_COL_;          // B has a scale per column (else per 128 columns)
     static constexpr bool GROUPED = false;
@@ -89,6 +93,8 @@ struct Fp8Config {
     static constexpr int OFF_DRAIN_LAST = OFF_DRAIN_POS + 4;
     static constexpr int OFF_DRAIN_BYTES = OFF_DRAIN_LAST + 4 * MAX_STAGES;
     static constexpr int SMEM_BYTES = OFF_DRAIN_BYTES + 4 * MAX_STAGES + 1024;
+    static_assert(!SPLIT || (CTA_GROUP == 1 && !MOE), "split tiles are dense single-CTA ones");
+    static_assert(!SPLIT || F8_EPI_WARPS * 32 * COLS * 4 <= STAGES * (A_BYTES + B_BYTES), "partial sums fit the ring");
     static_assert(STAGES >= 2 && STAGES <= MAX_STAGES, "ring depth");
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
     static_assert(OFF_BAR % 8 == 0, "barrier alignment");
@@ -280,6 +286,47 @@ __device__ __forceinline__ void store_rows(const float (&v)[CW], uint32_t stage,
     }
 }
 
+// Bias, GELU, rounding and the store of eight neighbouring columns of one row.
+__device__ __forceinline__ void finish_and_store8(float (&v)[8], const Problem& pr, const Fp8Params& x, int row, int n) {
+    if (row >= pr.M || n >= pr.N) return;
+    if (pr.epi != EPI_NONE) {
+        float b[8];
+        load_bias8(static_cast<const uint16_t*>(pr.bias), n, pr.N, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += b[i];
+        if (pr.epi == EPI_BIAS_GELU) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) gelu_tanh_f32x2(v[i], v[i + 1]);
+        }
+    }
+    const int64_t at = static_cast<int64_t>(row) * x.ldc + n;
+    const bool whole = x.vec_c && n + 8 <= pr.N;
+    if (pr.flags & FLAG_C_F32) {
+        float* c = static_cast<float*>(x.c) + at;
+        if (whole) {
+            reinterpret_cast<float4*>(c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (n + i < pr.N) c[i] = v[i];
+        }
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (pr.flags & FLAG_C_F16) ? pack_f16x2(v[2 * i], v[2 * i + 1]) : pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    uint16_t* c = static_cast<uint16_t*>(x.c) + at;
+    if (whole) {
+        *reinterpret_cast<uint4*>(c) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n + i < pr.N) c[i] = static_cast<uint16_t>(w[i / 2] >> ((i & 1) * 16));
+    }
+}
+
 }  // namespace f8
 
 // ----------------------------------------------------------------------------------------
@@ -311,7 +358,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
     const bool leader = rank == 0;
-    const int64_t unit = blockIdx.x / CG, num_units = gridDim.x / CG;
+    const uint32_t cta = ptx::cluster_ctarank();              // in the cluster: of a pair, or of a split tile
+    const int splits = Cfg::SPLIT ? x.splits : 1;
+    const int64_t unit = blockIdx.x / (CG * splits), num_units = gridDim.x / (CG * splits);
+    // this CTA's k-blocks of every tile
+    const int kb_begin = Cfg::SPLIT ? static_cast<int>(static_cast<int64_t>(p.dense.k_blocks) * cta / splits) : 0;
+    const int kb_end = Cfg::SPLIT ? static_cast<int>(static_cast<int64_t>(p.dense.k_blocks) * (cta + 1) / splits)
+                                  : p.dense.k_blocks;
 
     // ---- set-up
     if (threadIdx.x == 0) {
@@ -395,7 +448,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 g = find_problem<Cfg>(p, w.t, g, mt);
                 const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
                 const int nb0 = tc.n0 + static_cast<int>(rank) * Cfg::BN_CTA;
-                for (int kb = 0; kb < pr.k_blocks; ++kb) {
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
                     if (!ptx::mbar_test_wait(empty_bar(stage), phase ^ 1u) &&
                         !wait_bounded<CG>(empty_bar(stage), phase ^ 1u, p, abort_addr, ROLE_PRODUCER, w.slot, stage)) {
                         aborted = true;
@@ -455,7 +508,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 g = find_problem<Cfg>(p, w.t, g, mt);
                 uint32_t idesc = pr.idesc;
                 if (tile_coord<Cfg>(p, w.t, g, rank, mt).half) idesc = (idesc & ~(0x1Fu << 24)) | ((128u >> 4) << 24);
-                for (int kb = 0; kb < pr.k_blocks; ++kb) {
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
                     if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, ROLE_MMA, w.slot, 16 + acc) ||
                         !warp_wait(full_bar(stage), phase, ROLE_MMA, w.slot, stage)) {
                         aborted = true;
@@ -507,7 +560,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 }
             }
             const int64_t step = for_a ? x.sa_k : x.sb_k;
-            for (int kb = 0; kb < pr.k_blocks; kb += F8_GROUP) {
+            for (int kb = kb_begin; kb < kb_end; kb += F8_GROUP) {
                 if (!warp_wait(sempty_bar(slot), phase ^ 1u, ROLE_PRODUCER, w.slot, 32 + slot)) {
                     aborted = true;
                     break;
@@ -518,7 +571,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 for (int i = 0; i < F8_GROUP; ++i) {
 #pragma unroll
                     for (int j = 0; j < N_MAX; ++j) {
-                        if (j < n && kb + i < pr.k_blocks && (Cfg::SB_COL || for_a || lane < Cfg::SB_COUNT)) {
+                        if (j < n && kb + i < kb_end && (Cfg::SB_COL || for_a || lane < Cfg::SB_COUNT)) {
                             const bool in = ok >> j & 1u;
                             const int at = for_a || !Cfg::SB_COL ? (j * 32 + lane) * F8_GROUP + i : i * BN + j * 32 + lane;
                             f8::cp_async_4(dst + at * 4, in ? static_cast<const void*>(src[j] + (kb + i) * step) : x.sa, in);
@@ -540,7 +593,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         const uint32_t stage_c = sC + (warp - F8_EPI_WARP0) * F8_C_STAGE;
         int buf = 0, slot = 0, g = 0;
         uint32_t buf_phase = 0, slot_phase = 0;
-        const uint32_t lead_tempty = ptx::mapa(tempty_bar(0), 0), own_sempty = ptx::mapa(sempty_bar(0), rank);
+        const uint32_t lead_tempty = ptx::mapa(tempty_bar(0), CG == 2 ? 0 : cta), own_sempty = ptx::mapa(sempty_bar(0), cta);
         constexpr bool MAY_HALVE = CG == 2 && Cfg::MOE;
         Sched sc = sched_begin<Cfg>(p, unit);
         Work w;
@@ -605,12 +658,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 constexpr int CHUNKS = decltype(chunk_count)::value;
                 static_assert(F8_GROUP == 4, "a lane's scales of a group are one 16-byte word");
                 float f[F8_GROUP];
-                if (pr.k_blocks == 0) return true;
+                if (kb_begin == kb_end) return true;
                 if (!read_scales(f)) return false;
                 bool ready = ptx::mbar_test_wait(tfull_bar(buf), buf_phase);
 #pragma unroll 1
-                for (int kb = 0; kb < pr.k_blocks; ++kb) {
-                    const int u = kb % F8_GROUP;
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
+                    const int u = (kb - kb_begin) % F8_GROUP;
                     if (!__all_sync(0xffffffffu, ready) &&
                         !warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, w.slot, 16 + buf)) return false;
                     ptx::tc_fence_after_sync();
@@ -621,7 +674,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                     const uint32_t sb = sb_at + slot * Cfg::SLOT_BYTES + u * (BN * 4);      // SB_COL
                     f[0] = f[1]; f[1] = f[2]; f[2] = f[3];
                     if constexpr (!Cfg::SB_COL) {
-                        if (u == F8_GROUP - 1 && kb + 1 < pr.k_blocks && !read_scales(f)) return false;
+                        if (u == F8_GROUP - 1 && kb + 1 < kb_end && !read_scales(f)) return false;
                     }
                     f8::for_each<(CHUNKS > 0 ? CHUNKS : 1)>([&](auto ci) {
                         constexpr int C = decltype(ci)::value;
@@ -639,12 +692,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                         if constexpr (CHUNKS > 0) add(ci, r[C & 1], s, sb);
                     });
                     if constexpr (Cfg::SB_COL) {
-                        if (u == F8_GROUP - 1 || kb + 1 == pr.k_blocks) {
+                        if (u == F8_GROUP - 1 || kb + 1 == kb_end) {
                             // the columns' scales have been read: on to the next group's slot
                             __syncwarp();
                             f8::arrive_lane0(own_sempty + 8u * slot, lane);
                             if (++slot == Cfg::SLOTS) { slot = 0; slot_phase ^= 1u; }
-                            if (kb + 1 < pr.k_blocks && !read_scales(f)) return false;
+                            if (kb + 1 < kb_end && !read_scales(f)) return false;
                         }
                     }
                 }
@@ -656,6 +709,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             else ok = accumulate(std::integral_constant<int, COLS / 32>{});
             if (!ok) break;
             if (!active) continue;
+            if constexpr (Cfg::SPLIT) {
+                // the operand ring is idle (the last buffer's commit followed every MMA): leave this
+                // warp's sums there, [column][row], for the cluster
+                const uint32_t mine = sA + static_cast<uint32_t>(warp - F8_EPI_WARP0) * (COLS * 128);
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) st_shared_u32(mine + (j * 32 + lane) * 4, __float_as_uint(acc[j]));
+                continue;
+            }
 
             // epilogue: 32 (16-bit output) or 16 (fp32) columns at a time: bias, GELU, rounding, store
             const uint16_t* bias = static_cast<const uint16_t*>(pr.bias);
@@ -703,10 +764,37 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         }
     }
 
+    if constexpr (Cfg::SPLIT) {
+        // ================================ joining a split tile ================================
+        // CTA r of the cluster adds columns [r COLS / splits, ..) of every warp's part, in the order
+        // of the k ranges, and finishes them.
+        __syncwarp();
+        ptx::cluster_sync();
+        const TileCoord tc = tile_coord<Cfg>(p, unit, 0, 0, mt);
+        const int ew = warp - F8_EPI_WARP0;
+        const int row = tc.m0 + (warp % 4) * 32 + lane, per = Cfg::COLS / splits;
+        const int c_first = static_cast<int>(cta) * per;
+        const int n_first = tc.n0 + (ew / 4) * Cfg::COLS + c_first;
+        if (ew >= 0 && row - lane < pr.M && n_first < pr.N) {
+            const uint32_t from = sA + static_cast<uint32_t>(ew) * (Cfg::COLS * 128) + lane * 4;
+            for (int c = 0; c < per; c += 8) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+                for (int r = 0; r < splits; ++r) {
+                    const uint32_t at = ptx::mapa(from + static_cast<uint32_t>(c_first + c) * 128, static_cast<uint32_t>(r));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(ptx::ld_cluster_u32(at + i * 128));
+                }
+                f8::finish_and_store8(v, pr, x, row, n_first + c);
+            }
+        }
+    }
+
     // ---- teardown
     __syncwarp();
     ptx::tc_fence_before_sync();
-    if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
+    if constexpr (CG == 2 || Cfg::SPLIT) ptx::cluster_sync(); else __syncthreads();
     ptx::tc_fence_after_sync();
     if (warp == 1) ptx::tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
 }
