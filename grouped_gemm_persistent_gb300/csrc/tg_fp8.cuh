@@ -49,6 +49,7 @@ struct Fp8Params {
     int32_t sa_shift;          // 0: a scale per row, 7: per 128 rows
     uint32_t a_mn, b_mn;       // A stored M-contiguous, B stored N-contiguous
     uint32_t vec_c;            // rows of C are 16-byte aligned
+    uint32_t a_bytes;          // of A's box: all 128 rows, or as many as a short A has
     int32_t splits;            // SPLIT: CTAs that share a tile (the cluster's size)
     void* c;
     int64_t ldc;
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             int g = 0;
             bool aborted = false;
             bool withhold = p.withhold_kb >= 0 && blockIdx.x == static_cast<uint32_t>(p.withhold_block);
-            constexpr uint32_t TX = Cfg::A_BYTES + Cfg::B_BYTES;
+            const uint32_t tx = x.a_bytes + Cfg::B_BYTES;
             Sched sc = sched_begin<Cfg>(p, unit);
             Work w;
             while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                     }
                     if (!(withhold && kb == p.withhold_kb)) {
                         const uint32_t fb = CG == 2 ? ptx::mapa(full_bar(stage), 0) : full_bar(stage);
-                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), TX * CG);
+                        if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), tx * CG);
                         const int k0 = kb * F8_BK;
                         const uint32_t a_dst = sA + stage * Cfg::A_BYTES, b_dst = sB + stage * Cfg::B_BYTES;
                         const int ax = x.a_mn ? tc.m0 : k0, ay = x.a_mn ? k0 : tc.m0;
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                             else ptx::tma_load_2d(b_dst, &pr.tma_b, bx, by, fb);
                         }
                         st_shared_u32(base + Cfg::OFF_DRAIN_LAST + 4 * stage, pos);
-                        st_shared_u32(base + Cfg::OFF_DRAIN_BYTES + 4 * stage, TX);
+                        st_shared_u32(base + Cfg::OFF_DRAIN_BYTES + 4 * stage, tx);
                     }
                     ++pos;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
