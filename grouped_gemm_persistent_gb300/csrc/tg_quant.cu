@@ -10,9 +10,11 @@
 // even, and dequantising is exact in fp32; the factor of two that a power of two can
 // waste costs range (the type has 2^15 of it and more below its top), not precision.
 //
-// One block of 256 threads reads a 128 x 128 tile once into registers (8 rows of 8
-// columns a thread, 16-byte loads), reduces the magnitudes in the wanted direction as
-// integers (the bits of non-negative floats order like the values), and writes bytes.
+// One block of 256 threads reads a tile once into registers (8 rows of 8 columns a thread,
+// 16-byte loads), reduces the magnitudes in the wanted direction as integers (the bits of
+// non-negative floats order like the values), and writes bytes.  Tiles are 128 x 128, and
+// 32 x 512 for blocks along a row, which need no more than a row: 1 KiB of a bf16 row at a
+// time instead of 256 bytes.  QUANT_NOTE
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,9 +30,17 @@ namespace {
 
 enum : int { BLOCK_ROW = 0, BLOCK_COLUMN = 1, BLOCK_SQUARE = 2 };
 
-constexpr int QT = 128;          // tile edge: one scale block
+constexpr int QT = 128;          // values of a scale block
 constexpr int QTHREADS = 256;
-constexpr int QROWS = 8;         // rows a thread holds (ty, ty + 16, ...)
+constexpr int QROWS = 8;         // rows a thread holds (ty, ty + TY, ...)
+
+// Tile of a mode: TX threads of 8 columns by TY of QROWS rows
+template <int MODE>
+struct QTile {
+    static constexpr int TX = MODE == BLOCK_ROW ? 64 : 16;
+    static constexpr int TY = QTHREADS / TX;
+    static constexpr int COLS = 8 * TX, ROWS = QROWS * TY;
+};
 
 // Eight values of one row as they lie in memory, and what is needed of them.
 // 16-bit types: magnitudes compare as 15-bit integers.
@@ -56,6 +66,12 @@ struct Half8 {
         else return __uint_as_float(h << 16);
     }
     __device__ __forceinline__ float value(int i) const { return widen_value(bits(i)); }
+    // largest magnitude of the eight
+    __device__ __forceinline__ uint32_t max_mag() const {
+        const uint32_t a = __vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), b = __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu);
+        const uint32_t m = __vmaxu2(a, b);
+        return max(m & 0xffffu, m >> 16);
+    }
     // fp32 bits of a magnitude (any pattern from infinity's on when it is not finite)
     static __device__ __forceinline__ uint32_t widen(uint32_t m) {
         return m >= INF ? 0x7f800000u : __float_as_uint(widen_value(m));
@@ -79,6 +95,12 @@ struct Float8 {
     __device__ __forceinline__ void set(int i, const void* p) { w[i] = __ldg(static_cast<const uint32_t*>(p)); }
     __device__ __forceinline__ uint32_t mag(int i) const { return w[i] & 0x7fffffffu; }
     __device__ __forceinline__ float value(int i) const { return __uint_as_float(w[i]); }
+    __device__ __forceinline__ uint32_t max_mag() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, mag(i));
+        return m;
+    }
     static __device__ __forceinline__ uint32_t widen(uint32_t m) { return m; }
 };
 
@@ -98,16 +120,18 @@ __device__ __forceinline__ void block_scale(uint32_t a, int top_exp, float& s, f
     inv = __uint_as_float(static_cast<uint32_t>(127 - j) << 23);
 }
 
-// Two values, scaled and rounded to 8 bits (low byte: lo).  A reciprocal of 0 marks a block
-// that is not finite; its bytes are zeros.
+// Four values, scaled and rounded to 8 bits
 template <bool E5M2>
-__device__ __forceinline__ uint32_t pack8(float lo, float hi, float inv_lo, float inv_hi) {
-    lo = inv_lo == 0.0f ? 0.0f : lo * inv_lo;
-    hi = inv_hi == 0.0f ? 0.0f : hi * inv_hi;
-    uint16_t r;
-    if constexpr (E5M2) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
+__device__ __forceinline__ uint32_t pack8(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    if constexpr (E5M2) {
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    } else {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    }
+    return lo | static_cast<uint32_t>(hi) << 16;
 }
 
 struct QuantArgs {
@@ -126,20 +150,22 @@ struct QuantArgs {
 template <class E, int MODE, bool E5M2>
 __global__ void __launch_bounds__(QTHREADS) quantize_kernel(const QuantArgs p) {
     constexpr int TOP_EXP = E5M2 ? 15 : 8;
-    __shared__ uint32_t s_mag[QTHREADS / 32][QT];      // column mode: per warp; else a few words
+    using Tile = QTile<MODE>;
+    constexpr int TX = Tile::TX, TY = Tile::TY;
+    __shared__ uint32_t s_mag[QTHREADS / 32][QT];      // column mode: per warp; square: a word of each
     __shared__ float s_scale[QT], s_inv[QT];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t tile = blockIdx.x;
     const int64_t mb = tile / p.tiles_k;
     const int64_t kb = tile - mb * p.tiles_k;
-    const int64_t row0 = mb * QT, col0 = kb * QT + tx * 8;
+    const int64_t row0 = mb * Tile::ROWS, col0 = kb * Tile::COLS + tx * 8;
     const int cols = static_cast<int>(p.K - col0 < 8 ? (p.K > col0 ? p.K - col0 : 0) : 8);
 
     E v[QROWS];
 #pragma unroll
     for (int i = 0; i < QROWS; ++i) {
-        const int64_t row = row0 + ty + 16 * i;
+        const int64_t row = row0 + ty + TY * i;
         const uint8_t* src = p.x + row * p.ldx_bytes + col0 * E::BYTES;
         v[i].zero();
         if (row < p.M) {
@@ -154,19 +180,23 @@ __global__ void __launch_bounds__(QTHREADS) quantize_kernel(const QuantArgs p) {
     }
 
     if constexpr (MODE == BLOCK_ROW) {
+        // 16 lanes hold a scale block; s_scale is [block of the tile][row]
+        constexpr int ROWS = Tile::ROWS, BLOCKS = Tile::COLS / QT;
+        static_assert(ROWS * BLOCKS == QT, "a scale a thread of the first 128");
 #pragma unroll
         for (int i = 0; i < QROWS; ++i) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) m = max(m, v[i].mag(c));
+            uint32_t m = v[i].max_mag();
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-            if (tx == 0) block_scale(E::widen(m), TOP_EXP, s_scale[ty + 16 * i], s_inv[ty + 16 * i]);
+            const int at = tx / 16 * ROWS + ty + TY * i;
+            if (tx % 16 == 0) block_scale(E::widen(m), TOP_EXP, s_scale[at], s_inv[at]);
         }
         __syncthreads();
-        // scales lie block column after block column, a tile's 128 rows side by side
-        if (threadIdx.x < QT && row0 + threadIdx.x < p.M)
-            p.scale[kb * p.scale_ld + row0 + threadIdx.x] = s_scale[threadIdx.x];
+        // scales lie block column after block column, a tile's rows side by side
+        if (threadIdx.x < QT) {
+            const int64_t b = kb * BLOCKS + threadIdx.x / ROWS, row = row0 + threadIdx.x % ROWS;
+            if (b * QT < p.K && row < p.M) p.scale[b * p.scale_ld + row] = s_scale[threadIdx.x];
+        }
     } else if constexpr (MODE == BLOCK_COLUMN) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -192,9 +222,7 @@ __global__ void __launch_bounds__(QTHREADS) quantize_kernel(const QuantArgs p) {
     } else {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < QROWS; ++i)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) m = max(m, v[i].mag(c));
+        for (int i = 0; i < QROWS; ++i) m = max(m, v[i].max_mag());
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) s_mag[warp][0] = m;
         __syncthreads();
@@ -213,17 +241,26 @@ __global__ void __launch_bounds__(QTHREADS) quantize_kernel(const QuantArgs p) {
     }
 #pragma unroll
     for (int i = 0; i < QROWS; ++i) {
-        const int64_t row = row0 + ty + 16 * i;
-        if constexpr (MODE != BLOCK_COLUMN) {
-            const float f = s_inv[MODE == BLOCK_ROW ? ty + 16 * i : 0];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) inv[c] = f;
-        }
+        const int64_t row = row0 + ty + TY * i;
         uint32_t w[2];
+        if constexpr (MODE != BLOCK_COLUMN) {
+            const float f = s_inv[MODE == BLOCK_ROW ? tx / 16 * Tile::ROWS + ty + TY * i : 0];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            w[h] = pack8<E5M2>(v[i].value(4 * h), v[i].value(4 * h + 1), inv[4 * h], inv[4 * h + 1]) |
-                   pack8<E5M2>(v[i].value(4 * h + 2), v[i].value(4 * h + 3), inv[4 * h + 2], inv[4 * h + 3]) << 16;
+            for (int h = 0; h < 2; ++h) {
+                w[h] = pack8<E5M2>(v[i].value(4 * h) * f, v[i].value(4 * h + 1) * f, v[i].value(4 * h + 2) * f,
+                                   v[i].value(4 * h + 3) * f);
+                if (f == 0.0f) w[h] = 0u;          // a block that is not finite: zeros
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[h] = pack8<E5M2>(v[i].value(4 * h) * inv[4 * h], v[i].value(4 * h + 1) * inv[4 * h + 1],
+                                   v[i].value(4 * h + 2) * inv[4 * h + 2], v[i].value(4 * h + 3) * inv[4 * h + 3]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (inv[4 * h + c] == 0.0f) w[h] &= ~(0xffu << (8 * c));
+            }
+        }
         if (row < p.M) {
             uint8_t* dst = p.q + row * p.ldq + col0;
             if (cols == 8 && p.vec_out) {
@@ -279,10 +316,12 @@ extern "C" tg_status tg_quantize_blocks(const void* X, tg_dtype x_dtype, int64_t
     if (ldx > host::MAX_DIM || ldq > host::MAX_DIM) return fail(TG_ERR_UNSUPPORTED, "leading dimensions must be below 2^31");
     if (!host::aligned(X, esize)) return fail(TG_ERR_INVALID_ARG, "X is not aligned to its element size");
     if (!host::aligned(scale, 4)) return fail(TG_ERR_INVALID_ARG, "scale is not 4-byte aligned");
-    const int64_t tiles_m = (M + QT - 1) / QT, tiles_k = (K + QT - 1) / QT;
+    const int64_t tile_rows = mode == BLOCK_ROW ? QTile<BLOCK_ROW>::ROWS : QT;
+    const int64_t tile_cols = mode == BLOCK_ROW ? QTile<BLOCK_ROW>::COLS : QT;
+    const int64_t tiles_m = (M + tile_rows - 1) / tile_rows, tiles_k = (K + tile_cols - 1) / tile_cols;
     const int64_t need = mode == BLOCK_ROW ? M : mode == BLOCK_COLUMN ? K : tiles_k;
     if (scale_ld < need) return fail(TG_ERR_INVALID_ARG, "scale_ld=%lld < %lld", (long long)scale_ld, (long long)need);
-    if (tiles_m * tiles_k > host::MAX_DIM) return fail(TG_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles of 128 x 128");
+    if (tiles_m * tiles_k > host::MAX_DIM) return fail(TG_ERR_UNSUPPORTED, "X is too large (2^31 - 1 tiles of 2^14 values)");
     host::Device d;
     const tg_status s = host::device(&d);
     if (s != TG_OK) return s;
