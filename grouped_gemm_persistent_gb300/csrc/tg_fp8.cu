@@ -211,6 +211,8 @@ tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
     q.replicas = 1;
     q.idesc = ptx::idesc_f8(tile, tile, a_mn, b_mn, c.A->dtype == TG_E5M2, c.B->dtype == TG_E5M2);
     q.flags = c.c_dtype == TG_F32 ? FLAG_C_F32 : c.c_dtype == TG_F16 ? FLAG_C_F16 : 0u;
+    if (static_cast<int64_t>(q.tiles_m) * q.tiles_n > host::MAX_DIM / 2)
+        return fail(TG_ERR_UNSUPPORTED, "C has more than 2^30 tiles of %d x %d", tile, tile);
     p.num_problems = 1;
     p.total_tiles = moe ? 0 : static_cast<int64_t>(q.tiles_m) * q.tiles_n;
     int band = 1;

@@ -85,7 +85,7 @@ struct Fp8Config {
     static constexpr int OFF_SCALE = OFF_C + C_BYTES;
     static constexpr int OFF_TABLE = OFF_SCALE + SCALE_BYTES;
     static constexpr int OFF_BAR = OFF_TABLE + TABLE_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * SLOTS;
+    static constexpr int NUM_BARS = 2 * STAGES + 6 + 2 * SLOTS;
     static constexpr int OFF_TMEM_SLOT = OFF_BAR + 8 * NUM_BARS;
     static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
     static constexpr int OFF_MOE_TOTAL = OFF_ABORT + 4;
@@ -350,8 +350,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
-    auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
-    auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + Cfg::SLOTS + s); };
+    auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 6 + s); };
+    auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 6 + Cfg::SLOTS + s); };
     const uint32_t sS = base + Cfg::OFF_SCALE;
     const uint32_t abort_addr = base + Cfg::OFF_ABORT;
 
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     const bool leader = rank == 0;
     const uint32_t cta = ptx::cluster_ctarank();              // in the cluster: of a pair, or of a split tile
     const int splits = Cfg::SPLIT ? x.splits : 1;
-    const int64_t unit = blockIdx.x / (CG * splits), num_units = gridDim.x / (CG * splits);
+    const int unit = blockIdx.x / (CG * splits), num_units = gridDim.x / (CG * splits);
     // this CTA's k-blocks of every tile
     const int kb_begin = Cfg::SPLIT ? static_cast<int>(static_cast<int64_t>(p.dense.k_blocks) * cta / splits) : 0;
     const int kb_end = Cfg::SPLIT ? static_cast<int>(static_cast<int64_t>(p.dense.k_blocks) * (cta + 1) / splits)
@@ -378,10 +378,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             ptx::mbar_init(tempty_bar(b), F8_EPI_WARPS * CG);
         }
         for (int s = 0; s < Cfg::SLOTS; ++s) {
-            ptx::mbar_init(sfull_bar(s), 64);                 // every lane of both loaders
+            ptx::mbar_init(sfull_bar(s), 32);                 // every lane of the loader
             ptx::mbar_init(sempty_bar(s), F8_EPI_WARPS);
         }
         ptx::mbar_init(drain_bar, 1);
+        ptx::mbar_init(drain_bar + 8u, 1);
         st_shared_u32(abort_addr, 0u);
         st_shared_u32(base + Cfg::OFF_DRAIN_FLAG, 0u);
         st_shared_u32(base + Cfg::OFF_DRAIN_POS, 0u);
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     if constexpr (CG == 2) ptx::cluster_sync(); else __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + Cfg::OFF_TMEM_SLOT);
-    int64_t total_tiles = p.total_tiles;
+    int total_tiles = static_cast<int>(p.total_tiles);
     if constexpr (Cfg::MOE) total_tiles = *reinterpret_cast<volatile int32_t*>(smem + Cfg::OFF_MOE_TOTAL);
 
     // Registers: 384 x 168 at launch = 64512 = 128 x 72 + 256 x 216.  Each split stands at
@@ -420,16 +421,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     const Problem& pr = p.dense;
     // Warp-uniform bounded wait: every lane polls once; if the phase is not yet complete, lane 0
     // runs the bounded wait and tells the others how it ended.
-    auto warp_wait = [&](uint32_t bar, uint32_t par, uint32_t role, int64_t slot, uint32_t st) -> bool {
+    auto warp_wait = [&](uint32_t bar, uint32_t par, uint32_t role, int tile, uint32_t st) -> bool {
         if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, par))) return true;
         uint32_t ok = 1;
-        if (lane == 0) ok = wait_bounded<CG, false>(bar, par, p, abort_addr, role, slot, st) ? 1u : 0u;
+        if (lane == 0) ok = wait_bounded<CG, false>(bar, par, p, abort_addr, role, tile, st) ? 1u : 0u;
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
     // The same for warps that run ahead: lane 0 is suspended between its polls.
-    auto warp_wait_sleep = [&](uint32_t bar, uint32_t par, uint32_t role, int64_t slot, uint32_t st) -> bool {
+    auto warp_wait_sleep = [&](uint32_t bar, uint32_t par, uint32_t role, int tile, uint32_t st) -> bool {
         uint32_t ok = 1;
-        if (lane == 0) ok = wait_bounded<CG, true>(bar, par, p, abort_addr, role, slot, st) ? 1u : 0u;
+        if (lane == 0) ok = wait_bounded<CG, true>(bar, par, p, abort_addr, role, tile, st) ? 1u : 0u;
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
     if (warp < F8_EPI_WARP0) {
@@ -443,15 +444,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             bool aborted = false;
             bool withhold = p.withhold_kb >= 0 && blockIdx.x == static_cast<uint32_t>(p.withhold_block);
             const uint32_t tx = x.a_bytes + Cfg::B_BYTES;
-            Sched sc = sched_begin<Cfg>(p, unit);
-            Work w;
-            while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
-                g = find_problem<Cfg>(p, w.t, g, mt);
-                const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
+            for (int t = unit; t < total_tiles && !aborted; t += num_units) {
+                g = find_problem<Cfg>(p, t, g, mt);
+                const TileCoord tc = tile_coord<Cfg>(p, t, g, rank, mt);
                 const int nb0 = tc.n0 + static_cast<int>(rank) * Cfg::BN_CTA;
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
                     if (!ptx::mbar_test_wait(empty_bar(stage), phase ^ 1u) &&
-                        !wait_bounded<CG>(empty_bar(stage), phase ^ 1u, p, abort_addr, ROLE_PRODUCER, w.slot, stage)) {
+                        !wait_bounded<CG>(empty_bar(stage), phase ^ 1u, p, abort_addr, ROLE_PRODUCER, t, stage)) {
                         aborted = true;
                         break;
                     }
@@ -493,91 +492,97 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             ptx::st_release_cluster_u32(base + Cfg::OFF_DRAIN_FLAG, 1u);
             if (aborted && leader) drain_issued_loads<Cfg>(p, base);
         }
-    } else if (warp == 1) {
-        // ================================ MMA issuer ================================
+    } else if (warp == 1 || warp == 2) {
+        // ================================ MMA issuers ================================
+        // Warp 1 issues the even k-blocks (into TMEM buffer 0), warp 2 the odd ones (buffer 1): the
+        // waits, four MMAs and two commits of a k-block take one warp about 520 cycles, as long as
+        // the MMAs of a 256 x 256 tile and twice as long as those of a 128 x 128 one.
         if (leader) {
-            int stage = 0, acc = 0, g = 0;
+            const int mine = warp - 1;
+            int stage = mine, g = 0, before = 0;       // k-blocks of the tiles before this one
             uint32_t phase = 0, acc_phase = 0;
             bool aborted = false, any_mma = false;
             // 8-row (K-major) or 8-k (MN-major) groups are 1024 bytes apart; the next 32 k of a
             // stage are 32 bytes along the row, or 32 rows of 128 bytes down
             const uint64_t a_desc0 = ptx::smem_desc_sw128(sA, 16, 1024), b_desc0 = ptx::smem_desc_sw128(sB, 16, 1024);
             const uint64_t a_step = x.a_mn ? 4096u >> 4 : 32u >> 4, b_step = x.b_mn ? 4096u >> 4 : 32u >> 4;
-            Sched sc = sched_begin<Cfg>(p, unit);
-            Work w;
-            while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
-                g = find_problem<Cfg>(p, w.t, g, mt);
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(mine * BN);
+            const uint32_t tfull = tfull_bar(mine), tempty = tempty_bar(mine);
+            for (int t = unit; t < total_tiles && !aborted; t += num_units) {
+                g = find_problem<Cfg>(p, t, g, mt);
                 uint32_t idesc = pr.idesc;
-                if (tile_coord<Cfg>(p, w.t, g, rank, mt).half) idesc = (idesc & ~(0x1Fu << 24)) | ((128u >> 4) << 24);
-                for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    if (!warp_wait(tempty_bar(acc), acc_phase ^ 1u, ROLE_MMA, w.slot, 16 + acc) ||
-                        !warp_wait(full_bar(stage), phase, ROLE_MMA, w.slot, stage)) {
+                if (tile_coord<Cfg>(p, t, g, rank, mt).half) idesc = (idesc & ~(0x1Fu << 24)) | ((128u >> 4) << 24);
+                for (int i = (mine ^ before) & 1; i < kb_end - kb_begin; i += 2) {
+                    // both barriers are asked before either answer is needed
+                    const bool filled = ptx::mbar_test_wait(full_bar(stage), phase);
+                    const bool drained = ptx::mbar_test_wait(tempty, acc_phase ^ 1u);
+                    if (!__all_sync(0xffffffffu, filled && drained) &&
+                        (!warp_wait(full_bar(stage), phase, ROLE_MMA, t, stage) ||
+                         !warp_wait(tempty, acc_phase ^ 1u, ROLE_MMA, t, 16 + mine))) {
                         aborted = true;
                         break;
                     }
                     ptx::tc_fence_after_sync();
-                    f8::mma_block<CG>(tmem_base + static_cast<uint32_t>(acc * BN),
-                                      a_desc0 + static_cast<uint64_t>((stage * Cfg::A_BYTES) >> 4),
+                    f8::mma_block<CG>(d_tmem, a_desc0 + static_cast<uint64_t>((stage * Cfg::A_BYTES) >> 4),
                                       b_desc0 + static_cast<uint64_t>((stage * Cfg::B_BYTES) >> 4), a_step, b_step, idesc,
-                                      empty_bar(stage), tfull_bar(acc));
+                                      empty_bar(stage), tfull);
                     any_mma = true;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                    stage += 2;
+                    if (stage >= STAGES) { stage -= STAGES; phase ^= 1u; }
+                    acc_phase ^= 1u;
                 }
+                before += kb_end - kb_begin;
             }
             if (aborted && any_mma && lane == 0) {
-                if constexpr (CG == 2) ptx::mma_commit_pair(drain_bar, 0x1);
-                else ptx::mma_commit(drain_bar);
-                if (!wait_quiet(drain_bar, 0, p.wait_budget_ns)) report_timeout(p, ROLE_DRAIN, -1, 0, p.wait_budget_ns);
+                const uint32_t bar = drain_bar + 8u * mine;
+                if constexpr (CG == 2) ptx::mma_commit_pair(bar, 0x1);
+                else ptx::mma_commit(bar);
+                if (!wait_quiet(bar, 0, p.wait_budget_ns)) report_timeout(p, ROLE_DRAIN, -1, 0, p.wait_budget_ns);
             }
             __syncwarp();
         }
     } else {
-        // ================================ scale loaders ================================
+        // ================================ scale loader ================================
         // A slot: the scales of F8_GROUP k-blocks: [128 rows][k-block] of A, then of B
         // [k-block][columns], or [block of 128 columns][k-block].
-        const bool for_a = warp == 2;
         int slot = 0, g = 0;
         uint32_t phase = 0;
         bool aborted = false;
-        Sched sc = sched_begin<Cfg>(p, unit);
-        Work w;
-        while (!aborted && sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
-            g = find_problem<Cfg>(p, w.t, g, mt);
-            const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
-            constexpr int N_A = BM / 32, N_B = Cfg::SB_COL ? BN / 32 : 1, N_MAX = N_A > N_B ? N_A : N_B;
-            const float* src[N_MAX];
-            uint32_t ok = 0;
-#pragma unroll
-            for (int j = 0; j < N_MAX; ++j) {
-                if (for_a) {
-                    const int64_t row = tc.m0 + j * 32 + lane;
-                    if (j < N_A && row < pr.M) ok |= 1u << j;
-                    src[j] = x.sa + (row >> x.sa_shift) * x.sa_mn;
-                } else {
-                    const int64_t i = j * 32 + lane, n = tc.n0 + (Cfg::SB_COL ? i : i * 128);
-                    if (j < N_B && i < Cfg::SB_COUNT && n < pr.N) ok |= 1u << j;
-                    src[j] = x.sb + (Cfg::SB_COL ? n : n >> 7) * x.sb_mn + (Cfg::MOE ? g * x.sb_g : 0);
-                }
-            }
-            const int64_t step = for_a ? x.sa_k : x.sb_k;
+        for (int t = unit; t < total_tiles && !aborted; t += num_units) {
+            g = find_problem<Cfg>(p, t, g, mt);
+            const TileCoord tc = tile_coord<Cfg>(p, t, g, rank, mt);
             for (int kb = kb_begin; kb < kb_end; kb += F8_GROUP) {
-                if (!warp_wait(sempty_bar(slot), phase ^ 1u, ROLE_PRODUCER, w.slot, 32 + slot)) {
+                if (!warp_wait(sempty_bar(slot), phase ^ 1u, ROLE_PRODUCER, t, 32 + slot)) {
                     aborted = true;
                     break;
                 }
-                const uint32_t dst = sS + slot * Cfg::SLOT_BYTES + (for_a ? 0 : BM * F8_GROUP * 4);
-                const int n = for_a ? N_A : N_B;
+                const uint32_t dst = sS + slot * Cfg::SLOT_BYTES, dst_b = dst + BM * F8_GROUP * 4;
 #pragma unroll
-                for (int i = 0; i < F8_GROUP; ++i) {
+                for (int j = 0; j < BM / 32; ++j) {
+                    const int64_t row = tc.m0 + j * 32 + lane;
+                    const bool in = row < pr.M;
+                    const float* src = in ? x.sa + (row >> x.sa_shift) * x.sa_mn + kb * x.sa_k : x.sa;
 #pragma unroll
-                    for (int j = 0; j < N_MAX; ++j) {
-                        if (j < n && kb + i < kb_end && (Cfg::SB_COL || for_a || lane < Cfg::SB_COUNT)) {
-                            const bool in = ok >> j & 1u;
-                            const int at = for_a || !Cfg::SB_COL ? (j * 32 + lane) * F8_GROUP + i : i * BN + j * 32 + lane;
-                            f8::cp_async_4(dst + at * 4, in ? static_cast<const void*>(src[j] + (kb + i) * step) : x.sa, in);
-                        }
+                    for (int i = 0; i < F8_GROUP; ++i)
+                        if (kb + i < kb_end)
+                            f8::cp_async_4(dst + ((j * 32 + lane) * F8_GROUP + i) * 4, in ? src + i * x.sa_k : src, in);
+                }
+                if constexpr (Cfg::SB_COL) {
+#pragma unroll
+                    for (int j = 0; j < BN / 32; ++j) {
+                        const int64_t n = tc.n0 + j * 32 + lane;
+                        const bool in = n < pr.N;
+                        const float* src = in ? x.sb + n * x.sb_mn + kb * x.sb_k : x.sb;
+#pragma unroll
+                        for (int i = 0; i < F8_GROUP; ++i)
+                            if (kb + i < kb_end) f8::cp_async_4(dst_b + (i * BN + j * 32 + lane) * 4, in ? src + i * x.sb_k : src, in);
                     }
+                } else if (lane < Cfg::SB_COUNT * F8_GROUP) {
+                    const int64_t n = tc.n0 + lane / F8_GROUP * 128;
+                    const int i = lane % F8_GROUP;
+                    const bool in = n < pr.N && kb + i < kb_end;
+                    f8::cp_async_4(dst_b + lane * 4,
+                                   in ? x.sb + (n >> 7) * x.sb_mn + (kb + i) * x.sb_k + (Cfg::MOE ? g * x.sb_g : 0) : x.sb, in);
                 }
                 f8::cp_async_arrive(sfull_bar(slot));
                 if (++slot == Cfg::SLOTS) { slot = 0; phase ^= 1u; }
@@ -596,11 +601,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         uint32_t buf_phase = 0, slot_phase = 0;
         const uint32_t lead_tempty = ptx::mapa(tempty_bar(0), CG == 2 ? 0 : cta), own_sempty = ptx::mapa(sempty_bar(0), cta);
         constexpr bool MAY_HALVE = CG == 2 && Cfg::MOE;
-        Sched sc = sched_begin<Cfg>(p, unit);
-        Work w;
-        while (sched_next<Cfg>(p, unit, num_units, total_tiles, sc, w)) {
-            g = find_problem<Cfg>(p, w.t, g, mt);
-            const TileCoord tc = tile_coord<Cfg>(p, w.t, g, rank, mt);
+        for (int t = unit; t < total_tiles; t += num_units) {
+            g = find_problem<Cfg>(p, t, g, mt);
+            const TileCoord tc = tile_coord<Cfg>(p, t, g, rank, mt);
             // a half tile keeps 64 rows in lanes 0-63 (columns [0, BN/2)) and again in lanes 64-127
             // (columns [BN/2, BN)), in BN/2 TMEM columns: the two warps of a quarter split those
             const int local_row = tc.half ? (q % 2) * 32 : q * 32;
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             // next slot.  Read once per group, a k-block ahead: shared memory answers slowly
             // while the tensor cores and TMA use it.
             auto read_scales = [&](float (&f)[F8_GROUP]) -> bool {
-                if (!warp_wait(sfull_bar(slot), slot_phase, ROLE_EPILOGUE, w.slot, 32 + slot)) return false;
+                if (!warp_wait(sfull_bar(slot), slot_phase, ROLE_EPILOGUE, t, 32 + slot)) return false;
                 const uint32_t off = slot * Cfg::SLOT_BYTES;
                 const float4 a = ptx::ld_shared_f4(sa_at + off);
                 f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
                     const int u = (kb - kb_begin) % F8_GROUP;
                     if (!__all_sync(0xffffffffu, ready) &&
-                        !warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, w.slot, 16 + buf)) return false;
+                        !warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, t, 16 + buf)) return false;
                     ptx::tc_fence_after_sync();
                     const uint32_t tm = tm0 + static_cast<uint32_t>(buf * BN);
                     uint32_t r[2][32];
