@@ -232,11 +232,16 @@ tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
     x.a_mn = a_mn;
     x.b_mn = b_mn;
     x.splits = splits;
+    const char* env = std::getenv("TG_STREAM_K");
+    x.halves = env && env[0] == '0' ? 0u : 1u;
     x.c = c.C;
     x.ldc = c.ldc;
     x.vec_c = host::aligned(c.C, 16) && (c.ldc * (c.c_dtype == TG_F32 ? 4 : 2)) % 16 == 0;
     host::launch_params(&p, d.err);
-    const int64_t want = splits > 1 ? p.total_tiles * splits : moe || p.total_tiles > units ? units : p.total_tiles;
+    // every resident unit, or fewer when there are fewer tiles (half tiles) than units
+    int64_t want = pair && x.halves ? 2 * p.total_tiles : p.total_tiles;
+    if (moe || want > units) want = units;
+    if (splits > 1) want = p.total_tiles * splits;
     const cudaError_t e = v.launch(p, x, static_cast<int>(want) * v.cta_group, stream);
     if (e != cudaSuccess) return host::cuda_fail(e, "8-bit kernel launch");
     host::count_launches(1);

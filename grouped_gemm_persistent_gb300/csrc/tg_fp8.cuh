@@ -50,6 +50,7 @@ struct Fp8Params {
     uint32_t a_mn, b_mn;       // A stored M-contiguous, B stored N-contiguous
     uint32_t vec_c;            // rows of C are 16-byte aligned
     uint32_t a_bytes;          // of A's box: all 128 rows, or as many as a short A has
+    uint32_t halves;           // pairs: the last wave's tiles may run as half tiles
     int32_t splits;            // SPLIT: CTAs that share a tile (the cluster's size)
     void* c;
     int64_t ldc;
@@ -418,6 +419,23 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
 
     // Registers: 384 x 168 at launch = 64512 = 128 x 72 + 256 x 216.  Each split stands at
     // the head of its own branch: after a common one the compiler kept to the smaller count.
+    // The last, partial wave of a pair launch: its R = tiles mod units tiles, when two of them fit a
+    // unit each, run as 2R half tiles (128 rows of a pair, 64 a CTA), items whole, whole + 1, ..
+    constexpr bool MAY_HALVE = CG == 2;
+    const int last_wave = MAY_HALVE && x.halves ? total_tiles % num_units : 0;
+    const int halved = 2 * last_wave <= num_units ? last_wave : 0;
+    const int whole = total_tiles - halved, items = total_tiles + halved;
+    auto tile_of = [&](int t) { return MAY_HALVE && t >= whole ? whole + (t - whole) % halved : t; };
+    auto coord_of_item = [&](int t, int g) {
+        TileCoord c = tile_coord<Cfg>(p, tile_of(t), g, rank, mt);
+        if (MAY_HALVE && t >= whole) {
+            // (an expert's tile of at most 128 rows is a half tile already: its second half is empty)
+            if (!c.half) c.m0 -= static_cast<int>(rank) * (BM / 2);
+            c.m0 += (t - whole) / halved * BM;
+            c.half = true;
+        }
+        return c;
+    };
     const Problem& pr = p.dense;
     // Warp-uniform bounded wait: every lane polls once; if the phase is not yet complete, lane 0
     // runs the bounded wait and tells the others how it ended.
@@ -444,9 +462,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             bool aborted = false;
             bool withhold = p.withhold_kb >= 0 && blockIdx.x == static_cast<uint32_t>(p.withhold_block);
             const uint32_t tx = x.a_bytes + Cfg::B_BYTES;
-            for (int t = unit; t < total_tiles && !aborted; t += num_units) {
-                g = find_problem<Cfg>(p, t, g, mt);
-                const TileCoord tc = tile_coord<Cfg>(p, t, g, rank, mt);
+            for (int t = unit; t < items && !aborted; t += num_units) {
+                g = find_problem<Cfg>(p, tile_of(t), g, mt);
+                const TileCoord tc = coord_of_item(t, g);
                 const int nb0 = tc.n0 + static_cast<int>(rank) * Cfg::BN_CTA;
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
                     if (!ptx::mbar_test_wait(empty_bar(stage), phase ^ 1u) &&
@@ -508,10 +526,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             const uint64_t a_step = x.a_mn ? 4096u >> 4 : 32u >> 4, b_step = x.b_mn ? 4096u >> 4 : 32u >> 4;
             const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(mine * BN);
             const uint32_t tfull = tfull_bar(mine), tempty = tempty_bar(mine);
-            for (int t = unit; t < total_tiles && !aborted; t += num_units) {
-                g = find_problem<Cfg>(p, t, g, mt);
+            for (int t = unit; t < items && !aborted; t += num_units) {
+                g = find_problem<Cfg>(p, tile_of(t), g, mt);
                 uint32_t idesc = pr.idesc;
-                if (tile_coord<Cfg>(p, t, g, rank, mt).half) idesc = (idesc & ~(0x1Fu << 24)) | ((128u >> 4) << 24);
+                if (coord_of_item(t, g).half) idesc = (idesc & ~(0x1Fu << 24)) | ((128u >> 4) << 24);
                 for (int i = (mine ^ before) & 1; i < kb_end - kb_begin; i += 2) {
                     // both barriers are asked before either answer is needed
                     const bool filled = ptx::mbar_test_wait(full_bar(stage), phase);
@@ -548,9 +566,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         int slot = 0, g = 0;
         uint32_t phase = 0;
         bool aborted = false;
-        for (int t = unit; t < total_tiles && !aborted; t += num_units) {
-            g = find_problem<Cfg>(p, t, g, mt);
-            const TileCoord tc = tile_coord<Cfg>(p, t, g, rank, mt);
+        for (int t = unit; t < items && !aborted; t += num_units) {
+            g = find_problem<Cfg>(p, tile_of(t), g, mt);
+            const TileCoord tc = coord_of_item(t, g);
             for (int kb = kb_begin; kb < kb_end; kb += F8_GROUP) {
                 if (!warp_wait(sempty_bar(slot), phase ^ 1u, ROLE_PRODUCER, t, 32 + slot)) {
                     aborted = true;
@@ -600,10 +618,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         int buf = 0, slot = 0, g = 0;
         uint32_t buf_phase = 0, slot_phase = 0;
         const uint32_t lead_tempty = ptx::mapa(tempty_bar(0), CG == 2 ? 0 : cta), own_sempty = ptx::mapa(sempty_bar(0), cta);
-        constexpr bool MAY_HALVE = CG == 2 && Cfg::MOE;
-        for (int t = unit; t < total_tiles; t += num_units) {
-            g = find_problem<Cfg>(p, t, g, mt);
-            const TileCoord tc = tile_coord<Cfg>(p, t, g, rank, mt);
+        for (int t = unit; t < items; t += num_units) {
+            g = find_problem<Cfg>(p, tile_of(t), g, mt);
+            const TileCoord tc = coord_of_item(t, g);
             // a half tile keeps 64 rows in lanes 0-63 (columns [0, BN/2)) and again in lanes 64-127
             // (columns [BN/2, BN)), in BN/2 TMEM columns: the two warps of a quarter split those
             const int local_row = tc.half ? (q % 2) * 32 : q * 32;
@@ -664,22 +681,31 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 float f[F8_GROUP];
                 if (kb_begin == kb_end) return true;
                 if (!read_scales(f)) return false;
+                // AHEAD: the next buffer's first columns are asked for before the last ones of this buffer
+                // are added.  Measured at 8192^3: column scales 726 us with it and 775 without; block
+                // scales 418 us without and 623 with it (their shorter additions hide less, and the
+                // registers of the load in flight cost spills).
+                constexpr bool AHEAD = Cfg::SB_COL && CHUNKS > 0;
+                uint32_t r[2][32];
                 bool ready = ptx::mbar_test_wait(tfull_bar(buf), buf_phase);
-#pragma unroll 1
-                for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    const int u = (kb - kb_begin) % F8_GROUP;
+                auto open = [&]() -> bool {
                     if (!__all_sync(0xffffffffu, ready) &&
                         !warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, t, 16 + buf)) return false;
                     ptx::tc_fence_after_sync();
+                    if constexpr (CHUNKS > 0) ptx::tmem_ld_32x32b_x32(tm0 + static_cast<uint32_t>(buf * BN), r[0]);
+                    return true;
+                };
+                // One k-block, the u-th of its group; LAST (AHEAD only): no further one follows
+                auto block = [&](auto last, int u, bool more) -> bool {
+                    constexpr bool LAST = decltype(last)::value;
                     const uint32_t tm = tm0 + static_cast<uint32_t>(buf * BN);
-                    uint32_t r[2][32];
-                    if constexpr (CHUNKS > 0) ptx::tmem_ld_32x32b_x32(tm, r[0]);
-                    const float s = f[0];
-                    const uint32_t sb = sb_at + slot * Cfg::SLOT_BYTES + u * (BN * 4);      // SB_COL
+                    [[maybe_unused]] const float s = f[0];
+                    [[maybe_unused]] const uint32_t sb = sb_at + slot * Cfg::SLOT_BYTES + u * (BN * 4);   // SB_COL
                     f[0] = f[1]; f[1] = f[2]; f[2] = f[3];
                     if constexpr (!Cfg::SB_COL) {
-                        if (u == F8_GROUP - 1 && kb + 1 < kb_end && !read_scales(f)) return false;
+                        if (u == F8_GROUP - 1 && more && !read_scales(f)) return false;
                     }
+                    bool there = true;
                     f8::for_each<(CHUNKS > 0 ? CHUNKS : 1)>([&](auto ci) {
                         constexpr int C = decltype(ci)::value;
                         if constexpr (CHUNKS > 0) f8::tmem_ld_wait32(r[C & 1]);
@@ -687,30 +713,48 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                             ptx::tmem_ld_32x32b_x32(tm + (C + 1) * 32, r[(C + 1) & 1]);
                         } else {
                             // everything is in registers: the buffer goes back to the MMA issuer; the next
-                            // one is asked for early, so that the answer is there after the additions
+                            // one's barrier is asked early, so that the answer is there after the additions
                             ptx::tc_fence_before_sync();
                             f8::arrive_lane0(lead_tempty + 8u * buf, lane);
                             if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
                             ready = ptx::mbar_test_wait(tfull_bar(buf), buf_phase);
+                            if constexpr (AHEAD && !LAST) there = open();
                         }
                         if constexpr (CHUNKS > 0) add(ci, r[C & 1], s, sb);
                     });
                     if constexpr (Cfg::SB_COL) {
-                        if (u == F8_GROUP - 1 || kb + 1 == kb_end) {
+                        if (u == F8_GROUP - 1 || !more) {
                             // the columns' scales have been read: on to the next group's slot
                             __syncwarp();
                             f8::arrive_lane0(own_sempty + 8u * slot, lane);
                             if (++slot == Cfg::SLOTS) { slot = 0; slot_phase ^= 1u; }
-                            if (kb + 1 < kb_end && !read_scales(f)) return false;
+                            if (more && !read_scales(f)) return false;
                         }
                     }
+                    return there;
+                };
+                if constexpr (AHEAD) {
+                    static_assert(CHUNKS % 2 == 0, "a buffer's first columns sit in r[0], its last in r[1]");
+                    if (!open()) return false;
+#pragma unroll 1
+                    for (int kb = kb_begin; kb + 1 < kb_end; ++kb)
+                        if (!block(std::false_type{}, (kb - kb_begin) % F8_GROUP, true)) return false;
+                    return block(std::true_type{}, (kb_end - 1 - kb_begin) % F8_GROUP, false);
+                } else {
+#pragma unroll 1
+                    for (int kb = kb_begin; kb < kb_end; ++kb)
+                        if (!open() || !block(std::false_type{}, (kb - kb_begin) % F8_GROUP, kb + 1 < kb_end)) return false;
+                    return true;
                 }
-                return true;
             };
             bool ok;
-            if (!active) ok = accumulate(std::integral_constant<int, 0>{});
-            else if (MAY_HALVE && tc.half) ok = accumulate(std::integral_constant<int, COLS / 64>{});
-            else ok = accumulate(std::integral_constant<int, COLS / 32>{});
+            if (!active) {
+                ok = accumulate(std::integral_constant<int, 0>{});
+            } else if (MAY_HALVE && tc.half) {
+                if constexpr (MAY_HALVE) ok = accumulate(std::integral_constant<int, COLS / 64>{});
+            } else {
+                ok = accumulate(std::integral_constant<int, COLS / 32>{});
+            }
             if (!ok) break;
             if (!active) continue;
             if constexpr (Cfg::SPLIT) {
