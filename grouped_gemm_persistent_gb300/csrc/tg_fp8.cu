@@ -165,9 +165,12 @@ tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
     const bool moe = c.experts > 0;
     int form = moe ? FORM_MOE : c.B->block == 1 ? FORM_COLUMN : FORM_BLOCK;
 
-    // CTA pairs where their 256 x 256 tiles give every pair work, single CTAs (128 x 128) below
-    const int64_t pair_tiles = ((c.rows + 255) / 256) * ((c.N + 255) / 256);
-    int pair = pair_tiles * 2 >= d.sms ? 1 : 0;
+    // CTA pairs (256 x 256 tiles) once there are more 128 x 128 tiles than SMs.  4096 columns, K 4096:
+    // 512 rows 17.1 us in pairs and 15.2 us in single CTAs, 768 rows 21.1 and 26.0.  Experts fill pair
+    // tiles from an average of 256 rows on: 64 of them, K 1536, N 4096, 2048 rows 93 us in pairs and
+    // 72 us in single CTAs, 8192 rows 124 and 115, 16384 rows 182 and 184.
+    const int64_t tiles = ((c.rows + 127) / 128) * ((c.N + 127) / 128);
+    int pair = tiles > d.sms && (!moe || c.rows >= 256 * c.experts) ? 1 : 0;
     if (const char* env = std::getenv("TG_TILE")) {
         int cg = 0, bn = 0;
         if (std::sscanf(env, "%dx%d", &cg, &bn) == 2 && (cg == 1 || cg == 2)) pair = cg - 1;
