@@ -242,48 +242,163 @@ __device__ __forceinline__ void arrive_lane0(uint32_t cluster_bar, int lane) {
                  "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" :: "r"(cluster_bar), "r"(lane) : "memory");
 }
 
-// Columns [n, n + 64 / esize) of 32 rows, one row a lane: rounded, staged in 2 KiB of shared
-// memory (16-byte chunks swizzled by the row, so that neither side has bank conflicts), read back
-// four lanes to a row and stored as 64-byte row pieces.  v holds the fp32 values.
-template <bool F32, int CW>
-__device__ __forceinline__ void store_rows(const float (&v)[CW], uint32_t stage, const Fp8Params& x, bool c_f16,
-                                           int row0, int row_limit, int n, int N, int lane) {
-    constexpr int PER = F32 ? 4 : 8;      // columns in 16 bytes
-    static_assert(CW == 4 * PER, "64 bytes a row");
+// Where a lane of an epilogue warp stores: four lanes to a row, four columns a lane, rows
+// lane / 4, + 8, + 16, + 24 of the warp's 32.
+struct StorePlan {
+    uint8_t* at;            // this lane's first row, the warp's first column + 4 (lane % 4)
+    int64_t row_step;       // bytes to eight rows down
+    int rows;               // of its four rows, those inside C
+    int cols;               // columns of C from `at` on (may exceed the warp's)
+    const uint16_t* bias;   // of the column at `at`, or null
+};
+
+__device__ __forceinline__ void st_global_if(bool p, void* at, uint32_t a, uint32_t b) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.cs.v2.b32 [%1], {%2, %3};\n\t}"
+                 :: "r"(static_cast<uint32_t>(p)), "l"(at), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_global_if(bool p, void* at, const float4& w) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.cs.v4.f32 [%1], {%2, %3, %4, %5};\n\t}"
+                 :: "r"(static_cast<uint32_t>(p)), "l"(at), "f"(w.x), "f"(w.y), "f"(w.z), "f"(w.w) : "memory");
+}
+
+// 16 columns of 32 rows.  v holds one row a lane; the rows go through 2 KiB of shared memory
+// (16-byte chunks swizzled by the row, so that neither side has bank conflicts) and come back
+// four lanes to a row, where bias, GELU and rounding take place.  For what store_whole does not
+// take: ragged columns, unaligned rows, fp16.
+__device__ __forceinline__ void store16(const float* v, uint32_t stage, const StorePlan& sp, int chunk, int epi, uint32_t flags,
+                                        bool whole, int lane) {
     __syncwarp();                         // the previous chunk has been read back
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (F32) w[i] = __float_as_uint(v[4 * j + i]);
-            else w[i] = c_f16 ? pack_f16x2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1])
-                              : pack_bf16x2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(stage + lane * 64 + ((static_cast<uint32_t>(j) ^ (lane >> 1 & 3u)) << 4)), "r"(w[0]),
-                        "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-    }
+    for (int j = 0; j < 4; ++j)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(stage + lane * 64 + ((static_cast<uint32_t>(j) ^ (lane >> 1 & 3u)) << 4)), "f"(v[4 * j]),
+                        "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3]) : "memory");
     __syncwarp();
-    const int j = lane % 4, col = n + j * PER;
+    const int cols = sp.cols - chunk * 16;
+    // row i * 8 + lane / 4, chunk lane % 4; eight rows on, the swizzle is the same
+    const uint32_t from = stage + (lane / 4) * 64 + ((static_cast<uint32_t>(lane % 4) ^ (lane >> 3 & 3u)) << 4);
+    float4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4;
-        const float4 w = ptx::ld_shared_f4(stage + r * 64 + ((static_cast<uint32_t>(j) ^ (r >> 1 & 3u)) << 4));
-        if (row0 + r >= row_limit || col >= N) continue;
-        const int64_t at = static_cast<int64_t>(row0 + r) * x.ldc + col;
-        const uint32_t ws[4] = {__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w)};
-        if (x.vec_c && col + PER <= N) {
-            if constexpr (F32) __stcs(reinterpret_cast<float4*>(static_cast<float*>(x.c) + at), w);
-            else __stcs(reinterpret_cast<float4*>(static_cast<uint16_t*>(x.c) + at), w);
-        } else if constexpr (F32) {
+    for (int i = 0; i < 4; ++i) w[i] = ptx::ld_shared_f4(from + i * 512);
+    if (epi != EPI_NONE) {
+        float b[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (col + c < N) static_cast<uint32_t*>(x.c)[at + c] = ws[c];
+        for (int i = 0; i < 4; ++i)
+            b[i] = i < cols ? __uint_as_float(static_cast<uint32_t>(__ldg(sp.bias + chunk * 16 + i)) << 16) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { w[i].x += b[0]; w[i].y += b[1]; w[i].z += b[2]; w[i].w += b[3]; }
+        if (epi == EPI_BIAS_GELU) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                gelu_tanh_f32x2(w[i].x, w[i].y);
+                gelu_tanh_f32x2(w[i].z, w[i].w);
+            }
+        }
+    }
+    uint8_t* at = sp.at + chunk * (flags & FLAG_C_F32 ? 64 : 32);
+    if (flags & FLAG_C_F32) {
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_if(i < sp.rows, at + i * sp.row_step, w[i]);
         } else {
+#pragma unroll 1
+            for (int i = 0; i < 4 && i < sp.rows; ++i) {
+                float* c = reinterpret_cast<float*>(at + i * sp.row_step);
+                const float4 y = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+                if (cols > 0) c[0] = y.x;
+                if (cols > 1) c[1] = y.y;
+                if (cols > 2) c[2] = y.z;
+                if (cols > 3) c[3] = y.w;
+            }
+        }
+        return;
+    }
+    uint32_t lo[4], hi[4];
+    if (flags & FLAG_C_F16) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (col + c < N) static_cast<uint16_t*>(x.c)[at + c] = static_cast<uint16_t>(ws[c / 2] >> ((c & 1) * 16));
+        for (int i = 0; i < 4; ++i) { lo[i] = pack_f16x2(w[i].x, w[i].y); hi[i] = pack_f16x2(w[i].z, w[i].w); }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { lo[i] = pack_bf16x2(w[i].x, w[i].y); hi[i] = pack_bf16x2(w[i].z, w[i].w); }
+    }
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_global_if(i < sp.rows, at + i * sp.row_step, lo[i], hi[i]);
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 4 && i < sp.rows; ++i) {
+            uint16_t* c = reinterpret_cast<uint16_t*>(at + i * sp.row_step);
+            const uint32_t l = i == 0 ? lo[0] : i == 1 ? lo[1] : i == 2 ? lo[2] : lo[3];
+            const uint32_t u = i == 0 ? hi[0] : i == 1 ? hi[1] : i == 2 ? hi[2] : hi[3];
+            if (cols > 0) c[0] = static_cast<uint16_t>(l);
+            if (cols > 1) c[1] = static_cast<uint16_t>(l >> 16);
+            if (cols > 2) c[2] = static_cast<uint16_t>(u);
+            if (cols > 3) c[3] = static_cast<uint16_t>(u >> 16);
+        }
+    }
+}
+
+// COLS columns of 32 rows, all inside C, 16-byte aligned, fp32 or bf16: straight code without a branch
+// (rows past the end are predicated off).  Code runs once a tile here and every taken branch costs
+// an instruction fetch: with branches around the types and epilogues of each store, a 128 x 256
+// part of a tile took 5500 to 8000 cycles to store.
+template <bool F32, int EPI, int COLS>
+__device__ __forceinline__ void store_whole(const float* v, uint32_t stage, const StorePlan& sp, int lane) {
+    const uint32_t to = stage + lane * 64, sw = lane >> 1 & 3u;
+    const uint32_t from = stage + (lane / 4) * 64 + ((static_cast<uint32_t>(lane % 4) ^ (lane >> 3 & 3u)) << 4);
+    if constexpr (!F32 && EPI == EPI_NONE) {
+        // rounded first: 32 columns a pass, eight of a row in a lane afterwards (sp counts columns in
+        // fours: this lane's eight start another 4 (lane % 4) columns on)
+        uint8_t* at = sp.at + (lane % 4) * 8;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 32) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(to + ((static_cast<uint32_t>(j) ^ sw) << 4)), "r"(pack_bf16x2(v[c + 8 * j], v[c + 8 * j + 1])),
+                                "r"(pack_bf16x2(v[c + 8 * j + 2], v[c + 8 * j + 3])),
+                                "r"(pack_bf16x2(v[c + 8 * j + 4], v[c + 8 * j + 5])),
+                                "r"(pack_bf16x2(v[c + 8 * j + 6], v[c + 8 * j + 7])) : "memory");
+            __syncwarp();
+            float4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = ptx::ld_shared_f4(from + i * 512);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_if(i < sp.rows, at + i * sp.row_step + c * 2, w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(to + ((static_cast<uint32_t>(j) ^ sw) << 4)), "f"(v[c + 4 * j]), "f"(v[c + 4 * j + 1]),
+                                "f"(v[c + 4 * j + 2]), "f"(v[c + 4 * j + 3]) : "memory");
+            __syncwarp();
+            float4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = ptx::ld_shared_f4(from + i * 512);
+            if constexpr (EPI != EPI_NONE) {
+                float b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = __uint_as_float(static_cast<uint32_t>(__ldg(sp.bias + c + i)) << 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i].x += b[0]; w[i].y += b[1]; w[i].z += b[2]; w[i].w += b[3];
+                    if constexpr (EPI == EPI_BIAS_GELU) {
+                        gelu_tanh_f32x2(w[i].x, w[i].y);
+                        gelu_tanh_f32x2(w[i].z, w[i].w);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint8_t* at = sp.at + i * sp.row_step + c * (F32 ? 4 : 2);
+                if constexpr (F32) st_global_if(i < sp.rows, at, w[i]);
+                else st_global_if(i < sp.rows, at, pack_bf16x2(w[i].x, w[i].y), pack_bf16x2(w[i].z, w[i].w));
+            }
         }
     }
 }
@@ -426,8 +541,28 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     const int halved = 2 * last_wave <= num_units ? last_wave : 0;
     const int whole = total_tiles - halved, items = total_tiles + halved;
     auto tile_of = [&](int t) { return MAY_HALVE && t >= whole ? whole + (t - whole) % halved : t; };
+    // tile_coord in 32 bits (the host refuses more than 2^30 tiles): with 64-bit divisions this took
+    // each role 800 to 1900 cycles a tile.
     auto coord_of_item = [&](int t, int g) {
-        TileCoord c = tile_coord<Cfg>(p, tile_of(t), g, rank, mt);
+        int local = tile_of(t), tiles_m = p.dense.tiles_m, rows_left = p.dense.M;
+        TileCoord c;
+        c.g = g;
+        c.m0 = 0;
+        c.row_end = INT32_MAX;
+        if constexpr (Cfg::MOE) {
+            local -= mt.tile_pref[g];
+            c.m0 = mt.row_off[g];
+            c.row_end = mt.row_off[g + 1];
+            rows_left = c.row_end - c.m0;
+            tiles_m = (rows_left + Cfg::TILE_M - 1) / Cfg::TILE_M;
+        }
+        // bands of p.band N-tiles, as raster()
+        const int per_band = tiles_m * p.band, bi = local / per_band, r = local - bi * per_band;
+        const int left = p.dense.tiles_n - bi * p.band, width = left < p.band ? left : p.band;
+        const int row = r / width, mb = (bi & 1) ? tiles_m - 1 - row : row;
+        c.n0 = (bi * p.band + r - row * width) * BN;
+        c.half = MAY_HALVE && Cfg::MOE && rows_left - mb * Cfg::TILE_M <= BM;
+        c.m0 += mb * Cfg::TILE_M + static_cast<int>(rank) * (c.half ? BM / 2 : BM);
         if (MAY_HALVE && t >= whole) {
             // (an expert's tile of at most 128 rows is a half tile already: its second half is empty)
             if (!c.half) c.m0 -= static_cast<int>(rank) * (BM / 2);
@@ -766,48 +901,42 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 continue;
             }
 
-            // epilogue: 32 (16-bit output) or 16 (fp32) columns at a time: bias, GELU, rounding, store
-            const uint16_t* bias = static_cast<const uint16_t*>(pr.bias);
-            if constexpr (Cfg::MOE) { if (bias) bias += static_cast<int64_t>(g) * pr.N; }
-            const int epi = pr.epi;
-            // columns [C0, C0 + CW) of this warp's
-            auto finish = [&](auto first, auto& v) {
-                constexpr int C0 = decltype(first)::value;
-                constexpr int CW = static_cast<int>(sizeof(v) / sizeof(float));
-#pragma unroll
-                for (int j = 0; j < CW / 8; ++j) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[8 * j + i] = acc[C0 + 8 * j + i];
-                    if (epi != EPI_NONE) {
-                        float b[8];
-                        f8::load_bias8(bias, n0 + C0 + 8 * j, pr.N, b);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
-                        if (epi == EPI_BIAS_GELU) {
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) gelu_tanh_f32x2(v[8 * j + i], v[8 * j + i + 1]);
+            // epilogue, 16 columns at a time
+            const int esize = pr.flags & FLAG_C_F32 ? 4 : 2;
+            const int first = n0 + (lane % 4) * 4, my_row = row0 + lane / 4;
+            f8::StorePlan sp;
+            sp.at = static_cast<uint8_t*>(x.c) + (static_cast<int64_t>(my_row) * x.ldc + first) * esize;
+            sp.row_step = x.ldc * esize * 8;
+            sp.rows = (row_limit - my_row + 7) / 8;            // (at most 0 when this lane has none)
+            sp.cols = pr.N - first;
+            sp.bias = static_cast<const uint16_t*>(pr.bias) + first + (Cfg::MOE ? static_cast<int64_t>(g) * pr.N : 0);
+            if (x.vec_c && n0 + n_cols <= pr.N && !(pr.flags & FLAG_C_F16)) {
+                auto whole = [&](auto f32_tag, auto epi_tag) {
+                    constexpr bool F32 = decltype(f32_tag)::value;
+                    constexpr int EPI = decltype(epi_tag)::value;
+                    f8::store_whole<F32, EPI, 64>(acc, stage_c, sp, lane);
+                    if constexpr (COLS > 64) {
+                        if (n_cols > 64) {
+                            sp.at += 64 * esize;
+                            sp.bias += 64;
+                            f8::store_whole<F32, EPI, 64>(acc + 64, stage_c, sp, lane);
                         }
                     }
-                }
-            };
-            const bool f32 = (pr.flags & FLAG_C_F32) != 0, f16 = (pr.flags & FLAG_C_F16) != 0;
-            auto chunk = [&](auto first, auto f32_tag) {
-                constexpr int C0 = decltype(first)::value;
-                constexpr bool F32 = decltype(f32_tag)::value;
-                if (C0 < n_cols && n0 + C0 < pr.N) {
-                    float v[F32 ? 16 : 32];
-                    finish(first, v);
-                    f8::store_rows<F32>(v, stage_c, x, f16, row0, row_limit, n0 + C0, pr.N, lane);
-                }
-            };
-            auto chunks = [&](auto f32_tag) {
-                constexpr int CW = decltype(f32_tag)::value ? 16 : 32;
-                f8::for_each<COLS / CW>([&](auto i) {
-                    chunk(std::integral_constant<int, decltype(i)::value * CW>{}, f32_tag);
+                };
+                auto with_epi = [&](auto f32_tag) {
+                    if (pr.epi == EPI_NONE) whole(f32_tag, std::integral_constant<int, EPI_NONE>{});
+                    else if (pr.epi == EPI_BIAS) whole(f32_tag, std::integral_constant<int, EPI_BIAS>{});
+                    else whole(f32_tag, std::integral_constant<int, EPI_BIAS_GELU>{});
+                };
+                if (pr.flags & FLAG_C_F32) with_epi(std::true_type{});
+                else with_epi(std::false_type{});
+            } else {
+                f8::for_each<COLS / 16>([&](auto i) {
+                    constexpr int C = decltype(i)::value;
+                    if (C * 16 < n_cols && n0 + C * 16 < pr.N)
+                        f8::store16(acc + C * 16, stage_c, sp, C, pr.epi, pr.flags, x.vec_c && n0 + C * 16 + 16 <= pr.N, lane);
                 });
-            };
-            if (f32) chunks(std::true_type{});
-            else chunks(std::false_type{});
+            }
             __syncwarp();
         }
     }
@@ -818,7 +947,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         // of the k ranges, and finishes them.
         __syncwarp();
         ptx::cluster_sync();
-        const TileCoord tc = tile_coord<Cfg>(p, unit, 0, 0, mt);
+        const TileCoord tc = coord_of_item(unit, 0);
         const int ew = warp - F8_EPI_WARP0;
         const int row = tc.m0 + (warp % 4) * 32 + lane, per = Cfg::COLS / splits;
         const int c_first = static_cast<int>(cta) * per;
