@@ -333,6 +333,41 @@ def test_gemm_epilogues(monkeypatch, tile, out_dtype, epilogue):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("epilogue", ["none", "bias", "bias_gelu"])
+def test_gemm_many_tiles(out_dtype, epilogue):
+    """More tiles than CTA pairs, whole and ragged, with a last wave in half tiles."""
+    g = cuda_gen(20)
+    for M, N, K in ((2560, 2560, 256), (3000, 2200, 200), (2049, 5121, 384)):
+        a, sa, b, sb = make(g, M, N, K, sb="square")
+        sa, sb = sa * 2.0 ** -8, sb * 2.0 ** -8
+        bias = torch.randn(N, generator=g, device="cuda").bfloat16() if epilogue != "none" else None
+        out = tg.gemm_fp8(a, sa, b, sb, bias=bias, epilogue=epilogue, out_dtype=out_dtype)
+        tg.device_status()
+        check_product(out, a, sa, b, sb, bias, epilogue)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    g = cuda_gen(21)
+    M, N, K = 66000, 128, 128
+    a, sa, b, sb = make(g, M, N, K)
+    wide = torch.empty(M, 33000, dtype=torch.bfloat16, device="cuda")      # rows of C 33000 elements apart
+    out = wide[:, 32800:32800 + N]
+    tg.gemm_fp8(a, sa, b, sb, out)
+    tg.device_status()
+    check_product(out, a, sa, b, sb)
+    x = wide[:, :256]
+    x.copy_(torch.randn(M, 256, generator=g, device="cuda"))
+    for block in ((1, 128), (128, 1), (128, 128)):
+        q, s = tg.quantize_fp8(x, block)
+        tail = x[-80:]                                                       # 66000 = 515 * 128 + 80
+        wq, ws = ref.quantize(tail.cpu(), block, E4)
+        assert torch.equal(q[-80:].cpu().float(), wq.float())
+        assert torch.equal((s[-80:] if block == (1, 128) else s[-1:]).cpu(), ws)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("at,bt", [(E4, E5), (E5, E4), (E5, E5)])
 @pytest.mark.parametrize("M", [3, 300])
 def test_gemm_types(at, bt, M):
@@ -545,6 +580,21 @@ def test_moe_equals_the_dense_product_and_repeats():
     for _ in range(3):
         assert torch.equal(out, tg.moe_gemm_fp8(*t, out_dtype=torch.float32))
     check_moe(out, counts, *t[:4])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("epilogue", ["none", "bias_gelu"])
+def test_moe_many_tiles(epilogue):
+    """Enough rows an expert for CTA pairs, ragged and empty experts among them."""
+    g = cuda_gen(22)
+    counts = [1000, 0, 257, 1, 640, 129, 2048, 384]
+    a, sa, b, sb, c = make_moe(g, counts, 1160, 256)
+    sa, sb = sa * 2.0 ** -8, sb * 2.0 ** -8
+    bias = torch.randn(len(counts), 1160, generator=g, device="cuda").bfloat16() if epilogue != "none" else None
+    for dt in (torch.bfloat16, torch.float32):
+        out = tg.moe_gemm_fp8(a, sa, b, sb, c, bias=bias, epilogue=epilogue, out_dtype=dt)
+        tg.device_status()
+        check_moe(out, counts, a, sa, b, sb, bias, epilogue)
 
 
 @pytest.mark.gpu
