@@ -29,6 +29,7 @@ BF16, F32, F16, E4M3, E5M2 = 0, 1, 2, 3, 4
 _DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
 _FP8_CODE = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
 FP8_BLOCK = 128     # values that share a scale
+_ITEM_BYTES = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4, torch.float8_e4m3fn: 1, torch.float8_e5m2: 1}
 
 _lib = None
 _lock = threading.Lock()
@@ -340,33 +341,40 @@ def _blocks(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
-def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """torch.empty in the allocator's order of ``stream``, so that a block freed on another stream is not
-    handed out while that stream still uses it."""
-    if isinstance(stream, torch.cuda.Stream):
+def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
+    """An uninitialised tensor on ``like``'s device, in the allocator's order of ``stream``, so that a block freed
+    on another stream is not handed out while that stream still uses it."""
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty(shape, dtype=dtype, device=device)
+            return like.new_empty(shape, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
 
 
-def _rows_of_16_bytes(rows: int, cols: int, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """An uninitialised [rows, cols] tensor whose rows start on 16-byte boundaries."""
-    step = 16 // dtype.itemsize
+def _rows_of_16_bytes(like: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, stream) -> tuple[torch.Tensor, int]:
+    """An uninitialised [rows, cols] tensor whose rows start on 16-byte boundaries, and its leading dimension."""
+    step = 16 // _ITEM_BYTES[dtype]
     ld = -(-cols // step) * step
-    t = _empty((rows, ld), dtype, device, stream)
-    return t if ld == cols else t[:, :cols]
+    t = _empty(like, (rows, ld), dtype, stream)
+    return (t if ld == cols else t[:, :cols]), max(ld, 1)
 
 
 def _on_one_gpu(names: str, *tensors) -> None:
     """The tensors (None is left out) are on one CUDA device, the current one."""
-    current = None
-    for i, t in enumerate(tensors):
-        if t is not None:
-            dev = t.get_device()
-            if dev >= 0 and current is None:
-                current = torch.cuda.current_device()
-            if dev != current:
-                raise ValueError(f"{names.split()[i]} must be on the current CUDA device, got {t.device}")
+    first = tensors[0].get_device()
+    same = first >= 0 and first == torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not same or t.get_device() != first):
+            for name, u in zip(names.split(), tensors):
+                if u is not None and (u.get_device() < 0 or u.get_device() != torch.cuda.current_device()):
+                    raise ValueError(f"{name} must be on the current CUDA device, got {u.device}")
+
+
+def _row_major_ld(t: torch.Tensor, name: str, cols: int) -> int:
+    """Leading dimension of a row-major matrix of `cols` columns (a single row's is never stepped by)."""
+    s0, s1 = t.stride()
+    if s1 == 1 or cols <= 1:
+        return s0 if t.shape[0] > 1 else max(cols, 1)
+    raise ValueError(f"{name} must be row-major (strides {t.stride()})")
 
 
 def quantize_fp8(x: torch.Tensor, block: tuple[int, int] = (1, 128), q: torch.Tensor | None = None,
@@ -379,37 +387,43 @@ def quantize_fp8(x: torch.Tensor, block: tuple[int, int] = (1, 128), q: torch.Te
     row-major bf16, fp16 or fp32; ``q`` (allocated with rows of a multiple of 16 bytes if not given) has
     ``dtype`` torch.float8_e4m3fn or torch.float8_e5m2, and ``x`` is ``q * scale`` up to its rounding.
     """
-    if x.dtype not in _DTYPE_CODE:
+    xt = _DTYPE_CODE.get(x.dtype)
+    if xt is None:
         raise TypeError("x must be bf16, fp16 or fp32")
-    lx, ldx = _matrix(x, "x")
-    if lx != ROW_MAJOR:
-        raise ValueError("x must be row-major")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got shape {tuple(x.shape)}")
     M, K = x.shape
-    block = tuple(block)
-    shape = {(1, 128): (M, _blocks(K)), (128, 1): (_blocks(M), K), (128, 128): (_blocks(M), _blocks(K))}.get(block)
-    if shape is None:
+    ldx = _row_major_ld(x, "x", K)
+    br, bc = block
+    by_row = br == 1
+    if (br, bc) not in ((1, 128), (128, 1), (128, 128)):
         raise ValueError(f"block must be (1, 128), (128, 1) or (128, 128), got {block}")
+    rows, cols = M if by_row else (M + 127) // 128, K if bc == 1 else (K + 127) // 128     # of the scales
     if q is None:
         if dtype not in _FP8_CODE:
             raise TypeError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
-        q = _rows_of_16_bytes(M, K, dtype, x.device, stream)
-    if q.dtype not in _FP8_CODE or tuple(q.shape) != (M, K):
-        raise ValueError("q must be [M, K] float8_e4m3fn or float8_e5m2")
-    lq, ldq = _matrix(q, "q")
-    if lq != ROW_MAJOR:
-        raise ValueError("q must be row-major")
+        q, ldq = _rows_of_16_bytes(x, M, K, dtype, stream)
+    else:
+        dtype = q.dtype
+        if dtype not in _FP8_CODE or q.shape != x.shape:
+            raise ValueError("q must be [M, K] float8_e4m3fn or float8_e5m2")
+        ldq = _row_major_ld(q, "q", K)
     if scale is None:
-        scale = (_empty(shape[::-1], torch.float32, x.device, stream).t() if block == (1, 128)
-                 else _empty(shape, torch.float32, x.device, stream))
-    if scale.dtype != torch.float32 or tuple(scale.shape) != shape:
-        raise ValueError(f"scale must be fp32 {list(shape)}")
-    stored = scale.t() if block == (1, 128) else scale
-    if stored.shape[1] > 1 and stored.stride(1) != 1:
-        raise ValueError("scale must have " + ("contiguous columns" if block == (1, 128) else "contiguous rows"))
-    scale_ld = stored.stride(0) if stored.shape[0] > 1 else max(stored.shape[1], 1)
+        # a row's scales are the columns of the result: a block column's lie side by side
+        stored = _empty(x, (cols, rows) if by_row else (rows, cols), torch.float32, stream)
+        scale, scale_ld = (stored.t() if by_row else stored), max(rows if by_row else cols, 1)
+    else:
+        if scale.dtype != torch.float32 or tuple(scale.shape) != (rows, cols):
+            raise ValueError(f"scale must be fp32 {[rows, cols]}")
+        (inner, outer), (si, so) = ((rows, cols), scale.stride()) if by_row else ((cols, rows), scale.stride()[::-1])
+        if inner > 1 and si != 1:
+            raise ValueError("scale must have " + ("contiguous columns" if by_row else "contiguous rows"))
+        scale_ld = so if outer > 1 else max(inner, 1)
     _on_one_gpu("x q scale", x, q, scale)
-    _check(load().tg_quantize_blocks(_ptr(x), _DTYPE_CODE[x.dtype], ldx, M, K, block[0], block[1], _ptr(q),
-                                  _FP8_CODE[q.dtype], ldq, _ptr(scale), scale_ld, _stream_handle(stream)))
+    status = load().tg_quantize_blocks(x.data_ptr(), xt, ldx, M, K, br, bc, q.data_ptr(), _FP8_CODE[dtype], ldq,
+                                       scale.data_ptr(), scale_ld, _stream_handle(stream))
+    if status:
+        _check(status)
     return q, scale
 
 
@@ -431,12 +445,16 @@ def _fp8_matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
     raise ValueError(f"{name}: neither rows nor columns are contiguous (strides {t.stride()})")
 
 
-def _fp8_scale(s: torch.Tensor, name: str, rows: int, kb: int, dim: int) -> tuple[int, int, int]:
-    """(block, stride, k stride) of an operand's scales; ``dim`` is the operand's row (A) or column (B) dimension."""
-    if s.dtype != torch.float32 or s.dim() != 2 or s.shape[1 - dim] != kb or s.shape[dim] not in (rows, _blocks(rows)):
-        raise ValueError(f"{name} must be fp32 with {kb} blocks of K and {rows} or {_blocks(rows)} entries, "
-                         f"got {tuple(s.shape)} {s.dtype}")
-    return (1 if s.shape[dim] == rows else FP8_BLOCK), s.stride(dim), s.stride(1 - dim)
+def _bad_scale(s: torch.Tensor, name: str, rows: int, kb: int):
+    return ValueError(f"{name} must be fp32 with {kb} blocks of K and {rows} or {_blocks(rows)} entries, "
+                      f"got {tuple(s.shape)} {s.dtype}")
+
+
+def _fp8_types(a: torch.Tensor, b: torch.Tensor) -> tuple[int, int]:
+    ta, tb = _FP8_CODE.get(a.dtype), _FP8_CODE.get(b.dtype)
+    if ta is None or tb is None:
+        raise TypeError("a and b must be float8_e4m3fn or float8_e5m2")
+    return ta, tb
 
 
 def gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: torch.Tensor,
@@ -449,33 +467,50 @@ def gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: t
     [ceil(K / 128), ceil(N / 128)], with any strides; scales of which neighbouring rows lie side by side
     (quantize_fp8's) load fastest.  ``bias`` is bf16 [N]; ``out`` (allocated if not given) bf16, fp16 or fp32.
     """
-    if a.dtype not in _FP8_CODE or b.dtype not in _FP8_CODE:
-        raise TypeError("a and b must be float8_e4m3fn or float8_e5m2")
+    ta, tb = _fp8_types(a, b)
+    la, lda = _fp8_matrix(a, "a")
+    lb, ldb = _fp8_matrix(b, "b")
     M, K = a.shape
     K2, N = b.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    kb = (K + 127) // 128
+    if scale_a.dtype != torch.float32 or scale_a.dim() != 2:
+        raise _bad_scale(scale_a, "scale_a", M, kb)
+    rows, cols = scale_a.shape
+    if cols != kb or (rows != M and rows != (M + 127) // 128):
+        raise _bad_scale(scale_a, "scale_a", M, kb)
+    sa, sak = scale_a.stride()
+    ba = 1 if rows == M else 128
+    if scale_b.dtype != torch.float32 or scale_b.dim() != 2:
+        raise _bad_scale(scale_b, "scale_b", N, kb)
+    rows, cols = scale_b.shape
+    if rows != kb or (cols != N and cols != (N + 127) // 128):
+        raise _bad_scale(scale_b, "scale_b", N, kb)
+    sbk, sb = scale_b.stride()
+    bb = 1 if cols == N else 128
     if out is None:
-        if out_dtype not in _DTYPE_CODE:
+        ct = _DTYPE_CODE.get(out_dtype)
+        if ct is None:
             raise TypeError("out_dtype must be bf16, fp16 or fp32")
-        out = _rows_of_16_bytes(M, N, out_dtype, a.device, stream)
-    if out.dtype not in _DTYPE_CODE or tuple(out.shape) != (M, N):
-        raise ValueError("out must be [M, N] bf16, fp16 or fp32")
-    la, lda = _fp8_matrix(a, "a")
-    lb, ldb = _fp8_matrix(b, "b")
-    lc, ldc = _matrix(out, "out")
-    if lc != ROW_MAJOR:
-        raise ValueError("out must be row-major")
-    ba, sa, sak = _fp8_scale(scale_a, "scale_a", M, _blocks(K), 0)
-    bb, sb, sbk = _fp8_scale(scale_b, "scale_b", N, _blocks(K), 1)
+        out, ldc = _rows_of_16_bytes(a, M, N, out_dtype, stream)
+    else:
+        ct = _DTYPE_CODE.get(out.dtype)
+        if ct is None or tuple(out.shape) != (M, N):
+            raise ValueError("out must be [M, N] bf16, fp16 or fp32")
+        ldc = _row_major_ld(out, "out", N)
     epi = EPILOGUES[epilogue]
-    if epi and (bias is None or bias.dtype != torch.bfloat16 or bias.numel() != N or not bias.is_contiguous()):
+    if not epi:
+        bias = None
+    elif bias is None or bias.dtype != torch.bfloat16 or bias.numel() != N or not bias.is_contiguous():
         raise ValueError("this epilogue needs a contiguous bf16 bias of length N")
-    _on_one_gpu("a scale_a b scale_b out bias", a, scale_a, b, scale_b, out, bias if epi else None)
-    oa = Fp8Operand(_ptr(a), lda, _ptr(scale_a), sa, sak, _FP8_CODE[a.dtype], la, ba)
-    ob = Fp8Operand(_ptr(b), ldb, _ptr(scale_b), sb, sbk, _FP8_CODE[b.dtype], lb, bb)
-    _check(load().tg_gemm_scaled(ctypes.byref(oa), ctypes.byref(ob), _ptr(out), _DTYPE_CODE[out.dtype], ldc, M, N, K, epi,
-                              _ptr(bias) if epi else None, _stream_handle(stream)))
+    _on_one_gpu("a scale_a b scale_b out bias", a, scale_a, b, scale_b, out, bias)
+    oa = Fp8Operand(a.data_ptr(), lda, scale_a.data_ptr(), sa, sak, ta, la, ba)
+    ob = Fp8Operand(b.data_ptr(), ldb, scale_b.data_ptr(), sb, sbk, tb, lb, bb)
+    status = load().tg_gemm_scaled(oa, ob, out.data_ptr(), ct, ldc, M, N, K, epi, bias.data_ptr() if epi else None,
+                                   _stream_handle(stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -488,45 +523,51 @@ def moe_gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_
     row- or column-major, ``scale_b`` [G, ceil(K / 128), ceil(N / 128)]; ``counts`` int32 CUDA tensor [G];
     ``out`` [T, N], rows past sum(counts) not written; ``bias`` bf16 [G, N].
     """
-    if a.dtype not in _FP8_CODE or b.dtype not in _FP8_CODE:
-        raise TypeError("a and b must be float8_e4m3fn or float8_e5m2")
+    ta, tb = _fp8_types(a, b)
     if counts.dtype != torch.int32 or counts.dim() != 1 or not counts.is_contiguous():
         raise TypeError("counts must be a contiguous int32 tensor [G]")
+    la, lda = _fp8_matrix(a, "a")
+    if la != ROW_MAJOR:
+        raise ValueError("a must be row-major")
     T, K = a.shape
     if b.dim() != 3 or b.shape[1] != K or counts.shape[0] != b.shape[0]:
         raise ValueError("shapes: a [T, K], b [G, K, N], counts [G]")
     G, _, N = b.shape
-    la, lda = _fp8_matrix(a, "a")
-    if la != ROW_MAJOR:
-        raise ValueError("a must be row-major")
+    kb = (K + 127) // 128
+    if scale_a.dtype != torch.float32 or tuple(scale_a.shape) != (T, kb):
+        raise ValueError(f"scale_a must be fp32 {[T, kb]}")
+    if scale_b.dtype != torch.float32 or tuple(scale_b.shape) != (G, kb, (N + 127) // 128):
+        raise ValueError(f"scale_b must be fp32 {[G, kb, (N + 127) // 128]}")
     if out is None:
-        if out_dtype not in _DTYPE_CODE:
+        ct = _DTYPE_CODE.get(out_dtype)
+        if ct is None:
             raise TypeError("out_dtype must be bf16, fp16 or fp32")
-        out = _rows_of_16_bytes(T, N, out_dtype, a.device, stream)
-    if out.dtype not in _DTYPE_CODE or tuple(out.shape) != (T, N):
-        raise ValueError("out must be [T, N] bf16, fp16 or fp32")
-    lc, ldc = _matrix(out, "out")
-    if lc != ROW_MAJOR:
-        raise ValueError("out must be row-major")
-    ba, sa, sak = _fp8_scale(scale_a, "scale_a", T, _blocks(K), 0)
-    if ba != 1:
-        raise ValueError("scale_a must have a scale per row")
-    shape = (G, _blocks(K), _blocks(N))
-    if scale_b.dtype != torch.float32 or tuple(scale_b.shape) != shape:
-        raise ValueError(f"scale_b must be fp32 {list(shape)}")
+        out, ldc = _rows_of_16_bytes(a, T, N, out_dtype, stream)
+    else:
+        ct = _DTYPE_CODE.get(out.dtype)
+        if ct is None or tuple(out.shape) != (T, N):
+            raise ValueError("out must be [T, N] bf16, fp16 or fp32")
+        ldc = _row_major_ld(out, "out", N)
     epi = EPILOGUES[epilogue]
-    if epi and (bias is None or bias.dtype != torch.bfloat16 or tuple(bias.shape) != (G, N) or not bias.is_contiguous()):
+    if not epi:
+        bias = None
+    elif bias is None or bias.dtype != torch.bfloat16 or tuple(bias.shape) != (G, N) or not bias.is_contiguous():
         raise ValueError("this epilogue needs a contiguous bf16 bias [G, N]")
-    _on_one_gpu("a scale_a b scale_b counts out bias", a, scale_a, b, scale_b, counts, out, bias if epi else None)
+    _on_one_gpu("a scale_a b scale_b counts out bias", a, scale_a, b, scale_b, counts, out, bias)
     if G == 0:
         return out
+    expert = b.stride(0)
     lb, ldb = _fp8_matrix(b[0], "b")
-    per = (K if lb == ROW_MAJOR else N) * ldb
-    oa = Fp8Operand(_ptr(a), lda, _ptr(scale_a), sa, sak, _FP8_CODE[a.dtype], la, 1)
-    ob = Fp8Operand(_ptr(b), ldb, _ptr(scale_b), scale_b.stride(2), scale_b.stride(1), _FP8_CODE[b.dtype], lb, FP8_BLOCK)
-    _check(load().tg_moe_gemm_scaled(ctypes.byref(oa), T, K, ctypes.byref(ob), b.stride(0) if G > 1 else per,
-                                  scale_b.stride(0), G, N, _ptr(out), _DTYPE_CODE[out.dtype], ldc, counts.data_ptr(), epi,
-                                  _ptr(bias) if epi else None, _stream_handle(stream)))
+    if G == 1:
+        expert = (K if lb == ROW_MAJOR else N) * ldb
+    sg, sbk, sb = scale_b.stride()
+    sa, sak = scale_a.stride()
+    oa = Fp8Operand(a.data_ptr(), lda, scale_a.data_ptr(), sa, sak, ta, la, 1)
+    ob = Fp8Operand(b.data_ptr(), ldb, scale_b.data_ptr(), sb, sbk, tb, lb, 128)
+    status = load().tg_moe_gemm_scaled(oa, T, K, ob, expert, sg, G, N, out.data_ptr(), ct, ldc, counts.data_ptr(), epi,
+                                       bias.data_ptr() if epi else None, _stream_handle(stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -540,29 +581,36 @@ class Routing(NamedTuple):
     renormalize: bool
 
 
+def _logits(logits: torch.Tensor) -> tuple[int, int, int, int]:
+    """(type code, T, G, ld) of a row-major [T, G] matrix of logits."""
+    dt = _DTYPE_CODE.get(logits.dtype)
+    if dt is None:
+        raise TypeError("logits must be bf16, fp16 or fp32")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be 2-D, got shape {tuple(logits.shape)}")
+    T, G = logits.shape
+    return dt, T, G, _row_major_ld(logits, "logits", G)
+
+
 def moe_router(logits: torch.Tensor, top_k: int, *, renormalize: bool = False, stream=None) -> Routing:
     """Top-k experts of each token, their softmax weights, per-expert counts and balance loss (tg_moe_router).
 
     ``logits`` is row-major [T, G] bf16, fp16 or fp32; -infinity forbids an expert, a row of it is padding.
     ``counts`` is what moe_gemm_device and moe_gemm_fp8 read; the loss is G * sum(f * P), 1 when all is even.
     """
-    if logits.dtype not in _DTYPE_CODE:
-        raise TypeError("logits must be bf16, fp16 or fp32")
-    layout, ld = _matrix(logits, "logits")
-    if layout != ROW_MAJOR:
-        raise ValueError("logits must be row-major")
-    T, G = logits.shape
+    dt, T, G, ld = _logits(logits)
     if not isinstance(top_k, int) or top_k < 1:
         raise ValueError("top_k must be a positive integer")
     _on_one_gpu("logits", logits)
-
-    def new(shape, dtype):
-        return _empty(shape, dtype, logits.device, stream)
-
-    r = Routing(new((T, top_k), torch.int32), new((T, top_k), torch.float32), new((G,), torch.int32),
-                new((), torch.float32), new((G,), torch.float32), bool(renormalize))
-    _check(load().tg_moe_router(_ptr(logits), _DTYPE_CODE[logits.dtype], ld, T, G, top_k, int(renormalize), _ptr(r.experts),
-                                _ptr(r.weights), _ptr(r.counts), _ptr(r.loss), _ptr(r.slope), _stream_handle(stream)))
+    shape = (T, top_k)
+    r = Routing(_empty(logits, shape, torch.int32, stream), _empty(logits, shape, torch.float32, stream),
+                _empty(logits, G, torch.int32, stream), _empty(logits, (), torch.float32, stream),
+                _empty(logits, G, torch.float32, stream), bool(renormalize))
+    status = load().tg_moe_router(logits.data_ptr(), dt, ld, T, G, top_k, int(renormalize), r.experts.data_ptr(),
+                                  r.weights.data_ptr(), r.counts.data_ptr(), r.loss.data_ptr(), r.slope.data_ptr(),
+                                  _stream_handle(stream))
+    if status:
+        _check(status)
     return r
 
 
@@ -571,34 +619,31 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
                         stream=None) -> torch.Tensor:
     """The gradient of ``logits`` from those of routing.weights (fp32 [T, k]) and routing.loss (fp32, one
     element, on the GPU); None is zero (tg_moe_router_backward).  ``out`` has the logits' type."""
-    if logits.dtype not in _DTYPE_CODE:
-        raise TypeError("logits must be bf16, fp16 or fp32")
-    layout, ld = _matrix(logits, "logits")
-    if layout != ROW_MAJOR:
-        raise ValueError("logits must be row-major")
-    T, G = logits.shape
+    dt, T, G, ld = _logits(logits)
     k = routing.experts.shape[1]
-    for name, t, dt, shape in (("routing.experts", routing.experts, torch.int32, (T, k)),
-                               ("routing.weights", routing.weights, torch.float32, (T, k)),
-                               ("routing.slope", routing.slope, torch.float32, (G,)),
-                               ("d_weights", d_weights, torch.float32, (T, k))):
-        if t is not None and (t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)}")
+    for name, t, want, shape in (("routing.experts", routing.experts, torch.int32, (T, k)),
+                                 ("routing.weights", routing.weights, torch.float32, (T, k)),
+                                 ("routing.slope", routing.slope, torch.float32, (G,)),
+                                 ("d_weights", d_weights, torch.float32, (T, k))):
+        if t is not None and (t.dtype != want or t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {want} tensor {list(shape)}")
     if d_loss is not None and (d_loss.dtype != torch.float32 or d_loss.numel() != 1):
         raise ValueError("d_loss must be an fp32 tensor of one element")
     if out is None:
-        out = _empty((T, G), logits.dtype, logits.device, stream)
-    if out.dtype != logits.dtype or tuple(out.shape) != (T, G):
-        raise ValueError("out must be [T, G] of the logits' type")
-    lo, ldd = _matrix(out, "out")
-    if lo != ROW_MAJOR:
-        raise ValueError("out must be row-major")
+        out, ldd = _empty(logits, (T, G), logits.dtype, stream), max(G, 1)
+    else:
+        if out.dtype != logits.dtype or out.shape != logits.shape:
+            raise ValueError("out must be [T, G] of the logits' type")
+        ldd = _row_major_ld(out, "out", G)
     _on_one_gpu("logits routing.experts routing.weights routing.slope d_weights d_loss out", logits, routing.experts,
                 routing.weights, routing.slope, d_weights, d_loss, out)
-    _check(load().tg_moe_router_backward(_ptr(logits), _DTYPE_CODE[logits.dtype], ld, T, G, k, int(routing.renormalize),
-                                         _ptr(routing.experts), _ptr(routing.weights), _ptr(routing.slope),
-                                         _ptr(d_weights) or None, _ptr(d_loss) or None, _ptr(out), ldd,
-                                         _stream_handle(stream)))
+    status = load().tg_moe_router_backward(logits.data_ptr(), dt, ld, T, G, k, int(routing.renormalize),
+                                           routing.experts.data_ptr(), routing.weights.data_ptr(), routing.slope.data_ptr(),
+                                           None if d_weights is None else d_weights.data_ptr(),
+                                           None if d_loss is None else d_loss.data_ptr(), out.data_ptr(), ldd,
+                                           _stream_handle(stream))
+    if status:
+        _check(status)
     return out
 
 
