@@ -13,7 +13,12 @@
  * pre-training"): one problem per expert, ragged M, one persistent launch.
  * Around these sit a broadcast form for repeated A rows, an MoE form whose
  * token counts stay in device memory, and an RMS-normalised form (the
- * normalisation applied as a per-row factor in the epilogue).
+ * normalisation applied as a per-row factor in the epilogue).  For expert layers
+ * in 8-bit floating point there are the products of e4m3 / e5m2 operands with a
+ * scale for each block of 128 (tg_gemm_scaled, tg_moe_gemm_scaled), their
+ * quantiser (tg_quantize_blocks) and the gate with its balance loss
+ * (tg_moe_router, tg_moe_router_backward); the pages have no counterpart for
+ * these.
  *
  * Where it runs.  One persistent, warp-specialised CUDA kernel on the
  * current device: a TMA producer warp fills a shared-memory ring guarded by
@@ -475,7 +480,7 @@ tg_status tg_device_status(tg_stream_t stream);
 tg_status tg_set_wait_budget_ms(uint32_t ms);
 
 /*
- * Test hooks for the failure path.  The next launch made by this thread has
+ * Test hooks for the failure path.  The next GEMM launch made by this thread has
  * the TMA producer of CTA `block` (blockIdx.x; 0 for tg_debug_withhold_stage)
  * withhold the arrival and the loads for the k-block with index `k_block` of
  * its first work item (a k-block of a tile, counted from the tile's first), so
@@ -501,7 +506,8 @@ tg_status tg_debug_withhold_stage_in(int64_t k_block, int32_t block);
  *   cta_records[4 b .. 4 b + 3] for block b < cta_capacity:
  *       {kernel entry, set-up done, teardown start, exit}.
  * Capacities may be 0 to skip a buffer.  Grouped calls with several layout
- * classes trace only their first launch.
+ * classes trace only their first launch.  The 8-bit products record no trace and
+ * leave an armed one to the next GEMM that does.
  */
 tg_status tg_debug_trace(uint64_t *tile_records, int64_t tile_capacity,
                          uint64_t *cta_records, int64_t cta_capacity);
