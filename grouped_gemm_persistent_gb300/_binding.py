@@ -144,7 +144,7 @@ def _check(status: int) -> None:
 def _stream_handle(stream) -> int:
     if stream is None:
         if _raw_stream is not None:      # the handle alone, without the Stream object around it
-            return _raw_stream(torch._C._cuda_getDevice())
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -346,8 +346,8 @@ def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tenso
     on another stream is not handed out while that stream still uses it."""
     if stream is not None and isinstance(stream, torch.cuda.Stream):
         with torch.cuda.stream(stream):
-            return like.new_empty(shape, dtype=dtype)
-    return like.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=like.device)
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _rows_of_16_bytes(like: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, stream) -> tuple[torch.Tensor, int]:
@@ -621,12 +621,16 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
     element, on the GPU); None is zero (tg_moe_router_backward).  ``out`` has the logits' type."""
     dt, T, G, ld = _logits(logits)
     k = routing.experts.shape[1]
-    for name, t, want, shape in (("routing.experts", routing.experts, torch.int32, (T, k)),
-                                 ("routing.weights", routing.weights, torch.float32, (T, k)),
-                                 ("routing.slope", routing.slope, torch.float32, (G,)),
-                                 ("d_weights", d_weights, torch.float32, (T, k))):
-        if t is not None and (t.dtype != want or t.shape != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {want} tensor {list(shape)}")
+    experts, weights, slope = routing.experts, routing.weights, routing.slope
+    if experts.dtype != torch.int32 or experts.shape[0] != T or not experts.is_contiguous():
+        raise ValueError(f"routing.experts must be a contiguous int32 tensor {[T, k]}")
+    if weights.dtype != torch.float32 or weights.shape != experts.shape or not weights.is_contiguous():
+        raise ValueError(f"routing.weights must be a contiguous fp32 tensor {[T, k]}")
+    if slope.dtype != torch.float32 or tuple(slope.shape) != (G,) or not slope.is_contiguous():
+        raise ValueError(f"routing.slope must be a contiguous fp32 tensor {[G]}")
+    if d_weights is not None and (d_weights.dtype != torch.float32 or d_weights.shape != experts.shape
+                                  or not d_weights.is_contiguous()):
+        raise ValueError(f"d_weights must be a contiguous fp32 tensor {[T, k]}")
     if d_loss is not None and (d_loss.dtype != torch.float32 or d_loss.numel() != 1):
         raise ValueError("d_loss must be an fp32 tensor of one element")
     if out is None:
@@ -635,10 +639,10 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
         if out.dtype != logits.dtype or out.shape != logits.shape:
             raise ValueError("out must be [T, G] of the logits' type")
         ldd = _row_major_ld(out, "out", G)
-    _on_one_gpu("logits routing.experts routing.weights routing.slope d_weights d_loss out", logits, routing.experts,
-                routing.weights, routing.slope, d_weights, d_loss, out)
+    _on_one_gpu("logits routing.experts routing.weights routing.slope d_weights d_loss out", logits, experts,
+                weights, slope, d_weights, d_loss, out)
     status = load().tg_moe_router_backward(logits.data_ptr(), dt, ld, T, G, k, int(routing.renormalize),
-                                           routing.experts.data_ptr(), routing.weights.data_ptr(), routing.slope.data_ptr(),
+                                           experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
                                            None if d_weights is None else d_weights.data_ptr(),
                                            None if d_loss is None else d_loss.data_ptr(), out.data_ptr(), ldd,
                                            _stream_handle(stream))
