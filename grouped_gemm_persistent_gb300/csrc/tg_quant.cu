@@ -14,8 +14,9 @@
 // 16-byte loads), reduces the magnitudes in the wanted direction as integers (the bits of
 // non-negative floats order like the values), and writes bytes.  Tiles are 128 x 128, and
 // 32 x 512 for blocks along a row, which need no more than a row: 1 KiB of a bf16 row at a
-// time instead of 256 bytes. 65536 x 4096 bf16 to e4m3: 135 us,
-// 6.0 TB/s, with five blocks an SM (three, at 72 registers: 151 us; 128 x 128 tiles: 170 us).
+// time instead of 256 bytes.  65536 x 4096 bf16 to e4m3: 115 us,
+// 7.1 TB/s (128 x 128 tiles, three blocks an SM: 170 us; 32 x 512: 151; five blocks an SM: 135;
+// straight code for inner tiles and a thread a scale instead of a warp a row of them: 115).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -154,8 +155,8 @@ __global__ void __launch_bounds__(QTHREADS, E::BYTES == 4 ? 2 : MODE == BLOCK_CO
     constexpr int TOP_EXP = E5M2 ? 15 : 8;
     using Tile = QTile<MODE>;
     constexpr int TX = Tile::TX, TY = Tile::TY;
-    __shared__ uint32_t s_mag[QTHREADS / 32][QT];      // column mode: per warp; square: a word of each
-    __shared__ float s_scale[QT], s_inv[QT];
+    __shared__ uint32_t s_mag[QTHREADS / 32][QT];      // column mode: per warp; square: a word of each; row: the first
+    __shared__ float s_inv[QT];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t tile = blockIdx.x;
@@ -164,25 +165,33 @@ __global__ void __launch_bounds__(QTHREADS, E::BYTES == 4 ? 2 : MODE == BLOCK_CO
     const int64_t row0 = mb * Tile::ROWS, col0 = kb * Tile::COLS + tx * 8;
     const int cols = static_cast<int>(p.K - col0 < 8 ? (p.K > col0 ? p.K - col0 : 0) : 8);
 
+    // a tile inside X (and aligned) takes straight code: this kernel is as near to the issue limit as
+    // to the memory's
+    const bool inside = row0 + Tile::ROWS <= p.M && (kb + 1) * Tile::COLS <= p.K;
     E v[QROWS];
+    const uint8_t* src = p.x + (row0 + ty) * p.ldx_bytes + col0 * E::BYTES;
+    const int64_t src_step = p.ldx_bytes * TY;
+    if (inside && p.vec_in) {
 #pragma unroll
-    for (int i = 0; i < QROWS; ++i) {
-        const int64_t row = row0 + ty + TY * i;
-        const uint8_t* src = p.x + row * p.ldx_bytes + col0 * E::BYTES;
-        v[i].zero();
-        if (row < p.M) {
-            if (cols == 8 && p.vec_in) {
-                v[i].load(src);
-            } else {
+        for (int i = 0; i < QROWS; ++i) v[i].load(src + i * src_step);
+    } else {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (c < cols) v[i].set(c, src + c * E::BYTES);
+        for (int i = 0; i < QROWS; ++i) {
+            v[i].zero();
+            if (row0 + ty + TY * i < p.M) {
+                if (cols == 8 && p.vec_in) {
+                    v[i].load(src + i * src_step);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < cols) v[i].set(c, src + i * src_step + c * E::BYTES);
+                }
             }
         }
     }
 
     if constexpr (MODE == BLOCK_ROW) {
-        // 16 lanes hold a scale block; s_scale is [block of the tile][row]
+        // 16 lanes hold a scale block; s_mag and s_inv are [block of the tile][row]
         constexpr int ROWS = Tile::ROWS, BLOCKS = Tile::COLS / QT;
         static_assert(ROWS * BLOCKS == QT, "a scale a thread of the first 128");
 #pragma unroll
@@ -190,15 +199,18 @@ __global__ void __launch_bounds__(QTHREADS, E::BYTES == 4 ? 2 : MODE == BLOCK_CO
             uint32_t m = v[i].max_mag();
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const int at = tx / 16 * ROWS + ty + TY * i;
-            if (tx % 16 == 0) block_scale(E::widen(m), TOP_EXP, s_scale[at], s_inv[at]);
+            if (tx % 16 == 0) s_mag[0][tx / 16 * ROWS + ty + TY * i] = m;
         }
         __syncthreads();
         // scales lie block column after block column, a tile's rows side by side
         if (threadIdx.x < QT) {
+            float s, f;
+            block_scale(E::widen(s_mag[0][threadIdx.x]), TOP_EXP, s, f);
+            s_inv[threadIdx.x] = f;
             const int64_t b = kb * BLOCKS + threadIdx.x / ROWS, row = row0 + threadIdx.x % ROWS;
-            if (b * QT < p.K && row < p.M) p.scale[b * p.scale_ld + row] = s_scale[threadIdx.x];
+            if (b * QT < p.K && row < p.M) p.scale[b * p.scale_ld + row] = s;
         }
+        __syncthreads();
     } else if constexpr (MODE == BLOCK_COLUMN) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -215,7 +227,6 @@ __global__ void __launch_bounds__(QTHREADS, E::BYTES == 4 ? 2 : MODE == BLOCK_CO
             for (int w = 0; w < QTHREADS / 32; ++w) m = max(m, s_mag[w][threadIdx.x]);
             float s, inv;
             block_scale(E::widen(m), TOP_EXP, s, inv);
-            s_scale[threadIdx.x] = s;
             s_inv[threadIdx.x] = inv;
             const int64_t col = kb * QT + threadIdx.x;
             if (col < p.K) p.scale[mb * p.scale_ld + col] = s;
@@ -230,8 +241,10 @@ __global__ void __launch_bounds__(QTHREADS, E::BYTES == 4 ? 2 : MODE == BLOCK_CO
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int w = 1; w < QTHREADS / 32; ++w) m = max(m, s_mag[w][0]);
-            block_scale(E::widen(m), TOP_EXP, s_scale[0], s_inv[0]);
-            p.scale[mb * p.scale_ld + kb] = s_scale[0];
+            float s, f;
+            block_scale(E::widen(m), TOP_EXP, s, f);
+            s_inv[0] = f;
+            p.scale[mb * p.scale_ld + kb] = s;
         }
         __syncthreads();
     }
@@ -241,9 +254,8 @@ __global__ void __launch_bounds__(QTHREADS, E::BYTES == 4 ? 2 : MODE == BLOCK_CO
 #pragma unroll
         for (int c = 0; c < 8; ++c) inv[c] = s_inv[tx * 8 + c];
     }
-#pragma unroll
-    for (int i = 0; i < QROWS; ++i) {
-        const int64_t row = row0 + ty + TY * i;
+    // the eight bytes of row i
+    auto bytes = [&](int i) {
         uint32_t w[2];
         if constexpr (MODE != BLOCK_COLUMN) {
             const float f = s_inv[MODE == BLOCK_ROW ? tx / 16 * Tile::ROWS + ty + TY * i : 0];
@@ -263,14 +275,24 @@ __global__ void __launch_bounds__(QTHREADS, E::BYTES == 4 ? 2 : MODE == BLOCK_CO
                     if (inv[4 * h + c] == 0.0f) w[h] &= ~(0xffu << (8 * c));
             }
         }
-        if (row < p.M) {
-            uint8_t* dst = p.q + row * p.ldq + col0;
+        return make_uint2(w[0], w[1]);
+    };
+    uint8_t* dst = p.q + (row0 + ty) * p.ldq + col0;
+    const int64_t dst_step = p.ldq * TY;
+    if (inside && p.vec_out) {
+#pragma unroll
+        for (int i = 0; i < QROWS; ++i) *reinterpret_cast<uint2*>(dst + i * dst_step) = bytes(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < QROWS; ++i) {
+            const uint2 w = bytes(i);
+            if (row0 + ty + TY * i >= p.M) continue;
             if (cols == 8 && p.vec_out) {
-                *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(dst + i * dst_step) = w;
             } else {
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    if (c < cols) dst[c] = static_cast<uint8_t>(w[c >> 2] >> ((c & 3) * 8));
+                    if (c < cols) dst[i * dst_step + c] = static_cast<uint8_t>((c < 4 ? w.x : w.y) >> ((c & 3) * 8));
             }
         }
     }
