@@ -59,14 +59,17 @@ struct Logits {
     static constexpr uint32_t NEG_INF = DT == TG_F32 ? 0xff800000u : DT == TG_F16 ? 0xfc00fc00u : 0xff80ff80u;
     uint32_t w[WORDS];
 
+    __device__ __forceinline__ void load_whole(const uint8_t* p) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4) {
+            const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+            w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
+        }
+    }
     // n of the V are inside the row (the others become -infinity); vec: 16-byte loads allowed
     __device__ __forceinline__ void load(const uint8_t* p, int n, bool vec) {
         if (n == V && vec) {
-#pragma unroll
-            for (int i = 0; i < WORDS; i += 4) {
-                const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
-                w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
-            }
+            load_whole(p);
             return;
         }
 #pragma unroll
@@ -130,6 +133,19 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+
+template <int L>
+__device__ __forceinline__ float group_max_nan(float v) {
+    if constexpr (L == 32) {
+        float r;
+        asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+        return r;
+    } else {
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(FULL, v, d));
+        return v;
+    }
 }
 
 // e^x, zero below fp32's normal values: for probabilities that are summed.
@@ -220,8 +236,11 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const
     int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
     const int64_t warp_first = t - lane / L;
     Logits<DT, V> next;
+    const bool whole = a.vec && a.G == SPAN;      // every lane of every row loads V logits
     auto fetch = [&](int64_t row) {
-        next.load(a.logits + row * a.ld_bytes + first * Logits<DT, V>::ESIZE, row < a.T ? n : 0, a.vec != 0);
+        const uint8_t* at = a.logits + row * a.ld_bytes + first * Logits<DT, V>::ESIZE;
+        if (whole && row - lane / L + ROWS <= a.T) next.load_whole(at);
+        else next.load(at, row < a.T ? n : 0, a.vec != 0);
     };
     fetch(t);
     float sum[V];
@@ -234,14 +253,14 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_kernel(const
         float m = x.value(0);                     // the row's largest logit, NaN if it has one
 #pragma unroll
         for (int j = 1; j < V; ++j) m = max_nan(m, x.value(j));
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(FULL, m, d));
+        m = group_max_nan<L>(m);
         const bool any = m != __int_as_float(0xff800000);
+        m = any ? m : 0.0f;                       // (e^(-infinity - 0) = 0)
         float p[V];
         float total = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            p[j] = any ? exp_flush(x.value(j) - m) : 0.0f;
+            p[j] = exp_flush(x.value(j) - m);
             total += p[j];
         }
         total = group_sum<L>(total);
@@ -465,14 +484,14 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_backward_ker
         float m = x.value(0);
 #pragma unroll
         for (int j = 1; j < V; ++j) m = max_nan(m, x.value(j));
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(FULL, m, d));
+        m = group_max_nan<L>(m);
         const bool any = m != __int_as_float(0xff800000);
+        m = any ? m : 0.0f;                       // (e^(-infinity - 0) = 0)
         float p[V];
         float total = 0.0f, pu = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            p[j] = any ? exp_flush(x.value(j) - m) : 0.0f;
+            p[j] = exp_flush(x.value(j) - m);
             total += p[j];
             pu = fmaf(p[j], u[j], pu);
         }
