@@ -8,22 +8,24 @@
 // stage is one scale block (128 bytes of K per row, four MMAs of K = 32).
 //
 //   warp 0       TMA producer: A and B k-blocks into a STAGES-deep ring.
-//   warp 1       MMA issuer: per k-block, four MMAs into one of two TMEM buffers, then a
-//                commit that frees the ring stage and one that hands the buffer over.
-//                It also allocates and frees tensor memory.
-//   warps 2, 3   scale loaders: A's and B's scales of the k-blocks ahead, by cp.async into a
-//                ring of their own.  (Loaded by the accumulating warps into registers, four
-//                k-blocks ahead, they made every tcgen05.wait::ld wait for global loads:
-//                8192^3 took 1340 us.)
+//   warps 1, 2   MMA issuers, one for each of two TMEM buffers (even and odd k-blocks): four
+//                MMAs, then a commit that frees the ring stage and one that hands the
+//                buffer over.  Warp 1 also allocates and frees tensor memory.
+//   warp 3       scale loader: the scales of the k-blocks ahead, by cp.async into a ring of
+//                their own.  (Loaded by the accumulating warps into registers, four k-blocks
+//                ahead, they made every tcgen05.wait::ld wait for global loads: 8192^3 took
+//                1340 us.)
 //   warps 4-11   accumulation and epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and
 //                half the tile's columns: acc += scale * partial while the MMAs of the next
 //                k-block run; after the last k-block bias, GELU, rounding and the store.
 //
 // 256 x 256 tiles of a CTA pair: per k-block and SM the tensor cores need 512 cycles
-// (128 x 256 x 128 at 8192 MAC/cycle), reading back 128 x 256 fp32 takes 256 (one column
-// of 32 lanes a cycle and quarter) and the packed fma.rn.f32x2 additions 128 issue slots a
-// quarter, so the accumulation hides behind the MMAs; 128 accumulator registers a thread
-// for eight warps need the registers of the first four (setmaxnreg).
+// (128 x 256 x 128 at 8192 MAC/cycle) and the additions 256 issue slots a quarter of the SM, but
+// a k-block takes ~700: with two buffers, its MMAs wait for the read-back of the k-block two
+// before it, and that is a chain of four tensor-memory loads (~80 cycles each, 130 before the
+// first) and a barrier on either side.  8192^3, bf16 out: 398 us, 2760 TFLOP/s; the MMAs and
+// barriers without the read-back 296 us.  128 accumulator registers a thread for eight warps
+// need the registers of the first four (setmaxnreg).
 //
 // Waits, aborts and draining are those of tg_kernel.cuh.
 #pragma once
@@ -532,8 +534,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     int total_tiles = static_cast<int>(p.total_tiles);
     if constexpr (Cfg::MOE) total_tiles = *reinterpret_cast<volatile int32_t*>(smem + Cfg::OFF_MOE_TOTAL);
 
-    // Registers: 384 x 168 at launch = 64512 = 128 x 72 + 256 x 216.  Each split stands at
-    // the head of its own branch: after a common one the compiler kept to the smaller count.
     // The last, partial wave of a pair launch: its R = tiles mod units tiles, when two of them fit a
     // unit each, run as 2R half tiles (128 rows of a pair, 64 a CTA), items whole, whole + 1, ..
     constexpr bool MAY_HALVE = CG == 2;
@@ -541,8 +541,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     const int halved = 2 * last_wave <= num_units ? last_wave : 0;
     const int whole = total_tiles - halved, items = total_tiles + halved;
     auto tile_of = [&](int t) { return MAY_HALVE && t >= whole ? whole + (t - whole) % halved : t; };
-    // tile_coord in 32 bits (the host refuses more than 2^30 tiles): with 64-bit divisions this took
-    // each role 800 to 1900 cycles a tile.
+    // tile_coord in 32 bits (the host refuses more than 2^30 tiles): with 64-bit divisions it took the
+    // accumulating warps 1300 to 1900 cycles a tile, so ~800.
     auto coord_of_item = [&](int t, int g) {
         int local = tile_of(t), tiles_m = p.dense.tiles_m, rows_left = p.dense.M;
         TileCoord c;
@@ -573,19 +573,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
     };
     const Problem& pr = p.dense;
     // Warp-uniform bounded wait: every lane polls once; if the phase is not yet complete, lane 0
-    // runs the bounded wait and tells the others how it ended.
+    // runs the bounded wait and tells the others how it ended.  (Polling more than once before
+    // that, or by lane 0 alone, was slower: 730 and 795 us at 8192^3 when this form took 470.)
     auto warp_wait = [&](uint32_t bar, uint32_t par, uint32_t role, int tile, uint32_t st) -> bool {
         if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, par))) return true;
         uint32_t ok = 1;
         if (lane == 0) ok = wait_bounded<CG, false>(bar, par, p, abort_addr, role, tile, st) ? 1u : 0u;
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
-    // The same for warps that run ahead: lane 0 is suspended between its polls.
-    auto warp_wait_sleep = [&](uint32_t bar, uint32_t par, uint32_t role, int tile, uint32_t st) -> bool {
-        uint32_t ok = 1;
-        if (lane == 0) ok = wait_bounded<CG, true>(bar, par, p, abort_addr, role, tile, st) ? 1u : 0u;
-        return __shfl_sync(0xffffffffu, ok, 0) != 0;
-    };
+    // Registers: 384 x 168 at launch = 64512 = 128 x 72 + 256 x 216.  Each split stands at the head of
+    // its own branch: after a common one the compiler kept to the smaller count.
     if (warp < F8_EPI_WARP0) {
     f8::regs_dec<72>();
     if (warp == 0) {

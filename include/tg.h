@@ -322,7 +322,9 @@ typedef struct tg_scaled_operand {
  *
  * The products of one block of 128 k are summed by the tensor cores in fp32; the
  * blocks' sums are scaled and added in fp32 registers, in an order fixed by the sizes
- * (two identical calls write identical C), and the epilogue rounds once.  C, epi and
+ * (two identical calls write identical C), and the epilogue rounds once.  A block's two
+ * scales are multiplied first (when B has one for 128 columns): their product should be
+ * a normal fp32 number.  C, epi and
  * bias (bf16[N]) are as in tg_gemm, except that C needs only the alignment of its
  * elements.  K == 0 gives epilogue(0); M == 0 or N == 0 is a no-op.
  *

@@ -196,6 +196,25 @@ def test_router(T, G, k, renorm, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G,k", [(60, 4), (256, 8), (256, 32), (300, 5), (1000, 7)])
+def test_router_logits_that_differ_in_their_last_bits(G, k):
+    """fp32 logits a few steps apart: the choice goes by value to the last bit, at the last place too."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(64, G, generator=g, device="cuda")
+    for t in range(64):
+        n = min(G, (1, 2, k, k + 1, k + 2, G)[t % 6])              # so many near the top
+        steps = torch.randperm(4 * n, generator=g, device="cuda")[:n]
+        where = torch.randperm(G, generator=g, device="cuda")[:n]
+        x[t, where] = (torch.full((n,), 8.0 if t % 2 else -0.001, device="cuda").view(torch.int32) + steps.int()).view(torch.float32)
+        if t % 2 == 0:
+            x[t] = torch.where(x[t] > -0.002, x[t], x[t] - 10.0)   # the near ones lead there, too
+    x[5] = torch.where(torch.arange(G, device="cuda") % 2 == 0, 1.0, 1.0 + 2.0 ** -23)
+    r = tg.moe_router(x, k, renormalize=True)
+    tg.device_status()
+    check_forward(x, k, True, r)
+
+
+@pytest.mark.gpu
 def test_router_no_rows_and_no_live_rows():
     for x in (torch.zeros(0, 16, device="cuda"), torch.full((5, 16), -INF, device="cuda")):
         r = tg.moe_router(x, 3, renormalize=True)
