@@ -360,13 +360,10 @@ def _rows_of_16_bytes(like: torch.Tensor, rows: int, cols: int, dtype: torch.dty
 
 def _on_one_gpu(names: str, *tensors) -> None:
     """The tensors (None is left out) are on one CUDA device, the current one."""
-    first = tensors[0].get_device()
-    same = first >= 0 and first == torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (not same or t.get_device() != first):
-            for name, u in zip(names.split(), tensors):
-                if u is not None and (u.get_device() < 0 or u.get_device() != torch.cuda.current_device()):
-                    raise ValueError(f"{name} must be on the current CUDA device, got {u.device}")
+    current = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    for i, t in enumerate(tensors):
+        if t is not None and (t.get_device() != current or current < 0):
+            raise ValueError(f"{names.split()[i]} must be on the current CUDA device, got {t.device}")
 
 
 def _row_major_ld(t: torch.Tensor, name: str, cols: int) -> int:
@@ -427,13 +424,9 @@ def quantize_fp8(x: torch.Tensor, block: tuple[int, int] = (1, 128), q: torch.Te
     return q, scale
 
 
-def _fp8_matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
-    """(layout, ld) of a 2-D 8-bit tensor view.  A single row or column is never stepped past: its leading
-    dimension is reported as its extent rounded up to 16 elements."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    r, c = t.shape
-    s0, s1 = t.stride()
+def _fp8_layout(r: int, c: int, s0: int, s1: int, name: str) -> tuple[int, int]:
+    """(layout, ld) of an r x c matrix with strides (s0, s1).  A single row or column is never stepped past: its
+    leading dimension is reported as its extent rounded up to 16 elements."""
     if s1 == 1 and (c > 1 or r <= 1):
         return ROW_MAJOR, (s0 if r > 1 else -(-max(c, 1) // 16) * 16)
     if s0 == 1:
@@ -442,7 +435,14 @@ def _fp8_matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
         return ROW_MAJOR, s0
     if r == 1:
         return COL_MAJOR, s1
-    raise ValueError(f"{name}: neither rows nor columns are contiguous (strides {t.stride()})")
+    raise ValueError(f"{name}: neither rows nor columns are contiguous (strides {(s0, s1)})")
+
+
+def _fp8_matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """(layout, ld) of a 2-D 8-bit tensor view."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    return _fp8_layout(*t.shape, *t.stride(), name)
 
 
 def _bad_scale(s: torch.Tensor, name: str, rows: int, kb: int):
@@ -556,8 +556,8 @@ def moe_gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_
     _on_one_gpu("a scale_a b scale_b counts out bias", a, scale_a, b, scale_b, counts, out, bias)
     if G == 0:
         return out
-    expert = b.stride(0)
-    lb, ldb = _fp8_matrix(b[0], "b")
+    expert, s0, s1 = b.stride()
+    lb, ldb = _fp8_layout(K, N, s0, s1, "b")
     if G == 1:
         expert = (K if lb == ROW_MAJOR else N) * ldb
     sg, sbk, sb = scale_b.stride()
