@@ -76,7 +76,7 @@ struct Fp8Config {
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int C_BYTES = F8_EPI_WARPS * F8_C_STAGE;
     static constexpr int SB_COUNT = SB_COL ? BN : BN / 128;      // B scales of a tile and k-block
-    static constexpr int SLOTS = SB_COL ? 2 : 4;                 // groups of scales in flight
+    static constexpr int SLOTS = 4;                            // groups of scales in flight
     static constexpr int SLOT_BYTES = (BM + SB_COUNT) * F8_GROUP * 4;
     static constexpr int SCALE_BYTES = SLOTS * SLOT_BYTES;
     static constexpr int TABLE_BYTES = MOE ? 8 * (MOE_MAX_G + 1) : 0;
@@ -338,6 +338,65 @@ __device__ __forceinline__ void store16(const float* v, uint32_t stage, const St
             if (cols > 3) c[3] = static_cast<uint16_t>(u >> 16);
         }
     }
+}
+
+// Scales first .. first + COUNT of `blocks` k-blocks into lines of COUNT floats; those past `limit` are zero.
+// wide: four of a line are one aligned 16-byte word, a quarter of the copies (the weight gradient of 1536 x
+// 4096 over 5000 rows 56.0 us with them, 57.0 without).
+__device__ __forceinline__ bool lines_are_wide(const float* s, int64_t mn, int64_t k) {
+    return mn == 1 && k % 4 == 0 && reinterpret_cast<uintptr_t>(s) % 16 == 0;
+}
+template <int COUNT>
+__device__ __forceinline__ void scale_lines(uint32_t dst, const float* s, int first, int limit, int shift, int64_t mn,
+                                            int64_t k, int kb, int blocks, bool wide, int lane) {
+    if (wide) {
+#pragma unroll
+        for (int j = 0; j < COUNT; j += 128) {
+            const int at = first + j + lane * 4, left = min(max(limit - at, 0), 4);
+            const float* src = left > 0 ? s + at + kb * k : s;
+            for (int i = 0; i < blocks; ++i)
+                ptx::cp_async_16_part(dst + (i * COUNT + j + lane * 4) * 4, left > 0 ? src + i * k : s, left * 4);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < COUNT; j += 32) {
+            const int64_t at = first + j + lane;
+            const bool in = at < limit;
+            const float* src = in ? s + (at >> shift) * mn + kb * k : s;
+            for (int i = 0; i < blocks; ++i) cp_async_4(dst + (i * COUNT + j + lane) * 4, in ? src + i * k : s, in);
+        }
+    }
+}
+
+// From the lanes' rows and columns of tmem_ld_16x256b to a row a lane, 16 columns at a time through this
+// warp's staging rows of 64 bytes: v[16 c + 8 (rows / 16) + 4 (columns / 8 % 2) + e] holds row
+// lane / 4 + 8 (e / 2) of its 16 and column 2 (lane % 4) + e % 2 of its 8; v[n] is column n after.
+template <int COLS>
+__device__ __forceinline__ void turn(float* v, uint32_t stage, int lane) {
+    // a row's four 16-byte units are swapped by its bits 1 and 2, crossed, so that neither the eight
+    // bytes a lane writes (rows lane / 4) nor the sixteen it reads (row lane) meet in a bank
+    const uint32_t w_swz = static_cast<uint32_t>(lane >> 3 & 1) * 2 + static_cast<uint32_t>(lane >> 4 & 1);
+    const uint32_t r_swz = static_cast<uint32_t>(lane >> 1 & 1) * 2 + static_cast<uint32_t>(lane >> 2 & 1);
+#pragma unroll
+    for (int c = 0; c < COLS; c += 16) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t row = static_cast<uint32_t>(lane / 4 + i % 2 * 8 + i / 4 * 16);
+            const uint32_t unit = static_cast<uint32_t>(i / 2 % 2 * 2 + lane % 4 / 2) ^ w_swz;
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};"
+                         :: "r"(stage + row * 64 + (unit << 4) + (lane & 1) * 8),
+                            "f"(v[c + i / 4 * 8 + i / 2 % 2 * 4 + i % 2 * 2]),
+                            "f"(v[c + i / 4 * 8 + i / 2 % 2 * 4 + i % 2 * 2 + 1]) : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float4 w = ptx::ld_shared_f4(stage + lane * 64 + ((static_cast<uint32_t>(u) ^ r_swz) << 4));
+            v[c + 4 * u] = w.x; v[c + 4 * u + 1] = w.y; v[c + 4 * u + 2] = w.z; v[c + 4 * u + 3] = w.w;
+        }
+    }
+    __syncwarp();
 }
 
 // COLS columns of 32 rows, all inside C, 16-byte aligned, fp32 or bf16: straight code without a branch
@@ -693,8 +752,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
         }
     } else {
         // ================================ scale loader ================================
-        // A slot: the scales of F8_GROUP k-blocks: [128 rows][k-block] of A, then of B
-        // [k-block][columns], or [block of 128 columns][k-block].
+        // A slot: the scales of F8_GROUP k-blocks: [128 rows][k-block] of A, then [block of 128
+        // columns][k-block] of B; with column scales [k-block][rows], then [k-block][columns].
+        [[maybe_unused]] const bool wide_a = x.sa_shift == 0 && f8::lines_are_wide(x.sa, x.sa_mn, x.sa_k);
+        [[maybe_unused]] const bool wide_b = f8::lines_are_wide(x.sb, x.sb_mn, x.sb_k);
         int slot = 0, g = 0;
         uint32_t phase = 0;
         bool aborted = false;
@@ -707,32 +768,28 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                     break;
                 }
                 const uint32_t dst = sS + slot * Cfg::SLOT_BYTES, dst_b = dst + BM * F8_GROUP * 4;
-#pragma unroll
-                for (int j = 0; j < BM / 32; ++j) {
-                    const int64_t row = tc.m0 + j * 32 + lane;
-                    const bool in = row < pr.M;
-                    const float* src = in ? x.sa + (row >> x.sa_shift) * x.sa_mn + kb * x.sa_k : x.sa;
-#pragma unroll
-                    for (int i = 0; i < F8_GROUP; ++i)
-                        if (kb + i < kb_end)
-                            f8::cp_async_4(dst + ((j * 32 + lane) * F8_GROUP + i) * 4, in ? src + i * x.sa_k : src, in);
-                }
                 if constexpr (Cfg::SB_COL) {
+                    const int blocks = min(F8_GROUP, kb_end - kb);
+                    f8::scale_lines<BM>(dst, x.sa, tc.m0, pr.M, x.sa_shift, x.sa_mn, x.sa_k, kb, blocks, wide_a, lane);
+                    f8::scale_lines<BN>(dst_b, x.sb, tc.n0, pr.N, 0, x.sb_mn, x.sb_k, kb, blocks, wide_b, lane);
+                } else {
 #pragma unroll
-                    for (int j = 0; j < BN / 32; ++j) {
-                        const int64_t n = tc.n0 + j * 32 + lane;
-                        const bool in = n < pr.N;
-                        const float* src = in ? x.sb + n * x.sb_mn + kb * x.sb_k : x.sb;
+                    for (int j = 0; j < BM / 32; ++j) {
+                        const int64_t row = tc.m0 + j * 32 + lane;
+                        const bool in = row < pr.M;
+                        const float* src = in ? x.sa + (row >> x.sa_shift) * x.sa_mn + kb * x.sa_k : x.sa;
 #pragma unroll
                         for (int i = 0; i < F8_GROUP; ++i)
-                            if (kb + i < kb_end) f8::cp_async_4(dst_b + (i * BN + j * 32 + lane) * 4, in ? src + i * x.sb_k : src, in);
+                            if (kb + i < kb_end)
+                                f8::cp_async_4(dst + ((j * 32 + lane) * F8_GROUP + i) * 4, in ? src + i * x.sa_k : src, in);
                     }
-                } else if (lane < Cfg::SB_COUNT * F8_GROUP) {
-                    const int64_t n = tc.n0 + lane / F8_GROUP * 128;
-                    const int i = lane % F8_GROUP;
-                    const bool in = n < pr.N && kb + i < kb_end;
-                    f8::cp_async_4(dst_b + lane * 4,
-                                   in ? x.sb + (n >> 7) * x.sb_mn + (kb + i) * x.sb_k + (Cfg::MOE ? g * x.sb_g : 0) : x.sb, in);
+                    if (lane < Cfg::SB_COUNT * F8_GROUP) {
+                        const int64_t n = tc.n0 + lane / F8_GROUP * 128;
+                        const int i = lane % F8_GROUP;
+                        const bool in = n < pr.N && kb + i < kb_end;
+                        f8::cp_async_4(dst_b + lane * 4,
+                                       in ? x.sb + (n >> 7) * x.sb_mn + (kb + i) * x.sb_k + (Cfg::MOE ? g * x.sb_g : 0) : x.sb, in);
+                    }
                 }
                 f8::cp_async_arrive(sfull_bar(slot));
                 if (++slot == Cfg::SLOTS) { slot = 0; phase ^= 1u; }
@@ -764,39 +821,51 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             if constexpr (Cfg::MOE) row_limit = static_cast<int>(min(static_cast<int64_t>(tc.row_end), p.moe_rows));
             const bool active = row0 < row_limit && n0 < pr.N;
             const uint32_t tm0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + t_col;
-            const uint32_t sa_at = sS + (local_row + lane) * F8_GROUP * 4;
-            const uint32_t sb_at = sS + BM * F8_GROUP * 4 + (Cfg::SB_COL ? local_col : (local_col >> 7) * F8_GROUP) * 4;
+            const uint32_t sa_at = sS + (Cfg::SB_COL ? local_row + lane / 4 : (local_row + lane) * F8_GROUP) * 4;
+            const uint32_t sb_at = sS + BM * F8_GROUP * 4 +
+                                   (Cfg::SB_COL ? local_col + lane % 4 * 2 : (local_col >> 7) * F8_GROUP) * 4;
 
             float acc[COLS];
 #pragma unroll
             for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
-            // acc[32 C ..] += scale * partial columns [32 C, 32 C + 32).  Scalar: a warp's fused
-            // multiply-add measured 1.03 issue cycles, a packed pair of them 2.34.
-            auto add = [&](auto chunk_index, const uint32_t (&r)[32], float s, uint32_t sb) {
+            // Block scales: a lane has one row, acc[32 C ..] += scale * partial columns [32 C, 32 C + 32).
+            // Column scales: chunk C holds 64 columns of 16 rows, of which a lane has two rows and two
+            // columns of every eight, so that it needs 16 of the columns' scales (fc), which serve the
+            // next 16 rows too.  (With a row a lane every lane read all of them: 16 KB a warp and k-block
+            // out of shared memory, 1024 cycles at 128 bytes a cycle for the eight warps; 8192^3 took
+            // 744 us and takes 620.)  acc keeps 16 columns together, in the order turn() takes.
+            // Scalar: a warp's fused multiply-add measured 1.03 issue cycles, a packed pair of them 2.34.
+            auto add = [&](auto chunk_index, const uint32_t (&r)[32], const float* s, const float* fc) {
                 constexpr int C = decltype(chunk_index)::value;
                 if constexpr (Cfg::SB_COL) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 f = ptx::ld_shared_f4(sb + (C * 32 + i) * 4);
-                        acc[C * 32 + i] = fmaf(__uint_as_float(r[i]) * f.x, s, acc[C * 32 + i]);
-                        acc[C * 32 + i + 1] = fmaf(__uint_as_float(r[i + 1]) * f.y, s, acc[C * 32 + i + 1]);
-                        acc[C * 32 + i + 2] = fmaf(__uint_as_float(r[i + 2]) * f.z, s, acc[C * 32 + i + 2]);
-                        acc[C * 32 + i + 3] = fmaf(__uint_as_float(r[i + 3]) * f.w, s, acc[C * 32 + i + 3]);
+                    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float& sum = acc[(C / 2 * 4 + j / 2) * 16 + C % 2 * 8 + j % 2 * 4 + e];
+                            sum = fmaf(__uint_as_float(r[4 * j + e]) * fc[2 * j + e % 2], s[C % 2 * 2 + e / 2], sum);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[C * 32 + i] = fmaf(__uint_as_float(r[i]), s, acc[C * 32 + i]);
+                    for (int i = 0; i < 32; ++i) acc[C * 32 + i] = fmaf(__uint_as_float(r[i]), s[0], acc[C * 32 + i]);
                 }
             };
-            // This lane's scales of four k-blocks (times B's, one for all the warp's columns), from the
-            // next slot.  Read once per group, a k-block ahead: shared memory answers slowly
-            // while the tensor cores and TMA use it.
+            // Chunk C of the buffer at tm, into r
+            auto load = [&](auto chunk_index, uint32_t tm, uint32_t (&r)[32]) {
+                constexpr int C = decltype(chunk_index)::value;
+                if constexpr (Cfg::SB_COL) ptx::tmem_ld_16x256b_x8(tm + C / 2 * 64 + (static_cast<uint32_t>(C % 2 * 16) << 16), r);
+                else ptx::tmem_ld_32x32b_x32(tm + C * 32, r);
+            };
+            // Waits for the next slot.  Block scales: this lane's scales of four k-blocks (times B's, one
+            // for all the warp's columns).  Read once per group, a k-block ahead: shared memory answers
+            // slowly while the tensor cores and TMA use it.
             auto read_scales = [&](float (&f)[F8_GROUP]) -> bool {
                 if (!warp_wait(sfull_bar(slot), slot_phase, ROLE_EPILOGUE, t, 32 + slot)) return false;
-                const uint32_t off = slot * Cfg::SLOT_BYTES;
-                const float4 a = ptx::ld_shared_f4(sa_at + off);
-                f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
                 if constexpr (!Cfg::SB_COL) {
+                    const uint32_t off = slot * Cfg::SLOT_BYTES;
+                    const float4 a = ptx::ld_shared_f4(sa_at + off);
+                    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
                     const float4 b = ptx::ld_shared_f4(sb_at + off);
                     f[0] *= b.x; f[1] *= b.y; f[2] *= b.z; f[3] *= b.w;
                     __syncwarp();
@@ -813,36 +882,37 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                 float f[F8_GROUP];
                 if (kb_begin == kb_end) return true;
                 if (!read_scales(f)) return false;
-                // AHEAD: the next buffer's first columns are asked for before the last ones of this buffer
-                // are added.  Measured at 8192^3: column scales 726 us with it and 775 without; block
-                // scales 418 us without and 623 with it (their shorter additions hide less, and the
-                // registers of the load in flight cost spills).
-                constexpr bool AHEAD = Cfg::SB_COL && CHUNKS > 0;
+                // (Asking for the next buffer's first chunk ahead of the last additions cost spills in both
+                // forms: 623 us instead of 418 at 8192^3, with column scales 810 instead of 644.)
                 uint32_t r[2][32];
                 bool ready = ptx::mbar_test_wait(tfull_bar(buf), buf_phase);
                 auto open = [&]() -> bool {
                     if (!__all_sync(0xffffffffu, ready) &&
                         !warp_wait(tfull_bar(buf), buf_phase, ROLE_EPILOGUE, t, 16 + buf)) return false;
                     ptx::tc_fence_after_sync();
-                    if constexpr (CHUNKS > 0) ptx::tmem_ld_32x32b_x32(tm0 + static_cast<uint32_t>(buf * BN), r[0]);
+                    if constexpr (CHUNKS > 0) load(std::integral_constant<int, 0>{}, tm0 + static_cast<uint32_t>(buf * BN), r[0]);
                     return true;
                 };
-                // One k-block, the u-th of its group; LAST (AHEAD only): no further one follows
-                auto block = [&](auto last, int u, bool more) -> bool {
-                    constexpr bool LAST = decltype(last)::value;
+                // One k-block, the u-th of its group
+                auto block = [&](int u, bool more) -> bool {
                     const uint32_t tm = tm0 + static_cast<uint32_t>(buf * BN);
-                    [[maybe_unused]] const float s = f[0];
+                    float s[Cfg::SB_COL ? 4 : 1];
+                    [[maybe_unused]] float fc[16];
                     [[maybe_unused]] const uint32_t sb = sb_at + slot * Cfg::SLOT_BYTES + u * (BN * 4);   // SB_COL
-                    f[0] = f[1]; f[1] = f[2]; f[2] = f[3];
-                    if constexpr (!Cfg::SB_COL) {
+                    if constexpr (Cfg::SB_COL) {
+#pragma unroll
+                        for (int i = 0; i < (CHUNKS > 0 ? 4 : 0); ++i)
+                            s[i] = f8::ld_shared_f32(sa_at + slot * Cfg::SLOT_BYTES + u * (BM * 4) + i * 32);
+                    } else {
+                        s[0] = f[0];
+                        f[0] = f[1]; f[1] = f[2]; f[2] = f[3];
                         if (u == F8_GROUP - 1 && more && !read_scales(f)) return false;
                     }
-                    bool there = true;
                     f8::for_each<(CHUNKS > 0 ? CHUNKS : 1)>([&](auto ci) {
                         constexpr int C = decltype(ci)::value;
                         if constexpr (CHUNKS > 0) f8::tmem_ld_wait32(r[C & 1]);
                         if constexpr (C + 1 < CHUNKS) {
-                            ptx::tmem_ld_32x32b_x32(tm + (C + 1) * 32, r[(C + 1) & 1]);
+                            load(std::integral_constant<int, C + 1>{}, tm, r[(C + 1) & 1]);
                         } else {
                             // everything is in registers: the buffer goes back to the MMA issuer; the next
                             // one's barrier is asked early, so that the answer is there after the additions
@@ -850,9 +920,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                             f8::arrive_lane0(lead_tempty + 8u * buf, lane);
                             if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
                             ready = ptx::mbar_test_wait(tfull_bar(buf), buf_phase);
-                            if constexpr (AHEAD && !LAST) there = open();
                         }
-                        if constexpr (CHUNKS > 0) add(ci, r[C & 1], s, sb);
+                        if constexpr (Cfg::SB_COL && CHUNKS > 0 && C % 2 == 0) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 v = ptx::ld_shared_f2(sb + (C * 32 + j * 8) * 4);
+                                fc[2 * j] = v.x;
+                                fc[2 * j + 1] = v.y;
+                            }
+                        }
+                        if constexpr (CHUNKS > 0) add(ci, r[C & 1], s, fc);
                     });
                     if constexpr (Cfg::SB_COL) {
                         if (u == F8_GROUP - 1 || !more) {
@@ -863,21 +940,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
                             if (more && !read_scales(f)) return false;
                         }
                     }
-                    return there;
-                };
-                if constexpr (AHEAD) {
-                    static_assert(CHUNKS % 2 == 0, "a buffer's first columns sit in r[0], its last in r[1]");
-                    if (!open()) return false;
-#pragma unroll 1
-                    for (int kb = kb_begin; kb + 1 < kb_end; ++kb)
-                        if (!block(std::false_type{}, (kb - kb_begin) % F8_GROUP, true)) return false;
-                    return block(std::true_type{}, (kb_end - 1 - kb_begin) % F8_GROUP, false);
-                } else {
-#pragma unroll 1
-                    for (int kb = kb_begin; kb < kb_end; ++kb)
-                        if (!open() || !block(std::false_type{}, (kb - kb_begin) % F8_GROUP, kb + 1 < kb_end)) return false;
                     return true;
-                }
+                };
+#pragma unroll 1
+                for (int kb = kb_begin; kb < kb_end; ++kb)
+                    if (!open() || !block((kb - kb_begin) % F8_GROUP, kb + 1 < kb_end)) return false;
+                return true;
             };
             bool ok;
             if (!active) {
@@ -889,6 +957,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             }
             if (!ok) break;
             if (!active) continue;
+            if constexpr (Cfg::SB_COL) f8::turn<COLS>(acc, stage_c, lane);
             if constexpr (Cfg::SPLIT) {
                 // the operand ring is idle (the last buffer's commit followed every MMA): leave this
                 // warp's sums there, [column][row], for the cluster

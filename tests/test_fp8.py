@@ -413,6 +413,24 @@ def test_gemm_strided_scales_and_outputs(M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tile", ["1x128", "2x256", None])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("start,step,line", [(0, 1, 1024), (0, 1, 1023), (1, 1, 1024), (2, 1, 1020), (0, 2, 2048), (0, 1, 0)])
+def test_gemm_column_scales_of_any_stride(monkeypatch, tile, out_dtype, start, step, line):
+    # lines of scales in 16-byte words or not, ending inside a word, one line for all k-blocks
+    if tile:
+        monkeypatch.setenv("TG_TILE", tile)
+    g = cuda_gen(15)
+    for M, N, K in ((1, 3, 700), (126, 259, 700), (515, 642, 1300)):
+        a, _, b, _ = make(g, M, N, K, "col", "row")
+        kb = ref.blocks(K)
+        sa, sb = (scales(g, kb * 2048 + 4).as_strided((kb, n), (line, step), start) for n in (M, N))
+        out = tg.gemm_fp8(a, sa.t(), b, sb, out_dtype=out_dtype)
+        tg.device_status()
+        check_product(out, a, sa.t(), b, sb)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [2, 150, 600])
 def test_gemm_special_values(M):
     g = cuda_gen(8)
