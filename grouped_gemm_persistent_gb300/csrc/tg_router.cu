@@ -376,6 +376,9 @@ __global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(32 * JOIN_WA
     __shared__ double s_loss[JOIN_CTAS];           // in block 0: every block's share
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank();
+    // block 0's shared memory takes the others' shares below: it may be written once every block of
+    // the cluster has started (with few experts nothing else stands between the two)
+    ptx::cluster_sync();
     ptx::grid_dependency_wait();
     int n = 0;
     for (int b = threadIdx.x; b < blocks; b += 32 * JOIN_WARPS) n += a.part_n[b];
