@@ -491,6 +491,19 @@ __device__ __forceinline__ float tanh_approx(float x) {
     return y;
 }
 
+// 2^x and 1 / x, with errors of about 2^-22 and 2^-23 of the result
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two fp32 values in one 64-bit register for the packed f32x2 instructions of
 // sm_100 and later: each lane of add/mul/fma.rn.f32x2 rounds exactly like the
 // scalar instruction, at half the instruction count.

@@ -326,7 +326,9 @@ typedef struct tg_scaled_operand {
  * scales are multiplied first (when B has one for 128 columns): their product should be
  * a normal fp32 number.  C, epi and
  * bias (bf16[N]) are as in tg_gemm, except that C needs only the alignment of its
- * elements.  K == 0 gives epilogue(0); M == 0 or N == 0 is a no-op.
+ * elements, and that TG_EPI_BIAS_GELU with TG_F32 output is worked out to fp32's own
+ * precision (bf16 and fp16 output: tanh to 2^-11, as in tg_gemm).  K == 0 gives
+ * epilogue(0); M == 0 or N == 0 is a no-op.
  *
  * The three products of a linear layer Y = X W with X [T, in], W [in, out]:
  *   Y  = X . W          X in 1 x 128 blocks, W in 128 x 128 blocks
