@@ -341,13 +341,24 @@ def _blocks(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
+def _stream_object(stream, device) -> torch.cuda.Stream:
+    """The torch stream whose order a handle's work follows."""
+    handle = _stream_handle(stream)
+    # NULL, cudaStreamLegacy, and cudaStreamPerThread, which waits for the legacy stream's work and is waited for by it
+    if handle in (0, 1, 2):
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
 def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
-    """An uninitialised tensor on ``like``'s device, in the allocator's order of ``stream``, so that a block freed
-    on another stream is not handed out while that stream still uses it."""
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=like.device)
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    """An uninitialised tensor on ``like``'s device, in the allocator's order of ``stream`` (an object or a raw
+    handle), so that a block freed on another stream is not handed out while that stream still uses it."""
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = _stream_object(stream, like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _rows_of_16_bytes(like: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, stream) -> tuple[torch.Tensor, int]:
