@@ -438,7 +438,7 @@ def quantize_fp8(x: torch.Tensor, block: tuple[int, int] = (1, 128), q: torch.Te
 def _fp8_layout(r: int, c: int, s0: int, s1: int, name: str) -> tuple[int, int]:
     """(layout, ld) of an r x c matrix with strides (s0, s1).  A single row or column is never stepped past: its
     leading dimension is reported as its extent rounded up to 16 elements."""
-    if s1 == 1 and (c > 1 or r <= 1):
+    if s1 == 1 and (c != 1 or r <= 1):
         return ROW_MAJOR, (s0 if r > 1 else -(-max(c, 1) // 16) * 16)
     if s0 == 1:
         return COL_MAJOR, (s1 if c > 1 else -(-max(r, 1) // 16) * 16)
