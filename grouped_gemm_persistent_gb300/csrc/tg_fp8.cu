@@ -34,20 +34,21 @@ cudaError_t launch_fp8(const Params& p, const Fp8Params& x, int grid, cudaStream
     return cudaLaunchKernelEx(&cfg, &fp8_kernel<Cfg>, p, x);
 }
 
-// CTAs, or CTA pairs, that can be resident at once; asked once per device and kernel, before its
-// first launch there, and sets the kernel's shared memory limit.
+// Clusters of `cluster` CTAs (single CTAs, pairs, or the CTAs that share a tile) that can be resident
+// at once; asked once per device, kernel and size, before the first launch there, and sets the
+// kernel's shared memory limit.
 template <class Cfg>
-cudaError_t units_fp8(int* units) {
+cudaError_t units_fp8(int cluster, int* units) {
     auto kern = &fp8_kernel<Cfg>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(Cfg::CTA_GROUP, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster), 1, 1);
     cfg.blockDim = dim3(F8_THREADS, 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = Cfg::CTA_GROUP;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -57,7 +58,7 @@ cudaError_t units_fp8(int* units) {
 
 struct Fp8Variant {
     cudaError_t (*launch)(const Params&, const Fp8Params&, int, cudaStream_t);
-    cudaError_t (*units)(int*);
+    cudaError_t (*units)(int, int*);
     int cta_group;
 };
 
@@ -79,16 +80,18 @@ const Fp8Variant kFp8[FORMS][2] = {
 };
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxSplitLog = 3;                // at most 8 CTAs share a tile
 std::mutex g_units_mu;
-int g_units[kMaxDevices][FORMS][2];
+int g_units[kMaxDevices][FORMS][kMaxSplitLog + 1];      // [log2 of the cluster's size]
 
-tg_status resident(const host::Device& d, int form, int pair, int* units) {
+// Resident clusters of 2^log CTAs of a form's kernel
+tg_status resident(const host::Device& d, int form, int log, int* units) {
     std::lock_guard<std::mutex> lock(g_units_mu);
-    int& u = g_units[d.id][form][pair];
+    int& u = g_units[d.id][form][log];
     if (u <= 0) {
-        const cudaError_t e = kFp8[form][pair].units(&u);
+        const bool split = form == FORM_BLOCK_SPLIT || form == FORM_COLUMN_SPLIT;
+        const cudaError_t e = kFp8[form][split ? 0 : log].units(1 << log, &u);
         if (e != cudaSuccess) return host::cuda_fail(e, "occupancy query");
-        if (u <= 0) return fail(TG_ERR_UNSUPPORTED, "the 8-bit kernel cannot be resident on this device");
     }
     *units = u;
     return TG_OK;
@@ -146,16 +149,25 @@ struct Fp8Call {
     const int32_t* counts;
 };
 
-// CTAs that share each 128 x 128 tile of a dense launch with fewer tiles than SMs: the largest
-// power of two, at most 8, that keeps every CTA resident and gives each at least two k-blocks.
-// 1 x 4096 x 4096: 16.5 us with one CTA a tile (32 of them).  TG_STREAM_K=0 keeps tiles whole.
-int pick_splits(const Fp8Call& c, int sms) {
+// log2 of the CTAs that share each 128 x 128 tile of a dense launch with fewer tiles than SMs: the
+// largest, at most 3, with every cluster resident and at least two k-blocks a CTA.  A cluster lies
+// within one part of the GPU, so fewer fit than SMs would: 15 of eight CTAs and 36 of four, and one
+// more costs a second wave (a row, K 4096: 15 tiles 7.5 us, 16 tiles 12.4 in clusters of eight and
+// 8.0 in clusters of four).  1 x 4096 x 4096: 16.5 us with one CTA a tile (32 of them), 8.7 with four.
+// TG_STREAM_K=0 keeps tiles whole.
+tg_status pick_splits(const Fp8Call& c, const host::Device& d, int form, int* log) {
+    *log = 0;
     const char* env = std::getenv("TG_STREAM_K");
-    if (env && env[0] == '0') return 1;
+    if (env && env[0] == '0') return TG_OK;
     const int64_t tiles = ((c.rows + 127) / 128) * ((c.N + 127) / 128), kb = (c.K + F8_BK - 1) / F8_BK;
-    int s = 1;
-    while (s < 8 && tiles * s * 2 <= sms && kb >= s * 4) s *= 2;
-    return s;
+    while (*log < kMaxSplitLog && tiles << (*log + 1) <= d.sms && kb >= int64_t(4) << *log) {
+        int units = 0;
+        const tg_status s = resident(d, form, *log + 1, &units);
+        if (s != TG_OK) return s;
+        if (tiles > units) break;
+        ++*log;
+    }
+    return TG_OK;
 }
 
 tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
@@ -175,11 +187,16 @@ tg_status run_fp8(const Fp8Call& c, cudaStream_t stream) {
         int cg = 0, bn = 0;
         if (std::sscanf(env, "%dx%d", &cg, &bn) == 2 && (cg == 1 || cg == 2)) pair = cg - 1;
     }
-    const int splits = moe || pair ? 1 : pick_splits(c, d.sms);
-    if (splits > 1) form = form == FORM_COLUMN ? FORM_COLUMN_SPLIT : FORM_BLOCK_SPLIT;
+    int log = 0, units = 0;
+    if (!moe && !pair) {
+        const int split_form = form == FORM_COLUMN ? FORM_COLUMN_SPLIT : FORM_BLOCK_SPLIT;
+        if ((s = pick_splits(c, d, split_form, &log)) != TG_OK) return s;
+        if (log > 0) form = split_form;
+    }
+    const int splits = 1 << log;
     const Fp8Variant& v = kFp8[form][pair];
-    int units = 0;
-    if ((s = resident(d, form, pair, &units)) != TG_OK) return s;
+    if ((s = resident(d, form, log + pair, &units)) != TG_OK) return s;
+    if (units <= 0) return fail(TG_ERR_UNSUPPORTED, "the 8-bit kernel cannot be resident on this device");
 
     const int tile = 128 * v.cta_group;
     Params p;

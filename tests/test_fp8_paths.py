@@ -128,3 +128,37 @@ def test_moe_many_tiles_of_other_types(out_dtype):
     out = tg.moe_gemm_fp8(a, sa, b, sb, c, out_dtype=out_dtype)
     tg.device_status()
     check_moe(out, counts, a, sa, b, sb)
+
+
+def replay_us(f, n=20):
+    f()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            f()
+    times = []
+    for _ in range(9):
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        graph.replay()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(begin.elapsed_time(end) * 1e3 / n)
+    return sorted(times)[4]
+
+
+def test_split_tiles_run_in_one_wave():
+    """A tile is not cut into more CTAs than fit beside the other tiles': fewer columns never take much longer than more
+    (a second wave costs half as much again)."""
+    K, tiles = 4096, (15, 16, 19, 20, 36, 37, 38, 39)
+    g = cuda_gen(49)
+    us = {}
+    for n in tiles:
+        a, sa, b, sb = make(g, 1, n * 128, K)
+        out = torch.empty(1, n * 128, dtype=torch.bfloat16, device="cuda")
+        tg.gemm_fp8(a, sa, b, sb, out)
+        check_product(out, a, sa, b, sb)
+        us[n] = replay_us(lambda: tg.gemm_fp8(a, sa, b, sb, out))
+    for n in tiles[:-1]:
+        assert us[n] <= 1.25 * min(us[m] for m in tiles if m > n), us
