@@ -476,7 +476,8 @@ def gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_b: t
     ``a`` [M, K] and ``b`` [K, N] are float8_e4m3fn or float8_e5m2, each a row-major or column-major view.
     ``scale_a`` is fp32 [M, ceil(K / 128)] (or [ceil(M / 128), ...]), ``scale_b`` [ceil(K / 128), N] or
     [ceil(K / 128), ceil(N / 128)], with any strides; scales of which neighbouring rows lie side by side
-    (quantize_fp8's) load fastest.  ``bias`` is bf16 [N]; ``out`` (allocated if not given) bf16, fp16 or fp32.
+    (quantize_fp8's) load fastest.  ``bias`` is bf16 [N]; ``out`` is bf16, fp16 or fp32 (allocated if not given, its rows
+    on 16-byte boundaries: a view with a wider row stride where N is not a multiple of 16 bytes).
     """
     ta, tb = _fp8_types(a, b)
     la, lda = _fp8_matrix(a, "a")

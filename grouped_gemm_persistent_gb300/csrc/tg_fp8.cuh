@@ -23,11 +23,13 @@
 // (128 x 256 x 128 at 8192 MAC/cycle) and the additions 256 issue slots a quarter of the SM, but
 // a k-block takes ~700: with two buffers, its MMAs wait for the read-back of the k-block two
 // before it, and that is a chain of four tensor-memory loads (~80 cycles each, 130 before the
-// first) and a barrier on either side.  8192^3, bf16 out: 398 us, 2760 TFLOP/s; the MMAs and
-// barriers without the read-back 296 us.  128 accumulator registers a thread for eight warps
+// first) and a barrier on either side.  8192^3, bf16 out: 390 to 400 us, 2750 TFLOP/s, in a few launches
+// at a time, 430 to 447 us, 2490 TFLOP/s, back to back at the power limit; the MMAs and barriers
+// without the read-back 296 us.  128 accumulator registers a thread for eight warps
 // need the registers of the first four (setmaxnreg).
 //
-// Waits, aborts and draining are those of tg_kernel.cuh.
+// Spills: none with block scales; 28 bytes of stores and 116 of loads a thread in the pair form with a
+// scale per column.  Waits, aborts and draining are those of tg_kernel.cuh.
 #pragma once
 
 #include "tg_kernel.cuh"
@@ -858,7 +860,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) fp8_kernel(const __grid_constan
             // columns of every eight, so that it needs 16 of the columns' scales (fc), which serve the
             // next 16 rows too.  (With a row a lane every lane read all of them: 16 KB a warp and k-block
             // out of shared memory, 1024 cycles at 128 bytes a cycle for the eight warps; 8192^3 took
-            // 744 us and takes 620.)  acc keeps 16 columns together, in the order turn() takes.
+            // 744 us and takes 620, or up to 690 at the power limit.)  acc keeps 16 columns together, in the order turn() takes.
             // Scalar: a warp's fused multiply-add measured 1.03 issue cycles, a packed pair of them 2.34.
             auto add = [&](auto chunk_index, const uint32_t (&r)[32], const float* s, const float* fc) {
                 constexpr int C = decltype(chunk_index)::value;

@@ -395,7 +395,7 @@ tg_status tg_moe_router(const void *logits, tg_dtype dtype, int64_t ld, int64_t 
  *               not used.  NULL: zero (experts and weights may then be NULL).
  *   d_loss    : DEVICE fp32, the gradient of loss.  NULL: zero (slope may then be NULL).
  *   d_logits, ldd : T x G of the logits' type, rounded once.  Zero where the logit is
- *               -infinity.
+ *               -infinity; a row with a NaN or a +infinity is NaN throughout.
  * The counts are constant in the logits: the loss's gradient goes through p alone.
  */
 tg_status tg_moe_router_backward(const void *logits, tg_dtype dtype, int64_t ld, int64_t T, int64_t G, int64_t k,
