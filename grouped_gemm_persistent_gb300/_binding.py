@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 from typing import NamedTuple
 
@@ -112,6 +113,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_moe_router.argtypes = [vp, ci, i64, i64, i64, i64, ci, vp, vp, vp, vp, vp, vp]
         lib.tg_moe_router_backward.restype = ci
         lib.tg_moe_router_backward.argtypes = [vp, ci, i64, i64, i64, i64, ci, vp, vp, vp, vp, vp, vp, i64, vp]
+        lib.tg_rmsnorm.restype = ci
+        lib.tg_rmsnorm.argtypes = [ctypes.c_char_p, vp]
+        lib.tg_rmsnorm_backward.restype = ci
+        lib.tg_rmsnorm_backward.argtypes = [ctypes.c_char_p, vp]
         lib.tg_status_string.restype = ctypes.c_char_p
         lib.tg_status_string.argtypes = [ci]
         lib.tg_last_error_message.restype = ctypes.c_char_p
@@ -581,6 +586,143 @@ def moe_gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_
     if status:
         _check(status)
     return out
+
+
+# Records of arguments, packed straight into bytes: quicker than a ctypes structure or twenty converted arguments.
+_RMSNORM = struct.Struct("@qq" + 2 * "Qq" + "Q" + 4 * "Qq" + "Q" + "f5i")                    # tg_rmsnorm_args
+_RMSNORM_BACKWARD = struct.Struct("@qq" + 2 * "Qq" + "QQ" + 2 * "Qq" + "Q" + "3i4x")         # tg_rmsnorm_backward_args
+
+
+class Normed(NamedTuple):
+    """What rmsnorm returns, and rmsnorm_backward needs again."""
+    y: torch.Tensor | None        # the normalised rows
+    q: torch.Tensor | None        # their 8-bit copy
+    scale: torch.Tensor | None    # its scales
+    hidden: torch.Tensor          # x + residual (x itself without one)
+    row_scale: torch.Tensor       # fp32 [M], 1 / rms
+
+
+def _rows_like(t: torch.Tensor, name: str, like: torch.Tensor) -> int:
+    """Leading dimension of a row-major tensor of another's shape."""
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+    return _row_major_ld(t, name, like.shape[1])
+
+
+def _gain(gain: torch.Tensor | None, K: int) -> tuple[int, int]:
+    """(pointer, type code) of a gain vector."""
+    if gain is None:
+        return 0, 0
+    code = _DTYPE_CODE.get(gain.dtype)
+    if code is None:
+        raise TypeError("gain must be bf16, fp16 or fp32")
+    if gain.shape != (K,) or (K > 1 and gain.stride(0) != 1):
+        raise ValueError(f"gain must be a contiguous vector of length {K}")
+    return gain.data_ptr(), code
+
+
+def rmsnorm(x: torch.Tensor, gain: torch.Tensor | None = None, eps: float = 1e-6, *,
+            residual: torch.Tensor | None = None, hidden: torch.Tensor | None = None,
+            out_dtype: torch.dtype | None = torch.bfloat16, fp8_dtype: torch.dtype | None = None,
+            stream=None) -> Normed:
+    """RMS norm of the rows of ``x + residual``, in ``out_dtype`` and / or in 8 bits (tg_rmsnorm).
+
+    ``x`` [M, K] is row-major bf16, fp16 or fp32, ``residual`` (None: x alone) of x's type or fp32; their sum, rounded
+    to the residual's type, is the result's ``hidden`` (written to ``hidden`` if given, which may be the residual).
+    ``gain`` [K] is bf16, fp16 or fp32.  ``y`` is ``hidden / rms * gain`` in ``out_dtype`` (None: not wanted);
+    with ``fp8_dtype`` (torch.float8_e4m3fn or torch.float8_e5m2) ``q`` and ``scale`` are what
+    ``quantize_fp8(y, (1, 128))`` makes of the fp32 y: the operands of gemm_fp8 and moe_gemm_fp8.
+    """
+    xt = _DTYPE_CODE.get(x.dtype)
+    if xt is None:
+        raise TypeError("x must be bf16, fp16 or fp32")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got shape {tuple(x.shape)}")
+    M, K = x.shape
+    ldx = _row_major_ld(x, "x", K)
+    rt = ldr = ldh = 0
+    if residual is not None:
+        if residual.dtype != x.dtype and residual.dtype != torch.float32:
+            raise TypeError("residual must have x's type or fp32")
+        rt = _DTYPE_CODE[residual.dtype]
+        ldr = _rows_like(residual, "residual", x)
+        if hidden is None:
+            hidden, ldh = _rows_of_16_bytes(x, M, K, residual.dtype, stream)
+        else:
+            if hidden.dtype != residual.dtype:
+                raise TypeError("hidden must have the residual's type")
+            ldh = _rows_like(hidden, "hidden", x)
+    elif hidden is not None:
+        raise ValueError("hidden is written only with a residual")
+    gp, gt = _gain(gain, K)
+    y = q = scale = None
+    yp = yt = ldy = qp = qt = ldq = sp = 0
+    if out_dtype is not None:
+        yt = _DTYPE_CODE.get(out_dtype)
+        if yt is None:
+            raise TypeError("out_dtype must be bf16, fp16, fp32 or None")
+        y, ldy = _rows_of_16_bytes(x, M, K, out_dtype, stream)
+        yp = y.data_ptr()
+    if fp8_dtype is not None:
+        qt = _FP8_CODE.get(fp8_dtype)
+        if qt is None:
+            raise TypeError("fp8_dtype must be torch.float8_e4m3fn, torch.float8_e5m2 or None")
+        q, ldq = _rows_of_16_bytes(x, M, K, fp8_dtype, stream)
+        scale = _empty(x, (_blocks(K), M), torch.float32, stream).t()
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    elif y is None:
+        raise ValueError("out_dtype and fp8_dtype are both None: nothing is wanted")
+    row_scale = _empty(x, M, torch.float32, stream)
+    _on_one_gpu("x residual hidden gain", x, residual, hidden, gain)
+    status = load().tg_rmsnorm(
+        _RMSNORM.pack(M, K, x.data_ptr(), ldx, _ptr(residual), ldr, gp, _ptr(hidden), ldh, yp, ldy, qp, ldq, sp, M,
+                      row_scale.data_ptr(), eps, xt, rt, gt, yt, qt), _stream_handle(stream))
+    if status:
+        _check(status)
+    return Normed(y, q, scale, x if hidden is None else hidden, row_scale)
+
+
+def rmsnorm_backward(normed: Normed, dy: torch.Tensor, gain: torch.Tensor | None = None,
+                     d_hidden: torch.Tensor | None = None, out: torch.Tensor | None = None, *,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """(dx, d_gain): the gradients of rmsnorm's x (and residual: the same) and gain (tg_rmsnorm_backward).
+
+    ``dy`` [M, K], bf16, fp16 or fp32, is the gradient of the normalised rows (the 8-bit copy counts as y itself),
+    ``d_hidden`` (None: zero) what reaches ``normed.hidden`` past the norm, of its type.  ``out`` has hidden's type too
+    and may be ``d_hidden``; ``d_gain`` is fp32 [K], None without a gain.
+    """
+    hidden, row_scale = normed.hidden, normed.row_scale
+    ht, dt = _DTYPE_CODE.get(hidden.dtype), _DTYPE_CODE.get(dy.dtype)
+    if ht is None or dt is None:
+        raise TypeError("normed.hidden and dy must be bf16, fp16 or fp32")
+    if hidden.dim() != 2:
+        raise ValueError(f"normed.hidden must be 2-D, got shape {tuple(hidden.shape)}")
+    M, K = hidden.shape
+    ldh = _row_major_ld(hidden, "normed.hidden", K)
+    lddy = _rows_like(dy, "dy", hidden)
+    if row_scale.dtype != torch.float32 or row_scale.shape != (M,) or not row_scale.is_contiguous():
+        raise ValueError(f"normed.row_scale must be a contiguous fp32 tensor {[M]}")
+    gp, gt = _gain(gain, K)
+    lddh = 0
+    if d_hidden is not None:
+        if d_hidden.dtype != hidden.dtype:
+            raise TypeError("d_hidden must have hidden's type")
+        lddh = _rows_like(d_hidden, "d_hidden", hidden)
+    if out is None:
+        out, ldo = _rows_of_16_bytes(hidden, M, K, hidden.dtype, stream)
+    else:
+        if out.dtype != hidden.dtype:
+            raise TypeError("out must have hidden's type")
+        ldo = _rows_like(out, "out", hidden)
+    d_gain = None if gain is None else _empty(hidden, K, torch.float32, stream)
+    _on_one_gpu("normed.hidden normed.row_scale dy gain d_hidden out", hidden, row_scale, dy, gain, d_hidden, out)
+    status = load().tg_rmsnorm_backward(
+        _RMSNORM_BACKWARD.pack(M, K, dy.data_ptr(), lddy, hidden.data_ptr(), ldh, row_scale.data_ptr(), gp,
+                               _ptr(d_hidden), lddh, out.data_ptr(), ldo, _ptr(d_gain), dt, ht, gt),
+        _stream_handle(stream))
+    if status:
+        _check(status)
+    return out, d_gain
 
 
 class Routing(NamedTuple):

@@ -356,6 +356,80 @@ tg_status tg_moe_gemm_scaled(const tg_scaled_operand *A, int64_t T, int64_t K, c
                           void *C, tg_dtype c_dtype, int64_t ldc, const int32_t *counts,
                           tg_epilogue epi, const void *bias, tg_stream_t stream);
 
+/* Largest number of columns tg_rmsnorm and tg_rmsnorm_backward accept. */
+#define TG_RMSNORM_MAX_COLUMNS 32768
+
+/*
+ * tg_rmsnorm - the norm in front of a product: a residual stream takes a block's output, and
+ * its rows come out normalised, in 16 or 32 bits, in 8 bits with a scale for each 128 values
+ * of a row (what tg_gemm_scaled and tg_moe_gemm_scaled read), or both.
+ *
+ *   h         = x + residual, added in fp32 and rounded to the residual's type; x itself
+ *               without a residual
+ *   row_scale = 1 / sqrt(mean over the row of h^2 + eps), rounded to fp32 once (squares below
+ *               fp32's normal numbers may be lost beside eps)
+ *   y         = (h * row_scale) * gain, each product rounded to fp32, then to y's type
+ *   q, scale  = tg_quantize_blocks of the fp32 y in 1 x 128 blocks
+ *
+ *   M, K               : rows and columns, K <= TG_RMSNORM_MAX_COLUMNS.  M == 0 or K == 0 is a no-op.
+ *   x, ldx             : row-major bf16, fp16 or fp32, as every matrix here of any alignment
+ *                        (16-byte aligned rows are moved with wide accesses).
+ *   residual, ldr      : NULL, or x's type or fp32.
+ *   gain               : NULL (ones), or K values of any of the three types.
+ *   hidden, ldh        : where h goes, needed with a residual (and not used without); it may be
+ *                        the residual or, of x's type, x.
+ *   y, q               : each NULL when not wanted, not both.  q is TG_E4M3 or TG_E5M2;
+ *                        scale[(k / 128) * scale_ld + m], scale_ld >= M.
+ *   row_scale          : fp32 [M].
+ * Every pointer is DEVICE memory; the record itself is read during the call only.  Apart from
+ * hidden, outputs do not overlap inputs or one another.  A row with an infinity has row_scale 0,
+ * one with a NaN row_scale NaN.
+ */
+typedef struct tg_rmsnorm_args {
+    int64_t M, K;
+    const void *x;        int64_t ldx;
+    const void *residual; int64_t ldr;
+    const void *gain;
+    void *hidden;         int64_t ldh;
+    void *y;              int64_t ldy;
+    void *q;              int64_t ldq;
+    float *scale;         int64_t scale_ld;
+    float *row_scale;
+    float eps;            /* finite, not negative */
+    tg_dtype x_dtype, residual_dtype, gain_dtype, y_dtype, q_dtype;   /* those of NULL pointers are not used */
+} tg_rmsnorm_args;
+
+tg_status tg_rmsnorm(const tg_rmsnorm_args *args, tg_stream_t stream);
+
+/*
+ * tg_rmsnorm_backward - the gradients of tg_rmsnorm; the 8-bit copy is taken for y itself.
+ *
+ * With d = dy * gain, n = h * row_scale and S = sum over the row of d n:
+ *   dx     = row_scale (d - n S / K) + d_hidden, rounded once: the gradient of x and of the
+ *            residual
+ *   d_gain = sum over the rows of dy n, fp32
+ *
+ *   dy, lddy            : bf16, fp16 or fp32.
+ *   hidden, row_scale   : tg_rmsnorm's (x where there was no residual).
+ *   d_hidden, lddh      : the gradient that reaches h past the norm, of hidden's type; NULL: zero.
+ *   dx, lddx            : of hidden's type; may be d_hidden or, of the same type, dy.
+ *   d_gain              : DEVICE fp32 [K], NULL when not wanted.  M == 0 writes zeros.
+ * Deterministic.  With d_gain, a workspace of up to 4 KiB x K from the library's memory pool.
+ */
+typedef struct tg_rmsnorm_backward_args {
+    int64_t M, K;
+    const void *dy;       int64_t lddy;
+    const void *hidden;   int64_t ldh;
+    const float *row_scale;
+    const void *gain;
+    const void *d_hidden; int64_t lddh;
+    void *dx;             int64_t lddx;
+    float *d_gain;
+    tg_dtype dy_dtype, hidden_dtype, gain_dtype;
+} tg_rmsnorm_backward_args;
+
+tg_status tg_rmsnorm_backward(const tg_rmsnorm_backward_args *args, tg_stream_t stream);
+
 /* Largest number of experts and of choices per token tg_moe_router accepts. */
 #define TG_MOE_ROUTER_MAX_EXPERTS 1024
 #define TG_MOE_ROUTER_MAX_TOP_K 32
