@@ -117,6 +117,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_rmsnorm.argtypes = [ctypes.c_char_p, vp]
         lib.tg_rmsnorm_backward.restype = ci
         lib.tg_rmsnorm_backward.argtypes = [ctypes.c_char_p, vp]
+        lib.tg_moe_router_scored.restype = ci
+        lib.tg_moe_router_scored.argtypes = [ctypes.c_char_p, vp]
+        lib.tg_moe_router_scored_backward.restype = ci
+        lib.tg_moe_router_scored_backward.argtypes = [ctypes.c_char_p, vp]
         lib.tg_status_string.restype = ctypes.c_char_p
         lib.tg_status_string.argtypes = [ci]
         lib.tg_last_error_message.restype = ctypes.c_char_p
@@ -592,6 +596,10 @@ def moe_gemm_fp8(a: torch.Tensor, scale_a: torch.Tensor, b: torch.Tensor, scale_
 _RMSNORM = struct.Struct("@qq" + 2 * "Qq" + "Q" + 4 * "Qq" + "Q" + "f5i")                    # tg_rmsnorm_args
 _RMSNORM_BACKWARD = struct.Struct("@qq" + 2 * "Qq" + "QQ" + 2 * "Qq" + "Q" + "3i4x")         # tg_rmsnorm_backward_args
 
+_ROUTER = struct.Struct("@3q" + "Qq" + "Q" + "3q" + "5Q" + "f3i")                            # tg_router_args
+_ROUTER_BACKWARD = struct.Struct("@3q" + "Qq" + "5Q" + "Qq" + "f3i")                         # tg_router_backward_args
+SCORES = {"softmax": 0, "sigmoid": 1}
+
 
 class Normed(NamedTuple):
     """What rmsnorm returns, and rmsnorm_backward needs again."""
@@ -733,6 +741,8 @@ class Routing(NamedTuple):
     loss: torch.Tensor       # fp32, balance loss
     slope: torch.Tensor      # fp32 [G], d loss / d probability
     renormalize: bool
+    score: str = "softmax"
+    weight_scale: float = 1.0
 
 
 def _logits(logits: torch.Tensor) -> tuple[int, int, int, int]:
@@ -746,23 +756,40 @@ def _logits(logits: torch.Tensor) -> tuple[int, int, int, int]:
     return dt, T, G, _row_major_ld(logits, "logits", G)
 
 
-def moe_router(logits: torch.Tensor, top_k: int, *, renormalize: bool = False, stream=None) -> Routing:
-    """Top-k experts of each token, their softmax weights, per-expert counts and balance loss (tg_moe_router).
+def moe_router(logits: torch.Tensor, top_k: int, *, renormalize: bool = False, score: str = "softmax",
+               bias: torch.Tensor | None = None, groups: int = 1, top_groups: int | None = None, group_top: int = 1,
+               weight_scale: float = 1.0, stream=None) -> Routing:
+    """Top-k experts of each token, their weights, per-expert counts and balance loss (tg_moe_router, tg_moe_router_scored).
 
     ``logits`` is row-major [T, G] bf16, fp16 or fp32; -infinity forbids an expert, a row of it is padding.
     ``counts`` is what moe_gemm_device and moe_gemm_fp8 read; the loss is G * sum(f * P), 1 when all is even.
+
+    ``score`` is "softmax" or "sigmoid".  ``bias`` (fp32 [G]) is added to the scores for the choice alone, not for the
+    weights.  With ``groups`` groups of neighbouring experts, only the ``top_groups`` best are chosen from (None: all),
+    a group's score being the sum of its ``group_top`` (1 or 2) largest.  The weights are times ``weight_scale``.
     """
     dt, T, G, ld = _logits(logits)
     if not isinstance(top_k, int) or top_k < 1:
         raise ValueError("top_k must be a positive integer")
-    _on_one_gpu("logits", logits)
+    code = SCORES.get(score)
+    if code is None:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (G,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous fp32 tensor {[G]}")
+    _on_one_gpu("logits bias", logits, bias)
     shape = (T, top_k)
     r = Routing(_empty(logits, shape, torch.int32, stream), _empty(logits, shape, torch.float32, stream),
                 _empty(logits, G, torch.int32, stream), _empty(logits, (), torch.float32, stream),
-                _empty(logits, G, torch.float32, stream), bool(renormalize))
-    status = load().tg_moe_router(logits.data_ptr(), dt, ld, T, G, top_k, int(renormalize), r.experts.data_ptr(),
-                                  r.weights.data_ptr(), r.counts.data_ptr(), r.loss.data_ptr(), r.slope.data_ptr(),
-                                  _stream_handle(stream))
+                _empty(logits, G, torch.float32, stream), bool(renormalize), score, float(weight_scale))
+    if code == 0 and bias is None and groups == 1 and weight_scale == 1.0 and top_groups in (None, 1) and group_top == 1:
+        status = load().tg_moe_router(logits.data_ptr(), dt, ld, T, G, top_k, int(renormalize), r.experts.data_ptr(),
+                                      r.weights.data_ptr(), r.counts.data_ptr(), r.loss.data_ptr(), r.slope.data_ptr(),
+                                      _stream_handle(stream))
+    else:
+        status = load().tg_moe_router_scored(
+            _ROUTER.pack(T, G, top_k, logits.data_ptr(), ld, _ptr(bias), groups, groups if top_groups is None else top_groups,
+                         group_top, r.experts.data_ptr(), r.weights.data_ptr(), r.counts.data_ptr(), r.loss.data_ptr(),
+                         r.slope.data_ptr(), r.weight_scale, dt, code, r.renormalize), _stream_handle(stream))
     if status:
         _check(status)
     return r
@@ -795,11 +822,17 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
         ldd = _row_major_ld(out, "out", G)
     _on_one_gpu("logits routing.experts routing.weights routing.slope d_weights d_loss out", logits, experts,
                 weights, slope, d_weights, d_loss, out)
-    status = load().tg_moe_router_backward(logits.data_ptr(), dt, ld, T, G, k, int(routing.renormalize),
-                                           experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
-                                           None if d_weights is None else d_weights.data_ptr(),
-                                           None if d_loss is None else d_loss.data_ptr(), out.data_ptr(), ldd,
-                                           _stream_handle(stream))
+    if routing.score == "softmax" and routing.weight_scale == 1.0:
+        status = load().tg_moe_router_backward(logits.data_ptr(), dt, ld, T, G, k, int(routing.renormalize),
+                                               experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
+                                               None if d_weights is None else d_weights.data_ptr(),
+                                               None if d_loss is None else d_loss.data_ptr(), out.data_ptr(), ldd,
+                                               _stream_handle(stream))
+    else:
+        status = load().tg_moe_router_scored_backward(
+            _ROUTER_BACKWARD.pack(T, G, k, logits.data_ptr(), ld, experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
+                                  _ptr(d_weights), _ptr(d_loss), out.data_ptr(), ldd, routing.weight_scale, dt,
+                                  SCORES[routing.score], routing.renormalize), _stream_handle(stream))
     if status:
         _check(status)
     return out

@@ -37,123 +37,13 @@
 #include "tg.h"
 #include "tg_host.cuh"
 #include "tg_ptx.cuh"
+#include "tg_router.cuh"
 
 namespace tg {
 
+using namespace gate;
+
 namespace {
-
-constexpr int R_WARPS = 16;
-constexpr int R_THREADS = 32 * R_WARPS;
-constexpr int R_BLOCKS_PER_SM = 2;
-constexpr int R_MAX_G = TG_MOE_ROUTER_MAX_EXPERTS;
-constexpr int R_MAX_K = TG_MOE_ROUTER_MAX_TOP_K;
-constexpr uint32_t FULL = 0xffffffffu;
-
-// ----------------------------------------------------------------------------------------
-// a lane's V logits of one row, as they lie in memory
-
-template <int DT, int V>
-struct Logits {
-    static constexpr int ESIZE = DT == TG_F32 ? 4 : 2;
-    static constexpr int WORDS = V * ESIZE / 4;
-    static constexpr uint32_t NEG_INF = DT == TG_F32 ? 0xff800000u : DT == TG_F16 ? 0xfc00fc00u : 0xff80ff80u;
-    uint32_t w[WORDS];
-
-    __device__ __forceinline__ void load_whole(const uint8_t* p) {
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 4) {
-            const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
-            w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
-        }
-    }
-    // n of the V are inside the row (the others become -infinity); vec: 16-byte loads allowed
-    __device__ __forceinline__ void load(const uint8_t* p, int n, bool vec) {
-        if (n == V && vec) {
-            load_whole(p);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) {
-            if constexpr (DT == TG_F32) {
-                w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : NEG_INF;
-            } else {
-                const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-                const uint32_t lo = 2 * i < n ? __ldg(h + 2 * i) : NEG_INF & 0xffffu;
-                const uint32_t hi = 2 * i + 1 < n ? __ldg(h + 2 * i + 1) : NEG_INF & 0xffffu;
-                w[i] = lo | hi << 16;
-            }
-        }
-    }
-    __device__ __forceinline__ uint32_t bits(int j) const {
-        if constexpr (DT == TG_F32) return w[j];
-        else return j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu;
-    }
-    static __device__ __forceinline__ float widen(uint32_t b) {
-        if constexpr (DT == TG_F32) return __uint_as_float(b);
-        else if constexpr (DT == TG_F16) return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
-        else return __uint_as_float(b << 16);
-    }
-    __device__ __forceinline__ float value(int j) const { return widen(bits(j)); }
-    // logit g of the row at p
-    static __device__ __forceinline__ float one(const uint8_t* p, int g) {
-        if constexpr (DT == TG_F32) return __ldg(reinterpret_cast<const float*>(p) + g);
-        else return widen(__ldg(reinterpret_cast<const uint16_t*>(p) + g));
-    }
-};
-
-constexpr uint32_t KEY_MIN = 0x00800000u;      // keys of -infinity lie below it
-
-// The bits of a value that is not NaN, ordered like an unsigned integer; -0 equals +0.
-__device__ __forceinline__ uint32_t order_bits(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-}
-
-// Over the L lanes of a row
-template <int L>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-    if constexpr (L == 32) {
-        return __reduce_max_sync(FULL, v);
-    } else {
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(FULL, v, d));
-        return v;
-    }
-}
-
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(FULL, v, d);
-    return v;
-}
-
-// NaN if any is
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-template <int L>
-__device__ __forceinline__ float group_max_nan(float v) {
-    if constexpr (L == 32) {
-        float r;
-        asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-        return r;
-    } else {
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(FULL, v, d));
-        return v;
-    }
-}
-
-// e^x, zero below fp32's normal values: for probabilities that are summed.
-__device__ __forceinline__ float exp_flush(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
-    return r;
-}
 
 // The k choices of a row from its logits alone, in order of value (NaN first) and index: lane i
 // gets the i-th expert, or -1.  Every lane of the warp calls it; a row that need not choose
@@ -183,36 +73,6 @@ __device__ __noinline__ int choose_exactly(const Logits<DT, V>& x, int first, in
         }
     }
     return my_e;
-}
-
-struct RouterArgs {
-    const uint8_t* logits;
-    int64_t ld_bytes, T;
-    int G, k, renorm, vec;
-    int32_t* experts;     // [T, k]
-    float* weights;       // [T, k]
-    int32_t* counts;      // [G]
-    float* loss;
-    float* slope;         // [G]
-    // several blocks: each one's probability sums [G], counts [G] and number of rows
-    float* part_p;
-    int32_t* part_c;
-    int32_t* part_n;
-};
-
-// What turns an expert's count into its slope: G / (n k) / n.  Computed once a thread: this GPU's
-// double precision is slow, a division a warp and expert cost the join 7 us.
-__device__ __forceinline__ double slope_per_count(const RouterArgs& a, int64_t rows) {
-    const double n = rows > 0 ? static_cast<double>(rows) : 1.0;
-    return a.G / (n * n * a.k);
-}
-
-// counts, slope and this expert's term of the loss
-__device__ __forceinline__ double finish_expert(const RouterArgs& a, int g, float sum, int32_t count, double per_count) {
-    a.counts[g] = count;
-    const double slope = per_count * count;
-    a.slope[g] = static_cast<float>(slope);
-    return slope * sum;
 }
 
 template <int DT, int L, int V>
@@ -438,6 +298,7 @@ struct BackArgs {
     const float* d_loss;      // null: zero
     uint8_t* out;
     int64_t ldo_bytes;
+    float scale, inv_scale;   // the weights' factor
 };
 
 template <int DT, int L, int V>
@@ -470,8 +331,8 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_backward_ker
         e_next = -1;
         if (choice && row < a.T) {
             e_next = __ldg(a.experts + row * a.k + in);
-            w_next = __ldg(a.weights + row * a.k + in);
-            dw_next = __ldg(a.d_weights + row * a.k + in);
+            w_next = __ldg(a.weights + row * a.k + in) * a.inv_scale;
+            dw_next = __ldg(a.d_weights + row * a.k + in) * a.scale;
         }
         if (e_next < 0 || e_next >= a.G) {       // no choice (-1): nothing of it counts
             e_next = -1;
@@ -576,6 +437,10 @@ RouterVariant variant_for(tg_dtype dt, int G, int k) {
     return dt == TG_F32 ? variant_for<TG_F32>(G, k) : dt == TG_F16 ? variant_for<TG_F16>(G, k) : variant_for<TG_BF16>(G, k);
 }
 
+}  // namespace
+
+namespace gate {
+
 tg_status check_router(const void* logits, tg_dtype dt, int64_t ld, int64_t T, int64_t G, int64_t k) {
     using host::fail;
     if (dt != TG_BF16 && dt != TG_F16 && dt != TG_F32)
@@ -596,14 +461,62 @@ tg_status check_router(const void* logits, tg_dtype dt, int64_t ld, int64_t T, i
     return TG_OK;
 }
 
-// Raise a kernel's limit of dynamic shared memory where it needs more than the default.
-template <class K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+tg_status check_backward(int64_t G, tg_dtype dt, const int32_t* experts, const float* weights, bool weights_needed,
+                         const float* slope, const float* d_weights, const float* d_loss, const void* d_logits, int64_t ldd) {
+    using host::fail;
+    if (!d_logits) return fail(TG_ERR_INVALID_ARG, "d_logits is NULL");
+    if (d_weights && (!experts || (weights_needed && !weights)))
+        return fail(TG_ERR_INVALID_ARG, "%s is NULL (needed with d_weights)", !experts ? "experts" : "weights");
+    if (d_loss && !slope) return fail(TG_ERR_INVALID_ARG, "slope is NULL (needed with d_loss)");
+    if (ldd < G) return fail(TG_ERR_INVALID_ARG, "ldd=%lld < G=%lld", (long long)ldd, (long long)G);
+    if (ldd > host::MAX_DIM) return fail(TG_ERR_UNSUPPORTED, "ldd must be below 2^31");
+    if (!host::aligned(d_logits, dt == TG_F32 ? 4 : 2))
+        return fail(TG_ERR_INVALID_ARG, "d_logits is not aligned to its element size");
+    if (!host::aligned(experts, 4) || !host::aligned(weights, 4) || !host::aligned(slope, 4) ||
+        !host::aligned(d_weights, 4) || !host::aligned(d_loss, 4))
+        return fail(TG_ERR_INVALID_ARG, "an input is not 4-byte aligned");
+    return TG_OK;
 }
 
-}  // namespace
+cudaError_t launch_join(const RouterArgs& a, int blocks, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(JOIN_CTAS, 1, 1);
+    cfg.blockDim = dim3(32 * JOIN_WARPS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, router_join_kernel, a, blocks);
+}
+
+tg_status softmax_backward(const void* logits, tg_dtype dtype, int64_t ld, int64_t T, int64_t G, int64_t k, int renormalize,
+                           float weight_scale, const int32_t* experts, const float* weights, const float* slope,
+                           const float* d_weights, const float* d_loss, void* d_logits, int64_t ldd, cudaStream_t stream) {
+    host::Device d;
+    const tg_status s = host::device(&d);
+    if (s != TG_OK) return s;
+    const RouterVariant v = variant_for(dtype, static_cast<int>(G), static_cast<int>(k));
+    const int64_t esize = dtype == TG_F32 ? 4 : 2;
+    const BackArgs a{static_cast<const uint8_t*>(logits), ld * esize, T, int(G), int(k), renormalize != 0,
+                     host::aligned(logits, 16) && ld * esize % 16 == 0,
+                     host::aligned(d_logits, 16) && ldd * esize % 16 == 0, experts, weights, slope, d_weights, d_loss,
+                     static_cast<uint8_t*>(d_logits), ldd * esize, weight_scale, 1.0f / weight_scale};
+    const int64_t block_rows = R_WARPS * (32 / v.lanes);
+    const int64_t want = (T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
+    const size_t smem = static_cast<size_t>(R_WARPS) * 32 * v.per_lane * 4;
+    cudaError_t e = allow_smem(v.backward, smem);
+    if (e == cudaSuccess) {
+        v.backward<<<static_cast<unsigned>(want < cap ? want : cap), R_THREADS, smem, stream>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return host::cuda_fail(e, "router backward launch");
+    host::count_launches(1);
+    return TG_OK;
+}
+
+}  // namespace gate
 
 }  // namespace tg
 
@@ -650,16 +563,7 @@ extern "C" tg_status tg_moe_router(const void* logits, tg_dtype dtype, int64_t l
     if (e == cudaSuccess) {
         host::count_launches(1);
         if (blocks > 1) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(JOIN_CTAS, 1, 1);
-            cfg.blockDim = dim3(32 * JOIN_WARPS, 1, 1);
-            cfg.stream = st;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[0].val.programmaticStreamSerializationAllowed = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, router_join_kernel, static_cast<const RouterArgs&>(a), blocks);
+            e = launch_join(a, blocks, st);
             if (e == cudaSuccess) host::count_launches(1);
         }
     }
@@ -676,37 +580,9 @@ extern "C" tg_status tg_moe_router_backward(const void* logits, tg_dtype dtype, 
                                             const float* slope, const float* d_weights, const float* d_loss,
                                             void* d_logits, int64_t ldd, tg_stream_t stream) {
     using namespace tg;
-    using host::fail;
     tg_status s = check_router(logits, dtype, ld, T, G, k);
     if (s != TG_OK || T == 0) return s;
-    if (!d_logits) return fail(TG_ERR_INVALID_ARG, "d_logits is NULL");
-    if (d_weights && (!experts || !weights))
-        return fail(TG_ERR_INVALID_ARG, "%s is NULL (needed with d_weights)", !experts ? "experts" : "weights");
-    if (d_loss && !slope) return fail(TG_ERR_INVALID_ARG, "slope is NULL (needed with d_loss)");
-    if (ldd < G) return fail(TG_ERR_INVALID_ARG, "ldd=%lld < G=%lld", (long long)ldd, (long long)G);
-    if (ldd > host::MAX_DIM) return fail(TG_ERR_UNSUPPORTED, "ldd must be below 2^31");
-    if (!host::aligned(d_logits, dtype == TG_F32 ? 4 : 2))
-        return fail(TG_ERR_INVALID_ARG, "d_logits is not aligned to its element size");
-    if (!host::aligned(experts, 4) || !host::aligned(weights, 4) || !host::aligned(slope, 4) ||
-        !host::aligned(d_weights, 4) || !host::aligned(d_loss, 4))
-        return fail(TG_ERR_INVALID_ARG, "an input is not 4-byte aligned");
-    host::Device d;
-    if ((s = host::device(&d)) != TG_OK) return s;
-    const RouterVariant v = variant_for(dtype, static_cast<int>(G), static_cast<int>(k));
-    const int64_t esize = dtype == TG_F32 ? 4 : 2;
-    const BackArgs a{static_cast<const uint8_t*>(logits), ld * esize, T, int(G), int(k), renormalize != 0,
-                     host::aligned(logits, 16) && ld * esize % 16 == 0,
-                     host::aligned(d_logits, 16) && ldd * esize % 16 == 0, experts, weights, slope, d_weights, d_loss,
-                     static_cast<uint8_t*>(d_logits), ldd * esize};
-    const int64_t block_rows = R_WARPS * (32 / v.lanes);
-    const int64_t want = (T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
-    const size_t smem = static_cast<size_t>(R_WARPS) * 32 * v.per_lane * 4;
-    cudaError_t e = allow_smem(v.backward, smem);
-    if (e == cudaSuccess) {
-        v.backward<<<static_cast<unsigned>(want < cap ? want : cap), R_THREADS, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-        e = cudaGetLastError();
-    }
-    if (e != cudaSuccess) return host::cuda_fail(e, "router backward launch");
-    host::count_launches(1);
-    return TG_OK;
+    if ((s = check_backward(G, dtype, experts, weights, true, slope, d_weights, d_loss, d_logits, ldd)) != TG_OK) return s;
+    return softmax_backward(logits, dtype, ld, T, G, k, renormalize, 1.0f, experts, weights, slope, d_weights, d_loss, d_logits,
+                            ldd, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -1,0 +1,725 @@
+// tg_router_scored.cu - the gate with sigmoid or softmax scores, a bias for balance, groups of experts and a factor on the
+// weights (tg_moe_router_scored and tg_moe_router_scored_backward in include/tg.h).
+//
+//   s(t, g)     sigmoid(x) or softmax(x)                    v = s + bias[g]: what is chosen by
+//   group       its score is the sum of its group_top (1 or 2) largest v; the top_groups best are kept
+//   e(t, j)     the k experts of largest v in the kept groups; without a bias by x itself, of which v is a rising function
+//   w(t, j)     factor * s, over the sum of the chosen s when renormalised
+//   loss        G sum_g f_g P_g as in tg_router.cu, with P_g the mean of s / sum_g s
+// and, counts being constant, with u = d_loss * slope and c' the gradient of the chosen s through w
+//   sigmoid:    d x = s (1 - s) ((u - sum s u / sum s) / sum s + c')
+// (softmax: the other gate's backward kernel, which knows the factor).
+//
+// Choosing.  A choice by v is one of real numbers: with fp32 scores two experts next to each other in the order would change
+// places with the last bits of exp.  The kernel works in fp32 with a bound E on a score's error (sigmoid: ex2 2^-22
+// relative, times s (1 - s) <= 1/4; 1 + e and its reciprocal 1.5 * 2^-23: below 3e-7.  softmax: the same, the sum's 14
+// additions and the argument's roundings: below 1e-6), and sees where that does not decide: two neighbours among the first
+// k + 1 whose keys are within the bound, and a group at the border of the kept ones.  Such a row is worked out again in
+// 64 bits (choose_in_64): about one in 500 of 131072 x 256 fp32.  Neighbours whose logit and bias are both the same
+// are a true tie, which the index decides, and send no row there: with 16-bit logits and a bias of zeros they are common.
+//
+// Keys.  Without a bias as in tg_router.cu: the logit's ordered bits, the lowest ones replaced by the position counted down.
+// With one: v - lo in fixed point, 22 bits after the point for up to 256 positions (2^-22 is about what the scores are
+// known to), the position below it; lo is the smallest bias, or the largest minus 2.5 where they spread further (what lies
+// below lo has the lowest key, and a row in which such a one is among the first k + 1 goes to 64 bits).  v - lo is below 4.
+//
+// Positions.  A row is L lanes of V positions.  Each group has a power of two of positions, V at least, so that
+// a group is whole lanes and its sums are a few exchanges; the positions past its experts hold -infinity.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "tg.h"
+#include "tg_host.cuh"
+#include "tg_ptx.cuh"
+#include "tg_router.cuh"
+
+namespace tg {
+
+using namespace gate;
+
+namespace {
+
+constexpr float MINUS_INF = -__builtin_huge_valf();
+
+struct ScoredArgs {
+    RouterArgs r;
+    const float* bias;        // null: none
+    int each;                 // experts of a group
+    int shift;                // log2 of a group's positions (31: one group)
+    int groups, top_groups, group_top;
+    float factor;
+};
+
+// 2^x and 1 / x, zero below fp32's normal values
+__device__ __forceinline__ float ex2_flush(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_flush(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float sigmoid_approx(float x) { return rcp_flush(1.0f + ex2_flush(x * -1.4426950408889634f)); }
+
+template <int L>
+__device__ __forceinline__ float group_max_plain(float v) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, d));
+    return v;
+}
+
+// The votes of a row's lanes
+template <int L>
+__device__ __forceinline__ uint32_t row_ballot(bool v, int lane, int in) {
+    return __ballot_sync(FULL, v) >> (lane - in) & (L == 32 ? FULL : (1u << L % 32) - 1u);
+}
+
+// A double's place in the order: NaN above all, -infinity (what may not be chosen) 0
+__device__ __forceinline__ unsigned long long order64(double v) {
+    if (v != v) return ~0ull;
+    if (v == -__builtin_huge_val()) return 0ull;
+    const long long b = __double_as_longlong(v + 0.0);
+    return static_cast<unsigned long long>(b) ^ (static_cast<unsigned long long>(b >> 63) | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ double value64(unsigned long long o) {
+    if (o == ~0ull) return __longlong_as_double(0x7ff8000000000000ll);
+    return __longlong_as_double(static_cast<long long>(o >> 63 ? o ^ 0x8000000000000000ull : ~o));
+}
+
+__device__ __forceinline__ unsigned long long max64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+__device__ __forceinline__ unsigned long long min64(unsigned long long a, unsigned long long b) { return a < b ? a : b; }
+
+// The k choices of the row at `row` in 64 bits: lane i gets the i-th expert, or -1.  Every lane of the warp calls it; a row
+// that need not choose (!wanted) takes part and gets nothing.  n: this lane's experts e0, e0 + 1, ...
+template <int DT, int L, int V, bool SIGMOID>
+__device__ __noinline__ int choose_in_64(const ScoredArgs& a, const uint8_t* row, int e0, int n, bool wanted) {
+    const int lane = threadIdx.x % 32, in = lane % L;
+    if (!wanted) n = 0;
+    const bool by_logit = a.bias == nullptr;
+    double m = -__builtin_huge_val(), total = 1.0;
+    if constexpr (!SIGMOID) {
+        auto top = [](double p, double q) { return p != p ? p : q != q ? q : p > q ? p : q; };
+        for (int j = 0; j < n; ++j) m = top(m, Logits<DT, V>::one(row, e0 + j));
+        for (int d = L / 2; d > 0; d >>= 1) m = top(m, __shfl_xor_sync(FULL, m, d));
+        if (m == -__builtin_huge_val()) m = 0.0;
+        total = 0.0;
+        for (int j = 0; j < n; ++j) total += exp(Logits<DT, V>::one(row, e0 + j) - m);
+        for (int d = L / 2; d > 0; d >>= 1) total += __shfl_xor_sync(FULL, total, d);
+    }
+    unsigned long long key[V];
+    unsigned long long first = 0ull, second = 0ull;           // the lane's largest v
+    for (int j = 0; j < V; ++j) {
+        key[j] = 0ull;
+        if (j >= n) continue;
+        const double x = Logits<DT, V>::one(row, e0 + j);
+        if (x == -__builtin_huge_val()) continue;
+        double v = SIGMOID ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / total;
+        if (a.bias) v += static_cast<double>(a.bias[e0 + j]);
+        const unsigned long long by_v = order64(v), by_x = order64(x);
+        key[j] = by_logit ? by_x : by_v;
+        const unsigned long long o = by_logit && a.group_top == 1 ? by_x : by_v;
+        second = max64(second, min64(first, o));
+        first = max64(first, o);
+    }
+    if (a.groups > 1) {
+        const int lanes = (1 << a.shift) / V;
+        for (int d = 1; d < lanes; d <<= 1) {
+            const unsigned long long f = __shfl_xor_sync(FULL, first, d), g = __shfl_xor_sync(FULL, second, d);
+            second = max64(min64(first, f), max64(second, g));
+            first = max64(first, f);
+        }
+        unsigned long long score = first;
+        if (a.group_top == 2 && second != 0ull) score = order64(value64(first) + value64(second));
+        const int mine = in * V >> a.shift;
+        int before = 0;
+        for (int h = 0; h < a.groups; ++h) {
+            const unsigned long long o = __shfl_sync(FULL, score, h * lanes, L);
+            before += o > score || (o == score && h < mine) ? 1 : 0;
+        }
+        if (score == 0ull || before >= a.top_groups)
+            for (int j = 0; j < V; ++j) key[j] = 0ull;
+    }
+    int my_e = -1;
+    for (int i = 0; i < a.r.k; ++i) {
+        unsigned long long best = 0ull;
+        int at = 0;
+        for (int j = 0; j < V; ++j)
+            if (key[j] > best) { best = key[j]; at = j; }
+        unsigned long long top = best;
+        for (int d = L / 2; d > 0; d >>= 1) top = max64(top, __shfl_xor_sync(FULL, top, d));
+        const int who = __ffs(row_ballot<L>(best == top, lane, in)) - 1;     // the lowest lane holds the lowest indices
+        const int e = __shfl_sync(FULL, e0 + at, who, L);
+        if (top != 0ull) {
+            if (in == i) my_e = e;
+            if (in == who) key[at] = 0ull;
+        }
+    }
+    return my_e;
+}
+
+template <int DT, int L, int V, bool SIGMOID>
+__global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const __grid_constant__ ScoredArgs s) {
+    ptx::grid_launch_dependents();
+    const RouterArgs& a = s.r;
+    using X = Logits<DT, V>;
+    constexpr int SPAN = L * V;                   // positions of a row
+    constexpr int ROWS = 32 / L;                  // rows of a warp at once
+    constexpr uint32_t LOW = SPAN - 1 > 255 ? SPAN - 1 : 255;      // a key's bits of the position
+    constexpr int LOW_BITS = SPAN > 512 ? 10 : SPAN > 256 ? 9 : 8;
+    constexpr float E = SIGMOID ? 3.0e-7f : 1.0e-6f;               // a score's error
+    constexpr float U = 5.9604645e-8f;                             // 2^-24
+    constexpr float FIXED = static_cast<float>(1u << (30 - LOW_BITS));
+    // keys this near are not told apart: both scores' errors, v - lo's (below 4, two roundings), and the cut to fixed point
+    constexpr uint32_t NEAR = static_cast<uint32_t>(FIXED * 2.0f * (E + 8.0f * U)) + 2;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    float* s_sum = reinterpret_cast<float*>(dyn);                              // [warps][SPAN]
+    int32_t* s_count = reinterpret_cast<int32_t*>(s_sum + R_WARPS * SPAN);     // [SPAN], by expert
+    __shared__ int32_t s_rows[R_WARPS];
+    __shared__ double s_loss[R_WARPS];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, in = lane % L;
+    for (int i = threadIdx.x; i < SPAN; i += R_THREADS) s_count[i] = 0;
+    __syncthreads();
+
+    const int first = in * V;                     // this lane's positions [first, first + V): experts e0 and on, n of them
+    const int group = first >> s.shift, off = first & ((1u << s.shift) - 1u);
+    const int e0 = group * s.each + off;
+    const int n = group >= s.groups || s.each <= off ? 0 : s.each - off < V ? s.each - off : V;
+    auto expert_of = [&](uint32_t key) {
+        const uint32_t p = LOW - (key & LOW);
+        return static_cast<int>((p >> s.shift) * s.each + (p & ((1u << s.shift) - 1u)));
+    };
+    const bool biased = s.bias != nullptr;
+    float b[V], lo = 0.0f;
+    bool odd = false;                             // a bias of NaN or +infinity: 64 bits sort it out
+    if (biased) {
+        float small = __int_as_float(0x7f800000), large = MINUS_INF;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            b[j] = j < n ? __ldg(s.bias + e0 + j) : 0.0f;
+            odd |= b[j] != b[j] || b[j] == __int_as_float(0x7f800000);
+            if (j < n && fabsf(b[j]) < __int_as_float(0x7f800000)) {
+                small = fminf(small, b[j]);
+                large = fmaxf(large, b[j]);
+            }
+        }
+        odd = __any_sync(FULL, odd);
+        small = -group_max_plain<L>(-small);
+        large = group_max_plain<L>(large);
+        if (large > MINUS_INF) lo = fmaxf(small, large - 2.5f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) b[j] -= lo;
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) b[j] = 0.0f;
+    }
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R_WARPS * ROWS;
+    // (a warp's rows are neighbours; lanes past the last row keep -infinity and store nothing)
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
+    const int64_t warp_first = t - lane / L;
+    X next;
+    const bool whole_rows = a.vec && a.G == SPAN;      // every lane of every row loads V logits
+    auto fetch = [&](int64_t row) {
+        const uint8_t* at = a.logits + row * a.ld_bytes + static_cast<int64_t>(e0) * X::ESIZE;
+        if (whole_rows && row - lane / L + ROWS <= a.T) next.load_whole(at);
+        else next.load(at, row < a.T ? n : 0, a.vec != 0);
+    };
+    fetch(t);
+    float sum[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+    int rows = 0;
+    for (int64_t base = warp_first; base < a.T; base += step, t += step) {
+        const X x = next;
+        if (base + step < a.T) fetch(t + step);
+        float v[V];                               // the scores, then v - lo
+        float m = 0.0f, whole = 0.0f;
+        bool any = false;
+        if constexpr (SIGMOID) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] = sigmoid_approx(x.value(j));
+                any |= x.value(j) != MINUS_INF;
+                whole += v[j];
+            }
+            any = row_ballot<L>(any, lane, in) != 0u;
+        } else {
+            m = x.value(0);                       // the row's largest logit, NaN if it has one
+#pragma unroll
+            for (int j = 1; j < V; ++j) m = max_nan(m, x.value(j));
+            m = group_max_nan<L>(m);
+            any = m != MINUS_INF;
+            m = any ? m : 0.0f;                   // (e^(-infinity - 0) = 0)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] = exp_flush(x.value(j) - m);
+                whole += v[j];
+            }
+        }
+        whole = group_sum<L>(whole);
+        const float inv = whole != 0.0f ? 1.0f / whole : 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if constexpr (SIGMOID) {
+                sum[j] = fmaf(v[j], inv, sum[j]);
+            } else {
+                v[j] *= inv;
+                sum[j] += v[j];
+            }
+        }
+        rows += any && in == 0 ? 1 : 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = x.value(j) == MINUS_INF ? MINUS_INF : v[j] + b[j];
+
+        bool redo = whole != whole || (odd && any), kept = true;
+        if (s.groups > 1) {
+            const int lanes = (1 << s.shift) / V;
+            const bool exact = !biased && s.group_top == 1;        // the largest logit: nothing is rounded
+            float one, two = MINUS_INF;
+            if (exact) {
+                one = x.value(0);
+#pragma unroll
+                for (int j = 1; j < V; ++j) one = fmaxf(one, x.value(j));
+                for (int d = 1; d < lanes; d <<= 1) one = fmaxf(one, __shfl_xor_sync(FULL, one, d));
+            } else {
+                one = v[0];
+#pragma unroll
+                for (int j = 1; j < V; ++j) {
+                    two = fmaxf(two, fminf(one, v[j]));
+                    one = fmaxf(one, v[j]);
+                }
+                for (int d = 1; d < lanes; d <<= 1) {
+                    const float o = __shfl_xor_sync(FULL, one, d), p = __shfl_xor_sync(FULL, two, d);
+                    two = fmaxf(fminf(one, o), fmaxf(two, p));
+                    one = fmaxf(one, o);
+                }
+            }
+            float score = one, near = 0.0f;
+            if (!exact) {
+                if (s.group_top == 2) score += two > MINUS_INF ? two : -lo;         // (of sums less 2 lo)
+                // twice a sum's error: scores, biases less lo, the sum itself, and lo where it stands alone
+                near = 4.0f * (E + 8.0f * U) + 8.0f * U * fabsf(score) + 4.0f * U * fabsf(lo);
+                if (!(near < __int_as_float(0x7f800000))) near = 0.0f;              // (no expert that may be chosen)
+            }
+            const int mine = first >> s.shift;
+            int before = 0, maybe = 0;            // groups that come first for certain, and possibly
+            for (int h = 0; h < s.groups; ++h) {
+                const float o = __shfl_sync(FULL, score, h * lanes, L);
+                if (exact) {
+                    before += o > score || (o == score && h < mine) ? 1 : 0;
+                } else {
+                    const float gap = o - score;
+                    // (near is that of the larger score of the two to within its own size: twice it covers both)
+                    before += gap > 2.0f * near ? 1 : 0;
+                    maybe += h != mine && o > MINUS_INF && gap >= -2.0f * near ? 1 : 0;
+                }
+            }
+            const bool none = !(score > MINUS_INF);
+            kept = !none && before < s.top_groups;
+            if (!exact)
+                redo |= row_ballot<L>(!none && group < s.groups && before < s.top_groups && maybe >= s.top_groups, lane, in) != 0u;
+        }
+
+        // the i-th choice ends up with lane i of the row; one more is looked at, to see that the last one is apart from it
+        const uint32_t key_min = biased ? LOW + 1 : KEY_MIN;
+        uint32_t key[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            uint32_t high;
+            if (biased) {
+                const uint32_t fixed = max(__float2uint_rz(v[j] * FIXED), 1u);
+                high = v[j] > MINUS_INF ? fixed << LOW_BITS : 0u;
+            } else {
+                high = order_bits(x.value(j)) & ~LOW;
+            }
+            key[j] = (kept ? high : 0u) | (LOW - static_cast<uint32_t>(first + j));
+        }
+        uint32_t mine = 0u, top = 0u;
+        for (int i = 0; i <= a.k; ++i) {
+            uint32_t best = 0u;
+#pragma unroll
+            for (int j = 0; j < V; ++j) best = __viaddmax_u32(key[j], 0u - top, best);
+            top += group_max<L>(best);
+            if (in == i) mine = top;
+        }
+        // lane k (or, when there is none, every lane) has the first key left out
+        int my_e = mine >= key_min ? expert_of(mine) : -1;
+        if (DT == TG_F32 || biased) {
+            uint32_t after = __shfl_down_sync(FULL, mine, 1, L);
+            if (in == L - 1) after = top;
+            const uint32_t apart = (mine >> LOW_BITS) - (after >> LOW_BITS);
+            // (what lies below lo has the lowest key: it is never told apart)
+            bool close = in < a.k && after >= key_min && (biased ? apart <= NEAR || after >> LOW_BITS == 1u : apart == 0u);
+            if (__any_sync(FULL, close)) {
+                if (close) {
+                    const int e = expert_of(after);
+                    const uint8_t* row = a.logits + t * a.ld_bytes;
+                    const bool tie = X::one(row, my_e) == X::one(row, e) && (!biased || __ldg(s.bias + my_e) == __ldg(s.bias + e));
+                    close = !tie;
+                }
+                redo |= row_ballot<L>(close, lane, in) != 0u;
+            }
+        }
+        if (__any_sync(FULL, redo)) {
+            const int e = choose_in_64<DT, L, V, SIGMOID>(s, a.logits + t * a.ld_bytes, e0, n, redo);
+            if (redo) my_e = e;
+        }
+        float my_s = 0.0f;
+        if (in >= a.k) my_e = -1;
+        if (my_e >= 0) {
+            const float z = X::one(a.logits + t * a.ld_bytes, my_e);
+            my_s = SIGMOID ? 1.0f / (1.0f + __expf(-z)) : __expf(z - m) * inv;
+            atomicAdd(&s_count[my_e], 1);
+        }
+        const float chosen = a.renorm ? group_sum<L>(my_s) : 1.0f;
+        if (in < a.k && t < a.T) {
+            a.experts[t * a.k + in] = my_e;
+            a.weights[t * a.k + in] = my_s != 0.0f ? my_s / chosen * s.factor : 0.0f;
+        }
+    }
+    // the row slots of a warp, then the warps of the block
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int d = L; d < 32; d <<= 1) sum[j] += __shfl_xor_sync(FULL, sum[j], d);
+        if (lane < L) s_sum[warp * SPAN + first + j] = sum[j];
+    }
+    rows = __reduce_add_sync(FULL, rows);
+    if (lane == 0) s_rows[warp] = rows;
+    __syncthreads();
+    int block_rows = 0;
+#pragma unroll
+    for (int w = 0; w < R_WARPS; ++w) block_rows += s_rows[w];
+    double loss = 0.0, per_count = 0.0;
+    if (!a.part_p && warp * 32 < a.G) per_count = slope_per_count(a, block_rows);
+    for (int g = threadIdx.x; g < a.G; g += R_THREADS) {
+        const int p = s.groups > 1 ? (g / s.each << s.shift) + g % s.each : g;
+        float f = 0.0f;
+#pragma unroll
+        for (int w = 0; w < R_WARPS; ++w) f += s_sum[w * SPAN + p];
+        if (a.part_p) {
+            a.part_p[static_cast<int64_t>(blockIdx.x) * a.G + g] = f;
+            a.part_c[static_cast<int64_t>(blockIdx.x) * a.G + g] = s_count[g];
+        } else {
+            loss += finish_expert(a, g, f, s_count[g], per_count);
+        }
+    }
+    if (a.part_p) {
+        if (threadIdx.x == 0) a.part_n[blockIdx.x] = block_rows;
+        return;
+    }
+    // the only block finishes the loss itself
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) loss += __shfl_xor_sync(FULL, loss, d);
+    if (lane == 0) s_loss[warp] = loss;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < R_WARPS; ++w) loss += s_loss[w];
+        *a.loss = static_cast<float>(loss);
+    }
+}
+
+struct SigmoidBackArgs {
+    const uint8_t* logits;
+    int64_t ld_bytes, T;
+    int G, k, renorm, vec_in, vec_out;
+    const int32_t* experts;
+    const float* slope;
+    const float* d_weights;   // null: zero
+    const float* d_loss;      // null: zero
+    uint8_t* out;
+    int64_t ldo_bytes;
+    float factor;
+};
+
+template <int DT, int L, int V>
+__global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_kernel(const SigmoidBackArgs a) {
+    using X = Logits<DT, V>;
+    constexpr int ROWS = 32 / L;
+    // per warp: the gradient of the chosen experts' scores through the weights, by expert; zero elsewhere
+    extern __shared__ __align__(16) uint8_t dyn[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, in = lane % L;
+    float* extra = reinterpret_cast<float*>(dyn) + warp * 32 * V + (lane / L) * L * V;
+    const int first = in * V;
+    const int n = a.G - first < 0 ? 0 : a.G - first < V ? a.G - first : V;
+    const float dl = a.d_loss ? __ldg(a.d_loss) : 0.0f;
+    float u[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        u[j] = (a.d_loss && j < n) ? dl * __ldg(a.slope + first + j) : 0.0f;
+        extra[first + j] = 0.0f;
+    }
+    __syncwarp();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R_WARPS * ROWS;
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
+    const int64_t warp_first = t - lane / L;
+    const bool choice = a.d_weights != nullptr && in < a.k;
+    X next;
+    int e_next = -1;
+    float z_next = 0.0f, dw_next = 0.0f;
+    auto fetch = [&](int64_t row) {
+        const uint8_t* at = a.logits + row * a.ld_bytes;
+        next.load(at + first * X::ESIZE, row < a.T ? n : 0, a.vec_in != 0);
+        e_next = -1;
+        if (choice && row < a.T) {
+            e_next = __ldg(a.experts + row * a.k + in);
+            dw_next = __ldg(a.d_weights + row * a.k + in);
+        }
+        if (e_next < 0 || e_next >= a.G) {       // no choice (-1): nothing of it counts
+            e_next = -1;
+            dw_next = 0.0f;
+        } else {
+            z_next = X::one(at, e_next);
+        }
+    };
+    fetch(t);
+    for (int64_t base = warp_first; base < a.T; base += step, t += step) {
+        const X x = next;
+        const int e = e_next;
+        const float z = z_next, dw = dw_next;
+        if (base + step < a.T) fetch(t + step);
+        float p[V], rest[V];                     // s, and 1 - s
+        float whole = 0.0f, pu = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            // (the exponent is held where the reciprocal is a normal number: s below 2^-100 counts as that)
+            const float f = ex2_flush(fminf(x.value(j) * -1.4426950408889634f, 100.0f));
+            p[j] = rcp_flush(1.0f + f);
+            rest[j] = f * p[j];
+            if (x.value(j) != x.value(j)) p[j] = x.value(j);         // (fminf drops a NaN)
+            if (x.value(j) == MINUS_INF) p[j] = 0.0f;
+            whole += p[j];
+            pu = fmaf(p[j], u[j], pu);
+        }
+        whole = group_sum<L>(whole);
+        const float inv = whole != 0.0f ? 1.0f / whole : 0.0f;
+        const float c = group_sum<L>(pu) * inv;
+        if (a.d_weights) {
+            const float my = e >= 0 ? 1.0f / (1.0f + __expf(-z)) : 0.0f;
+            float g = a.factor * dw;
+            if (a.renorm) {
+                const float chosen = group_sum<L>(my), per = chosen != 0.0f ? 1.0f / chosen : 0.0f;
+                g = (g - group_sum<L>(my * g) * per) * per;
+            }
+            if (e >= 0) extra[e] = g;
+            __syncwarp();
+        }
+        float d[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[j] = (u[j] - c) * inv;
+        if (a.d_weights) {
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(extra + first + j);
+                d[j] += f.x; d[j + 1] += f.y; d[j + 2] += f.z; d[j + 3] += f.w;
+            }
+            __syncwarp();
+            if (e >= 0) extra[e] = 0.0f;
+            __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[j] = x.value(j) == MINUS_INF ? 0.0f : p[j] * rest[j] * d[j];
+        if (t >= a.T) continue;
+        uint8_t* dst = a.out + t * a.ldo_bytes + first * X::ESIZE;
+        uint32_t o[X::WORDS];
+#pragma unroll
+        for (int i = 0; i < X::WORDS; ++i) {
+            if constexpr (DT == TG_F32) {
+                o[i] = __float_as_uint(d[i]);
+            } else if constexpr (DT == TG_F16) {
+                const __half2 h = __floats2half2_rn(d[2 * i], d[2 * i + 1]);
+                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
+                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        if (n == V && a.vec_out) {
+#pragma unroll
+            for (int i = 0; i < X::WORDS; i += 4)
+                reinterpret_cast<uint4*>(dst)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (j >= n) continue;
+                if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(dst)[j] = o[j];
+                else reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(o[j / 2] >> ((j & 1) * 16));
+            }
+        }
+    }
+}
+
+using ScoredKernel = void (*)(const ScoredArgs);
+using SigmoidBackKernel = void (*)(const SigmoidBackArgs);
+
+// Positions a lane and lanes a row
+struct Shape {
+    int lanes, per_lane, shift;
+};
+
+// The narrowest row that holds the groups (each in a power of two of positions, a lane's at least) and k choices; false
+// when none does.
+bool shape_for(int64_t groups, int64_t each, int64_t k, Shape* out) {
+    for (int v = 8; v <= 32; v *= 2) {
+        int64_t span = each;
+        int shift = 31;
+        if (groups > 1) {
+            for (shift = 3; (int64_t(1) << shift) < each || (1 << shift) < v; ++shift) {}
+            span = groups << shift;
+        }
+        if (span > 32 * v) continue;
+        int lanes = v == 8 ? 8 : 32;
+        while (lanes * v < span || lanes < k) lanes *= 2;
+        *out = {lanes, v, shift};
+        return true;
+    }
+    return false;
+}
+
+template <int DT, bool SIGMOID>
+ScoredKernel scored_for(const Shape& s) {
+    if (s.per_lane == 32) return &scored_kernel<DT, 32, 32, SIGMOID>;
+    if (s.per_lane == 16) return &scored_kernel<DT, 32, 16, SIGMOID>;
+    return s.lanes == 32 ? &scored_kernel<DT, 32, 8, SIGMOID> : s.lanes == 16 ? &scored_kernel<DT, 16, 8, SIGMOID>
+                                                                             : &scored_kernel<DT, 8, 8, SIGMOID>;
+}
+
+ScoredKernel scored_for(tg_dtype dt, bool sigmoid, const Shape& s) {
+    if (sigmoid)
+        return dt == TG_F32 ? scored_for<TG_F32, true>(s) : dt == TG_F16 ? scored_for<TG_F16, true>(s) : scored_for<TG_BF16, true>(s);
+    return dt == TG_F32 ? scored_for<TG_F32, false>(s) : dt == TG_F16 ? scored_for<TG_F16, false>(s) : scored_for<TG_BF16, false>(s);
+}
+
+template <int DT>
+SigmoidBackKernel back_for(const Shape& s) {
+    if (s.per_lane == 32) return &sigmoid_backward_kernel<DT, 32, 32>;
+    if (s.per_lane == 16) return &sigmoid_backward_kernel<DT, 32, 16>;
+    return s.lanes == 32 ? &sigmoid_backward_kernel<DT, 32, 8> : s.lanes == 16 ? &sigmoid_backward_kernel<DT, 16, 8>
+                                                                              : &sigmoid_backward_kernel<DT, 8, 8>;
+}
+
+tg_status check_scores(tg_score score, float factor) {
+    using host::fail;
+    if (score != TG_SCORE_SOFTMAX && score != TG_SCORE_SIGMOID) return fail(TG_ERR_INVALID_ARG, "bad score %d", int(score));
+    if (!(factor > 0.0f) || factor > 3.0e38f) return fail(TG_ERR_INVALID_ARG, "weight_scale must be finite and positive");
+    return TG_OK;
+}
+
+}  // namespace
+
+}  // namespace tg
+
+extern "C" tg_status tg_moe_router_scored(const tg_router_args* args, tg_stream_t stream) {
+    using namespace tg;
+    using host::fail;
+    if (!args) return fail(TG_ERR_INVALID_ARG, "args is NULL");
+    const tg_router_args& p = *args;
+    tg_status s = check_router(p.logits, p.dtype, p.ld, p.T, p.G, p.k);
+    if (s != TG_OK || (s = check_scores(p.score, p.weight_scale)) != TG_OK) return s;
+    if (p.groups < 1 || p.groups > p.G || p.G % p.groups != 0)
+        return fail(TG_ERR_INVALID_ARG, "groups=%lld does not divide G=%lld", (long long)p.groups, (long long)p.G);
+    const int64_t each = p.G / p.groups;
+    if (p.top_groups < 1 || p.top_groups > p.groups)
+        return fail(TG_ERR_INVALID_ARG, "top_groups=%lld is not in [1, groups=%lld]", (long long)p.top_groups, (long long)p.groups);
+    if (p.group_top < 1 || p.group_top > 2 || p.group_top > each)
+        return fail(TG_ERR_INVALID_ARG, "group_top=%lld is not 1 or 2, or above the %lld experts of a group", (long long)p.group_top,
+                    (long long)each);
+    if (p.k > p.top_groups * each)
+        return fail(TG_ERR_INVALID_ARG, "k=%lld choices from %lld experts in the groups kept", (long long)p.k,
+                    (long long)(p.top_groups * each));
+    if (p.T > 0 && (!p.experts || !p.weights)) return fail(TG_ERR_INVALID_ARG, "%s is NULL", !p.experts ? "experts" : "weights");
+    if (!p.counts || !p.loss || !p.slope)
+        return fail(TG_ERR_INVALID_ARG, "%s is NULL", !p.counts ? "counts" : !p.loss ? "loss" : "slope");
+    if (!host::aligned(p.experts, 4) || !host::aligned(p.weights, 4) || !host::aligned(p.counts, 4) || !host::aligned(p.loss, 4) ||
+        !host::aligned(p.slope, 4) || !host::aligned(p.bias, 4))
+        return fail(TG_ERR_INVALID_ARG, "bias or an output is not 4-byte aligned");
+    Shape shape;
+    if (!shape_for(p.groups, each, p.k, &shape))
+        return fail(TG_ERR_UNSUPPORTED, "%lld groups of %lld experts: groups rounded up to powers of two of 8 at least hold at most %d",
+                    (long long)p.groups, (long long)each, R_MAX_G);
+    host::Device d;
+    if ((s = host::device(&d)) != TG_OK) return s;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t esize = p.dtype == TG_F32 ? 4 : 2;
+    const int64_t block_rows = R_WARPS * (32 / shape.lanes);
+    // one block (no second kernel, no workspace) while it has at most four rows a slot, as the other gate
+    const int64_t want = (p.T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
+    const int blocks = want <= 4 ? 1 : static_cast<int>(want < cap ? want : cap);
+    const int vec = host::aligned(p.logits, 16) && p.ld * esize % 16 == 0 && (p.groups == 1 || each * esize % 16 == 0);
+    ScoredArgs a{{static_cast<const uint8_t*>(p.logits), p.ld * esize, p.T, int(p.G), int(p.k), p.renormalize != 0, vec, p.experts,
+                  p.weights, p.counts, p.loss, p.slope, nullptr, nullptr, nullptr},
+                 p.bias, int(each), shape.shift, int(p.groups), int(p.top_groups), int(p.group_top), p.weight_scale};
+    void* ws = nullptr;
+    if (blocks > 1) {
+        const size_t words = static_cast<size_t>(blocks) * (2 * p.G + 1);
+        if ((s = host::workspace(words * 4, st, "cudaMallocFromPoolAsync(router partial sums)", &ws)) != TG_OK) return s;
+        a.r.part_p = static_cast<float*>(ws);
+        a.r.part_c = static_cast<int32_t*>(ws) + blocks * p.G;
+        a.r.part_n = static_cast<int32_t*>(ws) + 2 * blocks * p.G;
+    }
+    const ScoredKernel kernel = scored_for(p.dtype, p.score == TG_SCORE_SIGMOID, shape);
+    const size_t smem = static_cast<size_t>(R_WARPS + 1) * shape.lanes * shape.per_lane * 4;
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e == cudaSuccess) {
+        kernel<<<blocks, R_THREADS, smem, st>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) {
+        host::count_launches(1);
+        if (blocks > 1) {
+            e = launch_join(a.r, blocks, st);
+            if (e == cudaSuccess) host::count_launches(1);
+        }
+    }
+    s = e == cudaSuccess ? TG_OK : host::cuda_fail(e, "router launch");
+    if (ws) {
+        e = cudaFreeAsync(ws, st);
+        if (e != cudaSuccess && s == TG_OK) s = host::cuda_fail(e, "cudaFreeAsync(router partial sums)");
+    }
+    return s;
+}
+
+extern "C" tg_status tg_moe_router_scored_backward(const tg_router_backward_args* args, tg_stream_t stream) {
+    using namespace tg;
+    using host::fail;
+    if (!args) return fail(TG_ERR_INVALID_ARG, "args is NULL");
+    const tg_router_backward_args& p = *args;
+    tg_status s = check_router(p.logits, p.dtype, p.ld, p.T, p.G, p.k);
+    if (s != TG_OK || (s = check_scores(p.score, p.weight_scale)) != TG_OK || p.T == 0) return s;
+    const bool softmax = p.score == TG_SCORE_SOFTMAX;
+    s = check_backward(p.G, p.dtype, p.experts, p.weights, softmax, p.slope, p.d_weights, p.d_loss, p.d_logits, p.ldd);
+    if (s != TG_OK) return s;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (softmax)
+        return softmax_backward(p.logits, p.dtype, p.ld, p.T, p.G, p.k, p.renormalize, p.weight_scale, p.experts, p.weights, p.slope,
+                                p.d_weights, p.d_loss, p.d_logits, p.ldd, st);
+    host::Device d;
+    if ((s = host::device(&d)) != TG_OK) return s;
+    Shape shape;
+    shape_for(1, p.G, p.k, &shape);
+    const int64_t esize = p.dtype == TG_F32 ? 4 : 2;
+    const SigmoidBackArgs a{static_cast<const uint8_t*>(p.logits), p.ld * esize, p.T, int(p.G), int(p.k), p.renormalize != 0,
+                            host::aligned(p.logits, 16) && p.ld * esize % 16 == 0,
+                            host::aligned(p.d_logits, 16) && p.ldd * esize % 16 == 0, p.experts, p.slope, p.d_weights, p.d_loss,
+                            static_cast<uint8_t*>(p.d_logits), p.ldd * esize, p.weight_scale};
+    const SigmoidBackKernel kernel = p.dtype == TG_F32 ? back_for<TG_F32>(shape) : p.dtype == TG_F16 ? back_for<TG_F16>(shape)
+                                                                                                     : back_for<TG_BF16>(shape);
+    const int64_t block_rows = R_WARPS * (32 / shape.lanes);
+    const int64_t want = (p.T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
+    const size_t smem = static_cast<size_t>(R_WARPS) * 32 * shape.per_lane * 4;
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e == cudaSuccess) {
+        kernel<<<static_cast<unsigned>(want < cap ? want : cap), R_THREADS, smem, st>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return host::cuda_fail(e, "router backward launch");
+    host::count_launches(1);
+    return TG_OK;
+}

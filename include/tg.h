@@ -477,6 +477,72 @@ tg_status tg_moe_router_backward(const void *logits, tg_dtype dtype, int64_t ld,
                                  const float *d_weights, const float *d_loss, void *d_logits, int64_t ldd,
                                  tg_stream_t stream);
 
+typedef enum {
+    TG_SCORE_SOFTMAX = 0,  /* s = softmax of the row's logits */
+    TG_SCORE_SIGMOID = 1   /* s = 1 / (1 + e^-logit) */
+} tg_score;
+
+/*
+ * tg_moe_router_scored - tg_moe_router with other scores, a bias for balance, groups of
+ * experts and a factor on the weights.
+ *
+ * With s[t][g] the score of expert g, v = s + bias[g] what is chosen by (s without a bias), and
+ * the experts in `groups` groups of G / groups neighbours:
+ *   group score  the sum of the group's group_top (1 or 2) largest v above -infinity
+ *   kept         the top_groups groups of largest score, ties to the lowest index
+ *   experts      the k experts of largest v in the kept groups, ties to the lowest index
+ *   weights      weight_scale * s (without the bias), divided by the sum of the row's chosen s
+ *                when renormalize is not 0 (0 where that sum is)
+ *   counts, loss, slope : as tg_moe_router, with p[t][g] = s[t][g] / sum_g s[t][g]
+ * Scores are compared as the real numbers they are, to 64 bits (without a bias, where v rises
+ * with the logit, logits are compared); fp32 rounding decides no choice.  An expert with a
+ * logit or a bias of -infinity is not chosen; v that is NaN counts as above every number.
+ * Scores below 2^-126 may count as 0.  The rest as tg_moe_router.
+ *
+ *   groups divides G; top_groups * (G / groups) >= k; the groups, each rounded up to a power of
+ *   two of 8 experts or more (above 256 of them in all 16, above 512 32), hold at most
+ *   TG_MOE_ROUTER_MAX_EXPERTS.  bias is DEVICE fp32 [G] or NULL.
+ */
+typedef struct tg_router_args {
+    int64_t T, G, k;
+    const void *logits; int64_t ld;
+    const float *bias;
+    int64_t groups, top_groups, group_top;
+    int32_t *experts;
+    float *weights;
+    int32_t *counts;
+    float *loss;
+    float *slope;
+    float weight_scale;   /* finite and positive */
+    tg_dtype dtype;
+    tg_score score;
+    int renormalize;
+} tg_router_args;
+
+tg_status tg_moe_router_scored(const tg_router_args *args, tg_stream_t stream);
+
+/*
+ * tg_moe_router_scored_backward - the gradient of tg_moe_router_scored's logits; arguments as
+ * tg_moe_router_backward.  The choice, and with it the groups and the bias, is constant.  weights
+ * is read with TG_SCORE_SOFTMAX only.
+ */
+typedef struct tg_router_backward_args {
+    int64_t T, G, k;
+    const void *logits; int64_t ld;
+    const int32_t *experts;
+    const float *weights;
+    const float *slope;
+    const float *d_weights;
+    const float *d_loss;
+    void *d_logits; int64_t ldd;
+    float weight_scale;
+    tg_dtype dtype;
+    tg_score score;
+    int renormalize;
+} tg_router_backward_args;
+
+tg_status tg_moe_router_scored_backward(const tg_router_backward_args *args, tg_stream_t stream);
+
 /*
  * Largest number of non-empty problems tg_grouped_gemm_noalloc accepts in one
  * call: the size of its fixed device-side problem table.
