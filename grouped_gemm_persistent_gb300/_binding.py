@@ -121,6 +121,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_moe_router_scored.argtypes = [ctypes.c_char_p, vp]
         lib.tg_moe_router_scored_backward.restype = ci
         lib.tg_moe_router_scored_backward.argtypes = [ctypes.c_char_p, vp]
+        lib.tg_lora_add.restype = ci
+        lib.tg_lora_add.argtypes = [ctypes.c_char_p, vp]
         lib.tg_status_string.restype = ctypes.c_char_p
         lib.tg_status_string.argtypes = [ci]
         lib.tg_last_error_message.restype = ctypes.c_char_p
@@ -598,6 +600,7 @@ _RMSNORM_BACKWARD = struct.Struct("@qq" + 2 * "Qq" + "QQ" + 2 * "Qq" + "Q" + "3i
 
 _ROUTER = struct.Struct("@3q" + "Qq" + "Q" + "3q" + "5Q" + "f3i")                            # tg_router_args
 _ROUTER_BACKWARD = struct.Struct("@3q" + "Qq" + "5Q" + "Qq" + "f3i")                         # tg_router_backward_args
+_LORA = struct.Struct("@5q" + "Qq" + 2 * "Qqq" + "QQ" + 2 * "Qq" + "2i")                     # tg_lora_args
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
@@ -731,6 +734,53 @@ def rmsnorm_backward(normed: Normed, dy: torch.Tensor, gain: torch.Tensor | None
     if status:
         _check(status)
     return out, d_gain
+
+
+def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapters: torch.Tensor,
+             scale: torch.Tensor | None = None, out: torch.Tensor | None = None, *, stream=None) -> torch.Tensor:
+    """out[t] = base[t] + scale[g] * (x[t] @ a[g].T) @ b[g].T with g = adapters[t]: each row's own low-rank adapter beside
+    a shared projection (tg_lora_add).
+
+    ``base`` [T, N] is the projection's result (gemm's or gemm_fp8's), bf16, fp16 or fp32; ``x`` [T, K], ``a`` [G, r, K] and
+    ``b`` [G, N, r] are all bf16 or all fp16, their last dimension contiguous, r at most 128; ``adapters`` is an int32 CUDA
+    tensor [T] in any order (rows of one request side by side are fastest), -1 (or any value outside [0, G)) for a row
+    without; ``scale`` is fp32 [G].  ``out`` (allocated if not given) has base's shape and type and may be ``base``.
+    """
+    xt, bt = _DTYPE_CODE.get(x.dtype), _DTYPE_CODE.get(base.dtype)
+    if xt is None or xt == F32 or a.dtype != x.dtype or b.dtype != x.dtype:
+        raise TypeError("x, a and b must all be torch.bfloat16 or all torch.float16")
+    if bt is None:
+        raise TypeError("base must be bf16, fp16 or fp32")
+    if base.dim() != 2 or x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("shapes: base [T, N], x [T, K], a [G, r, K], b [G, N, r]")
+    T, N = base.shape
+    K = x.shape[1]
+    G, r, _ = a.shape
+    if x.shape[0] != T or a.shape[2] != K or b.shape != (G, N, r):
+        raise ValueError(f"shapes: base [T, N], x [T, K], a [G, r, K], b [G, N, r]; got {list(base.shape)}, {list(x.shape)}, "
+                         f"{list(a.shape)}, {list(b.shape)}")
+    if adapters.dtype != torch.int32 or adapters.shape != (T,) or not adapters.is_contiguous():
+        raise ValueError(f"adapters must be a contiguous int32 tensor {[T]}")
+    if scale is not None and (scale.dtype != torch.float32 or scale.shape != (G,) or not scale.is_contiguous()):
+        raise ValueError(f"scale must be a contiguous fp32 tensor {[G]}")
+    ldx, ldbase = _row_major_ld(x, "x", K), _row_major_ld(base, "base", N)
+    (sa, lda, a1), (sb, ldb, b1) = a.stride(), b.stride()
+    if (a1 != 1 and K > 1) or (b1 != 1 and r > 1):
+        raise ValueError("the last dimension of a and b must be contiguous")
+    if out is None:
+        out, ldo = _rows_of_16_bytes(base, T, N, base.dtype, stream)
+    else:
+        if out.dtype != base.dtype or out.shape != base.shape:
+            raise ValueError("out must have base's shape and type")
+        ldo = _row_major_ld(out, "out", N)
+    _on_one_gpu("base x a b adapters scale out", base, x, a, b, adapters, scale, out)
+    status = load().tg_lora_add(
+        _LORA.pack(T, K, N, r, G, x.data_ptr(), ldx, a.data_ptr(), lda if r > 1 else K, sa if G > 1 else 0, b.data_ptr(),
+                   ldb if N > 1 else r, sb if G > 1 else 0, adapters.data_ptr(), _ptr(scale), base.data_ptr(), ldbase,
+                   out.data_ptr(), ldo, xt, bt), _stream_handle(stream))
+    if status:
+        _check(status)
+    return out
 
 
 class Routing(NamedTuple):

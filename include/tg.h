@@ -543,6 +543,44 @@ typedef struct tg_router_backward_args {
 
 tg_status tg_moe_router_scored_backward(const tg_router_backward_args *args, tg_stream_t stream);
 
+/* Largest rank tg_lora_add accepts. */
+#define TG_LORA_MAX_RANK 128
+
+/*
+ * tg_lora_add - low-rank adapters of many requests beside a shared projection: to the
+ * projection's result for each row (tg_gemm's, tg_gemm_scaled's) the row's own adapter is added,
+ *   out[t] = base[t] + scale[g] * (x[t] . A_g^T) . B_g^T,   g = adapters[t].
+ *
+ *   T, K, N, r, G    : rows, inputs, outputs, rank (<= TG_LORA_MAX_RANK; smaller adapters are
+ *                      padded with zeros) and number of adapters.
+ *   x, ldx           : T x K row-major, dtype (bf16 or fp16), as A and B.
+ *   a, lda, a_stride : A_g, r x K row-major, starts at a + g * a_stride (elements).
+ *   b, ldb, b_stride : B_g, N x r row-major, starts at b + g * b_stride.
+ *   adapters         : DEVICE int32 [T]; a row whose value is not in [0, G) (-1) has none and
+ *                      out[t] is base[t].  Any order; neighbouring rows of one adapter are
+ *                      fastest.
+ *   scale            : DEVICE fp32 [G], or NULL for ones.
+ *   base, out        : T x N row-major, base_dtype (bf16, fp16 or fp32), any alignment, as the
+ *                      other matrices (16-byte aligned rows are moved with wide accesses); out may
+ *                      be base.
+ * Both products are summed in fp32; the one between them is held to 2^-17 (bf16) or better, and
+ * the sum with base is rounded once.  A row's result depends on its own values and adapter alone.
+ * Deterministic.  T == 0 or N == 0 is a no-op; without K, r or G out is base.
+ */
+typedef struct tg_lora_args {
+    int64_t T, K, N, r, G;
+    const void *x;    int64_t ldx;
+    const void *a;    int64_t lda, a_stride;
+    const void *b;    int64_t ldb, b_stride;
+    const int32_t *adapters;
+    const float *scale;
+    const void *base; int64_t ldbase;
+    void *out;        int64_t ldo;
+    tg_dtype dtype, base_dtype;
+} tg_lora_args;
+
+tg_status tg_lora_add(const tg_lora_args *args, tg_stream_t stream);
+
 /*
  * Largest number of non-empty problems tg_grouped_gemm_noalloc accepts in one
  * call: the size of its fixed device-side problem table.
