@@ -8,15 +8,16 @@
 //  - Rows (few rows of small rank): a row's u = x A^T is cut along K over blocks of 512, then a block takes a part of a
 //    row's columns and adds the cuts.  Every row reads its own adapter, from L2 where rows share one: T r (K + N) 2 bytes.
 //    Two launches, the second of which has its part of B and base in registers before it waits for the first.
-//  - Tiles (more rows): a block of eight warps takes 16 or 32 rows.  The warps share K, each adding its part with
-//    mma.sync (the products are few: tensor memory, which one thread feeds from shared-memory tiles, would have to be
-//    refilled for every adapter of a tile); the parts are added in shared memory, u is scaled and cut into two
-//    16-bit numbers, and the warps share the columns of the second product.  A tile whose rows have several adapters
-//    goes through them one after the other, a row keeping only its own's result: a NaN of another adapter or row does
-//    not reach it.
-// Operands come straight from global memory in 16-byte loads: the order of k in a product is free, so a lane's eight
-// neighbouring values stand for the two pairs that each of two mma.sync instructions wants of it; and the order of
-// the columns is free, so a lane's results of four instructions are eight neighbouring columns of a row.
+//  - Tiles (more rows).  A kernel of one block orders the rows by adapter, each adapter's filled up to whole tiles of 16 or 64
+//    rows, so that any order of the rows reads an adapter once a tile.  A cluster takes a tile: its blocks share k,
+//    add their parts of u over distributed shared memory, and share the columns.  k goes through a ring of stages
+//    (cp.async: the rows are gathered) into mma.sync; u is cut into two 16-bit numbers for the second product, whose B comes
+//    straight from global memory.  (mma.sync and not the tensor memory's: the rows are gathered, the products are few,
+//    and an accumulator of 16 to 128 columns is read back after a few thousand cycles.)  A tile may hold several
+//    adapters (more than 512 of them share buckets): it goes through them one after the other, a row keeping only its own's
+//    result, so that a NaN of another adapter or row does not reach it.
+// The order of a product's k and columns is free: a lane's eight neighbouring values of B stand for the two pairs that each of
+// two mma.sync instructions wants of it, and its results of four instructions are eight neighbouring columns of a row.
 //
 // Precision.  u is summed in fp32, times scale, and enters the second product as hi + lo of the operands' type (bf16: 16
 // bits, 2^-17; fp16, of the row's power-of-two multiple that brings its largest value to 1..2: 22 bits): a single 16-bit u would
@@ -88,51 +89,60 @@ __device__ __forceinline__ void store_value(uint8_t* p, int dt, float f) {
     else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(dt == TG_F16 ? round16<TG_F16>(f) : round16<TG_BF16>(f));
 }
 
-// Eight neighbouring values of base or out (plain loads: base may be out)
-__device__ __forceinline__ void load_eight(float (&f)[8], const uint8_t* p, int dt, int n, bool vec) {
-    if (n >= 8 && vec) {
-        const uint4 t = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-        if (dt == TG_F32) {
-            const uint4 s = *(reinterpret_cast<const uint4*>(p) + 1);
-            const uint32_t v[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[i] = __uint_as_float(w[i]);
-                f[4 + i] = __uint_as_float(v[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t b = w[i / 2] >> (i % 2 * 16) & 0xffffu;
-                f[i] = dt == TG_F16 ? widen<TG_F16>(b) : widen<TG_BF16>(b);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < n ? load_value(p + i * type_bytes(dt), dt) : 0.0f;
-}
+// Eight neighbouring values of base and then out, as they lie in memory (plain loads: base may be out)
+template <int BT>
+struct Eight {
+    static constexpr int WORDS = BT == TG_F32 ? 8 : 4;
+    uint32_t w[WORDS];
 
-__device__ __forceinline__ void store_eight(uint8_t* p, const float (&f)[8], int dt, int n, bool vec) {
-    if (n >= 8 && vec) {
-        if (dt == TG_F32) {
-            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-            *(reinterpret_cast<float4*>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-            uint32_t w[4];
+    // n of the eight exist; vec: whole vectors, n a multiple of 8
+    __device__ __forceinline__ void load(const uint8_t* p, int n, bool vec) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = dt == TG_F16 ? round16<TG_F16>(f[2 * i]) | round16<TG_F16>(f[2 * i + 1]) << 16
-                                    : round16<TG_BF16>(f[2 * i]) | round16<TG_BF16>(f[2 * i + 1]) << 16;
-            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+        if (vec) {
+            if (n <= 0) return;
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4) {
+                const uint4 t = *(reinterpret_cast<const uint4*>(p) + i / 4);
+                w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
+            }
+            return;
         }
-        return;
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) store_value(p + i * type_bytes(dt), dt, f[i]);
-}
+        for (int i = 0; i < 8; ++i) {
+            if (i >= n) continue;
+            if constexpr (BT == TG_F32) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+            else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (i % 2 * 16);
+        }
+    }
+    // a and b added to values 2 i and 2 i + 1, in fp32, rounded to the type
+    __device__ __forceinline__ void add2(int i, float a, float b) {
+        if constexpr (BT == TG_F32) {
+            w[2 * i] = __float_as_uint(__uint_as_float(w[2 * i]) + a);
+            w[2 * i + 1] = __float_as_uint(__uint_as_float(w[2 * i + 1]) + b);
+        } else if constexpr (BT == TG_F16) {
+            const __half2 h = __floats2half2_rn(widen<TG_F16>(w[i] & 0xffffu) + a, widen<TG_F16>(w[i] >> 16) + b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + a, __uint_as_float(w[i] & 0xffff0000u) + b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* p, int n, bool vec) const {
+        if (vec) {
+            if (n <= 0) return;
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= n) continue;
+            if constexpr (BT == TG_F32) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+            else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+        }
+    }
+};
 
 template <int DT>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -245,90 +255,270 @@ __global__ void __launch_bounds__(L_THREADS) lora_rows_up_kernel(const LoraArgs 
 
 // ---------------------------------------------------------------------------------------------------------- tiles
 
-// Ranks a block holds: 16, 32, 64 or 128; MT: 16-row parts of its tile
-template <int RT, int MT>
-struct TileShape {
-    static constexpr int ROWS = 16 * MT;
-    static constexpr int SUM_LD = RT + 8;                    // floats of a row of a warp's sums: no two rows of a store meet in a bank
-    static constexpr int U_LD = RT + 8;                      // 16-bit values of a row of u
-    static constexpr int SUM_BYTES = L_WARPS * ROWS * SUM_LD * 4;
-    static constexpr int BYTES = SUM_BYTES + 2 * ROWS * U_LD * 2;
+// Where the tiles' rows are: an adapter's rows side by side in their own order, each bucket of adapters (those that agree
+// modulo `buckets`; the rows without one are a bucket of their own) filled up to whole tiles with -1.
+struct Plan {
+    int2* rows;         // [tiles * tile_rows]: a row, and its adapter or -1
+    int32_t* tiles;
+    int buckets, tile_rows;
 };
 
-template <int DT, int RT, int MT>
-__global__ void __launch_bounds__(L_THREADS, RT <= 64 ? 2 : 1) lora_tile_kernel(const __grid_constant__ LoraArgs p) {
-    using S = TileShape<RT, MT>;
-    constexpr int ROWS = S::ROWS, NT = RT / 8;
-    extern __shared__ __align__(16) uint8_t dyn[];
-    float* sums = reinterpret_cast<float*>(dyn);                                     // [warp][row][rank]
-    uint16_t* u_hi = reinterpret_cast<uint16_t*>(dyn + S::SUM_BYTES);                // [row][rank]
+constexpr int PLAN_WARPS = 32;
+constexpr int PLAN_BATCH = 8;          // rows of a lane in registers
+constexpr int MAX_BUCKETS = 512;
+
+// One block: two passes over the adapters, counting and placing.  A warp's 32 rows are most often one bucket's, which a vote
+// sees; only others take match.any, which is slow.
+__global__ void __launch_bounds__(32 * PLAN_WARPS) lora_plan_kernel(const int32_t* __restrict__ adapters, int64_t T, int G, const Plan plan) {
+    ptx::grid_launch_dependents();
+    extern __shared__ int32_t place[];                           // [warp][bucket], buckets + 1 of them
+    __shared__ int32_t s_scan[PLAN_WARPS];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, count = plan.buckets + 1;
+    int32_t* mine = place + warp * count;
+    for (int i = threadIdx.x; i < PLAN_WARPS * count; i += 32 * PLAN_WARPS) place[i] = 0;
+    __syncthreads();
+    // a warp's rows are neighbours: 32 at a time, the same bucket's in the order of the lanes
+    const int64_t each = (T + 32 * PLAN_WARPS - 1) / (32 * PLAN_WARPS) * 32;
+    const int64_t begin = warp * each, end = begin + each < T ? begin + each : T;
+    auto pass = [&](bool write) {
+        for (int64_t base = begin; base < end; base += 32 * PLAN_BATCH) {
+            int id[PLAN_BATCH];
+#pragma unroll
+            for (int i = 0; i < PLAN_BATCH; ++i) {
+                const int64_t row = base + 32 * i + lane;
+                id[i] = row < end ? adapters[row] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < PLAN_BATCH; ++i) {
+                const int64_t row = base + 32 * i + lane;
+                if (base + 32 * i >= end) break;
+                const bool valid = id[i] >= 0 && id[i] < G;
+                const int key = row >= end ? -1 : !valid ? plan.buckets : G > plan.buckets ? id[i] % plan.buckets : id[i];
+                const uint32_t same = __all_sync(FULL, key == __shfl_sync(FULL, key, 0)) ? FULL : __match_any_sync(FULL, key);
+                const int at = key >= 0 ? mine[key] : 0;
+                const int before = __popc(same & ((1u << lane) - 1u));
+                if (write && key >= 0) plan.rows[at + before] = make_int2(static_cast<int>(row), valid ? id[i] : -1);
+                __syncwarp();
+                if (key >= 0 && before == 0) mine[key] = at + __popc(same);
+                __syncwarp();
+            }
+        }
+    };
+    pass(false);
+    __syncthreads();
+    // a thread a bucket: its rows, and where it starts
+    const int b = threadIdx.x;
+    int n[PLAN_WARPS], total = 0;
+    if (b < count) {
+#pragma unroll
+        for (int w = 0; w < PLAN_WARPS; ++w) n[w] = place[w * count + b];
+#pragma unroll
+        for (int w = 0; w < PLAN_WARPS; ++w) total += n[w];
+    }
+    const int padded = (total + plan.tile_rows - 1) / plan.tile_rows * plan.tile_rows;
+    int start = padded;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(FULL, start, d);
+        if (lane >= d) start += o;
+    }
+    if (lane == 31) s_scan[warp] = start;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) start += s_scan[w];
+    start -= padded;
+    if (b < count) {
+        int at = start;
+#pragma unroll
+        for (int w = 0; w < PLAN_WARPS; ++w) {
+            place[w * count + b] = at;
+            at += n[w];
+        }
+        for (; at < start + padded; ++at) plan.rows[at] = make_int2(-1, -1);
+        if (b == count - 1) *plan.tiles = (start + padded) / plan.tile_rows;
+    }
+    __syncthreads();
+    pass(true);
+}
+
+// A block: RT ranks (16, 32, 64 or 128) and ROWS rows.  Eight warps: WM along the rows, two along the ranks, WK along k.
+template <int RT, int ROWS>
+struct Tile {
+    static constexpr int WM = ROWS / 16, WN = 2, WK = L_WARPS / (WM * WN);
+    static constexpr int NW = RT / 8 / WN;                       // instructions' columns of a warp
+    static constexpr int STAGE = (ROWS + RT) * 128;              // 64 k: 128 bytes of each row of x and of A
+    static constexpr int STAGES = STAGE > 20480 ? 3 : STAGE > 12288 ? 4 : STAGE > 6144 ? 6 : 8;
+    static constexpr int SUM_LD = RT + 8;                        // floats: no two rows of a store meet in a bank
+    static constexpr int U_LD = RT + 8;                          // 16-bit values of a row of u
+    static constexpr int SUM_BYTES = WK * ROWS * SUM_LD * 4;
+    static constexpr int BYTES = STAGES * STAGE + SUM_BYTES;
+    static_assert(2 * ROWS * U_LD * 2 <= STAGES * STAGE, "u takes the stages' place");
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+
+__device__ __forceinline__ void ldmatrix2(uint32_t& r0, uint32_t& r1, uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(at));
+}
+
+// Sixteen bytes of a row into shared memory, n values of them (the rest zero), where they are not copied whole
+__device__ __forceinline__ void copy_values(uint32_t dst, const uint8_t* src, int n) {
+    Half8 h;
+    h.load(src, n, false);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(dst), "r"(h.w[0]), "r"(h.w[1]), "r"(h.w[2]), "r"(h.w[3]) : "memory");
+}
+
+template <int DT, int BT, int RT, int ROWS>
+__global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_constant__ LoraArgs p, const Plan plan) {
+    using S = Tile<RT, ROWS>;
+    extern __shared__ __align__(128) uint8_t dyn[];
+    float* sums = reinterpret_cast<float*>(dyn + S::STAGES * S::STAGE);              // [WK][row][rank]
+    uint16_t* u_hi = reinterpret_cast<uint16_t*>(dyn);                               // [row][rank], once the stages are done
     uint16_t* u_lo = u_hi + ROWS * S::U_LD;
-    __shared__ int s_id[ROWS], s_adapter[ROWS], s_count;
+    __shared__ int s_row[ROWS], s_id[ROWS], s_adapter[ROWS], s_count;
     __shared__ float s_up[ROWS];                                                     // what takes a row's u back to its size
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row8 = lane / 4, quad = lane % 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * ROWS;
-    const int rows = p.T - t0 < ROWS ? static_cast<int>(p.T - t0) : ROWS;
+    const int ctas = static_cast<int>(ptx::cluster_nctarank()), rank = static_cast<int>(ptx::cluster_ctarank());
+    const int tile = blockIdx.x / ctas;
+    ptx::grid_dependency_wait();
+    int2 own = make_int2(-1, -1);
+    if (threadIdx.x < ROWS) own = plan.rows[static_cast<int64_t>(tile) * ROWS + threadIdx.x];
+    if (tile >= *plan.tiles) return;                 // (the whole cluster)
+    if (threadIdx.x < ROWS) {
+        s_row[threadIdx.x] = own.x;
+        s_id[threadIdx.x] = own.y;
+    }
+    __syncthreads();
     if (warp == 0) {
         // the rows' adapters, each once, in the order of their first rows
-        int g = lane < rows ? p.adapters[t0 + lane] : -1;
-        if (!has_adapter(p, g)) g = -1;
-        const uint32_t same = __match_any_sync(FULL, g);
-        const uint32_t first = __ballot_sync(FULL, g >= 0 && __ffs(same) - 1 == lane);
-        if (lane < ROWS) s_id[lane] = g;
-        if (first >> lane & 1u) s_adapter[__popc(first & ((1u << lane) - 1u))] = g;
-        if (lane == 0) s_count = __popc(first);
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < ROWS; i += 32) {
+            const int g = i + lane < ROWS ? s_id[i + lane] : -1;
+            bool seen = g < 0;
+            for (int j = 0; j < count; ++j) seen |= s_adapter[j] == g;
+            const uint32_t same = __match_any_sync(FULL, g);
+            const uint32_t first = __ballot_sync(FULL, !seen && __ffs(same) - 1 == lane);
+            __syncwarp();
+            if (first >> lane & 1u) s_adapter[count + __popc(first & ((1u << lane) - 1u))] = g;
+            count += __popc(first);
+            __syncwarp();
+        }
+        if (lane == 0) s_count = count;
     }
     __syncthreads();
     const int count = s_count;
 
-    // this warp's part of K, a multiple of 32
-    const int blocks = (p.K + 31) / 32;
-    const int k_begin = static_cast<int>(static_cast<int64_t>(blocks) * warp / L_WARPS) * 32;
-    const int k_end = static_cast<int>(static_cast<int64_t>(blocks) * (warp + 1) / L_WARPS) * 32;
-    const uint8_t* xr[2 * MT];
-#pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) xr[m] = p.x + (t0 + m * 8 + row8) * p.ldx;
+    // ---- u = x A^T: this block's part of k, 64 at a time through a ring of stages.  A thread copies the same 16 bytes of a row's
+    // 128 in every stage.
+    constexpr int XN = (ROWS * 8 + L_THREADS - 1) / L_THREADS, AN = (RT * 8 + L_THREADS - 1) / L_THREADS;
+    const int blocks = (p.K + 63) / 64;
+    const int first_block = static_cast<int>(static_cast<int64_t>(blocks) * rank / ctas);
+    const int steps = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / ctas) - first_block;
+    const int wm = warp % S::WM, wn = warp / S::WM % S::WN, wk = warp / (S::WM * S::WN);
+    const uint32_t ring = ptx::smem_u32(dyn);
+    const int my_row = threadIdx.x / 8, k_mine = first_block * 64 + threadIdx.x % 8 * 8;
+    const uint32_t copy_at = ring + my_row * 128 + ((threadIdx.x ^ my_row) & 7) * 16;     // (the same place in every 32nd row on)
+    const uint32_t x_at = ring + (wm * 16 + lane % 16) * 128 + ((lane / 16) ^ lane % 8) * 16;
+    const uint32_t a_at = ring + ROWS * 128 + (wn * S::NW * 8 + lane % 8 + (S::NW > 1 ? lane / 16 * 8 : 0)) * 128 + ((lane / 8 % 2) ^ lane % 8) * 16;
     for (int d = 0; d < count; ++d) {
         const int g = s_adapter[d];
-        const uint8_t* ag = p.a + g * p.a_stride + row8 * p.lda;
-        float acc[MT][NT][4];
+        const uint8_t *xp[XN], *ap[AN];
+        bool x_on[XN], a_on[AN];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < XN; ++i) {
+            const int row = my_row + 32 * i;
+            x_on[i] = row < ROWS && s_id[row < ROWS ? row : 0] == g;
+            xp[i] = p.x + (x_on[i] ? s_row[row] * p.ldx + static_cast<int64_t>(k_mine) * 2 : 0);
+        }
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+        for (int i = 0; i < AN; ++i) {
+            const int row = my_row + 32 * i;
+            a_on[i] = row < p.r;
+            ap[i] = p.a + (a_on[i] ? g * p.a_stride + row * p.lda + static_cast<int64_t>(k_mine) * 2 : 0);
+        }
+        auto fetch = [&](int step, uint32_t slot) {
+            const uint32_t to = copy_at + slot * S::STAGE;
+            const int left = p.K - k_mine - step * 64, n = left < 0 ? 0 : left < 8 ? left : 8;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-#pragma unroll 2
-        for (int k = k_begin; k < k_end; k += 32) {
-            const int kl = k + quad * 8, left = p.K - kl;
-            Half8 x[2 * MT], a[NT];
+            for (int i = 0; i < XN; ++i) {
+                if (ROWS < 32 && threadIdx.x >= ROWS * 8) break;
+                const uint8_t* src = n > 0 && x_on[i] ? xp[i] + static_cast<int64_t>(step) * 128 : p.x;
+                if (p.vec_x) ptx::cp_async_16_part(to + i * 4096, src, x_on[i] ? 2 * n : 0);
+                else copy_values(to + i * 4096, src, x_on[i] ? n : 0);
+            }
 #pragma unroll
-            for (int m = 0; m < 2 * MT; ++m) x[m].load(xr[m] + static_cast<int64_t>(kl) * 2, m * 8 + row8 < rows ? left : 0, p.vec_x);
+            for (int i = 0; i < AN; ++i) {
+                if (RT < 32 && threadIdx.x >= RT * 8) break;
+                const uint8_t* src = n > 0 && a_on[i] ? ap[i] + static_cast<int64_t>(step) * 128 : p.a;
+                if (p.vec_a) ptx::cp_async_16_part(to + ROWS * 128 + i * 4096, src, a_on[i] ? 2 * n : 0);
+                else copy_values(to + ROWS * 128 + i * 4096, src, a_on[i] ? n : 0);
+            }
+        };
+        float acc[S::NW][4];
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                a[j].load(ag + j * 8 * p.lda + static_cast<int64_t>(kl) * 2, j * 8 + row8 < p.r ? left : 0, p.vec_a);
+        for (int j = 0; j < S::NW; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < S::STAGES - 1; ++i) {
+            if (i < steps) fetch(i, i);
+            ptx::cp_async_commit();
+        }
+        uint32_t slot = 0, next = S::STAGES - 1;
+        for (int step = 0; step < steps; ++step) {
+            ptx::cp_async_wait<S::STAGES - 2>();
+            __syncthreads();
+            if (step + S::STAGES - 1 < steps) fetch(step + S::STAGES - 1, next);
+            ptx::cp_async_commit();
+            const uint32_t xs = x_at + slot * S::STAGE, as = a_at + slot * S::STAGE;
+            slot = slot + 1 == S::STAGES ? 0 : slot + 1;
+            next = next + 1 == S::STAGES ? 0 : next + 1;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        mma<DT>(acc[m][j], x[2 * m].w[2 * h], x[2 * m + 1].w[2 * h], x[2 * m].w[2 * h + 1], x[2 * m + 1].w[2 * h + 1],
-                                a[j].w[2 * h], a[j].w[2 * h + 1]);
+            for (int kk = 0; kk < 4; kk += S::WK) {
+                const uint32_t flip = static_cast<uint32_t>(kk + wk) * 32;                 // (chunk ^ row is (chunk's low bit ^ row) ^ its others)
+                uint32_t a[4];
+                ldmatrix4(a, xs ^ flip);
+                if constexpr (S::NW == 1) {
+                    uint32_t b0, b1;
+                    ldmatrix2(b0, b1, as ^ flip);
+                    mma<DT>(acc[0], a[0], a[1], a[2], a[3], b0, b1);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < S::NW; n += 2) {
+                        uint32_t b[4];
+                        ldmatrix4(b, (as ^ flip) + n * 1024);
+                        mma<DT>(acc[n], a[0], a[1], a[2], a[3], b[0], b[1]);
+                        mma<DT>(acc[n + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+                    }
+                }
+            }
         }
         // a row keeps its own adapter's sums
 #pragma unroll
-        for (int m = 0; m < 2 * MT; ++m) {
-            const int row = m * 8 + row8;
+        for (int h = 0; h < 2; ++h) {
+            const int row = wm * 16 + h * 8 + row8;
             if (s_id[row] != g) continue;
-            float* dst = sums + (warp * ROWS + row) * S::SUM_LD + quad * 2;
+            float* dst = sums + (wk * ROWS + row) * S::SUM_LD + wn * S::NW * 8 + quad * 2;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                *reinterpret_cast<float2*>(dst + j * 8) = make_float2(acc[m / 2][j][m % 2 * 2], acc[m / 2][j][m % 2 * 2 + 1]);
+            for (int j = 0; j < S::NW; ++j) *reinterpret_cast<float2*>(dst + j * 8) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+        }
+        __syncthreads();                             // the next adapter's first stages, and u, go where these were
+    }
+    if constexpr (S::WK > 1) {
+        for (int i = threadIdx.x; i < ROWS * RT; i += L_THREADS) {
+            float* at = sums + i / RT * S::SUM_LD + i % RT;
+            float s = at[0];
+#pragma unroll
+            for (int w = 1; w < S::WK; ++w) s += at[w * ROWS * S::SUM_LD];
+            at[0] = s;
         }
     }
-    __syncthreads();
-    // u of a row: the warps' parts added in order, times scale, as hi + lo
+    if (ctas > 1) ptx::cluster_sync();
+    else __syncthreads();
+    // u of a row: the blocks' parts added in order, times scale, as hi + lo
     for (int row = warp; row < ROWS; row += L_WARPS) {
         const int g = s_id[row];
         const float scale = g >= 0 && p.scale ? p.scale[g] : 1.0f;
@@ -340,8 +530,13 @@ __global__ void __launch_bounds__(L_THREADS, RT <= 64 ? 2 : 1) lora_tile_kernel(
             const int j = lane + 32 * i;
             u[i] = 0.0f;
             if (g >= 0 && j < RT) {
-#pragma unroll
-                for (int w = 0; w < L_WARPS; ++w) u[i] += sums[(w * ROWS + row) * S::SUM_LD + j];
+                const float* at = sums + row * S::SUM_LD + j;
+                if (ctas == 1) {
+                    u[i] = *at;
+                } else {
+                    const uint32_t here = ptx::smem_u32(at);
+                    for (int c = 0; c < ctas; ++c) u[i] += __uint_as_float(ptx::ld_cluster_u32(ptx::mapa(here, c)));
+                }
                 u[i] *= scale;
             }
             top = fmaxf(top, fabsf(u[i]));
@@ -367,17 +562,30 @@ __global__ void __launch_bounds__(L_THREADS, RT <= 64 ? 2 : 1) lora_tile_kernel(
         }
         if (lane == 0) s_up[row] = up;
     }
+    if (ctas > 1) ptx::cluster_arrive();             // (no block leaves before the others have read its sums)
     __syncthreads();
 
-    // the columns, 32 a warp and step: a lane has the eight n = quad * 8 and on of its rows
-    const int size = type_bytes(p.dt);
-    for (int n0 = warp * 32; n0 < p.N; n0 += L_WARPS * 32) {
-        const int n = n0 + quad * 8, left = p.N - n;
-        float y[2 * MT][8];
+    // ---- out = base + u B^T: this block's columns, 32 a warp and step; a lane has the eight n = quad * 8 and on of its rows
+    constexpr int MT = ROWS >= 32 ? 2 : 1, SIDES = ROWS / (16 * MT);                 // a warp's 16-row parts; warps beside one another
+    constexpr int SIZE = BT == TG_F32 ? 4 : 2;
+    const int m0 = warp % SIDES * 16 * MT;
+    const int nblocks = (p.N + 31) / 32;
+    const int n_begin = static_cast<int>(static_cast<int64_t>(nblocks) * rank / ctas);
+    const int n_end = static_cast<int>(static_cast<int64_t>(nblocks) * (rank + 1) / ctas);
+    int row[2 * MT], id[2 * MT];
+    float up[2 * MT];
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m) {
+        row[m] = s_row[m0 + m * 8 + row8];
+        id[m] = s_id[m0 + m * 8 + row8];
+        up[m] = s_up[m0 + m * 8 + row8];
+    }
+    for (int nb = n_begin + warp / SIDES; nb < n_end; nb += L_WARPS / SIDES) {
+        const int n0 = nb * 32, n = n0 + quad * 8, left = p.N - n;
+        Eight<BT> y[2 * MT];
 #pragma unroll
         for (int m = 0; m < 2 * MT; ++m)
-            load_eight(y[m], p.base + (t0 + m * 8 + row8) * p.ldbase + static_cast<int64_t>(n) * size, p.dt,
-                       m * 8 + row8 < rows ? left : 0, p.vec_base);
+            y[m].load(p.base + (row[m] < 0 ? 0 : row[m]) * p.ldbase + static_cast<int64_t>(n) * SIZE, row[m] < 0 ? 0 : left, p.vec_base);
         for (int d = 0; d < count; ++d) {
             const int g = s_adapter[d];
             // column c of instruction i stands for n0 + (c / 2) * 8 + 2 i + c % 2
@@ -395,22 +603,24 @@ __global__ void __launch_bounds__(L_THREADS, RT <= 64 ? 2 : 1) lora_tile_kernel(
                 uint2 b[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    Half8 h;
                     const int have = col + 2 * i < p.N ? p.r - quad * 4 : 0;
                     const uint8_t* at = bg + 2 * i * p.ldb + quad * 8;
-                    if (have >= 4 && p.vec_b) b[i] = __ldg(reinterpret_cast<const uint2*>(at));
-                    else {
+                    b[i] = make_uint2(0u, 0u);
+                    if (p.vec_b) {                   // (r is a multiple of 8)
+                        if (have > 0) b[i] = __ldg(reinterpret_cast<const uint2*>(at));
+                    } else {
+                        Half8 h;
                         h.load(at, have < 4 ? have : 4, false);
                         b[i] = make_uint2(h.w[0], h.w[1]);
                     }
                 }
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
-                    const uint16_t* us = part ? u_lo : u_hi;
+                    const uint16_t* us = (part ? u_lo : u_hi) + (m0 + row8) * S::U_LD + quad * 4;
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        const uint2 a = *reinterpret_cast<const uint2*>(us + (m * 16 + row8) * S::U_LD + quad * 4);
-                        const uint2 c = *reinterpret_cast<const uint2*>(us + (m * 16 + 8 + row8) * S::U_LD + quad * 4);
+                        const uint2 a = *reinterpret_cast<const uint2*>(us + m * 16 * S::U_LD);
+                        const uint2 c = *reinterpret_cast<const uint2*>(us + (m * 16 + 8) * S::U_LD);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) mma<DT>(acc[m][i], a.x, c.x, a.y, c.y, b[i].x, b[i].y);
                     }
@@ -418,21 +628,31 @@ __global__ void __launch_bounds__(L_THREADS, RT <= 64 ? 2 : 1) lora_tile_kernel(
             } else {
 #pragma unroll
                 for (int j = 0; j < RT; j += 32) {
-                    Half8 b[4];
+                    uint4 b[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        b[i].load(bg + 2 * i * p.ldb + (j + quad * 8) * 2, col + 2 * i < p.N ? p.r - j - quad * 8 : 0, p.vec_b);
+                    for (int i = 0; i < 4; ++i) {
+                        const int have = col + 2 * i < p.N ? p.r - j - quad * 8 : 0;
+                        const uint8_t* at = bg + 2 * i * p.ldb + (j + quad * 8) * 2;
+                        b[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (p.vec_b) {               // (r is a multiple of 8)
+                            if (have > 0) b[i] = __ldg(reinterpret_cast<const uint4*>(at));
+                        } else {
+                            Half8 h;
+                            h.load(at, have, false);
+                            b[i] = make_uint4(h.w[0], h.w[1], h.w[2], h.w[3]);
+                        }
+                    }
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
-                        const uint16_t* us = part ? u_lo : u_hi;
+                        const uint16_t* us = (part ? u_lo : u_hi) + (m0 + row8) * S::U_LD + j + quad * 8;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            const uint4 a = *reinterpret_cast<const uint4*>(us + (m * 16 + row8) * S::U_LD + j + quad * 8);
-                            const uint4 c = *reinterpret_cast<const uint4*>(us + (m * 16 + 8 + row8) * S::U_LD + j + quad * 8);
+                            const uint4 a = *reinterpret_cast<const uint4*>(us + m * 16 * S::U_LD);
+                            const uint4 c = *reinterpret_cast<const uint4*>(us + (m * 16 + 8) * S::U_LD);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                mma<DT>(acc[m][i], a.x, c.x, a.y, c.y, b[i].w[0], b[i].w[1]);
-                                mma<DT>(acc[m][i], a.z, c.z, a.w, c.w, b[i].w[2], b[i].w[3]);
+                                mma<DT>(acc[m][i], a.x, c.x, a.y, c.y, b[i].x, b[i].y);
+                                mma<DT>(acc[m][i], a.z, c.z, a.w, c.w, b[i].z, b[i].w);
                             }
                         }
                     }
@@ -440,41 +660,43 @@ __global__ void __launch_bounds__(L_THREADS, RT <= 64 ? 2 : 1) lora_tile_kernel(
             }
 #pragma unroll
             for (int m = 0; m < 2 * MT; ++m) {
-                const int row = m * 8 + row8;
-                if (s_id[row] != g) continue;
-                const float up = s_up[row];
+                if (id[m] != g) continue;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[m][2 * i] = fmaf(acc[m / 2][i][m % 2 * 2], up, y[m][2 * i]);
-                    y[m][2 * i + 1] = fmaf(acc[m / 2][i][m % 2 * 2 + 1], up, y[m][2 * i + 1]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    y[m].add2(i, acc[m / 2][i][m % 2 * 2] * up[m], acc[m / 2][i][m % 2 * 2 + 1] * up[m]);
             }
         }
 #pragma unroll
         for (int m = 0; m < 2 * MT; ++m)
-            if (m * 8 + row8 < rows)
-                store_eight(p.out + (t0 + m * 8 + row8) * p.ldo + static_cast<int64_t>(n) * size, y[m], p.dt, left, p.vec_out);
+            if (row[m] >= 0) y[m].store(p.out + row[m] * p.ldo + static_cast<int64_t>(n) * SIZE, left, p.vec_out);
     }
+    if (ctas > 1) ptx::cluster_wait();
 }
 
-using TileKernel = void (*)(const LoraArgs);
+using TileKernel = void (*)(const LoraArgs, const Plan);
 struct TileVariant {
     TileKernel kernel;
     int rows, bytes;
 };
 
-template <int DT, int RT, int MT>
-TileVariant variant() { return {&lora_tile_kernel<DT, RT, MT>, TileShape<RT, MT>::ROWS, TileShape<RT, MT>::BYTES}; }
+template <int DT, int BT, int RT, int ROWS>
+TileVariant variant() { return {&lora_tile_kernel<DT, BT, RT, ROWS>, ROWS, Tile<RT, ROWS>::BYTES}; }
 
-// Tiles of 32 rows read an adapter half as often; they are taken once 16-row tiles are more than two a SM.  (128 ranks:
-// the sums of 32 rows would fill the registers.)
+// Tiles of 64 rows read an adapter a quarter as often; tiles of 16 where an adapter has fewer than 32 rows on average, if all
+// of them are in use.
+template <int DT, int BT>
+TileVariant variant_for(int64_t T, int G, int r) {
+    const bool tall = T >= 32 * static_cast<int64_t>(G);
+    if (r > 64) return tall ? variant<DT, BT, 128, 64>() : variant<DT, BT, 128, 16>();
+    if (r > 32) return tall ? variant<DT, BT, 64, 64>() : variant<DT, BT, 64, 16>();
+    if (r > 16) return tall ? variant<DT, BT, 32, 64>() : variant<DT, BT, 32, 16>();
+    return tall ? variant<DT, BT, 16, 64>() : variant<DT, BT, 16, 16>();
+}
+
 template <int DT>
-TileVariant variant_for(int64_t T, int r, int sms) {
-    const bool wide = (T + 15) / 16 > 2 * sms;
-    if (r > 64) return variant<DT, 128, 1>();
-    if (r > 32) return wide ? variant<DT, 64, 2>() : variant<DT, 64, 1>();
-    if (r > 16) return wide ? variant<DT, 32, 2>() : variant<DT, 32, 1>();
-    return wide ? variant<DT, 16, 2>() : variant<DT, 16, 1>();
+TileVariant variant_for(tg_dtype base, int64_t T, int G, int r) {
+    return base == TG_F32 ? variant_for<DT, TG_F32>(T, G, r) : base == TG_F16 ? variant_for<DT, TG_F16>(T, G, r)
+                                                                              : variant_for<DT, TG_BF16>(T, G, r);
 }
 
 // The rows form reads T r (K + N) 16-bit values through L2, whoever shares an adapter; the tile form streams an adapter
@@ -549,9 +771,9 @@ extern "C" tg_status tg_lora_add(const tg_lora_args* args, tg_stream_t stream) {
     auto vec = [](const void* q, int64_t ld, int64_t stride) { return host::aligned(q, 16) && ld % 16 == 0 && stride % 16 == 0; };
     a.vec_x = vec(p.x, a.ldx, 0);
     a.vec_a = vec(p.a, a.lda, a.a_stride);
-    a.vec_b = vec(p.b, a.ldb, a.b_stride);
-    a.vec_base = vec(p.base, a.ldbase, 0);
-    a.vec_out = vec(p.out, a.ldo, 0);
+    a.vec_b = vec(p.b, a.ldb, a.b_stride) && a.r % 8 == 0;          // (whole vectors only, as of base and out)
+    a.vec_base = vec(p.base, a.ldbase, 0) && a.N % 8 == 0;
+    a.vec_out = vec(p.out, a.ldo, 0) && a.N % 8 == 0;
     cudaError_t e;
     if (any && p.T * p.r <= ROWS_FORM) {
         a.cuts = (a.K + ROW_CUT - 1) / ROW_CUT;
@@ -586,13 +808,48 @@ extern "C" tg_status tg_lora_add(const tg_lora_args* args, tg_stream_t stream) {
         if (e != cudaSuccess && s == TG_OK) s = host::cuda_fail(e, "cudaFreeAsync(adapters' sums)");
         return s;
     }
-    const TileVariant v = p.dtype == TG_F16 ? variant_for<TG_F16>(p.T, a.r, d.sms) : variant_for<TG_BF16>(p.T, a.r, d.sms);
-    e = v.bytes > 48 * 1024 ? cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.bytes) : cudaSuccess;
+    const TileVariant v = p.dtype == TG_F16 ? variant_for<TG_F16>(p.base_dtype, p.T, a.G, a.r)
+                                               : variant_for<TG_BF16>(p.base_dtype, p.T, a.G, a.r);
+    // at most one tile a bucket is not full
+    const int64_t buckets = a.G < 1 ? 1 : a.G < MAX_BUCKETS ? a.G : MAX_BUCKETS;
+    const int64_t used = p.T < buckets + 1 ? p.T : buckets + 1, tiles = (p.T + v.rows - 1) / v.rows + used;
+    if (tiles * v.rows > host::MAX_DIM) return fail(TG_ERR_UNSUPPORTED, "T=%lld rows are too many", (long long)p.T);
+    void* ws = nullptr;
+    if ((s = host::workspace(static_cast<size_t>(tiles * v.rows + 2) * 8, st, "cudaMallocFromPoolAsync(adapters' plan)", &ws)) != TG_OK) return s;
+    const Plan plan{static_cast<int2*>(ws) + 2, static_cast<int32_t*>(ws), int(buckets), v.rows};
+    // Few tiles share each one's k and columns among the blocks of a cluster, up to about two blocks an SM.
+    const int64_t likely = (p.T + v.rows - 1) / v.rows > used - 1 ? (p.T + v.rows - 1) / v.rows : used - 1;
+    int ctas = 1;
+    while (ctas < 8 && likely * ctas * 2 <= 2 * d.sms && a.K >= ctas * 512) ctas *= 2;
+    const int plan_bytes = PLAN_WARPS * int(buckets + 1) * 4;
+    e = plan_bytes > 48 * 1024 ? cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_bytes) : cudaSuccess;
+    if (e == cudaSuccess && v.bytes > 48 * 1024)
+        e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.bytes);
     if (e == cudaSuccess) {
-        v.kernel<<<static_cast<unsigned>((p.T + v.rows - 1) / v.rows), L_THREADS, v.bytes, st>>>(a);
+        lora_plan_kernel<<<1, 32 * PLAN_WARPS, plan_bytes, st>>>(p.adapters, p.T, a.G, plan);
         e = cudaGetLastError();
     }
-    if (e != cudaSuccess) return host::cuda_fail(e, "adapters launch");
-    host::count_launches(1);
-    return TG_OK;
+    if (e == cudaSuccess) {
+        host::count_launches(1);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(tiles * ctas), 1, 1);
+        cfg.blockDim = dim3(L_THREADS, 1, 1);
+        cfg.dynamicSmemBytes = v.bytes;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, v.kernel, static_cast<const LoraArgs&>(a), plan);
+        if (e == cudaSuccess) host::count_launches(1);
+    }
+    s = e == cudaSuccess ? TG_OK : host::cuda_fail(e, "adapters launch");
+    e = cudaFreeAsync(ws, st);
+    if (e != cudaSuccess && s == TG_OK) s = host::cuda_fail(e, "cudaFreeAsync(adapters' plan)");
+    return s;
 }
