@@ -8,7 +8,7 @@
 //  - Rows (few rows of small rank): a row's u = x A^T is cut along K over blocks of 512, then a block takes a part of a
 //    row's columns and adds the cuts.  Every row reads its own adapter, from L2 where rows share one: T r (K + N) 2 bytes.
 //    Two launches, the second of which has its part of B and base in registers before it waits for the first.
-//  - Tiles (more rows).  A kernel of one block orders the rows by adapter, each adapter's filled up to whole tiles of 16 or 64
+//  - Tiles (more rows).  A kernel of one cluster orders the rows by adapter, each adapter's filled up to whole tiles of 16 or 64
 //    rows, so that any order of the rows reads an adapter once a tile.  A cluster takes a tile: its blocks share k,
 //    add their parts of u over distributed shared memory, and share the columns.  k goes through a ring of stages
 //    (cp.async: the rows are gathered) into mma.sync; u is cut into two 16-bit numbers for the second product, whose B comes
@@ -89,30 +89,22 @@ __device__ __forceinline__ void store_value(uint8_t* p, int dt, float f) {
     else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(dt == TG_F16 ? round16<TG_F16>(f) : round16<TG_BF16>(f));
 }
 
-// Eight neighbouring values of base and then out, as they lie in memory (plain loads: base may be out)
-template <int BT>
-struct Eight {
-    static constexpr int WORDS = BT == TG_F32 ? 8 : 4;
+// Neighbouring values of a row of base and then of out, as they lie in memory
+template <int BT, int COUNT>
+struct Columns {
+    static constexpr int SIZE = BT == TG_F32 ? 4 : 2, WORDS = COUNT * SIZE / 4;
     uint32_t w[WORDS];
 
-    // n of the eight exist; vec: whole vectors, n a multiple of 8
-    __device__ __forceinline__ void load(const uint8_t* p, int n, bool vec) {
+    // from column `col` of a row in shared memory whose 16-byte pieces are where piece ^ key says
+    __device__ __forceinline__ void read(uint32_t row, int col, int key) {
+        if constexpr (WORDS == 2) {
+            const int at = col * SIZE;
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(row + (((at / 16) ^ key) * 16) + at % 16));
+        } else {
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
-        if (vec) {
-            if (n <= 0) return;
-#pragma unroll
-            for (int i = 0; i < WORDS; i += 4) {
-                const uint4 t = *(reinterpret_cast<const uint4*>(p) + i / 4);
-                w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i >= n) continue;
-            if constexpr (BT == TG_F32) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-            else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (i % 2 * 16);
+            for (int i = 0; i < WORDS; i += 4)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                             : "r"(row + (((col * SIZE / 16 + i / 4) ^ key) * 16)));
         }
     }
     // a and b added to values 2 i and 2 i + 1, in fp32, rounded to the type
@@ -128,15 +120,20 @@ struct Eight {
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
+    // n of them exist; vec: whole vectors, n a multiple of their count
     __device__ __forceinline__ void store(uint8_t* p, int n, bool vec) const {
         if (vec) {
             if (n <= 0) return;
+            if constexpr (WORDS == 2) {
+                *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < WORDS; i += 4) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                for (int i = 0; i < WORDS; i += 4) reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            }
             return;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < COUNT; ++i) {
             if (i >= n) continue;
             if constexpr (BT == TG_F32) reinterpret_cast<uint32_t*>(p)[i] = w[i];
             else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
@@ -266,20 +263,26 @@ struct Plan {
 constexpr int PLAN_WARPS = 32;
 constexpr int PLAN_BATCH = 8;          // rows of a lane in registers
 constexpr int MAX_BUCKETS = 512;
+constexpr int MAX_CTAS = 8;            // of a tile's cluster
 
-// One block: two passes over the adapters, counting and placing.  A warp's 32 rows are most often one bucket's, which a vote
-// sees; only others take match.any, which is slow.
-__global__ void __launch_bounds__(32 * PLAN_WARPS) lora_plan_kernel(const int32_t* __restrict__ adapters, int64_t T, int G, const Plan plan) {
+// A cluster's blocks, and a block's warps, take neighbouring rows: two passes, counting and placing.  A warp's 32 rows are most
+// often one bucket's, which a vote sees; only others take match.any, which is slow.  (One block of 32 warps is short of issue
+// slots: 9 us for 8191 rows.)
+constexpr int PLAN_CTAS = 8;
+
+__global__ void __cluster_dims__(PLAN_CTAS, 1, 1) __launch_bounds__(32 * PLAN_WARPS)
+    lora_plan_kernel(const int32_t* __restrict__ adapters, int64_t T, int G, const Plan plan) {
     ptx::grid_launch_dependents();
     extern __shared__ int32_t place[];                           // [warp][bucket], buckets + 1 of them
-    __shared__ int32_t s_scan[PLAN_WARPS];
+    __shared__ int32_t s_scan[PLAN_WARPS], s_total[MAX_BUCKETS + 1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, count = plan.buckets + 1;
+    const uint32_t rank = ptx::cluster_ctarank();
     int32_t* mine = place + warp * count;
     for (int i = threadIdx.x; i < PLAN_WARPS * count; i += 32 * PLAN_WARPS) place[i] = 0;
     __syncthreads();
-    // a warp's rows are neighbours: 32 at a time, the same bucket's in the order of the lanes
-    const int64_t each = (T + 32 * PLAN_WARPS - 1) / (32 * PLAN_WARPS) * 32;
-    const int64_t begin = warp * each, end = begin + each < T ? begin + each : T;
+    constexpr int CHUNK = 32 * PLAN_WARPS * PLAN_CTAS;
+    const int64_t each = (T + CHUNK - 1) / CHUNK * 32;
+    const int64_t begin = (static_cast<int64_t>(rank) * PLAN_WARPS + warp) * each, end = begin + each < T ? begin + each : T;
     auto pass = [&](bool write) {
         for (int64_t base = begin; base < end; base += 32 * PLAN_BATCH) {
             int id[PLAN_BATCH];
@@ -308,13 +311,26 @@ __global__ void __launch_bounds__(32 * PLAN_WARPS) lora_plan_kernel(const int32_
     __syncthreads();
     // a thread a bucket: its rows, and where it starts
     const int b = threadIdx.x;
-    int n[PLAN_WARPS], total = 0;
+    int n[PLAN_WARPS], total = 0, ahead = 0;
     if (b < count) {
 #pragma unroll
         for (int w = 0; w < PLAN_WARPS; ++w) n[w] = place[w * count + b];
 #pragma unroll
         for (int w = 0; w < PLAN_WARPS; ++w) total += n[w];
+        s_total[b] = total;
     }
+    ptx::cluster_sync();
+    if (b < count) {
+        const uint32_t here = ptx::smem_u32(s_total + b);
+        total = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < PLAN_CTAS; ++c) {
+            const int other = static_cast<int>(ptx::ld_cluster_u32(ptx::mapa(here, c)));
+            total += other;
+            ahead += c < rank ? other : 0;
+        }
+    }
+    ptx::cluster_arrive();                                       // (no block leaves before the others have read its totals)
     const int padded = (total + plan.tile_rows - 1) / plan.tile_rows * plan.tile_rows;
     int start = padded;
 #pragma unroll
@@ -327,31 +343,40 @@ __global__ void __launch_bounds__(32 * PLAN_WARPS) lora_plan_kernel(const int32_
     for (int w = 0; w < warp; ++w) start += s_scan[w];
     start -= padded;
     if (b < count) {
-        int at = start;
+        int at = start + ahead;
 #pragma unroll
         for (int w = 0; w < PLAN_WARPS; ++w) {
             place[w * count + b] = at;
             at += n[w];
         }
-        for (; at < start + padded; ++at) plan.rows[at] = make_int2(-1, -1);
-        if (b == count - 1) *plan.tiles = (start + padded) / plan.tile_rows;
+        if (rank == 0) {
+            for (int i = total; i < padded; ++i) plan.rows[start + i] = make_int2(-1, -1);
+            if (b == count - 1) *plan.tiles = (start + padded) / plan.tile_rows;
+        }
     }
     __syncthreads();
     pass(true);
+    ptx::cluster_wait();
 }
 
-// A block: RT ranks (16, 32, 64 or 128) and ROWS rows.  Eight warps: WM along the rows, two along the ranks, WK along k.
-template <int RT, int ROWS>
+// A block: RT ranks (16, 32, 64 or 128) and ROWS rows.  Eight warps.  First product: WM along the rows, two along the ranks, WK
+// along k.  Second: WM along the rows, the others along the columns, TILES instructions of eight columns each.
+template <int RT, int ROWS, int SIZE>
 struct Tile {
     static constexpr int WM = ROWS / 16, WN = 2, WK = L_WARPS / (WM * WN);
-    static constexpr int NW = RT / 8 / WN;                       // instructions' columns of a warp
+    static constexpr int NW = RT / 8 / WN;                       // instructions' columns of a warp in the first product
     static constexpr int STAGE = (ROWS + RT) * 128;              // 64 k: 128 bytes of each row of x and of A
-    static constexpr int STAGES = STAGE > 20480 ? 3 : STAGE > 12288 ? 4 : STAGE > 6144 ? 6 : 8;
+    static constexpr int STAGES = STAGE > 18432 ? 3 : STAGE > 12288 ? 4 : STAGE > 6144 ? 6 : 8;
+    static constexpr int TILES = WM == 4 ? 4 : 2, COLS = L_WARPS / WM * TILES * 8;
+    static constexpr int BASE_ROW = COLS * SIZE;                 // bytes of a row's part of base
+    static constexpr int OUT_STAGE = COLS * RT * 2 + ROWS * BASE_ROW;
+    static constexpr int FIT = STAGES * STAGE / OUT_STAGE;
+    static constexpr int OUT_STAGES = FIT < 2 ? 2 : FIT > 6 ? 6 : FIT;
+    static constexpr int RING = STAGES * STAGE > OUT_STAGES * OUT_STAGE ? STAGES * STAGE : OUT_STAGES * OUT_STAGE;
     static constexpr int SUM_LD = RT + 8;                        // floats: no two rows of a store meet in a bank
     static constexpr int U_LD = RT + 8;                          // 16-bit values of a row of u
     static constexpr int SUM_BYTES = WK * ROWS * SUM_LD * 4;
-    static constexpr int BYTES = STAGES * STAGE + SUM_BYTES;
-    static_assert(2 * ROWS * U_LD * 2 <= STAGES * STAGE, "u takes the stages' place");
+    static constexpr int BYTES = RING + SUM_BYTES + 2 * ROWS * U_LD * 2;
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
@@ -370,13 +395,26 @@ __device__ __forceinline__ void copy_values(uint32_t dst, const uint8_t* src, in
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(dst), "r"(h.w[0]), "r"(h.w[1]), "r"(h.w[2]), "r"(h.w[3]) : "memory");
 }
 
+// The same of values of SIZE bytes: 16 bytes, n values of them
+template <int SIZE>
+__device__ __forceinline__ void copy_piece(uint32_t dst, const uint8_t* src, int n) {
+    if constexpr (SIZE == 2) {
+        copy_values(dst, src, n);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = i < n ? reinterpret_cast<const uint32_t*>(src)[i] : 0u;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+}
+
 template <int DT, int BT, int RT, int ROWS>
 __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_constant__ LoraArgs p, const Plan plan) {
-    using S = Tile<RT, ROWS>;
+    constexpr int SIZE = BT == TG_F32 ? 4 : 2;
+    using S = Tile<RT, ROWS, SIZE>;
     extern __shared__ __align__(128) uint8_t dyn[];
-    float* sums = reinterpret_cast<float*>(dyn + S::STAGES * S::STAGE);              // [WK][row][rank]
-    uint16_t* u_hi = reinterpret_cast<uint16_t*>(dyn);                               // [row][rank], once the stages are done
-    uint16_t* u_lo = u_hi + ROWS * S::U_LD;
+    float* sums = reinterpret_cast<float*>(dyn + S::RING);                           // [WK][row][rank]
+    uint16_t* u_hi = reinterpret_cast<uint16_t*>(dyn + S::RING + S::SUM_BYTES);      // [row][rank], and u_lo behind it
     __shared__ int s_row[ROWS], s_id[ROWS], s_adapter[ROWS], s_count;
     __shared__ float s_up[ROWS];                                                     // what takes a row's u back to its size
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row8 = lane / 4, quad = lane % 4;
@@ -426,35 +464,52 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
     for (int d = 0; d < count; ++d) {
         const int g = s_adapter[d];
         const uint8_t *xp[XN], *ap[AN];
-        bool x_on[XN], a_on[AN];
+        int x_size[XN], a_size[AN];                  // bytes of a whole copy: 16, or none
 #pragma unroll
         for (int i = 0; i < XN; ++i) {
             const int row = my_row + 32 * i;
-            x_on[i] = row < ROWS && s_id[row < ROWS ? row : 0] == g;
-            xp[i] = p.x + (x_on[i] ? s_row[row] * p.ldx + static_cast<int64_t>(k_mine) * 2 : 0);
+            x_size[i] = row < ROWS && s_id[row < ROWS ? row : 0] == g ? 16 : 0;
+            xp[i] = p.x + (x_size[i] ? s_row[row] * p.ldx + static_cast<int64_t>(k_mine) * 2 : 0);
         }
 #pragma unroll
         for (int i = 0; i < AN; ++i) {
             const int row = my_row + 32 * i;
-            a_on[i] = row < p.r;
-            ap[i] = p.a + (a_on[i] ? g * p.a_stride + row * p.lda + static_cast<int64_t>(k_mine) * 2 : 0);
+            a_size[i] = row < p.r ? 16 : 0;
+            ap[i] = p.a + (a_size[i] ? g * p.a_stride + row * p.lda + static_cast<int64_t>(k_mine) * 2 : 0);
         }
+        // stages are fetched one after the other: the pointers go along
+        const int whole = p.vec_x && p.vec_a ? p.K / 64 - first_block : 0;       // stages before this one are whole
         auto fetch = [&](int step, uint32_t slot) {
             const uint32_t to = copy_at + slot * S::STAGE;
+            if (step < whole) {
+#pragma unroll
+                for (int i = 0; i < XN; ++i) {
+                    if (ROWS >= 32 || threadIdx.x < ROWS * 8) ptx::cp_async_16_part(to + i * 4096, xp[i], x_size[i]);
+                    xp[i] += x_size[i] * 8;
+                }
+#pragma unroll
+                for (int i = 0; i < AN; ++i) {
+                    if (RT >= 32 || threadIdx.x < RT * 8) ptx::cp_async_16_part(to + ROWS * 128 + i * 4096, ap[i], a_size[i]);
+                    ap[i] += a_size[i] * 8;
+                }
+                return;
+            }
             const int left = p.K - k_mine - step * 64, n = left < 0 ? 0 : left < 8 ? left : 8;
 #pragma unroll
             for (int i = 0; i < XN; ++i) {
                 if (ROWS < 32 && threadIdx.x >= ROWS * 8) break;
-                const uint8_t* src = n > 0 && x_on[i] ? xp[i] + static_cast<int64_t>(step) * 128 : p.x;
-                if (p.vec_x) ptx::cp_async_16_part(to + i * 4096, src, x_on[i] ? 2 * n : 0);
-                else copy_values(to + i * 4096, src, x_on[i] ? n : 0);
+                const uint8_t* src = n > 0 && x_size[i] ? xp[i] : p.x;
+                if (p.vec_x) ptx::cp_async_16_part(to + i * 4096, src, x_size[i] ? 2 * n : 0);
+                else copy_values(to + i * 4096, src, x_size[i] ? n : 0);
+                xp[i] += x_size[i] * 8;
             }
 #pragma unroll
             for (int i = 0; i < AN; ++i) {
                 if (RT < 32 && threadIdx.x >= RT * 8) break;
-                const uint8_t* src = n > 0 && a_on[i] ? ap[i] + static_cast<int64_t>(step) * 128 : p.a;
-                if (p.vec_a) ptx::cp_async_16_part(to + ROWS * 128 + i * 4096, src, a_on[i] ? 2 * n : 0);
-                else copy_values(to + ROWS * 128 + i * 4096, src, a_on[i] ? n : 0);
+                const uint8_t* src = n > 0 && a_size[i] ? ap[i] : p.a;
+                if (p.vec_a) ptx::cp_async_16_part(to + ROWS * 128 + i * 4096, src, a_size[i] ? 2 * n : 0);
+                else copy_values(to + ROWS * 128 + i * 4096, src, a_size[i] ? n : 0);
+                ap[i] += a_size[i] * 8;
             }
         };
         float acc[S::NW][4];
@@ -476,24 +531,28 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
             const uint32_t xs = x_at + slot * S::STAGE, as = a_at + slot * S::STAGE;
             slot = slot + 1 == S::STAGES ? 0 : slot + 1;
             next = next + 1 == S::STAGES ? 0 : next + 1;
+            // the operands of as many k as fit, then their products: the loads' latencies lie over one another
+            constexpr int KS = 4 / S::WK, BATCH = S::NW > 4 && KS > 2 ? 2 : KS;
 #pragma unroll
-            for (int kk = 0; kk < 4; kk += S::WK) {
-                const uint32_t flip = static_cast<uint32_t>(kk + wk) * 32;                 // (chunk ^ row is (chunk's low bit ^ row) ^ its others)
-                uint32_t a[4];
-                ldmatrix4(a, xs ^ flip);
-                if constexpr (S::NW == 1) {
-                    uint32_t b0, b1;
-                    ldmatrix2(b0, b1, as ^ flip);
-                    mma<DT>(acc[0], a[0], a[1], a[2], a[3], b0, b1);
-                } else {
+            for (int k0 = 0; k0 < KS; k0 += BATCH) {
+                uint32_t a[BATCH][4], b[BATCH][S::NW * 2];
 #pragma unroll
-                    for (int n = 0; n < S::NW; n += 2) {
-                        uint32_t b[4];
-                        ldmatrix4(b, (as ^ flip) + n * 1024);
-                        mma<DT>(acc[n], a[0], a[1], a[2], a[3], b[0], b[1]);
-                        mma<DT>(acc[n + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+                for (int k = 0; k < BATCH; ++k) {
+                    const uint32_t flip = static_cast<uint32_t>((k0 + k) * S::WK + wk) * 32;   // (chunk ^ row: its low bit with the row, then its others)
+                    ldmatrix4(a[k], xs ^ flip);
+                    if constexpr (S::NW == 1) {
+                        ldmatrix2(b[k][0], b[k][1], as ^ flip);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < S::NW; n += 2)
+                            ldmatrix4(*reinterpret_cast<uint32_t(*)[4]>(b[k] + 2 * n), (as ^ flip) + n * 1024);
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+                    for (int n = 0; n < S::NW; ++n)
+                        mma<DT>(acc[n], a[k][0], a[k][1], a[k][2], a[k][3], b[k][2 * n], b[k][2 * n + 1]);
             }
         }
         // a row keeps its own adapter's sums
@@ -507,6 +566,91 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
         }
         __syncthreads();                             // the next adapter's first stages, and u, go where these were
     }
+    // ---- out = base + u B^T: this block's columns, COLS at a time through the same ring (its first stages are on their way while u
+    // is put together).  With several adapters a part of the columns takes a step for each of them, base coming with the first.
+    const int groups = (p.N + S::COLS - 1) / S::COLS;
+    const int first_group = static_cast<int>(static_cast<int64_t>(groups) * rank / ctas);
+    const int turns = count > 0 ? count : 1;         // (no adapter: base alone)
+    const int out_steps = (static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / ctas) - first_group) * turns;
+    constexpr int CHUNKS = RT / 8;                   // 16 bytes of a row of B
+    constexpr int COPIES = S::COLS * CHUNKS, BN = (COPIES + L_THREADS - 1) / L_THREADS, YN = ROWS * S::BASE_ROW / 16 / L_THREADS;
+    static_assert(YN > 0 && (COPIES < L_THREADS || COPIES % L_THREADS == 0) && ROWS * S::BASE_ROW / 16 % L_THREADS == 0, "whole copies");
+    constexpr int KEYS = CHUNKS < 8 ? CHUNKS : 8, KEY_SHIFT = CHUNKS == 2 ? 2 : CHUNKS == 4 ? 1 : 0;
+    constexpr int GROUP = S::TILES * 8, LANE = S::TILES * 2;     // columns of a warp, and of a lane (neighbours)
+    constexpr int PIECES = S::BASE_ROW / 16;
+    // where a thread's copies go, and for whole groups of columns and one adapter where they come from (the pointers go along)
+    uint32_t b_to[BN], y_to[YN];
+    const uint8_t *bp[BN], *yp[YN];
+    int b_size[BN], y_size[YN];
+#pragma unroll
+    for (int i = 0; i < BN; ++i) {
+        // a row of B goes where ldmatrix wants it: column c of instruction i of a warp stands for its column
+        // (c / 2) * LANE + 2 i + c % 2, so that a lane's results are neighbours
+        const int c = threadIdx.x + i * L_THREADS, chunk = c % CHUNKS, col = c / CHUNKS, in = col % GROUP;
+        const int at = col - in + in % LANE / 2 * 8 + in / LANE * 2 + in % 2;
+        b_to[i] = ring + at * (RT * 2) + ((chunk ^ (at >> KEY_SHIFT & (KEYS - 1))) * 16);
+        b_size[i] = count > 0 && chunk * 8 < p.r ? 16 : 0;
+        bp[i] = p.b + (b_size[i] ? s_adapter[0] * p.b_stride + (static_cast<int64_t>(first_group) * S::COLS + col) * p.ldb + chunk * 16 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < YN; ++i) {
+        const int c = threadIdx.x + i * L_THREADS, piece = c % PIECES, at = c / PIECES, row = s_row[at];
+        y_to[i] = ring + S::COLS * RT * 2 + at * S::BASE_ROW + ((piece ^ (at & 7)) * 16);
+        y_size[i] = row >= 0 ? 16 : 0;
+        yp[i] = p.base + (row >= 0 ? row * p.ldbase + static_cast<int64_t>(first_group) * S::BASE_ROW + piece * 16 : 0);
+    }
+    const int64_t b_step = S::COLS * p.ldb;
+    const int whole_out = p.vec_b && p.vec_base && turns == 1 ? p.N / S::COLS - first_group : 0;
+    int fetch_turn = 0, fetch_group = 0;             // of the next step to be fetched
+    auto fetch_out = [&](uint32_t slot) {
+        const uint32_t shift = slot * S::OUT_STAGE;
+        if (fetch_group < whole_out) {
+#pragma unroll
+            for (int i = 0; i < BN; ++i) {
+                if (COPIES >= L_THREADS || threadIdx.x < COPIES) ptx::cp_async_16_part(b_to[i] + shift, bp[i], b_size[i]);
+                bp[i] += b_size[i] ? b_step : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < YN; ++i) {
+                ptx::cp_async_16_part(y_to[i] + shift, yp[i], y_size[i]);
+                yp[i] += y_size[i] * (S::BASE_ROW / 16);
+            }
+            ++fetch_group;
+            return;
+        }
+        const int n0 = (first_group + fetch_group) * S::COLS;
+        if (count > 0) {
+            const uint8_t* bg = p.b + s_adapter[fetch_turn] * p.b_stride;
+#pragma unroll
+            for (int i = 0; i < BN; ++i) {
+                const int c = threadIdx.x + i * L_THREADS, chunk = c % CHUNKS, n = n0 + c / CHUNKS;
+                if (COPIES < L_THREADS && c >= COPIES) break;
+                const int have = n < p.N ? p.r - chunk * 8 : 0;
+                const uint8_t* src = have > 0 ? bg + n * p.ldb + chunk * 16 : p.b;
+                if (p.vec_b) ptx::cp_async_16_part(b_to[i] + shift, src, have > 0 ? 16 : 0);       // (r is a multiple of 8)
+                else copy_values(b_to[i] + shift, src, have);
+            }
+        }
+        if (fetch_turn == 0) {
+#pragma unroll
+            for (int i = 0; i < YN; ++i) {
+                const int c = threadIdx.x + i * L_THREADS, row = s_row[c / PIECES], n = n0 + c % PIECES * (16 / SIZE);
+                const bool wanted = row >= 0 && n < p.N;
+                const uint8_t* src = wanted ? p.base + row * p.ldbase + static_cast<int64_t>(n) * SIZE : p.base;
+                if (p.vec_base) ptx::cp_async_16_part(y_to[i] + shift, src, wanted ? 16 : 0);      // (N is a multiple of 8)
+                else copy_piece<SIZE>(y_to[i] + shift, src, wanted ? p.N - n : 0);
+            }
+        }
+        if (++fetch_turn == turns) {
+            fetch_turn = 0;
+            ++fetch_group;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < S::OUT_STAGES - 1; ++i) {
+        if (i < out_steps) fetch_out(i);
+        ptx::cp_async_commit();
+    }
     if constexpr (S::WK > 1) {
         for (int i = threadIdx.x; i < ROWS * RT; i += L_THREADS) {
             float* at = sums + i / RT * S::SUM_LD + i % RT;
@@ -518,27 +662,38 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
     }
     if (ctas > 1) ptx::cluster_sync();
     else __syncthreads();
-    // u of a row: the blocks' parts added in order, times scale, as hi + lo
-    for (int row = warp; row < ROWS; row += L_WARPS) {
+    // u of a row: the blocks' parts added in order, times scale, as hi + lo.  A block does its share of the rows for the whole
+    // cluster.
+    constexpr int PER = RT < 64 ? 2 : RT / 32;       // neighbouring ranks of a lane
+    for (int row = ROWS * static_cast<int>(rank) / ctas + warp; row < ROWS * (static_cast<int>(rank) + 1) / ctas; row += L_WARPS) {
         const int g = s_id[row];
+        const bool on = lane * PER < RT;
         const float scale = g >= 0 && p.scale ? p.scale[g] : 1.0f;
-        constexpr int PER = RT < 32 ? 1 : RT / 32;
         float u[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) u[i] = 0.0f;
+        if (g >= 0 && on) {
+            const uint32_t here = ptx::smem_u32(sums + row * S::SUM_LD + lane * PER);
+            if (ctas == 1) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) u[i] = sums[row * S::SUM_LD + lane * PER + i];
+            } else {
+                float part[MAX_CTAS][PER];
+#pragma unroll
+                for (int c = 0; c < MAX_CTAS; ++c)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        part[c][i] = c < ctas ? __uint_as_float(ptx::ld_cluster_u32(ptx::mapa(here, c) + 4 * i)) : 0.0f;
+#pragma unroll
+                for (int c = 0; c < MAX_CTAS; ++c)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) u[i] += part[c][i];
+            }
+        }
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int j = lane + 32 * i;
-            u[i] = 0.0f;
-            if (g >= 0 && j < RT) {
-                const float* at = sums + row * S::SUM_LD + j;
-                if (ctas == 1) {
-                    u[i] = *at;
-                } else {
-                    const uint32_t here = ptx::smem_u32(at);
-                    for (int c = 0; c < ctas; ++c) u[i] += __uint_as_float(ptx::ld_cluster_u32(ptx::mapa(here, c)));
-                }
-                u[i] *= scale;
-            }
+            u[i] *= scale;
             top = fmaxf(top, fabsf(u[i]));
         }
         float down = 1.0f, up = 1.0f;
@@ -550,127 +705,110 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
                 up = __uint_as_float(e << 23);
             }
         }
+        uint32_t hi[PER / 2], lo[PER / 2];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int j = lane + 32 * i;
-            if (j >= RT) continue;
             const float v = u[i] * down;
-            const uint32_t hi = round16<DT>(v);
-            const float rest = v - widen<DT>(hi);
-            u_hi[row * S::U_LD + j] = static_cast<uint16_t>(hi);
-            u_lo[row * S::U_LD + j] = static_cast<uint16_t>(fabsf(rest) < __int_as_float(0x7f800000) ? round16<DT>(rest) : 0u);
+            const uint32_t h = round16<DT>(v);
+            const float rest = v - widen<DT>(h);
+            const uint32_t l = fabsf(rest) < __int_as_float(0x7f800000) ? round16<DT>(rest) : 0u;
+            hi[i / 2] = i % 2 ? hi[i / 2] | h << 16 : h;
+            lo[i / 2] = i % 2 ? lo[i / 2] | l << 16 : l;
         }
-        if (lane == 0) s_up[row] = up;
-    }
-    if (ctas > 1) ptx::cluster_arrive();             // (no block leaves before the others have read its sums)
-    __syncthreads();
-
-    // ---- out = base + u B^T: this block's columns, 32 a warp and step; a lane has the eight n = quad * 8 and on of its rows
-    constexpr int MT = ROWS >= 32 ? 2 : 1, SIDES = ROWS / (16 * MT);                 // a warp's 16-row parts; warps beside one another
-    constexpr int SIZE = BT == TG_F32 ? 4 : 2;
-    const int m0 = warp % SIDES * 16 * MT;
-    const int nblocks = (p.N + 31) / 32;
-    const int n_begin = static_cast<int>(static_cast<int64_t>(nblocks) * rank / ctas);
-    const int n_end = static_cast<int>(static_cast<int64_t>(nblocks) * (rank + 1) / ctas);
-    int row[2 * MT], id[2 * MT];
-    float up[2 * MT];
+        const uint32_t at = ptx::smem_u32(u_hi + row * S::U_LD + lane * PER), scale_at = ptx::smem_u32(s_up + row);
+        for (int c = 0; c < ctas; ++c) {
+            const uint32_t there = ptx::mapa(at, c);
+            if (on) {
 #pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) {
-        row[m] = s_row[m0 + m * 8 + row8];
-        id[m] = s_id[m0 + m * 8 + row8];
-        up[m] = s_up[m0 + m * 8 + row8];
-    }
-    for (int nb = n_begin + warp / SIDES; nb < n_end; nb += L_WARPS / SIDES) {
-        const int n0 = nb * 32, n = n0 + quad * 8, left = p.N - n;
-        Eight<BT> y[2 * MT];
-#pragma unroll
-        for (int m = 0; m < 2 * MT; ++m)
-            y[m].load(p.base + (row[m] < 0 ? 0 : row[m]) * p.ldbase + static_cast<int64_t>(n) * SIZE, row[m] < 0 ? 0 : left, p.vec_base);
-        for (int d = 0; d < count; ++d) {
-            const int g = s_adapter[d];
-            // column c of instruction i stands for n0 + (c / 2) * 8 + 2 i + c % 2
-            const int col = n0 + (row8 / 2) * 8 + row8 % 2;
-            const uint8_t* bg = p.b + g * p.b_stride + col * p.ldb;
-            float acc[MT][4][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[m][i][c] = 0.0f;
-            if constexpr (RT == 16) {
-                // one instruction's 16 ranks: a lane's four neighbours
-                uint2 b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int have = col + 2 * i < p.N ? p.r - quad * 4 : 0;
-                    const uint8_t* at = bg + 2 * i * p.ldb + quad * 8;
-                    b[i] = make_uint2(0u, 0u);
-                    if (p.vec_b) {                   // (r is a multiple of 8)
-                        if (have > 0) b[i] = __ldg(reinterpret_cast<const uint2*>(at));
-                    } else {
-                        Half8 h;
-                        h.load(at, have < 4 ? have : 4, false);
-                        b[i] = make_uint2(h.w[0], h.w[1]);
-                    }
-                }
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    const uint16_t* us = (part ? u_lo : u_hi) + (m0 + row8) * S::U_LD + quad * 4;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const uint2 a = *reinterpret_cast<const uint2*>(us + m * 16 * S::U_LD);
-                        const uint2 c = *reinterpret_cast<const uint2*>(us + (m * 16 + 8) * S::U_LD);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mma<DT>(acc[m][i], a.x, c.x, a.y, c.y, b[i].x, b[i].y);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < RT; j += 32) {
-                    uint4 b[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int have = col + 2 * i < p.N ? p.r - j - quad * 8 : 0;
-                        const uint8_t* at = bg + 2 * i * p.ldb + (j + quad * 8) * 2;
-                        b[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (p.vec_b) {               // (r is a multiple of 8)
-                            if (have > 0) b[i] = __ldg(reinterpret_cast<const uint4*>(at));
-                        } else {
-                            Half8 h;
-                            h.load(at, have, false);
-                            b[i] = make_uint4(h.w[0], h.w[1], h.w[2], h.w[3]);
-                        }
-                    }
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        const uint16_t* us = (part ? u_lo : u_hi) + (m0 + row8) * S::U_LD + j + quad * 8;
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            const uint4 a = *reinterpret_cast<const uint4*>(us + m * 16 * S::U_LD);
-                            const uint4 c = *reinterpret_cast<const uint4*>(us + (m * 16 + 8) * S::U_LD);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                mma<DT>(acc[m][i], a.x, c.x, a.y, c.y, b[i].x, b[i].y);
-                                mma<DT>(acc[m][i], a.z, c.z, a.w, c.w, b[i].z, b[i].w);
-                            }
-                        }
-                    }
+                for (int i = 0; i < PER / 2; ++i) {
+                    ptx::st_cluster_u32(there + 4 * i, hi[i]);
+                    ptx::st_cluster_u32(there + ROWS * S::U_LD * 2 + 4 * i, lo[i]);
                 }
             }
+            if (DT == TG_F16 && lane == 0) ptx::st_cluster_u32(ptx::mapa(scale_at, c), __float_as_uint(up));
+        }
+    }
+    if (ctas > 1) {
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    // this warp's 16 rows of u, for all of its columns: k = 16 j and on of part h
+    uint32_t u[2][RT / 16][4];
 #pragma unroll
-            for (int m = 0; m < 2 * MT; ++m) {
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < RT / 16; ++j)
+            ldmatrix4(u[h][j], ptx::smem_u32(u_hi + (h * ROWS + wm * 16 + lane % 16) * S::U_LD + j * 16 + lane / 16 * 8));
+    const int group = warp / S::WM;                  // of columns
+    const int low = wm * 16 + row8, row[2] = {s_row[low], s_row[low + 8]}, id[2] = {s_id[low], s_id[low + 8]};
+    const float up[2] = {s_up[low], s_up[low + 8]};
+    const uint32_t b_row = group * GROUP + lane % 8 + lane / 16 * 8;
+    const uint32_t b_at = ring + b_row * (RT * 2), b_key = b_row >> KEY_SHIFT & (KEYS - 1);
+    const uint32_t y_at = ring + S::COLS * RT * 2 + low * S::BASE_ROW;
+    Columns<BT, LANE> y[2];
+    uint8_t* out[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        out[m] = p.out + (row[m] < 0 ? 0 : row[m]) * p.ldo + (static_cast<int64_t>(first_group) * S::COLS + group * GROUP + quad * LANE) * SIZE;
+    int turn = 0, left = p.N - first_group * S::COLS - group * GROUP - quad * LANE;      // columns from this lane's first on
+    uint32_t slot = 0, next = S::OUT_STAGES - 1;
+    for (int step = 0; step < out_steps; ++step) {
+        ptx::cp_async_wait<S::OUT_STAGES - 2>();
+        __syncthreads();
+        if (step + S::OUT_STAGES - 1 < out_steps) fetch_out(next);
+        ptx::cp_async_commit();
+        const uint32_t shift = slot * S::OUT_STAGE;
+        slot = slot + 1 == S::OUT_STAGES ? 0 : slot + 1;
+        next = next + 1 == S::OUT_STAGES ? 0 : next + 1;
+        if (turn == 0) {
+            y[0].read(y_at + shift, group * GROUP + quad * LANE, low & 7);
+            y[1].read(y_at + shift + 8 * S::BASE_ROW, group * GROUP + quad * LANE, low & 7);
+        }
+        if (count > 0) {
+            float acc[S::TILES][4];
+#pragma unroll
+            for (int i = 0; i < S::TILES; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+            constexpr int KS = RT / 16, BATCH = S::TILES == 4 && KS > 2 ? 2 : KS < 4 ? KS : 4;
+#pragma unroll
+            for (int j0 = 0; j0 < KS; j0 += BATCH) {
+                uint32_t b[BATCH][S::TILES * 2];
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+                    for (int i = 0; i < S::TILES; i += 2)
+                        ldmatrix4(*reinterpret_cast<uint32_t(*)[4]>(b[j] + 2 * i),
+                                  b_at + shift + i * 8 * (RT * 2) + (((2 * (j0 + j) + lane / 8 % 2) ^ b_key) * 16));
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < S::TILES; ++i)
+                            mma<DT>(acc[i], u[h][j0 + j][0], u[h][j0 + j][1], u[h][j0 + j][2], u[h][j0 + j][3], b[j][2 * i], b[j][2 * i + 1]);
+            }
+            const int g = s_adapter[turn];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
                 if (id[m] != g) continue;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[m].add2(i, acc[m / 2][i][m % 2 * 2] * up[m], acc[m / 2][i][m % 2 * 2 + 1] * up[m]);
+                for (int i = 0; i < S::TILES; ++i)
+                    y[m].add2(i, DT == TG_F16 ? acc[i][2 * m] * up[m] : acc[i][2 * m], DT == TG_F16 ? acc[i][2 * m + 1] * up[m] : acc[i][2 * m + 1]);
             }
         }
+        if (++turn == turns) {
+            turn = 0;
 #pragma unroll
-        for (int m = 0; m < 2 * MT; ++m)
-            if (row[m] >= 0) y[m].store(p.out + row[m] * p.ldo + static_cast<int64_t>(n) * SIZE, left, p.vec_out);
+            for (int m = 0; m < 2; ++m) {
+                if (row[m] >= 0) y[m].store(out[m], left, p.vec_out);
+                out[m] += S::COLS * SIZE;
+            }
+            left -= S::COLS;
+        }
     }
-    if (ctas > 1) ptx::cluster_wait();
 }
 
 using TileKernel = void (*)(const LoraArgs, const Plan);
@@ -680,14 +818,14 @@ struct TileVariant {
 };
 
 template <int DT, int BT, int RT, int ROWS>
-TileVariant variant() { return {&lora_tile_kernel<DT, BT, RT, ROWS>, ROWS, Tile<RT, ROWS>::BYTES}; }
+TileVariant variant() { return {&lora_tile_kernel<DT, BT, RT, ROWS>, ROWS, Tile<RT, ROWS, BT == TG_F32 ? 4 : 2>::BYTES}; }
 
 // Tiles of 64 rows read an adapter a quarter as often; tiles of 16 where an adapter has fewer than 32 rows on average, if all
 // of them are in use.
 template <int DT, int BT>
 TileVariant variant_for(int64_t T, int G, int r) {
     const bool tall = T >= 32 * static_cast<int64_t>(G);
-    if (r > 64) return tall ? variant<DT, BT, 128, 64>() : variant<DT, BT, 128, 16>();
+    if (r > 64) return tall ? variant<DT, BT, 128, 32>() : variant<DT, BT, 128, 16>();
     if (r > 32) return tall ? variant<DT, BT, 64, 64>() : variant<DT, BT, 64, 16>();
     if (r > 16) return tall ? variant<DT, BT, 32, 64>() : variant<DT, BT, 32, 16>();
     return tall ? variant<DT, BT, 16, 64>() : variant<DT, BT, 16, 16>();
@@ -699,9 +837,9 @@ TileVariant variant_for(tg_dtype base, int64_t T, int G, int r) {
                                                                               : variant_for<DT, TG_BF16>(T, G, r);
 }
 
-// The rows form reads T r (K + N) 16-bit values through L2, whoever shares an adapter; the tile form streams an adapter
-// through one SM at a time.
-constexpr int64_t ROWS_FORM = 4096;      // largest T * r
+// The rows form reads T r (K + N) 16-bit values through L2, whoever shares an adapter; the tile form takes about 14 us for K = N =
+// 4096 however few the rows are.  At that size, rank 16: 128 rows 10.2 us against 14, 256 rows 17.5 against 14.
+constexpr int64_t ROWS_FORM = 21 << 20, ROWS_FORM_T = 4096;      // largest T r (K + N), and T
 
 tg_status check_operand(const char* name, const void* p, int64_t ld, int64_t cols, int64_t esize) {
     using host::fail;
@@ -775,7 +913,7 @@ extern "C" tg_status tg_lora_add(const tg_lora_args* args, tg_stream_t stream) {
     a.vec_base = vec(p.base, a.ldbase, 0) && a.N % 8 == 0;
     a.vec_out = vec(p.out, a.ldo, 0) && a.N % 8 == 0;
     cudaError_t e;
-    if (any && p.T * p.r <= ROWS_FORM) {
+    if (any && p.T <= ROWS_FORM_T && p.T * p.r * (p.K + p.N) <= ROWS_FORM) {
         a.cuts = (a.K + ROW_CUT - 1) / ROW_CUT;
         void* ws = nullptr;
         const size_t bytes = static_cast<size_t>(a.cuts) * p.T * p.r * 4;
@@ -820,13 +958,13 @@ extern "C" tg_status tg_lora_add(const tg_lora_args* args, tg_stream_t stream) {
     // Few tiles share each one's k and columns among the blocks of a cluster, up to about two blocks an SM.
     const int64_t likely = (p.T + v.rows - 1) / v.rows > used - 1 ? (p.T + v.rows - 1) / v.rows : used - 1;
     int ctas = 1;
-    while (ctas < 8 && likely * ctas * 2 <= 2 * d.sms && a.K >= ctas * 512) ctas *= 2;
+    while (ctas < MAX_CTAS && likely * ctas * 2 <= 2 * d.sms && a.K >= ctas * 512) ctas *= 2;
     const int plan_bytes = PLAN_WARPS * int(buckets + 1) * 4;
     e = plan_bytes > 48 * 1024 ? cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_bytes) : cudaSuccess;
     if (e == cudaSuccess && v.bytes > 48 * 1024)
         e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.bytes);
     if (e == cudaSuccess) {
-        lora_plan_kernel<<<1, 32 * PLAN_WARPS, plan_bytes, st>>>(p.adapters, p.T, a.G, plan);
+        lora_plan_kernel<<<PLAN_CTAS, 32 * PLAN_WARPS, plan_bytes, st>>>(p.adapters, p.T, a.G, plan);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess) {

@@ -116,6 +116,10 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
     return v;
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(cluster_addr), "r"(v) : "memory");
+}
+
 // Store to own shared memory, ordered after this thread's earlier shared-memory
 // stores for any CTA of the cluster that reads it with ld_cluster_acquire_u32.
 __device__ __forceinline__ void st_release_cluster_u32(uint32_t smem_addr, uint32_t v) {
