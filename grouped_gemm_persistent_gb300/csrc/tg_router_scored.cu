@@ -19,9 +19,12 @@
 // are a true tie, which the index decides, and send no row there: with 16-bit logits and a bias of zeros they are common.
 //
 // Keys.  Without a bias as in tg_router.cu: the logit's ordered bits, the lowest ones replaced by the position counted down.
-// With one: v - lo in fixed point, 22 bits after the point for up to 256 positions (2^-22 is about what the scores are
-// known to), the position below it; lo is the smallest bias, or the largest minus 2.5 where they spread further (what lies
-// below lo has the lowest key, and a row in which such a one is among the first k + 1 goes to 64 bits).  v - lo is below 4.
+// With one: v - lo + 4 is a number from 4 to 8, whose bits below the exponent are a fixed-point number of 21 binary places (about
+// what the scores are known to); they and the position below them are the key, one shift and add.  lo is the smallest bias, or the
+// largest minus 2.5 where they spread further: what then lies below lo is left out, and a row whose k-th choice is not clear of lo
+// goes to 64 bits.  Above 256 positions the key has room for a bit or two less.
+// The groups are chosen the same way, by their scores' bits and their indices, while each has its group_top experts to choose
+// from and none below lo; otherwise, and without a bias by the largest logit itself, by counting the groups that come before each.
 //
 // Positions.  A row is L lanes of V positions.  Each group has a power of two of positions, V at least, so that
 // a group is whole lanes and its sums are a few exchanges; the positions past its experts hold -infinity.
@@ -97,6 +100,12 @@ __device__ __forceinline__ double value64(unsigned long long o) {
 __device__ __forceinline__ unsigned long long max64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
 __device__ __forceinline__ unsigned long long min64(unsigned long long a, unsigned long long b) { return a < b ? a : b; }
 
+// A sigmoid score with its bias, in 64 bits
+__device__ __forceinline__ double sigmoid64(double x, const float* bias, int e) {
+    const double v = 1.0 / (1.0 + exp(-x));
+    return bias ? v + static_cast<double>(__ldg(bias + e)) : v;
+}
+
 // The k choices of the row at `row` in 64 bits: lane i gets the i-th expert, or -1.  Every lane of the warp calls it; a row
 // that need not choose (!wanted) takes part and gets nothing.  n: this lane's experts e0, e0 + 1, ...
 template <int DT, int L, int V, bool SIGMOID>
@@ -116,6 +125,7 @@ __device__ __noinline__ int choose_in_64(const ScoredArgs& a, const uint8_t* row
     }
     unsigned long long key[V];
     unsigned long long first = 0ull, second = 0ull;           // the lane's largest v
+#pragma unroll 4
     for (int j = 0; j < V; ++j) {
         key[j] = 0ull;
         if (j >= n) continue;
@@ -176,9 +186,14 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
     constexpr int LOW_BITS = SPAN > 512 ? 10 : SPAN > 256 ? 9 : 8;
     constexpr float E = SIGMOID ? 3.0e-7f : 1.0e-6f;               // a score's error
     constexpr float U = 5.9604645e-8f;                             // 2^-24
-    constexpr float FIXED = static_cast<float>(1u << (30 - LOW_BITS));
-    // keys this near are not told apart: both scores' errors, v - lo's (below 4, two roundings), and the cut to fixed point
-    constexpr uint32_t NEAR = static_cast<uint32_t>(FIXED * 2.0f * (E + 8.0f * U)) + 2;
+    // How far a computed v may be off: the score, and the roundings of b - lo, of 4 more and of v itself (2^-23, 2^-22 and 2^-22).
+    // Keys that are nearer than twice that, in their steps of 2^-21, are not told apart; nor are groups' scores, of one such v or of
+    // two, whose sum is rounded by 2^-21 and has steps of 2^-20.
+    constexpr float OFF = E + 10.0f * U;
+    constexpr int CUT = LOW_BITS - 8;                              // bits of v that a key leaves out
+    constexpr uint32_t STEPS = static_cast<uint32_t>(2097152.0f * 2.0f * OFF) + 2;
+    constexpr uint32_t NEAR = (STEPS >> CUT) + 1;
+    constexpr uint32_t PAIR_STEPS = static_cast<uint32_t>(1048576.0f * 2.0f * (2.0f * OFF + 8.0f * U)) + 2;
     extern __shared__ __align__(16) uint8_t dyn[];
     float* s_sum = reinterpret_cast<float*>(dyn);                              // [warps][SPAN]
     int32_t* s_count = reinterpret_cast<int32_t*>(s_sum + R_WARPS * SPAN);     // [SPAN], by expert
@@ -197,8 +212,8 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
         return static_cast<int>((p >> s.shift) * s.each + (p & ((1u << s.shift) - 1u)));
     };
     const bool biased = s.bias != nullptr;
-    float b[V], lo = 0.0f;
-    bool odd = false;                             // a bias of NaN or +infinity: 64 bits sort it out
+    float b[V], lo = 0.0f;                        // b: the bias - lo + 4
+    bool odd = false, below = false;              // a bias of NaN or +infinity (64 bits sort it out), or below lo
     if (biased) {
         float small = __int_as_float(0x7f800000), large = MINUS_INF;
 #pragma unroll
@@ -214,12 +229,10 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
         small = -group_max_plain<L>(-small);
         large = group_max_plain<L>(large);
         if (large > MINUS_INF) lo = fmaxf(small, large - 2.5f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) b[j] -= lo;
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) b[j] = 0.0f;
+        below = small < lo;
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = biased ? b[j] - lo + 4.0f : 4.0f;
     const int64_t step = static_cast<int64_t>(gridDim.x) * R_WARPS * ROWS;
     // (a warp's rows are neighbours; lanes past the last row keep -infinity and store nothing)
     int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
@@ -239,17 +252,23 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
     for (int64_t base = warp_first; base < a.T; base += step, t += step) {
         const X x = next;
         if (base + step < a.T) fetch(t + step);
-        float v[V];                               // the scores, then v - lo
+        float v[V];                               // the scores, then v - lo + 4, -infinity for what may not be chosen
         float m = 0.0f, whole = 0.0f;
-        bool any = false;
+        bool any;
         if constexpr (SIGMOID) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 v[j] = sigmoid_approx(x.value(j));
-                any |= x.value(j) != MINUS_INF;
                 whole += v[j];
             }
-            any = row_ballot<L>(any, lane, in) != 0u;
+            whole = group_sum<L>(whole);
+            any = whole != 0.0f;
+            if (__any_sync(FULL, !any)) {         // padding, or scores that are all 0 in fp32
+                bool live = false;
+#pragma unroll
+                for (int j = 0; j < V; ++j) live |= x.value(j) != MINUS_INF;
+                any = row_ballot<L>(live, lane, in) != 0u;
+            }
         } else {
             m = x.value(0);                       // the row's largest logit, NaN if it has one
 #pragma unroll
@@ -262,9 +281,9 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                 v[j] = exp_flush(x.value(j) - m);
                 whole += v[j];
             }
+            whole = group_sum<L>(whole);
         }
-        whole = group_sum<L>(whole);
-        const float inv = whole != 0.0f ? 1.0f / whole : 0.0f;
+        const float inv = whole != 0.0f ? rcp_flush(whole) : 0.0f;          // (whole is a normal number: so are scores that are not 0)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if constexpr (SIGMOID) {
@@ -301,45 +320,97 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                     one = fmaxf(one, o);
                 }
             }
-            float score = one, near = 0.0f;
-            if (!exact) {
-                if (s.group_top == 2) score += two > MINUS_INF ? two : -lo;         // (of sums less 2 lo)
-                // twice a sum's error: scores, biases less lo, the sum itself, and lo where it stands alone
-                near = 4.0f * (E + 8.0f * U) + 8.0f * U * fabsf(score) + 4.0f * U * fabsf(lo);
-                if (!(near < __int_as_float(0x7f800000))) near = 0.0f;              // (no expert that may be chosen)
-            }
             const int mine = first >> s.shift;
-            int before = 0, maybe = 0;            // groups that come first for certain, and possibly
-            for (int h = 0; h < s.groups; ++h) {
-                const float o = __shfl_sync(FULL, score, h * lanes, L);
-                if (exact) {
-                    before += o > score || (o == score && h < mine) ? 1 : 0;
-                } else {
-                    const float gap = o - score;
-                    // (near is that of the larger score of the two to within its own size: twice it covers both)
-                    before += gap > 2.0f * near ? 1 : 0;
-                    maybe += h != mine && o > MINUS_INF && gap >= -2.0f * near ? 1 : 0;
+            const float least = s.group_top == 2 ? two : one;
+            if (!exact && __all_sync(FULL, least >= 4.0f || group >= s.groups || !any)) {
+                // scores from 4 to 8, or of two from 8 to 16: their bits below the exponent, and the group counted down
+                const float score = s.group_top == 2 ? one + two : one;
+                const uint32_t key = group < s.groups && any
+                                         ? __float_as_uint(score) << 8 | 0x80000000u | static_cast<uint32_t>(31 - mine) : 0u;
+                uint32_t edge = 0u, after = 0u;
+                for (int i = 0; i <= s.top_groups; ++i) {
+                    edge = after;
+                    after += group_max<L>(__viaddmax_u32(key, 0u - after, 0u));
                 }
+                kept = key >= edge;
+                const bool open = after >= 0x80000000u && (edge >> 8) - (after >> 8) <= (s.group_top == 2 ? PAIR_STEPS : STEPS);
+                if (__any_sync(FULL, open)) {
+                    // the groups at the border are not told apart.  A group's score in 64 bits needs its largest experts alone, if
+                    // they are apart from the next.
+                    bool clear = SIGMOID;
+                    int e[2] = {0, 0};
+                    uint32_t last = 0u;
+                    for (int i = 0; i <= s.group_top; ++i) {
+                        uint32_t best = 0u;
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const uint32_t low = LOW - static_cast<uint32_t>(first + j);
+                            best = __viaddmax_u32(v[j] >= 4.0f ? (__float_as_uint(v[j]) << 8 & ~LOW) + low : low, 0u - last, best);
+                        }
+                        for (int d = 1; d < lanes; d <<= 1) best = max(best, __shfl_xor_sync(FULL, best, d));
+                        const uint32_t now = last + best;
+                        if (i < s.group_top) e[i] = expert_of(now);
+                        else clear &= now < 0x80000000u || (last >> LOW_BITS) - (now >> LOW_BITS) > NEAR;
+                        last = now;
+                    }
+                    const uint32_t all_clear = row_ballot<L>(clear || group >= s.groups, lane, in);
+                    const bool whole_row = all_clear == (L == 32 ? FULL : (1u << L % 32) - 1u);
+                    redo |= open && !whole_row;
+                    double score64 = 0.0;
+                    if (SIGMOID && open && whole_row && group < s.groups) {
+                        const uint8_t* row = a.logits + t * a.ld_bytes;
+                        score64 = sigmoid64(X::one(row, e[0]), s.bias, e[0]);
+                        if (s.group_top == 2) score64 += sigmoid64(X::one(row, e[1]), s.bias, e[1]);
+                    }
+                    int before = 0;
+                    for (int h = 0; h < s.groups; ++h) {
+                        const double o = __shfl_sync(FULL, score64, h * lanes, L);
+                        before += o > score64 || (o == score64 && h < mine) ? 1 : 0;
+                    }
+                    if (open && whole_row) kept = before < s.top_groups;
+                }
+            } else {
+                float score = one, near = 0.0f;
+                if (!exact) {
+                    if (s.group_top == 2) score += two > MINUS_INF ? two : 4.0f - lo;    // (of sums less 2 lo and 8 more)
+                    // twice a sum's error: scores, biases less lo, the sum itself, and lo where it stands alone
+                    near = 4.0f * OFF + 8.0f * U * (8.0f + fabsf(score)) + 4.0f * U * fabsf(lo);
+                    if (!(near < __int_as_float(0x7f800000))) near = 0.0f;              // (no expert that may be chosen)
+                }
+                int before = 0, maybe = 0;        // groups that come first for certain, and possibly
+                for (int h = 0; h < s.groups; ++h) {
+                    const float o = __shfl_sync(FULL, score, h * lanes, L);
+                    if (exact) {
+                        before += o > score || (o == score && h < mine) ? 1 : 0;
+                    } else {
+                        const float gap = o - score;
+                        // (near goes with this score; the other's error is as large only where it is as large itself)
+                        before += gap > 2.0f * near ? 1 : 0;
+                        maybe += h != mine && o > MINUS_INF && gap >= -2.0f * near ? 1 : 0;
+                    }
+                }
+                const bool none = !(score > MINUS_INF);
+                kept = !none && before < s.top_groups;
+                if (!exact)
+                    redo |= row_ballot<L>(!none && group < s.groups && before < s.top_groups && maybe >= s.top_groups, lane, in) != 0u;
             }
-            const bool none = !(score > MINUS_INF);
-            kept = !none && before < s.top_groups;
-            if (!exact)
-                redo |= row_ballot<L>(!none && group < s.groups && before < s.top_groups && maybe >= s.top_groups, lane, in) != 0u;
         }
 
         // the i-th choice ends up with lane i of the row; one more is looked at, to see that the last one is apart from it
-        const uint32_t key_min = biased ? LOW + 1 : KEY_MIN;
+        const uint32_t key_min = biased ? 0x80000000u : KEY_MIN;
         uint32_t key[V];
+        if (biased) {
+            const float least = kept ? 4.0f : __int_as_float(0x7f800000);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            uint32_t high;
-            if (biased) {
-                const uint32_t fixed = max(__float2uint_rz(v[j] * FIXED), 1u);
-                high = v[j] > MINUS_INF ? fixed << LOW_BITS : 0u;
-            } else {
-                high = order_bits(x.value(j)) & ~LOW;
+            for (int j = 0; j < V; ++j) {
+                const uint32_t low = LOW - static_cast<uint32_t>(first + j);
+                const uint32_t bits = CUT == 0 ? __float_as_uint(v[j]) << 8 : __float_as_uint(v[j]) << 8 & ~LOW;
+                key[j] = v[j] >= least ? bits + low : low;
             }
-            key[j] = (kept ? high : 0u) | (LOW - static_cast<uint32_t>(first + j));
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                key[j] = (kept ? order_bits(x.value(j)) & ~LOW : 0u) | (LOW - static_cast<uint32_t>(first + j));
         }
         uint32_t mine = 0u, top = 0u;
         for (int i = 0; i <= a.k; ++i) {
@@ -355,8 +426,9 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
             uint32_t after = __shfl_down_sync(FULL, mine, 1, L);
             if (in == L - 1) after = top;
             const uint32_t apart = (mine >> LOW_BITS) - (after >> LOW_BITS);
-            // (what lies below lo has the lowest key: it is never told apart)
-            bool close = in < a.k && after >= key_min && (biased ? apart <= NEAR || after >> LOW_BITS == 1u : apart == 0u);
+            // the last choice has to be clear of what lies below lo
+            if (below) redo |= row_ballot<L>(in == a.k - 1 && any && mine < (0x80000000u | (NEAR << LOW_BITS)), lane, in) != 0u;
+            bool close = in < a.k && after >= key_min && (biased ? apart <= NEAR : apart == 0u);
             if (__any_sync(FULL, close)) {
                 if (close) {
                     const int e = expert_of(after);
@@ -364,7 +436,34 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                     const bool tie = X::one(row, my_e) == X::one(row, e) && (!biased || __ldg(s.bias + my_e) == __ldg(s.bias + e));
                     close = !tie;
                 }
-                redo |= row_ballot<L>(close, lane, in) != 0u;
+                // The first k + 1 in 64 bits, each by its lane, and put in order: enough if the one after them is apart from them.
+                const bool some = row_ballot<L>(close, lane, in) != 0u;
+                uint32_t best = 0u;
+#pragma unroll
+                for (int j = 0; j < V; ++j) best = __viaddmax_u32(key[j], 0u - top, best);
+                const uint32_t past = top + group_max<L>(best);
+                const uint32_t gap = (top >> LOW_BITS) - (past >> LOW_BITS);
+                const bool clear = past >= top || past < key_min || gap > (biased ? NEAR : 0u);
+                const bool order = some && clear && a.k < L && (SIGMOID || !biased);
+                redo |= some && !order;
+                if (__any_sync(FULL, order)) {
+                    unsigned long long my_v = 0ull;
+                    if (order && in <= a.k && my_e >= 0) {
+                        const double z = X::one(a.logits + t * a.ld_bytes, my_e);
+                        my_v = order64(biased ? sigmoid64(z, s.bias, my_e) : z);
+                    }
+                    int place = 0, got = -1;
+                    for (int i = 0; i <= a.k; ++i) {
+                        const unsigned long long o = __shfl_sync(FULL, my_v, i, L);
+                        const int e = __shfl_sync(FULL, my_e, i, L);
+                        place += o > my_v || (o == my_v && e < my_e) ? 1 : 0;
+                    }
+                    for (int i = 0; i <= a.k; ++i) {
+                        const int to = __shfl_sync(FULL, place, i, L), e = __shfl_sync(FULL, my_e, i, L);
+                        if (e >= 0 && to == in) got = e;          // (those there are come first, before and after)
+                    }
+                    if (order) my_e = got;
+                }
             }
         }
         if (__any_sync(FULL, redo)) {
@@ -375,13 +474,13 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
         if (in >= a.k) my_e = -1;
         if (my_e >= 0) {
             const float z = X::one(a.logits + t * a.ld_bytes, my_e);
-            my_s = SIGMOID ? 1.0f / (1.0f + __expf(-z)) : __expf(z - m) * inv;
+            my_s = SIGMOID ? sigmoid_approx(z) : exp_flush(z - m) * inv;
             atomicAdd(&s_count[my_e], 1);
         }
         const float chosen = a.renorm ? group_sum<L>(my_s) : 1.0f;
         if (in < a.k && t < a.T) {
             a.experts[t * a.k + in] = my_e;
-            a.weights[t * a.k + in] = my_s != 0.0f ? my_s / chosen * s.factor : 0.0f;
+            a.weights[t * a.k + in] = my_s != 0.0f ? my_s * rcp_flush(chosen) * s.factor : 0.0f;
         }
     }
     // the row slots of a warp, then the warps of the block
@@ -485,18 +584,16 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
         const int e = e_next;
         const float z = z_next, dw = dw_next;
         if (base + step < a.T) fetch(t + step);
-        float p[V], rest[V];                     // s, and 1 - s
+        // with e = e^-|x| and t = 1 / (1 + e): s is t or e t, s (1 - s) is e t^2 on either side of zero, 0 at both infinities
+        float p[V];                              // s (1 - s)
         float whole = 0.0f, pu = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            // (the exponent is held where the reciprocal is a normal number: s below 2^-100 counts as that)
-            const float f = ex2_flush(fminf(x.value(j) * -1.4426950408889634f, 100.0f));
-            p[j] = rcp_flush(1.0f + f);
-            rest[j] = f * p[j];
-            if (x.value(j) != x.value(j)) p[j] = x.value(j);         // (fminf drops a NaN)
-            if (x.value(j) == MINUS_INF) p[j] = 0.0f;
-            whole += p[j];
-            pu = fmaf(p[j], u[j], pu);
+            const float f = ex2_flush(fabsf(x.value(j)) * -1.4426950408889634f), q = rcp_flush(1.0f + f), r = f * q;
+            const float score = x.value(j) < 0.0f ? r : q;
+            p[j] = r * q;
+            whole += score;
+            pu = fmaf(score, u[j], pu);
         }
         whole = group_sum<L>(whole);
         const float inv = whole != 0.0f ? 1.0f / whole : 0.0f;
@@ -513,7 +610,7 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
         }
         float d[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = (u[j] - c) * inv;
+        for (int j = 0; j < V; ++j) d[j] = fmaf(u[j], inv, -c * inv);
         if (a.d_weights) {
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
@@ -525,7 +622,7 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
             __syncwarp();
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = x.value(j) == MINUS_INF ? 0.0f : p[j] * rest[j] * d[j];
+        for (int j = 0; j < V; ++j) d[j] *= p[j];
         if (t >= a.T) continue;
         uint8_t* dst = a.out + t * a.ldo_bytes + first * X::ESIZE;
         uint32_t o[X::WORDS];

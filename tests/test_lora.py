@@ -162,6 +162,22 @@ def test_sizes(T, K, N, r, G, dt):
     tg.device_status()
 
 
+TILES = [  # more rows, or more work a row: 64-, 32- and 16-row tiles of every width of ranks, clusters, adapters that share a bucket
+    (4200, 259, 70, 12, 3), (4200, 64, 72, 31, 5), (4200, 200, 136, 60, 4), (4200, 257, 33, 128, 2), (4500, 257, 33, 9, 200),
+    (4500, 96, 200, 24, 200), (4300, 130, 64, 50, 300), (4500, 64, 129, 100, 150), (4200, 72, 40, 8, 700), (5000, 40, 72, 40, 2000),
+    (600, 4096, 2000, 64, 2), (600, 4100, 500, 16, 100), (520, 4104, 1500, 32, 3), (700, 2056, 1000, 128, 1), (300, 5000, 4096, 20, 40)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r,G", TILES)
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_tiles(T, K, N, r, G, dt):
+    for i, (bt, kind) in enumerate(((dt, "rows"), (F, "requests"), (dt, "one"))):
+        base, x, a, b, ids, scale = make(i, T, K, N, r, G, dt, bt, kind)
+        check(base, x, a, b, ids, scale, tg.lora_add(base, x, a, b, ids, scale))
+    tg.device_status()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,r", [(20, 16), (90, 64), (300, 100), (5000, 32)])
 @pytest.mark.parametrize("pad", [2, 8, 6])

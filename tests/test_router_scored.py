@@ -304,6 +304,25 @@ def test_choices_that_32_bits_do_not_tell_apart(score, group_top, G, groups):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("G,groups,k", [(64, 8, 8), (64, 8, 5), (256, 8, 8), (256, 16, 7), (40, 1, 6), (320, 4, 9)])
+def test_a_few_choices_that_32_bits_do_not_tell_apart(score, group_top, G, groups, k):
+    """Biases that bring the experts' values to within 1e-7 of steps of a fortieth: pairs and more of them next to each other."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    row = torch.randn(1, G, generator=g, device="cuda") * 0.5
+    x = row + torch.randn(200, G, generator=g, device="cuda") * 2e-7
+    s = scores(row, score)[0]
+    for seed in range(3):
+        wish = torch.randint(0, 40, (G,), generator=g, device="cuda") / 40
+        if seed == 1:
+            wish[::2] += 0.003 * torch.rand(wish[::2].shape, generator=g, device="cuda")
+        bias = (wish - s).float()
+        kw = dict(score=score, bias=bias, groups=groups, top_groups=max(1, groups // 2), group_top=group_top)
+        check(x, k, tg.moe_router(x, k, renormalize=True, **kw), renorm=True, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("dt", [F, BF, HF])
 def test_ties_and_biases(score, dt):
     """Equal logits under a bias of zeros, biases that spread far, forbid an expert or force one."""
