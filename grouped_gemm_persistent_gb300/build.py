@@ -31,10 +31,11 @@ FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", I
 
 UNITS = [("tg_api", "tg_api.cu", []), ("tg_aux", "tg_aux.cu", []), ("tg_fp8", "tg_fp8.cu", []),
          ("tg_quant", "tg_quant.cu", []), ("tg_router", "tg_router.cu", []), ("tg_norm", "tg_norm.cu", []),
+         ("tg_norm_backward", "tg_norm_backward.cu", []),
          ("tg_router_scored", "tg_router_scored.cu", []), ("tg_lora", "tg_lora.cu", [])] + [
     (f"tg_inst_f{f}_m{m}", "tg_inst.cu", [f"-DTG_INST_F32={f}", f"-DTG_INST_MODE={m}"])
     for f in (0, 1) for m in (0, 1, 2)
-]
+] + [(f"tg_norm_inst_{x}", "tg_norm_inst.cu", [f"-DTG_NORM_X={x}"]) for x in (0, 1, 2)]
 
 
 def nvcc() -> str:

@@ -1,0 +1,290 @@
+// tg_norm_inst.cu - the norm's kernel for one type of x (TG_NORM_X, a tg_dtype's number), chosen and launched by tg_norm.cu, where the
+// mathematics and the reasons stand.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "tg.h"
+#include "tg_block_scale.cuh"
+#include "tg_norm.cuh"
+#include "tg_ptx.cuh"
+
+namespace tg {
+
+namespace norm {
+
+namespace {
+
+// A number as the sum of two fp32 ones, the second what rounding the first lost
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+    return {s, __fadd_rn(e, __fadd_rn(a.lo, b.lo))};
+}
+
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const Pair o{__shfl_xor_sync(FULL, v.hi, d), __shfl_xor_sync(FULL, v.lo, d)};
+        v = pair_add(v, o);
+    }
+    return v;
+}
+
+// 1 / sqrt(sum / K + eps), 1 / K given as a pair.  A sum that is not finite, or zero with eps zero, takes the plain
+// function of its value (0, infinity or NaN).
+__device__ __forceinline__ float row_factor(Pair sum, float inv_hi, float inv_lo, float eps) {
+    if (!(sum.hi < __int_as_float(0x7f800000))) return rsqrtf(sum.hi);
+    const float p = __fmul_rn(sum.hi, inv_hi);
+    const float pe = __fmaf_rn(sum.hi, inv_hi, -p) + (sum.hi * inv_lo + sum.lo * inv_hi);
+    const Pair m0 = pair_add({p, pe}, {eps, 0.0f});
+    const float m = __fadd_rn(m0.hi, m0.lo), ml = __fsub_rn(m0.lo, __fsub_rn(m, m0.hi));
+    const float r = rsqrtf(m);
+    if (!(m >= 1.17549435e-38f)) return r;            // below fp32's normal numbers r^2 would overflow
+    const float t = __fmul_rn(r, r), tl = __fmaf_rn(r, r, -t);
+    const float q = __fmul_rn(m, t), ql = __fmaf_rn(m, t, -q) + (m * tl + ml * t);
+    const float e = __fsub_rn(1.0f, q) - ql;          // 1 - m r^2
+    return __fmaf_rn(0.5f * r, e, r);
+}
+
+// The sum of eight values' squares, the values times f (1, or 2^-70): a product's, a fused and two additions' roundings
+template <int DT>
+__device__ __forceinline__ float squares(const Oct<DT>& o, float f) {
+    const uint64_t ff = ptx::f32x2_pack(f, f);
+    uint64_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f == 1.0f ? o.pair(i) : ptx::f32x2_mul(o.pair(i), ff);
+    const uint64_t s = ptx::f32x2_add(ptx::f32x2_fma(v[1], v[1], ptx::f32x2_mul(v[0], v[0])),
+                                      ptx::f32x2_fma(v[3], v[3], ptx::f32x2_mul(v[2], v[2])));
+    float lo, hi;
+    ptx::f32x2_unpack(s, lo, hi);
+    return lo + hi;
+}
+
+// x + residual in the residual's type.  Two 16-bit numbers are added with one rounding, which is the rounding of their fp32 sum: where
+// that is not exact, the smaller is below a quarter step of the larger, and both round to the larger.
+template <int XT, int HT>
+__device__ __forceinline__ void add_rows(Oct<HT>& h, const Oct<XT>& x, const Oct<HT>& residual) {
+    if constexpr (XT == HT && HT == TG_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(h.w[i]) : "r"(x.w[i]), "r"(residual.w[i]));
+    } else if constexpr (XT == HT && HT == TG_F16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("add.rn.f16x2 %0, %1, %2;" : "=r"(h.w[i]) : "r"(x.w[i]), "r"(residual.w[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h.set2(i, x.value(2 * i) + residual.value(2 * i), x.value(2 * i + 1) + residual.value(2 * i + 1));
+    }
+}
+
+// The largest magnitude, NaN if one is
+__device__ __forceinline__ float max_magnitude(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+
+// Add the parts of a row's warps in a fixed order (every thread gets the sum).  `part` is written anew by each row: two in turn, a
+// warp being at most one row ahead of the others.
+__device__ __forceinline__ Pair block_sum(Pair v, Pair* part) {
+    v = warp_sum(v);
+    const int warps = blockDim.x / 32;
+    if (warps == 1) return v;
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (warps > 4) return warp_sum(threadIdx.x % 32 < warps ? part[threadIdx.x % 32] : Pair{0.0f, 0.0f});
+    Pair s = part[0];
+    for (int w = 1; w < warps; ++w) s = pair_add(s, part[w]);
+    return s;
+}
+
+// What a row's thread writes: y in 16 or 32 bits or not at all, and the 8-bit copy
+enum : int { Y_NONE = 0, Y_HALF = 1, Y_FLOAT = 2 };
+
+template <int HT, int NV, bool WHOLE, bool STAGED, int Y, bool Q>
+__device__ __forceinline__ void finish_row(const NormArgs& a, const Oct<HT> (&h)[NV], float r, int64_t row, int in, int tpr,
+                                           const float* gain, const float (&g0)[8]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = in + j * tpr, col = v * 8;
+        if ((v & ~31) * 8 >= a.K) return;                // (a whole warp: the shuffles below stay together)
+        const int n = a.K - col;                         // below 1: nothing here
+        float y[8], g[8];
+        if constexpr (STAGED) {
+            if (n > 0) read_gain(g, gain + col);
+            else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = g0[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            ptx::f32x2_unpack(ptx::f32x2_mul(ptx::f32x2_mul(h[j].pair(i), ptx::f32x2_pack(r, r)), ptx::f32x2_pack(g[2 * i], g[2 * i + 1])),
+                              y[2 * i], y[2 * i + 1]);
+        if constexpr (Y == Y_HALF) {
+            Oct<TG_BF16> o;
+            if (a.y_dtype == TG_BF16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o.set2(i, y[2 * i], y[2 * i + 1]);
+            } else {
+                Oct<TG_F16> f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f.set2(i, y[2 * i], y[2 * i + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o.w[i] = f.w[i];
+            }
+            o.template store<WHOLE>(a.y + row * a.ldy + col * 2, n);
+        } else if constexpr (Y == Y_FLOAT) {
+            store8<TG_F32, WHOLE>(a.y + row * a.ldy + static_cast<int64_t>(col) * 4, y, n);
+        }
+        if constexpr (Q) {
+            // 16 lanes hold a block.  Values past the row's end count as zero (0 times r may be NaN).
+            float top = 0.0f;
+            if constexpr (WHOLE) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) top = max_magnitude(top, y[i], y[i + 1]);
+                if (n <= 0) top = 0.0f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) top = max_magnitude(top, i < n ? y[i] : 0.0f, i + 1 < n ? y[i + 1] : 0.0f);
+            }
+            uint32_t m = __float_as_uint(top);           // (as integers magnitudes compare alike, NaN above all)
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(FULL, m, d));
+            float s, inv;
+            block_scale(m, a.e5m2 ? 15 : 8, s, inv);
+            if (v % 16 == 0 && n > 0) a.scale[static_cast<int64_t>(v / 16) * a.scale_ld + row] = s;
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ptx::f32x2_unpack(ptx::f32x2_mul(ptx::f32x2_pack(y[2 * i], y[2 * i + 1]), ptx::f32x2_pack(inv, inv)), y[2 * i], y[2 * i + 1]);
+            if (a.e5m2) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) w[i] = pack8<true>(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) w[i] = pack8<false>(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            }
+            if (inv == 0.0f) w[0] = w[1] = 0u;           // a block that is not finite: zeros
+            uint8_t* dst = a.q + row * a.ldq + col;
+            if constexpr (WHOLE) {
+                if (n > 0) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n) dst[i] = static_cast<uint8_t>(w[i / 4] >> (i % 4 * 8));
+            }
+        }
+    }
+}
+
+// Rows unit, unit + units, ..., a unit being the block (NV vectors of eight values a thread) or, with ROWS, for short rows, a warp.
+// WHOLE: rows of whole vectors on 16-byte boundaries.  STAGED: the gain waits in shared memory (otherwise, with one vector a thread
+// and about one row a block, in registers).
+template <int XT, int RT, int NV, bool ROWS, bool WHOLE>
+__global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int HT = RT == N_NONE ? XT : RT;
+    constexpr bool STAGED = NV > 1;
+    extern __shared__ __align__(16) float gain[];
+    __shared__ Pair part[ROWS ? 1 : 2][32];
+    const int tpr = ROWS ? 32 : blockDim.x;
+    const int in = ROWS ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t unit = ROWS ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+    const int64_t units = ROWS ? static_cast<int64_t>(gridDim.x) * (blockDim.x / 32) : gridDim.x;
+    // the next row's values are on their way while a row is finished
+    Oct<XT> x[NV];
+    Oct<HT> h[NV], add[RT == N_NONE ? 1 : NV];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (in + j * tpr) * 8;
+            x[j].template load<WHOLE>(a.x + row * a.ldx + static_cast<int64_t>(col) * item_bytes(XT), a.K - col);
+            if constexpr (RT != N_NONE)
+                add[j].template load<WHOLE>(a.residual + row * a.ldr + static_cast<int64_t>(col) * item_bytes(HT), a.K - col);
+        }
+    };
+    if (unit < a.M) fetch(unit);
+    float g0[8];
+    if constexpr (STAGED) {
+        stage_gain(gain, a.gain, a.gain_dtype, a.K);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g0[i] = in * 8 + i < a.K ? gain_value(a.gain, a.gain_dtype, in * 8 + i) : 0.0f;
+    }
+    int turn = 0;
+    for (int64_t row = unit; row < a.M; row += units, turn ^= 1) {
+        Pair sum{0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (RT != N_NONE) {
+                add_rows(h[j], x[j], add[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < Oct<HT>::WORDS; ++i) h[j].w[i] = x[j].w[i];
+            }
+        }
+        if (row + units < a.M) fetch(row + units);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (RT != N_NONE) {
+                const int col = (in + j * tpr) * 8;
+                h[j].template store<WHOLE>(a.hidden + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col);
+            }
+            sum = pair_add(sum, {squares(h[j], 1.0f), 0.0f});
+        }
+        Pair* parts = part[ROWS ? 0 : turn];
+        sum = ROWS ? warp_sum(sum) : block_sum(sum, parts);
+        float r = row_factor(sum, a.inv_hi, a.inv_lo, a.eps);
+        if (!(sum.hi < __int_as_float(0x7f800000))) {
+            // a row whose squares' sum is past fp32's range (or that has an infinity or a NaN, and keeps it): once more,
+            // scaled down; eps is nothing beside it
+            constexpr float DOWN = 8.470329473e-22f;      // 2^-70
+            Pair low{0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < NV; ++j) low = pair_add(low, {squares(h[j], DOWN), 0.0f});
+            if (!ROWS) __syncthreads();                  // the parts are read above
+            low = ROWS ? warp_sum(low) : block_sum(low, parts);
+            r = row_factor(low, a.inv_hi, a.inv_lo, 0.0f) * DOWN;
+        }
+        if (in == 0) a.r[row] = r;
+        if (!a.y) {
+            finish_row<HT, NV, WHOLE, STAGED, Y_NONE, true>(a, h, r, row, in, tpr, gain, g0);
+        } else if (a.y_dtype == TG_F32) {
+            if (a.q) finish_row<HT, NV, WHOLE, STAGED, Y_FLOAT, true>(a, h, r, row, in, tpr, gain, g0);
+            else finish_row<HT, NV, WHOLE, STAGED, Y_FLOAT, false>(a, h, r, row, in, tpr, gain, g0);
+        } else {
+            if (a.q) finish_row<HT, NV, WHOLE, STAGED, Y_HALF, true>(a, h, r, row, in, tpr, gain, g0);
+            else finish_row<HT, NV, WHOLE, STAGED, Y_HALF, false>(a, h, r, row, in, tpr, gain, g0);
+        }
+    }
+}
+
+// (Rows that are not whole: eight vectors a thread, whatever their length.)
+template <int XT, int RT>
+NormKernel pick(const Spread& s, bool whole) {
+    if (!whole) return s.rows ? &norm_kernel<XT, RT, 4, true, false> : &norm_kernel<XT, RT, 8, false, false>;
+    if (s.rows) return &norm_kernel<XT, RT, 4, true, true>;
+    return s.nv == 1 ? &norm_kernel<XT, RT, 1, false, true> : s.nv == 4 ? &norm_kernel<XT, RT, 4, false, true> : &norm_kernel<XT, RT, 8, false, true>;
+}
+
+}  // namespace
+
+template <>
+NormKernel norm_for<TG_NORM_X>(bool residual, tg_dtype rt, const Spread& s, bool whole) {
+    if (!residual) return pick<TG_NORM_X, N_NONE>(s, whole);
+    if (TG_NORM_X == TG_F32 || rt == TG_F32) return pick<TG_NORM_X, TG_F32>(s, whole);
+    return pick<TG_NORM_X, TG_NORM_X>(s, whole);
+}
+
+}  // namespace norm
+
+}  // namespace tg
