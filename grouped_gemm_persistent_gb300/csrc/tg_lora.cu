@@ -532,7 +532,14 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
             slot = slot + 1 == S::STAGES ? 0 : slot + 1;
             next = next + 1 == S::STAGES ? 0 : next + 1;
             // the operands of as many k as fit, then their products: the loads' latencies lie over one another
+            // (a stage's products are added up by themselves: an instruction's sum is cut off, not rounded, and a chain of them along
+            // the whole of k would drift)
             constexpr int KS = 4 / S::WK, BATCH = S::NW > 4 && KS > 2 ? 2 : KS;
+            float part[S::NW][4];
+#pragma unroll
+            for (int n = 0; n < S::NW; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[n][i] = 0.0f;
 #pragma unroll
             for (int k0 = 0; k0 < KS; k0 += BATCH) {
                 uint32_t a[BATCH][4], b[BATCH][S::NW * 2];
@@ -552,8 +559,12 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
                 for (int k = 0; k < BATCH; ++k)
 #pragma unroll
                     for (int n = 0; n < S::NW; ++n)
-                        mma<DT>(acc[n], a[k][0], a[k][1], a[k][2], a[k][3], b[k][2 * n], b[k][2 * n + 1]);
+                        mma<DT>(part[n], a[k][0], a[k][1], a[k][2], a[k][3], b[k][2 * n], b[k][2 * n + 1]);
             }
+#pragma unroll
+            for (int n = 0; n < S::NW; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][i] += part[n][i];
         }
         // a row keeps its own adapter's sums
 #pragma unroll

@@ -40,14 +40,14 @@ NormKernel norm_for<TG_F32>(bool residual, tg_dtype rt, const Spread& s, bool wh
 namespace {
 
 // A row a warp up to 1024 values.  Longer ones, of 16-bit streams, four vectors a thread (eight above 16384: a block has 512
-// threads then, and rows that are not whole vectors); of 32-bit streams one, up to 8192 values, and for few rows of any, so that a row takes one round of loads.
+// threads then); of 32-bit streams one, up to 8192 values, and for few rows of any, so that a row takes one round of loads.
 // 40960 x 4096, x bf16: into e4m3 with a bf16 residual 181 us with four a thread, 243 with one; into bf16 with an fp32 residual 344
 // and 324.
-Spread spread_for(int64_t K, bool whole, bool few, bool wide, bool q) {
+Spread spread_for(int64_t K, bool few, bool wide, bool q) {
     const int64_t vectors = (K + 7) / 8;
-    if (whole && vectors > 32 && vectors <= 1024 && (few || (wide && !q && vectors > 128))) return spread(K, 1);
+    if (vectors > 32 && vectors <= 1024 && (few || (wide && !q && vectors > 128))) return spread(K, 1);
     if (vectors <= 128) return {32, 4, true};
-    return spread(K, whole && vectors <= 2048 ? 4 : 8);
+    return spread(K, vectors <= 2048 ? 4 : 8);
 }
 
 }  // namespace
@@ -99,19 +99,19 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
     a.ldx = p.ldx * xs;
     a.gain = static_cast<const uint8_t*>(p.gain);
     a.gain_dtype = p.gain_dtype;
-    bool whole = p.K % 8 == 0 && vectors_of(p.x, a.ldx);
+    bool vec = vectors_of(p.x, a.ldx);
     if (residual) {
         a.residual = static_cast<const uint8_t*>(p.residual);
         a.ldr = p.ldr * hs;
         a.hidden = static_cast<uint8_t*>(p.hidden);
         a.ldh = p.ldh * hs;
-        whole = whole && vectors_of(p.residual, a.ldr) && vectors_of(p.hidden, a.ldh);
+        vec = vec && vectors_of(p.residual, a.ldr) && vectors_of(p.hidden, a.ldh);
     }
     if (p.y) {
         a.y = static_cast<uint8_t*>(p.y);
         a.ldy = p.ldy * ys;
         a.y_dtype = p.y_dtype;
-        whole = whole && vectors_of(p.y, a.ldy);
+        vec = vec && vectors_of(p.y, a.ldy);
     }
     if (p.q) {
         a.q = static_cast<uint8_t*>(p.q);
@@ -119,8 +119,10 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
         a.scale = p.scale;
         a.scale_ld = p.scale_ld;
         a.e5m2 = p.q_dtype == TG_E5M2;
-        whole = whole && host::aligned(p.q, 8) && p.ldq % 8 == 0;
+        vec = vec && host::aligned(p.q, 8) && p.ldq % 8 == 0;
     }
+    const bool whole = vec && p.K % 8 == 0;
+    a.vec = vec;
     a.r = p.row_scale;
     a.M = p.M;
     a.K = static_cast<int>(p.K);
@@ -128,7 +130,7 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
     const double inv = 1.0 / static_cast<double>(p.K);
     a.inv_hi = static_cast<float>(inv);
     a.inv_lo = static_cast<float>(inv - a.inv_hi);
-    const Spread shape = spread_for(p.K, whole, p.M <= 2 * d.sms, ht == TG_F32, p.q != nullptr);
+    const Spread shape = spread_for(p.K, p.M <= 2 * d.sms, ht == TG_F32, p.q != nullptr);
     const NormKernel kernel = p.x_dtype == TG_F32 ? norm_for<TG_F32>(residual, p.residual_dtype, shape, whole)
                             : p.x_dtype == TG_F16 ? norm_for<TG_F16>(residual, p.residual_dtype, shape, whole)
                                                   : norm_for<TG_BF16>(residual, p.residual_dtype, shape, whole);

@@ -45,12 +45,14 @@ struct Oct {
             w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
         }
     }
-    // n of the eight are inside the row (the others are zero); WHOLE: eight or none, 16-byte loads
+    // n of the eight are inside the row (the others are zero); WHOLE: eight or none, 16-byte loads; otherwise vec: eight are loaded so
     template <bool WHOLE>
-    __device__ __forceinline__ void load(const uint8_t* p, int n) {
+    __device__ __forceinline__ void load(const uint8_t* p, int n, bool vec) {
         zero();
         if constexpr (WHOLE) {
             if (n > 0) load_whole(p);
+        } else if (vec && n >= 8) {
+            load_whole(p);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -81,13 +83,12 @@ struct Oct {
         }
     }
     template <bool WHOLE>
-    __device__ __forceinline__ void store(uint8_t* p, int n) const {
-        if constexpr (WHOLE) {
-            if (n <= 0) return;
+    __device__ __forceinline__ void store(uint8_t* p, int n, bool vec) const {
+        if (WHOLE ? n > 0 : vec && n >= 8) {
 #pragma unroll
             for (int i = 0; i < WORDS; i += 4)
                 reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-        } else {
+        } else if constexpr (!WHOLE) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (i >= n) continue;
@@ -99,11 +100,11 @@ struct Oct {
 };
 
 template <int DT, bool WHOLE>
-__device__ __forceinline__ void store8(uint8_t* p, const float (&f)[8], int n) {
+__device__ __forceinline__ void store8(uint8_t* p, const float (&f)[8], int n, bool vec) {
     Oct<DT> o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.set2(i, f[2 * i], f[2 * i + 1]);
-    o.template store<WHOLE>(p, n);
+    o.template store<WHOLE>(p, n, vec);
 }
 
 // One value of the gain, or 1
@@ -119,14 +120,13 @@ template <int DT>
 __device__ __forceinline__ void stage_values(float* to, const uint8_t* gain, int K) {
     constexpr int AHEAD = 4;
     const int vectors = (K + 7) / 8;
-    const bool whole = K % 8 == 0 && reinterpret_cast<uintptr_t>(gain) % 16 == 0;
+    const bool vec = reinterpret_cast<uintptr_t>(gain) % 16 == 0;
     for (int base = threadIdx.x; base < vectors; base += AHEAD * blockDim.x) {
         Oct<DT> o[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int v = base + i * blockDim.x, n = v < vectors ? K - v * 8 : 0;
-            if (whole) o[i].template load<true>(gain + static_cast<int64_t>(v) * 8 * item_bytes(DT), n);
-            else o[i].template load<false>(gain + static_cast<int64_t>(v) * 8 * item_bytes(DT), n);
+            o[i].template load<false>(gain + static_cast<int64_t>(v) * 8 * item_bytes(DT), n, vec);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
@@ -176,6 +176,7 @@ struct NormArgs {
     int64_t M;
     int K;
     int gain_dtype, y_dtype, e5m2;
+    int vec;                     // rows on 16-byte boundaries (of 8-bit values 8-byte)
     float eps, inv_hi, inv_lo;
 };
 

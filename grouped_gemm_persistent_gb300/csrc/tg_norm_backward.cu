@@ -34,6 +34,7 @@ struct NormBackArgs {
     int64_t M;
     int K;
     int gain_dtype;
+    int vec;                     // rows on 16-byte boundaries
     float inv_k;
 };
 
@@ -60,14 +61,14 @@ __global__ void __launch_bounds__(ROWS ? 256 : 512) norm_backward_kernel(const _
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (in + j * tpr) * 8;
-            dy[j].template load<WHOLE>(a.dy + row * a.lddy + static_cast<int64_t>(col) * item_bytes(DT), a.K - col);
-            h[j].template load<WHOLE>(a.h + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col);
+            dy[j].template load<WHOLE>(a.dy + row * a.lddy + static_cast<int64_t>(col) * item_bytes(DT), a.K - col, a.vec);
+            h[j].template load<WHOLE>(a.h + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
         }
         if (a.d_hidden) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int col = (in + j * tpr) * 8;
-                dh[j].template load<WHOLE>(a.d_hidden + row * a.lddh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col);
+                dh[j].template load<WHOLE>(a.d_hidden + row * a.lddh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
             }
         } else {
 #pragma unroll
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(ROWS ? 256 : 512) norm_backward_kernel(const _
             read_gain(g, gain + col);
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = fmaf(dy[j].value(i) * g[i], r, fmaf(-(h[j].value(i) * r), c, dh[j].value(i)));
-            store8<HT, WHOLE>(a.dx + row * a.lddx + static_cast<int64_t>(col) * item_bytes(HT), o, a.K - col);
+            store8<HT, WHOLE>(a.dx + row * a.lddx + static_cast<int64_t>(col) * item_bytes(HT), o, a.K - col, a.vec);
         }
     }
     if (a.part) {
@@ -143,17 +144,19 @@ __global__ void __launch_bounds__(1024) norm_gain_kernel(const float* part, int6
 
 using NormBackKernel = void (*)(const NormBackArgs);
 
-// A row a warp up to 1024 values, beyond that two vectors a thread up to 8192 and eight above (and where rows are not whole vectors).  40960 x 4096 bf16 with d_hidden: two a
+// A row a warp up to 1024 values, beyond that two vectors a thread up to 8192 and eight above.  40960 x 4096 bf16 with d_hidden: two a
 // thread 206 us, four 211, one 264.
-Spread spread_for(int64_t K, bool whole) {
+Spread spread_for(int64_t K) {
     const int64_t vectors = (K + 7) / 8;
     if (vectors <= 128) return {32, 4, true};
-    return spread(K, whole && vectors <= 1024 ? 2 : 8);
+    return spread(K, vectors <= 1024 ? 2 : 8);
 }
 
 template <int DT, int HT>
 NormBackKernel back_for(const Spread& s, bool whole) {
-    if (!whole) return s.rows ? &norm_backward_kernel<DT, HT, 4, true, false> : &norm_backward_kernel<DT, HT, 8, false, false>;
+    if (!whole)
+        return s.rows ? &norm_backward_kernel<DT, HT, 4, true, false>
+                      : s.nv == 2 ? &norm_backward_kernel<DT, HT, 2, false, false> : &norm_backward_kernel<DT, HT, 8, false, false>;
     if (s.rows) return &norm_backward_kernel<DT, HT, 4, true, true>;
     return s.nv == 2 ? &norm_backward_kernel<DT, HT, 2, false, true> : &norm_backward_kernel<DT, HT, 8, false, true>;
 }
@@ -215,10 +218,12 @@ extern "C" tg_status tg_rmsnorm_backward(const tg_rmsnorm_backward_args* args, t
     a.lddx = p.lddx * hs;
     a.M = p.M;
     a.K = static_cast<int>(p.K);
-    const bool whole = p.K % 8 == 0 && vectors_of(p.dy, a.lddy) && vectors_of(p.hidden, a.ldh) &&
+    const bool vec = vectors_of(p.dy, a.lddy) && vectors_of(p.hidden, a.ldh) &&
                        (!p.d_hidden || vectors_of(p.d_hidden, a.lddh)) && vectors_of(p.dx, a.lddx);
+    const bool whole = vec && p.K % 8 == 0;
+    a.vec = vec;
     a.inv_k = 1.0f / static_cast<float>(p.K);
-    const Spread shape = spread_for(p.K, whole);
+    const Spread shape = spread_for(p.K);
     const NormBackKernel kernel = p.dy_dtype == TG_F32 ? back_for<TG_F32>(p.hidden_dtype, shape, whole)
                                 : p.dy_dtype == TG_F16 ? back_for<TG_F16>(p.hidden_dtype, shape, whole)
                                                        : back_for<TG_BF16>(p.hidden_dtype, shape, whole);

@@ -142,9 +142,9 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Oct<HT> (&h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o.w[i] = f.w[i];
             }
-            o.template store<WHOLE>(a.y + row * a.ldy + col * 2, n);
+            o.template store<WHOLE>(a.y + row * a.ldy + col * 2, n, a.vec);
         } else if constexpr (Y == Y_FLOAT) {
-            store8<TG_F32, WHOLE>(a.y + row * a.ldy + static_cast<int64_t>(col) * 4, y, n);
+            store8<TG_F32, WHOLE>(a.y + row * a.ldy + static_cast<int64_t>(col) * 4, y, n, a.vec);
         }
         if constexpr (Q) {
             // 16 lanes hold a block.  Values past the row's end count as zero (0 times r may be NaN).
@@ -176,9 +176,9 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Oct<HT> (&h)
             }
             if (inv == 0.0f) w[0] = w[1] = 0u;           // a block that is not finite: zeros
             uint8_t* dst = a.q + row * a.ldq + col;
-            if constexpr (WHOLE) {
-                if (n > 0) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-            } else {
+            if (WHOLE ? n > 0 : a.vec && n >= 8) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            } else if constexpr (!WHOLE) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (i < n) dst[i] = static_cast<uint8_t>(w[i / 4] >> (i % 4 * 8));
@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (in + j * tpr) * 8;
-            x[j].template load<WHOLE>(a.x + row * a.ldx + static_cast<int64_t>(col) * item_bytes(XT), a.K - col);
+            x[j].template load<WHOLE>(a.x + row * a.ldx + static_cast<int64_t>(col) * item_bytes(XT), a.K - col, a.vec);
             if constexpr (RT != N_NONE)
-                add[j].template load<WHOLE>(a.residual + row * a.ldr + static_cast<int64_t>(col) * item_bytes(HT), a.K - col);
+                add[j].template load<WHOLE>(a.residual + row * a.ldr + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
         }
     };
     if (unit < a.M) fetch(unit);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel
         for (int j = 0; j < NV; ++j) {
             if constexpr (RT != N_NONE) {
                 const int col = (in + j * tpr) * 8;
-                h[j].template store<WHOLE>(a.hidden + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col);
+                h[j].template store<WHOLE>(a.hidden + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
             }
             sum = pair_add(sum, {squares(h[j], 1.0f), 0.0f});
         }
@@ -268,10 +268,12 @@ __global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel
     }
 }
 
-// (Rows that are not whole: eight vectors a thread, whatever their length.)
 template <int XT, int RT>
 NormKernel pick(const Spread& s, bool whole) {
-    if (!whole) return s.rows ? &norm_kernel<XT, RT, 4, true, false> : &norm_kernel<XT, RT, 8, false, false>;
+    if (!whole) {
+        if (s.rows) return &norm_kernel<XT, RT, 4, true, false>;
+        return s.nv == 1 ? &norm_kernel<XT, RT, 1, false, false> : s.nv == 4 ? &norm_kernel<XT, RT, 4, false, false> : &norm_kernel<XT, RT, 8, false, false>;
+    }
     if (s.rows) return &norm_kernel<XT, RT, 4, true, true>;
     return s.nv == 1 ? &norm_kernel<XT, RT, 1, false, true> : s.nv == 4 ? &norm_kernel<XT, RT, 4, false, true> : &norm_kernel<XT, RT, 8, false, true>;
 }
