@@ -11,12 +11,17 @@
 // (softmax: the other gate's backward kernel, which knows the factor).
 //
 // Choosing.  A choice by v is one of real numbers: with fp32 scores two experts next to each other in the order would change
-// places with the last bits of exp.  The kernel works in fp32 with a bound E on a score's error (sigmoid: ex2 2^-22
-// relative, times s (1 - s) <= 1/4; 1 + e and its reciprocal 1.5 * 2^-23: below 3e-7.  softmax: the same, the sum's 14
-// additions and the argument's roundings: below 1e-6), and sees where that does not decide: two neighbours among the first
-// k + 1 whose keys are within the bound, and a group at the border of the kept ones.  Such a row is worked out again in
-// 64 bits (choose_in_64): about one in 500 of 131072 x 256 fp32.  Neighbours whose logit and bias are both the same
-// are a true tie, which the index decides, and send no row there: with 16-bit logits and a bias of zeros they are common.
+// places with the last bits of exp.  The kernel works in fp32 with a bound E on a score's error and sees where that does not decide:
+// two neighbours among the first k + 1 whose keys are within the bound, or two groups at the border of the kept ones.  Then the k + 1
+// candidates, or the groups' largest experts, are worked out in 64 bits, each by a lane, and put in order; a row whose next
+// candidate is within the bound too is done again as a whole (choose_in_64).  Double precision is slow here (a row of 256 takes the
+// SM some 5 us): with the whole row always, 131072 x 256 fp32 took 118 us instead of 105, and 8191 rows 43 instead of 24.
+// Neighbours whose logit and bias are both the same are a true tie, which the index decides: with 16-bit logits and a bias of zeros
+// they are common.
+//   sigmoid  e^-x: 2^-22 of itself and |x| 2^-24 for its argument, which s (1 - s) <= 1/4 takes down to 7.3e-8; 1 + e^-x and the
+//            reciprocal 1.5 * 2^-23 of s: E = 3e-7.
+//   softmax  of the row's largest score: 3.4e-7 for its own exponential, twice in a pair; the sum's terms, up to 36 additions and its
+//            reciprocal 3.1e-6, the same for all of the row and so once in a pair: E = 2e-6.
 //
 // Keys.  Without a bias as in tg_router.cu: the logit's ordered bits, the lowest ones replaced by the position counted down.
 // With one: v - lo + 4 is a number from 4 to 8, whose bits below the exponent are a fixed-point number of 21 binary places (about
@@ -100,9 +105,30 @@ __device__ __forceinline__ double value64(unsigned long long o) {
 __device__ __forceinline__ unsigned long long max64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
 __device__ __forceinline__ unsigned long long min64(unsigned long long a, unsigned long long b) { return a < b ? a : b; }
 
-// A sigmoid score with its bias, in 64 bits
-__device__ __forceinline__ double sigmoid64(double x, const float* bias, int e) {
-    const double v = 1.0 / (1.0 + exp(-x));
+// What a row's softmax scores are made of, in 64 bits: the largest logit (0 in a row of -infinity) and 1 / sum of e^(x - it)
+struct Softmax64 {
+    double m, inv;
+};
+
+// The row at `row`, of which this lane has experts e0, e0 + 1, ... (n of them).  Every lane of the warp calls it.
+template <int DT, int L, int V>
+__device__ __noinline__ Softmax64 softmax64(const uint8_t* row, int e0, int n) {
+    auto top = [](double p, double q) { return p != p ? p : q != q ? q : p > q ? p : q; };
+    double m = -__builtin_huge_val(), total = 0.0;
+    for (int j = 0; j < n; ++j) m = top(m, Logits<DT, V>::one(row, e0 + j));
+    for (int d = L / 2; d > 0; d >>= 1) m = top(m, __shfl_xor_sync(FULL, m, d));
+    if (m == -__builtin_huge_val()) m = 0.0;
+#pragma unroll 4
+    for (int j = 0; j < V; ++j)
+        if (j < n) total += exp(Logits<DT, V>::one(row, e0 + j) - m);
+    for (int d = L / 2; d > 0; d >>= 1) total += __shfl_xor_sync(FULL, total, d);
+    return {m, 1.0 / total};
+}
+
+// A score with its bias, in 64 bits (sigmoid: `of` is not used)
+template <bool SIGMOID>
+__device__ __forceinline__ double value_of(double x, const Softmax64& of, const float* bias, int e) {
+    const double v = SIGMOID ? 1.0 / (1.0 + exp(-x)) : exp(x - of.m) * of.inv;
     return bias ? v + static_cast<double>(__ldg(bias + e)) : v;
 }
 
@@ -113,16 +139,8 @@ __device__ __noinline__ int choose_in_64(const ScoredArgs& a, const uint8_t* row
     const int lane = threadIdx.x % 32, in = lane % L;
     if (!wanted) n = 0;
     const bool by_logit = a.bias == nullptr;
-    double m = -__builtin_huge_val(), total = 1.0;
-    if constexpr (!SIGMOID) {
-        auto top = [](double p, double q) { return p != p ? p : q != q ? q : p > q ? p : q; };
-        for (int j = 0; j < n; ++j) m = top(m, Logits<DT, V>::one(row, e0 + j));
-        for (int d = L / 2; d > 0; d >>= 1) m = top(m, __shfl_xor_sync(FULL, m, d));
-        if (m == -__builtin_huge_val()) m = 0.0;
-        total = 0.0;
-        for (int j = 0; j < n; ++j) total += exp(Logits<DT, V>::one(row, e0 + j) - m);
-        for (int d = L / 2; d > 0; d >>= 1) total += __shfl_xor_sync(FULL, total, d);
-    }
+    Softmax64 of{0.0, 0.0};
+    if constexpr (!SIGMOID) of = softmax64<DT, L, V>(row, e0, n);
     unsigned long long key[V];
     unsigned long long first = 0ull, second = 0ull;           // the lane's largest v
 #pragma unroll 4
@@ -131,9 +149,7 @@ __device__ __noinline__ int choose_in_64(const ScoredArgs& a, const uint8_t* row
         if (j >= n) continue;
         const double x = Logits<DT, V>::one(row, e0 + j);
         if (x == -__builtin_huge_val()) continue;
-        double v = SIGMOID ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / total;
-        if (a.bias) v += static_cast<double>(a.bias[e0 + j]);
-        const unsigned long long by_v = order64(v), by_x = order64(x);
+        const unsigned long long by_v = order64(value_of<SIGMOID>(x, of, a.bias, e0 + j)), by_x = order64(x);
         key[j] = by_logit ? by_x : by_v;
         const unsigned long long o = by_logit && a.group_top == 1 ? by_x : by_v;
         second = max64(second, min64(first, o));
@@ -184,16 +200,14 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
     constexpr int ROWS = 32 / L;                  // rows of a warp at once
     constexpr uint32_t LOW = SPAN - 1 > 255 ? SPAN - 1 : 255;      // a key's bits of the position
     constexpr int LOW_BITS = SPAN > 512 ? 10 : SPAN > 256 ? 9 : 8;
-    constexpr float E = SIGMOID ? 3.0e-7f : 1.0e-6f;               // a score's error
+    constexpr float E = SIGMOID ? 3.0e-7f : 2.0e-6f;               // a score's error
     constexpr float U = 5.9604645e-8f;                             // 2^-24
-    // How far a computed v may be off: the score, and the roundings of b - lo, of 4 more and of v itself (2^-23, 2^-22 and 2^-22).
-    // Keys that are nearer than twice that, in their steps of 2^-21, are not told apart; nor are groups' scores, of one such v or of
-    // two, whose sum is rounded by 2^-21 and has steps of 2^-20.
-    constexpr float OFF = E + 10.0f * U;
+    // How far a computed v may be off: the score (softmax: E of itself, and so of the row's largest, 1 / whole), and the roundings of
+    // b - lo, of 4 more and of v itself (2^-23, 2^-22 and 2^-22).  Keys that are nearer than twice that, in their steps of 2^-21, are
+    // not told apart; nor are groups' scores, of one such v or of two, whose sum is rounded by 2^-21 and has steps of 2^-20.
     constexpr int CUT = LOW_BITS - 8;                              // bits of v that a key leaves out
-    constexpr uint32_t STEPS = static_cast<uint32_t>(2097152.0f * 2.0f * OFF) + 2;
-    constexpr uint32_t NEAR = (STEPS >> CUT) + 1;
-    constexpr uint32_t PAIR_STEPS = static_cast<uint32_t>(1048576.0f * 2.0f * (2.0f * OFF + 8.0f * U)) + 2;
+    auto steps_of = [](float off) { return static_cast<uint32_t>(2097152.0f * 2.0f * off) + 2; };
+    auto pair_steps_of = [](float off) { return static_cast<uint32_t>(1048576.0f * 2.0f * (2.0f * off + 8.0f * U)) + 2; };
     extern __shared__ __align__(16) uint8_t dyn[];
     float* s_sum = reinterpret_cast<float*>(dyn);                              // [warps][SPAN]
     int32_t* s_count = reinterpret_cast<int32_t*>(s_sum + R_WARPS * SPAN);     // [SPAN], by expert
@@ -294,6 +308,8 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
             }
         }
         rows += any && in == 0 ? 1 : 0;
+        const float off = (SIGMOID ? E : E * fminf(inv, 1.0f)) + 10.0f * U;
+        const uint32_t steps = steps_of(off), apart_from = (steps >> CUT) + 1;
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = x.value(j) == MINUS_INF ? MINUS_INF : v[j] + b[j];
 
@@ -333,11 +349,11 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                     after += group_max<L>(__viaddmax_u32(key, 0u - after, 0u));
                 }
                 kept = key >= edge;
-                const bool open = after >= 0x80000000u && (edge >> 8) - (after >> 8) <= (s.group_top == 2 ? PAIR_STEPS : STEPS);
+                const bool open = after >= 0x80000000u && (edge >> 8) - (after >> 8) <= (s.group_top == 2 ? pair_steps_of(off) : steps);
                 if (__any_sync(FULL, open)) {
                     // the groups at the border are not told apart.  A group's score in 64 bits needs its largest experts alone, if
                     // they are apart from the next.
-                    bool clear = SIGMOID;
+                    bool clear = true;
                     int e[2] = {0, 0};
                     uint32_t last = 0u;
                     for (int i = 0; i <= s.group_top; ++i) {
@@ -350,17 +366,21 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                         for (int d = 1; d < lanes; d <<= 1) best = max(best, __shfl_xor_sync(FULL, best, d));
                         const uint32_t now = last + best;
                         if (i < s.group_top) e[i] = expert_of(now);
-                        else clear &= now < 0x80000000u || (last >> LOW_BITS) - (now >> LOW_BITS) > NEAR;
+                        else clear &= now < 0x80000000u || (last >> LOW_BITS) - (now >> LOW_BITS) > apart_from;
                         last = now;
                     }
                     const uint32_t all_clear = row_ballot<L>(clear || group >= s.groups, lane, in);
                     const bool whole_row = all_clear == (L == 32 ? FULL : (1u << L % 32) - 1u);
                     redo |= open && !whole_row;
                     double score64 = 0.0;
-                    if (SIGMOID && open && whole_row && group < s.groups) {
-                        const uint8_t* row = a.logits + t * a.ld_bytes;
-                        score64 = sigmoid64(X::one(row, e[0]), s.bias, e[0]);
-                        if (s.group_top == 2) score64 += sigmoid64(X::one(row, e[1]), s.bias, e[1]);
+                    const uint8_t* row = a.logits + t * a.ld_bytes;
+                    Softmax64 of{0.0, 0.0};
+                    if constexpr (!SIGMOID) {
+                        if (__any_sync(FULL, open && whole_row)) of = softmax64<DT, L, V>(row, e0, open && whole_row ? n : 0);
+                    }
+                    if (open && whole_row && group < s.groups) {
+                        score64 = value_of<SIGMOID>(X::one(row, e[0]), of, s.bias, e[0]);
+                        if (s.group_top == 2) score64 += value_of<SIGMOID>(X::one(row, e[1]), of, s.bias, e[1]);
                     }
                     int before = 0;
                     for (int h = 0; h < s.groups; ++h) {
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                 if (!exact) {
                     if (s.group_top == 2) score += two > MINUS_INF ? two : 4.0f - lo;    // (of sums less 2 lo and 8 more)
                     // twice a sum's error: scores, biases less lo, the sum itself, and lo where it stands alone
-                    near = 4.0f * OFF + 8.0f * U * (8.0f + fabsf(score)) + 4.0f * U * fabsf(lo);
+                    near = 4.0f * off + 8.0f * U * (8.0f + fabsf(score)) + 4.0f * U * fabsf(lo);
                     if (!(near < __int_as_float(0x7f800000))) near = 0.0f;              // (no expert that may be chosen)
                 }
                 int before = 0, maybe = 0;        // groups that come first for certain, and possibly
@@ -427,8 +447,8 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
             if (in == L - 1) after = top;
             const uint32_t apart = (mine >> LOW_BITS) - (after >> LOW_BITS);
             // the last choice has to be clear of what lies below lo
-            if (below) redo |= row_ballot<L>(in == a.k - 1 && any && mine < (0x80000000u | (NEAR << LOW_BITS)), lane, in) != 0u;
-            bool close = in < a.k && after >= key_min && (biased ? apart <= NEAR : apart == 0u);
+            if (below) redo |= row_ballot<L>(in == a.k - 1 && any && mine < (0x80000000u | (apart_from << LOW_BITS)), lane, in) != 0u;
+            bool close = in < a.k && after >= key_min && (biased ? apart <= apart_from : apart == 0u);
             if (__any_sync(FULL, close)) {
                 if (close) {
                     const int e = expert_of(after);
@@ -443,14 +463,19 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                 for (int j = 0; j < V; ++j) best = __viaddmax_u32(key[j], 0u - top, best);
                 const uint32_t past = top + group_max<L>(best);
                 const uint32_t gap = (top >> LOW_BITS) - (past >> LOW_BITS);
-                const bool clear = past >= top || past < key_min || gap > (biased ? NEAR : 0u);
-                const bool order = some && clear && a.k < L && (SIGMOID || !biased);
+                const bool clear = past >= top || past < key_min || gap > (biased ? apart_from : 0u);
+                const bool order = some && clear && a.k < L;
                 redo |= some && !order;
                 if (__any_sync(FULL, order)) {
                     unsigned long long my_v = 0ull;
+                    const uint8_t* row = a.logits + t * a.ld_bytes;
+                    Softmax64 of{0.0, 0.0};
+                    if constexpr (!SIGMOID) {
+                        if (biased) of = softmax64<DT, L, V>(row, e0, order ? n : 0);
+                    }
                     if (order && in <= a.k && my_e >= 0) {
-                        const double z = X::one(a.logits + t * a.ld_bytes, my_e);
-                        my_v = order64(biased ? sigmoid64(z, s.bias, my_e) : z);
+                        const double z = X::one(row, my_e);
+                        my_v = order64(biased ? value_of<SIGMOID>(z, of, s.bias, my_e) : z);
                     }
                     int place = 0, got = -1;
                     for (int i = 0; i <= a.k; ++i) {
