@@ -851,6 +851,9 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
     """The gradient of ``logits`` from those of routing.weights (fp32 [T, k]) and routing.loss (fp32, one
     element, on the GPU); None is zero (tg_moe_router_backward).  ``out`` has the logits' type."""
     dt, T, G, ld = _logits(logits)
+    code = SCORES.get(routing.score)
+    if code is None:
+        raise ValueError(f"routing.score must be one of {sorted(SCORES)}, got {routing.score!r}")
     k = routing.experts.shape[1]
     experts, weights, slope = routing.experts, routing.weights, routing.slope
     if experts.dtype != torch.int32 or experts.shape[0] != T or not experts.is_contiguous():
@@ -872,7 +875,7 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
         ldd = _row_major_ld(out, "out", G)
     _on_one_gpu("logits routing.experts routing.weights routing.slope d_weights d_loss out", logits, experts,
                 weights, slope, d_weights, d_loss, out)
-    if routing.score == "softmax" and routing.weight_scale == 1.0:
+    if code == 0 and routing.weight_scale == 1.0:
         status = load().tg_moe_router_backward(logits.data_ptr(), dt, ld, T, G, k, int(routing.renormalize),
                                                experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
                                                None if d_weights is None else d_weights.data_ptr(),
@@ -882,7 +885,7 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
         status = load().tg_moe_router_scored_backward(
             _ROUTER_BACKWARD.pack(T, G, k, logits.data_ptr(), ld, experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
                                   _ptr(d_weights), _ptr(d_loss), out.data_ptr(), ldd, routing.weight_scale, dt,
-                                  SCORES[routing.score], routing.renormalize), _stream_handle(stream))
+                                  code, routing.renormalize), _stream_handle(stream))
     if status:
         _check(status)
     return out

@@ -371,7 +371,8 @@ tg_status tg_moe_gemm_scaled(const tg_scaled_operand *A, int64_t T, int64_t K, c
  *   y         = (h * row_scale) * gain, each product rounded to fp32, then to y's type
  *   q, scale  = tg_quantize_blocks of the fp32 y in 1 x 128 blocks
  *
- *   M, K               : rows and columns, K <= TG_RMSNORM_MAX_COLUMNS.  M == 0 or K == 0 is a no-op.
+ *   M, K               : rows and columns, K <= TG_RMSNORM_MAX_COLUMNS.  M == 0 or K == 0 is a no-op
+ *                        (row_scale is not written).
  *   x, ldx             : row-major bf16, fp16 or fp32, as every matrix here of any alignment
  *                        (16-byte aligned rows are moved with wide accesses).
  *   residual, ldr      : NULL, or x's type or fp32.
