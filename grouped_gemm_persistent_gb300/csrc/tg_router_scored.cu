@@ -227,10 +227,11 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
         return static_cast<int>((p >> s.shift) * s.each + (p & ((1u << s.shift) - 1u)));
     };
     const bool biased = s.bias != nullptr;
-    float b[V], lo = 0.0f;                        // b: the bias - lo + 4
+    float lo = 0.0f;
+    float* s_bias = reinterpret_cast<float*>(s_count + SPAN) + first;          // this lane's: the bias - lo + 4
     bool odd = false, below = false;              // a bias of NaN or +infinity (64 bits sort it out), or below lo
     if (biased) {
-        float small = __int_as_float(0x7f800000), large = MINUS_INF;
+        float small = __int_as_float(0x7f800000), large = MINUS_INF, b[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             b[j] = j < n ? __ldg(s.bias + e0 + j) : 0.0f;
@@ -245,28 +246,36 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
         large = group_max_plain<L>(large);
         if (large > MINUS_INF) lo = fmaxf(small, large - 2.5f);
         below = small < lo;
-    }
+        // (every row of the block writes the same)
 #pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = biased ? b[j] - lo + 4.0f : 4.0f;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * R_WARPS * ROWS;
-    // (a warp's rows are neighbours; lanes past the last row keep -infinity and store nothing)
-    int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
-    const int64_t warp_first = t - lane / L;
+        for (int j = 0; j < V; ++j) s_bias[j] = b[j] - lo + 4.0f;
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s_bias[j] = 4.0f;
+    }
+    __syncwarp();
+    // (a warp's rows are neighbours; lanes past the last row keep -infinity and store nothing.  T * k is below 2^31.)
+    const uint32_t rows_in = static_cast<uint32_t>(a.T), step = gridDim.x * R_WARPS * ROWS;
+    const uint32_t warp_first = (blockIdx.x * R_WARPS + warp) * ROWS;
+    uint32_t t = warp_first + lane / L;
+    const int64_t ahead = step * a.ld_bytes;
+    const uint8_t* row = a.logits + t * a.ld_bytes;                // row t
     X next;
     const bool whole_rows = a.vec && a.G == SPAN;      // every lane of every row loads V logits
-    auto fetch = [&](int64_t row) {
-        const uint8_t* at = a.logits + row * a.ld_bytes + static_cast<int64_t>(e0) * X::ESIZE;
-        if (whole_rows && row - lane / L + ROWS <= a.T) next.load_whole(at);
-        else next.load(at, row < a.T ? n : 0, a.vec != 0);
+    // row `first` + lane / L, the warp's rows beginning at `first`, at `from`
+    auto fetch = [&](uint32_t first, const uint8_t* from) {
+        const uint8_t* at = from + e0 * X::ESIZE;
+        if (whole_rows && first + ROWS <= rows_in) next.load_whole(at);
+        else next.load(at, first + lane / L < rows_in ? n : 0, a.vec != 0);
     };
-    fetch(t);
+    fetch(warp_first, row);
     float sum[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] = 0.0f;
     int rows = 0;
-    for (int64_t base = warp_first; base < a.T; base += step, t += step) {
+    for (uint32_t base = warp_first; base < rows_in; base += step, t += step, row += ahead) {
         const X x = next;
-        if (base + step < a.T) fetch(t + step);
+        if (base + step < rows_in) fetch(base + step, row + ahead);
         float v[V];                               // the scores, then v - lo + 4, -infinity for what may not be chosen
         float m = 0.0f, whole = 0.0f;
         bool any;
@@ -312,7 +321,13 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
         const float off = (SIGMOID ? E : E * fminf(inv, 1.0f)) + 10.0f * U;
         const uint32_t steps = steps_of(off), apart_from = (steps >> CUT) + 1;
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = x.value(j) == MINUS_INF ? MINUS_INF : v[j] + b[j];
+        for (int j = 0; j < V; j += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(s_bias + j);
+            v[j] = x.value(j) == MINUS_INF ? MINUS_INF : v[j] + b.x;
+            v[j + 1] = x.value(j + 1) == MINUS_INF ? MINUS_INF : v[j + 1] + b.y;
+            v[j + 2] = x.value(j + 2) == MINUS_INF ? MINUS_INF : v[j + 2] + b.z;
+            v[j + 3] = x.value(j + 3) == MINUS_INF ? MINUS_INF : v[j + 3] + b.w;
+        }
 
         bool redo = whole != whole || (odd && any), kept = true;
         if (s.groups > 1) {
@@ -374,7 +389,6 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                     const bool whole_row = all_clear == (L == 32 ? FULL : (1u << L % 32) - 1u);
                     redo |= open && !whole_row;
                     double score64 = 0.0;
-                    const uint8_t* row = a.logits + t * a.ld_bytes;
                     Softmax64 of{0.0, 0.0};
                     if constexpr (!SIGMOID) {
                         if (__any_sync(FULL, open && whole_row)) of = softmax64<DT, L, V>(row, e0, open && whole_row ? n : 0);
@@ -453,7 +467,6 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
             if (__any_sync(FULL, close)) {
                 if (close) {
                     const int e = expert_of(after);
-                    const uint8_t* row = a.logits + t * a.ld_bytes;
                     const bool tie = X::one(row, my_e) == X::one(row, e) && (!biased || __ldg(s.bias + my_e) == __ldg(s.bias + e));
                     close = !tie;
                 }
@@ -469,7 +482,6 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
                 redo |= some && !order;
                 if (__any_sync(FULL, order)) {
                     unsigned long long my_v = 0ull;
-                    const uint8_t* row = a.logits + t * a.ld_bytes;
                     Softmax64 of{0.0, 0.0};
                     if constexpr (!SIGMOID) {
                         if (biased) of = softmax64<DT, L, V>(row, e0, order ? n : 0);
@@ -493,20 +505,21 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
             }
         }
         if (__any_sync(FULL, redo)) {
-            const int e = choose_in_64<DT, L, V, SIGMOID>(s, a.logits + t * a.ld_bytes, e0, n, redo);
+            const int e = choose_in_64<DT, L, V, SIGMOID>(s, row, e0, n, redo);
             if (redo) my_e = e;
         }
         float my_s = 0.0f;
         if (in >= a.k) my_e = -1;
         if (my_e >= 0) {
-            const float z = X::one(a.logits + t * a.ld_bytes, my_e);
+            const float z = X::one(row, my_e);
             my_s = SIGMOID ? sigmoid_approx(z) : exp_flush(z - m) * inv;
             atomicAdd(&s_count[my_e], 1);
         }
         const float chosen = a.renorm ? group_sum<L>(my_s) : 1.0f;
-        if (in < a.k && t < a.T) {
-            a.experts[t * a.k + in] = my_e;
-            a.weights[t * a.k + in] = my_s != 0.0f ? my_s * rcp_flush(chosen) * s.factor : 0.0f;
+        if (in < a.k && t < rows_in) {
+            const uint32_t at = t * a.k + in;
+            a.experts[at] = my_e;
+            a.weights[at] = my_s != 0.0f ? my_s * rcp_flush(chosen) * s.factor : 0.0f;
         }
     }
     // the row slots of a warp, then the warps of the block
@@ -629,20 +642,25 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
         extra[first + j] = 0.0f;
     }
     __syncwarp();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * R_WARPS * ROWS;
-    int64_t t = (static_cast<int64_t>(blockIdx.x) * R_WARPS + warp) * ROWS + lane / L;
-    const int64_t warp_first = t - lane / L;
-    const bool choice = a.d_weights != nullptr && in < a.k;
+    // (T * k is below 2^31)
+    const uint32_t rows_in = static_cast<uint32_t>(a.T), step = gridDim.x * R_WARPS * ROWS;
+    const uint32_t warp_first = (blockIdx.x * R_WARPS + warp) * ROWS;
+    uint32_t t = warp_first + lane / L;
+    const int64_t ahead = step * a.ld_bytes, out_ahead = step * a.ldo_bytes;
+    const uint8_t* row = a.logits + t * a.ld_bytes;
+    uint8_t* out = a.out + t * a.ldo_bytes + first * X::ESIZE;
+    const bool choice = a.d_weights != nullptr && in < a.k, whole_rows = a.vec_in && a.G == L * V;
     X next;
     int e_next = -1;
     float z_next = 0.0f, dw_next = 0.0f;
-    auto fetch = [&](int64_t row) {
-        const uint8_t* at = a.logits + row * a.ld_bytes;
-        next.load(at + first * X::ESIZE, row < a.T ? n : 0, a.vec_in != 0);
+    auto fetch = [&](uint32_t from, const uint8_t* at) {
+        const uint32_t r = from + lane / L;
+        if (whole_rows && from + ROWS <= rows_in) next.load_whole(at + first * X::ESIZE);
+        else next.load(at + first * X::ESIZE, r < rows_in ? n : 0, a.vec_in != 0);
         e_next = -1;
-        if (choice && row < a.T) {
-            e_next = __ldg(a.experts + row * a.k + in);
-            dw_next = __ldg(a.d_weights + row * a.k + in);
+        if (choice && r < rows_in) {
+            e_next = __ldg(a.experts + r * a.k + in);
+            dw_next = __ldg(a.d_weights + r * a.k + in);
         }
         if (e_next < 0 || e_next >= a.G) {       // no choice (-1): nothing of it counts
             e_next = -1;
@@ -651,12 +669,12 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
             z_next = X::one(at, e_next);
         }
     };
-    fetch(t);
-    for (int64_t base = warp_first; base < a.T; base += step, t += step) {
+    fetch(warp_first, row);
+    for (uint32_t base = warp_first; base < rows_in; base += step, t += step, row += ahead, out += out_ahead) {
         const X x = next;
         const int e = e_next;
         const float z = z_next, dw = dw_next;
-        if (base + step < a.T) fetch(t + step);
+        if (base + step < rows_in) fetch(base + step, row + ahead);
         // with e = e^-|x| and t = 1 / (1 + e): s is t or e t, s (1 - s) is e t^2 on either side of zero, 0 at both infinities
         float p[V];                              // s (1 - s)
         float whole = 0.0f, pu = 0.0f;
@@ -696,8 +714,7 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) d[j] *= p[j];
-        if (t >= a.T) continue;
-        uint8_t* dst = a.out + t * a.ldo_bytes + first * X::ESIZE;
+        if (t >= rows_in) continue;
         uint32_t o[X::WORDS];
 #pragma unroll
         for (int i = 0; i < X::WORDS; ++i) {
@@ -714,13 +731,13 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
         if (n == V && a.vec_out) {
 #pragma unroll
             for (int i = 0; i < X::WORDS; i += 4)
-                reinterpret_cast<uint4*>(dst)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                reinterpret_cast<uint4*>(out)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (j >= n) continue;
-                if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(dst)[j] = o[j];
-                else reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(o[j / 2] >> ((j & 1) * 16));
+                if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(out)[j] = o[j];
+                else reinterpret_cast<uint16_t*>(out)[j] = static_cast<uint16_t>(o[j / 2] >> ((j & 1) * 16));
             }
         }
     }
@@ -837,7 +854,7 @@ extern "C" tg_status tg_moe_router_scored(const tg_router_args* args, tg_stream_
         a.r.part_n = static_cast<int32_t*>(ws) + 2 * blocks * p.G;
     }
     const ScoredKernel kernel = scored_for(p.dtype, p.score == TG_SCORE_SIGMOID, shape);
-    const size_t smem = static_cast<size_t>(R_WARPS + 1) * shape.lanes * shape.per_lane * 4;
+    const size_t smem = static_cast<size_t>(R_WARPS + 2) * shape.lanes * shape.per_lane * 4;
     cudaError_t e = allow_smem(kernel, smem);
     if (e == cudaSuccess && cluster && blocks > 1) {
         cudaLaunchConfig_t cfg = {};
