@@ -6,7 +6,9 @@ behind the C ABI in include/tg.h.  This package holds the ctypes binding
 (argument marshalling only), the in-tree build script, the seeded input
 generators (``workloads``) shared by the tests and the benchmark, and an example
 layer (``moe_layer``) on the 8-bit products (``quantize_fp8``, ``gemm_fp8``,
-``moe_gemm_fp8``) and the expert gate (``moe_router``, ``moe_router_backward``).
+``moe_gemm_fp8``), the expert gate (``moe_router``, ``moe_router_backward``) and the
+residual stream's norm (``rmsnorm``, ``rmsnorm_backward``).  ``lora_add`` adds the
+requests' low-rank adapters to a projection's result.
 """
 from ._binding import (BF16, COL_MAJOR, E4M3, E5M2, EPILOGUES, F16, F32, FP8_BLOCK, ROW_MAJOR, Fp8Operand, Routing, TG_ERR_CUDA, TG_ERR_INVALID_ARG,
                        TG_ERR_NO_DEVICE, TG_ERR_TIMEOUT, TG_ERR_UNSUPPORTED, TG_OK, GroupProblem, TGError,

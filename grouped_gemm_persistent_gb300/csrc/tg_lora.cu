@@ -8,16 +8,22 @@
 //  - Rows (few rows of small rank): a row's u = x A^T is cut along K over blocks of 512, then a block takes a part of a
 //    row's columns and adds the cuts.  Every row reads its own adapter, from L2 where rows share one: T r (K + N) 2 bytes.
 //    Two launches, the second of which has its part of B and base in registers before it waits for the first.
-//  - Tiles (more rows).  A kernel of one cluster orders the rows by adapter, each adapter's filled up to whole tiles of 16 or 64
-//    rows, so that any order of the rows reads an adapter once a tile.  A cluster takes a tile: its blocks share k,
-//    add their parts of u over distributed shared memory, and share the columns.  k goes through a ring of stages
-//    (cp.async: the rows are gathered) into mma.sync; u is cut into two 16-bit numbers for the second product, whose B comes
-//    straight from global memory.  (mma.sync and not the tensor memory's: the rows are gathered, the products are few,
-//    and an accumulator of 16 to 128 columns is read back after a few thousand cycles.)  A tile may hold several
-//    adapters (more than 512 of them share buckets): it goes through them one after the other, a row keeping only its own's
-//    result, so that a NaN of another adapter or row does not reach it.
-// The order of a product's k and columns is free: a lane's eight neighbouring values of B stand for the two pairs that each of
-// two mma.sync instructions wants of it, and its results of four instructions are eight neighbouring columns of a row.
+//  - Tiles (more rows).  A kernel of one cluster orders the rows by adapter, each adapter's filled up to whole tiles, so that
+//    any order of the rows reads an adapter once a tile.  A cluster takes a tile: its blocks share k, add their parts of u over
+//    distributed shared memory, and share the columns.  x and A go through a ring of stages (cp.async: the rows are gathered) into
+//    mma.sync; u is cut into two 16-bit numbers for the second product, whose B and base come through the same ring.  (mma.sync
+//    and not tcgen05.mma: the operations take 16 % of its rate, 605 TFLOP/s measured, and an accumulator of 16 to 128 columns
+//    would be read back after a few thousand cycles, for every adapter of a tile anew.)  A tile may hold several adapters (more
+//    than 512 of them share buckets): it goes through them one after the other, a row keeping only its own's result, so that a
+//    NaN of another adapter or row does not reach it.
+// The order of the second product's columns is free: B's rows are laid out so that a lane's results are neighbouring columns.
+//
+// What it took, 8191 rows of K 4096, N 1536, rank 64, 16 adapters (19 us at the copy rate): operands from global memory to
+// registers, tiles of neighbouring rows 131 us (tiles of several adapters took as many times as long); rows ordered, k through the
+// ring, clusters 81; fewer instructions a stage 54; the order by a cluster instead of a block 52; B and base through the ring and u
+// put together by rows 49; whole stages copied without checks, a stage's operands loaded before its products 43.  Now about 10 us of
+// it go before the first stage (the order, two launches), 19 into the first product (141 MB through L2: A is read once a tile)
+// and 14 into the second.
 //
 // Precision.  u is summed in fp32, times scale, and enters the second product as hi + lo of the operands' type (bf16: 16
 // bits, 2^-17; fp16, of the row's power-of-two multiple that brings its largest value to 1..2: 22 bits): a single 16-bit u would
@@ -831,8 +837,9 @@ struct TileVariant {
 template <int DT, int BT, int RT, int ROWS>
 TileVariant variant() { return {&lora_tile_kernel<DT, BT, RT, ROWS>, ROWS, Tile<RT, ROWS, BT == TG_F32 ? 4 : 2>::BYTES}; }
 
-// Tiles of 64 rows read an adapter a quarter as often; tiles of 16 where an adapter has fewer than 32 rows on average, if all
-// of them are in use.
+// Tiles of 64 rows (32 above 64 ranks, for their sums' room) read an adapter less often; tiles of 16 where an adapter has fewer than 32
+// rows on average, if all of them are in use.  8191 rows of one adapter: 64-row tiles 49 us, 16-row tiles 56; spread over 200 adapters
+// 75 (64 rows), over 300 88 (16 rows).
 template <int DT, int BT>
 TileVariant variant_for(int64_t T, int G, int r) {
     const bool tall = T >= 32 * static_cast<int64_t>(G);

@@ -9,7 +9,11 @@
 //   dx = r d - n S r / K + d_hidden              d_hidden: what reaches h past the norm
 //   d_gain = sum_t dy n
 //
-// Bound by memory: a row is read once, held in registers between the sum and the scaling, and written once.
+// Bound by memory: a row is read once, held in registers between the sum and the scaling, and written once.  Blocks are persistent
+// (as many as are resident), keep the gain in shared memory and load the next row while they finish one.  65536 x 4096 bf16 with a
+// bf16 residual into e4m3 (279 us at the copy rate): a block a row 341 us, 38 instructions a value, with loads and outputs
+// chosen inside the loop; persistent, the next row on its way, 326; packed arithmetic (two values an instruction) 296; the gain
+// staged by wide loads 285, 6.6 TB/s.
 //
 // The row factor.  An 8-bit value next to a rounding border, and a scale next to a power of two, fall on one side or
 // the other with the last bit of r, so r is worked out to well below fp32's half step and rounded once: every

@@ -31,6 +31,10 @@
 // The groups are chosen the same way, by their scores' bits and their indices, while each has its group_top experts to choose
 // from and none below lo; otherwise, and without a bias by the largest logit itself, by counting the groups that come before each.
 //
+// Bound by instruction issue: 594 warp instructions a row of 256 with 8 groups and k = 8, 73 % of the issue rate, 93 us for 131072
+// rows whose logits are read in 20 us; a choice more costs 2.2 us, the groups 15.  The gradient: 292 instructions a row, 55 us (40 us
+// at the copy rate).
+//
 // Positions.  A row is L lanes of V positions.  Each group has a power of two of positions, V at least, so that
 // a group is whole lanes and its sums are a few exchanges; the positions past its experts hold -infinity.
 #include <cuda_bf16.h>

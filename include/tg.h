@@ -17,8 +17,11 @@
  * in 8-bit floating point there are the products of e4m3 / e5m2 operands with a
  * scale for each block of 128 (tg_gemm_scaled, tg_moe_gemm_scaled), their
  * quantiser (tg_quantize_blocks) and the gate with its balance loss
- * (tg_moe_router, tg_moe_router_backward); the pages have no counterpart for
- * these.
+ * (tg_moe_router, tg_moe_router_backward).  Between and beside the products of a
+ * block there are the residual stream's norm with an 8-bit output (tg_rmsnorm,
+ * tg_rmsnorm_backward), the gate with other scores, a bias and groups
+ * (tg_moe_router_scored, tg_moe_router_scored_backward) and the adapters of many
+ * requests (tg_lora_add).  The pages have no counterpart for these.
  *
  * Where it runs.  One persistent, warp-specialised CUDA kernel on the
  * current device: a TMA producer warp fills a shared-memory ring guarded by
@@ -415,7 +418,8 @@ tg_status tg_rmsnorm(const tg_rmsnorm_args *args, tg_stream_t stream);
  *   d_hidden, lddh      : the gradient that reaches h past the norm, of hidden's type; NULL: zero.
  *   dx, lddx            : of hidden's type; may be d_hidden or, of the same type, dy.
  *   d_gain              : DEVICE fp32 [K], NULL when not wanted.  M == 0 writes zeros.
- * Deterministic.  With d_gain, a workspace of up to 4 KiB x K from the library's memory pool.
+ * Deterministic.  With d_gain, a workspace of 4 K bytes for each block (each warp up to 1024 columns)
+ * that is resident, from the library's memory pool, released on the stream.
  */
 typedef struct tg_rmsnorm_backward_args {
     int64_t M, K;
@@ -566,7 +570,8 @@ tg_status tg_moe_router_scored_backward(const tg_router_backward_args *args, tg_
  *                      be base.
  * Both products are summed in fp32; the one between them is held to 2^-17 (bf16) or better, and
  * the sum with base is rounded once.  A row's result depends on its own values and adapter alone.
- * Deterministic.  T == 0 or N == 0 is a no-op; without K, r or G out is base.
+ * Deterministic.  T == 0 or N == 0 is a no-op; without K, r or G out is base.  A workspace of some
+ * bytes a row from the library's memory pool, released on the stream.
  */
 typedef struct tg_lora_args {
     int64_t T, K, N, r, G;
