@@ -43,15 +43,14 @@ NormKernel norm_for<TG_F32>(bool residual, tg_dtype rt, const Spread& s, bool wh
 
 namespace {
 
-// A row a warp up to 1024 values.  Longer ones, of 16-bit streams, four vectors a thread (eight above 16384: a block has 512
-// threads then); of 32-bit streams one, up to 8192 values, and for few rows of any, so that a row takes one round of loads.
-// 40960 x 4096, x bf16: into e4m3 with a bf16 residual 181 us with four a thread, 243 with one; into bf16 with an fp32 residual 344
-// and 324.
+// One vector a thread up to 256 values, two up to 1024 (65536 x 512 into e4m3 40 us, 48 with four).  Longer rows: four of 16-bit streams
+// (eight above 16384: a block has 512 threads then); one of 32-bit streams that are not quantised, up to 8192 values, and of few
+// rows, so that a row takes one round of loads.  40960 x 4096, x bf16: into e4m3 with a bf16 residual 181 us with four a thread, 198
+// with two, 243 with one; into bf16 with an fp32 residual 344, 351 and 324.
 Spread spread_for(int64_t K, bool few, bool wide, bool q) {
     const int64_t vectors = (K + 7) / 8;
-    if (vectors > 32 && vectors <= 1024 && (few || (wide && !q && vectors > 128))) return spread(K, 1);
-    if (vectors <= 128) return {32, 4, true};
-    return spread(K, vectors <= 2048 ? 4 : 8);
+    if (vectors <= 32 || (vectors <= 1024 && (few || (wide && !q && vectors > 128)))) return spread(K, 1);
+    return spread(K, vectors <= 128 ? 2 : vectors <= 2048 ? 4 : 8);
 }
 
 }  // namespace
@@ -127,6 +126,11 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
     }
     const bool whole = vec && p.K % 8 == 0;
     a.vec = vec;
+    a.wide = 0;
+    if (vec) {
+        a.wide = wide_rows(p.M, p.K, p.ldx);
+        if (residual && wide_rows(p.M, p.K, p.ldr) < a.wide) a.wide = wide_rows(p.M, p.K, p.ldr);
+    }
     a.r = p.row_scale;
     a.M = p.M;
     a.K = static_cast<int>(p.K);
@@ -138,16 +142,15 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
     const NormKernel kernel = p.x_dtype == TG_F32 ? norm_for<TG_F32>(residual, p.residual_dtype, shape, whole)
                             : p.x_dtype == TG_F16 ? norm_for<TG_F16>(residual, p.residual_dtype, shape, whole)
                                                   : norm_for<TG_BF16>(residual, p.residual_dtype, shape, whole);
-    const int threads = shape.rows ? 256 : shape.threads, per_block = shape.rows ? 8 : 1;
     const size_t smem = shape.nv == 1 ? 0 : static_cast<size_t>((p.K + 7) / 8) * 32;
-    int64_t blocks = (p.M + per_block - 1) / per_block;
+    int64_t blocks = p.M;
     cudaError_t e = cudaSuccess;
     if (blocks > 2 * d.sms || smem > 48 * 1024) {       // (it also lets the kernel have that much)
         int n = 0;
-        if ((e = resident(kernel, threads, smem, d.id, &n)) != cudaSuccess) return host::cuda_fail(e, "occupancy of the norm");
+        if ((e = resident(kernel, shape.threads, smem, d.id, &n)) != cudaSuccess) return host::cuda_fail(e, "occupancy of the norm");
         if (blocks > static_cast<int64_t>(n) * d.sms) blocks = static_cast<int64_t>(n) * d.sms;
     }
-    kernel<<<static_cast<unsigned>(blocks), threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    kernel<<<static_cast<unsigned>(blocks), shape.threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return host::cuda_fail(e, "norm launch");
     host::count_launches(1);

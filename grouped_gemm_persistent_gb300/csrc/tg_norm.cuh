@@ -45,14 +45,13 @@ struct Oct {
             w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
         }
     }
-    // n of the eight are inside the row (the others are zero); WHOLE: eight or none, 16-byte loads; otherwise vec: eight are loaded so
+    // n of the eight are inside the row; WHOLE: eight or none, 16-byte loads; otherwise wide: the same, with values past the row's end
+    // that cut() takes away (one by one they would have to be waited for here)
     template <bool WHOLE>
-    __device__ __forceinline__ void load(const uint8_t* p, int n, bool vec) {
+    __device__ __forceinline__ void load(const uint8_t* p, int n, bool wide) {
         zero();
-        if constexpr (WHOLE) {
+        if (WHOLE || wide) {
             if (n > 0) load_whole(p);
-        } else if (vec && n >= 8) {
-            load_whole(p);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -60,6 +59,16 @@ struct Oct {
                 if constexpr (DT == TG_F32) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
                 else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (i % 2 * 16);
             }
+        }
+    }
+    // the values from n on become zero
+    template <bool WHOLE>
+    __device__ __forceinline__ void cut(int n) {
+        if (WHOLE || n >= 8 || n <= 0) return;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (DT == TG_F32) w[i] = i < n ? w[i] : 0u;
+            else w[i] &= 2 * i + 1 < n ? 0xffffffffu : 2 * i < n ? 0xffffu : 0u;
         }
     }
     __device__ __forceinline__ float value(int i) const {
@@ -126,7 +135,7 @@ __device__ __forceinline__ void stage_values(float* to, const uint8_t* gain, int
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int v = base + i * blockDim.x, n = v < vectors ? K - v * 8 : 0;
-            o[i].template load<false>(gain + static_cast<int64_t>(v) * 8 * item_bytes(DT), n, vec);
+            o[i].template load<false>(gain + static_cast<int64_t>(v) * 8 * item_bytes(DT), n, vec && n >= 8);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
@@ -177,6 +186,7 @@ struct NormArgs {
     int K;
     int gain_dtype, y_dtype, e5m2;
     int vec;                     // rows on 16-byte boundaries (of 8-bit values 8-byte)
+    int64_t wide;                // rows before this one may be read in whole vectors
     float eps, inv_hi, inv_lo;
 };
 
@@ -184,15 +194,14 @@ constexpr int N_NONE = -1;          // no residual
 
 using NormKernel = void (*)(const NormArgs);
 
-// How a row is spread: threads of a row and vectors of eight values a thread; `rows`: a row a warp, eight a block.
+// How a row is spread over a block: its threads, and vectors of eight values a thread
 struct Spread {
     int threads, nv;
-    bool rows;
 };
 
 inline Spread spread(int64_t K, int nv) {
     const int64_t vectors = (K + 7) / 8;
-    return {static_cast<int>((vectors + 32 * nv - 1) / (32 * nv) * 32), nv, false};
+    return {static_cast<int>((vectors + 32 * nv - 1) / (32 * nv) * 32), nv};
 }
 
 // The kernel for x of type XT and a residual (none, or of x's type or fp32); whole: rows of whole vectors on 16-byte boundaries.  Defined
@@ -245,6 +254,12 @@ inline tg_status check_sizes(int64_t M, int64_t K) {
     if (M > host::MAX_DIM) return fail(TG_ERR_UNSUPPORTED, "M must be below 2^31");
     if (K > N_MAX_K) return fail(TG_ERR_UNSUPPORTED, "K=%lld columns; the norm takes at most %d", (long long)K, N_MAX_K);
     return TG_OK;
+}
+
+// How many of a matrix's M rows of K values may be read in whole vectors of eight without passing the end of its last row
+inline int64_t wide_rows(int64_t M, int64_t K, int64_t ld) {
+    const int64_t past = (K + 7) / 8 * 8 - K, last = (past + ld - 1) / ld;
+    return M > last ? M - last : 0;
 }
 
 inline bool vectors_of(const void* p, int64_t ld_bytes) { return host::aligned(p, 16) && ld_bytes % 16 == 0; }

@@ -36,19 +36,18 @@ struct NormBackArgs {
     int K;
     int gain_dtype;
     int vec;                     // rows on 16-byte boundaries
+    int64_t wide;                // rows before this one may be read in whole vectors
     float inv_k;
 };
 
-// Rows and units as in norm_kernel; the gain waits in shared memory, its gradient is summed in registers over a unit's rows.
-template <int DT, int HT, int NV, bool ROWS, bool WHOLE>
-__global__ void __launch_bounds__(ROWS ? 256 : 512) norm_backward_kernel(const __grid_constant__ NormBackArgs a) {
+// Rows as in norm_kernel; the gain waits in shared memory, its gradient is summed in registers over a block's rows.
+template <int DT, int HT, int NV, bool WHOLE>
+__global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constant__ NormBackArgs a) {
     ptx::grid_launch_dependents();
     extern __shared__ __align__(16) float gain[];
     __shared__ float part[2][16];
-    const int tpr = ROWS ? 32 : blockDim.x;
-    const int in = ROWS ? threadIdx.x % 32 : threadIdx.x;
-    const int64_t unit = ROWS ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-    const int64_t units = ROWS ? static_cast<int64_t>(gridDim.x) * (blockDim.x / 32) : gridDim.x;
+    const int tpr = blockDim.x, in = threadIdx.x;
+    const int64_t units = gridDim.x, unit = blockIdx.x;
     stage_gain(gain, a.gain, a.gain_dtype, a.K);
     float acc[NV][8];
 #pragma unroll
@@ -57,19 +56,20 @@ __global__ void __launch_bounds__(ROWS ? 256 : 512) norm_backward_kernel(const _
         for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
     int turn = 0;
     for (int64_t row = unit; row < a.M; row += units, turn ^= 1) {
+        const bool wide = row < a.wide;
         Oct<DT> dy[NV];
         Oct<HT> h[NV], dh[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (in + j * tpr) * 8;
-            dy[j].template load<WHOLE>(a.dy + row * a.lddy + static_cast<int64_t>(col) * item_bytes(DT), a.K - col, a.vec);
-            h[j].template load<WHOLE>(a.h + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
+            dy[j].template load<WHOLE>(a.dy + row * a.lddy + static_cast<int64_t>(col) * item_bytes(DT), a.K - col, wide);
+            h[j].template load<WHOLE>(a.h + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, wide);
         }
         if (a.d_hidden) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int col = (in + j * tpr) * 8;
-                dh[j].template load<WHOLE>(a.d_hidden + row * a.lddh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
+                dh[j].template load<WHOLE>(a.d_hidden + row * a.lddh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, wide);
             }
         } else {
 #pragma unroll
@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(ROWS ? 256 : 512) norm_backward_kernel(const _
         for (int j = 0; j < NV; ++j) {
             const int col = (in + j * tpr) * 8;
             if (col >= a.K) continue;
+            dy[j].template cut<WHOLE>(a.K - col);
+            h[j].template cut<WHOLE>(a.K - col);
             float g[8];
             read_gain(g, gain + col);
             float t = 0.0f;
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(ROWS ? 256 : 512) norm_backward_kernel(const _
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(FULL, s, d);
-        if (!ROWS && blockDim.x > 32) {
+        if (blockDim.x > 32) {
             // (two rows' sums in turn: a warp is at most one row ahead of the others)
             if (threadIdx.x % 32 == 0) part[turn][threadIdx.x / 32] = s;
             __syncthreads();
@@ -145,21 +147,13 @@ __global__ void __launch_bounds__(1024) norm_gain_kernel(const float* part, int6
 
 using NormBackKernel = void (*)(const NormBackArgs);
 
-// A row a warp up to 1024 values, beyond that two vectors a thread up to 8192 and eight above.  40960 x 4096 bf16 with d_hidden: two a
-// thread 206 us, four 211, one 264.
-Spread spread_for(int64_t K) {
-    const int64_t vectors = (K + 7) / 8;
-    if (vectors <= 128) return {32, 4, true};
-    return spread(K, vectors <= 1024 ? 2 : 8);
-}
+// Two vectors a thread up to 8192 values, eight above.  40960 x 4096 bf16 with d_hidden: two 206 us, four 211, one 264.
+Spread spread_for(int64_t K) { return spread(K, K <= 8192 ? 2 : 8); }
 
 template <int DT, int HT>
 NormBackKernel back_for(const Spread& s, bool whole) {
-    if (!whole)
-        return s.rows ? &norm_backward_kernel<DT, HT, 4, true, false>
-                      : s.nv == 2 ? &norm_backward_kernel<DT, HT, 2, false, false> : &norm_backward_kernel<DT, HT, 8, false, false>;
-    if (s.rows) return &norm_backward_kernel<DT, HT, 4, true, true>;
-    return s.nv == 2 ? &norm_backward_kernel<DT, HT, 2, false, true> : &norm_backward_kernel<DT, HT, 8, false, true>;
+    if (s.nv == 2) return whole ? &norm_backward_kernel<DT, HT, 2, true> : &norm_backward_kernel<DT, HT, 2, false>;
+    return whole ? &norm_backward_kernel<DT, HT, 8, true> : &norm_backward_kernel<DT, HT, 8, false>;
 }
 
 template <int DT>
@@ -223,25 +217,30 @@ extern "C" tg_status tg_rmsnorm_backward(const tg_rmsnorm_backward_args* args, t
                        (!p.d_hidden || vectors_of(p.d_hidden, a.lddh)) && vectors_of(p.dx, a.lddx);
     const bool whole = vec && p.K % 8 == 0;
     a.vec = vec;
+    a.wide = 0;
+    if (vec) {
+        a.wide = wide_rows(p.M, p.K, p.lddy);
+        if (wide_rows(p.M, p.K, p.ldh) < a.wide) a.wide = wide_rows(p.M, p.K, p.ldh);
+        if (p.d_hidden && wide_rows(p.M, p.K, p.lddh) < a.wide) a.wide = wide_rows(p.M, p.K, p.lddh);
+    }
     a.inv_k = 1.0f / static_cast<float>(p.K);
     const Spread shape = spread_for(p.K);
     const NormBackKernel kernel = p.dy_dtype == TG_F32 ? back_for<TG_F32>(p.hidden_dtype, shape, whole)
                                 : p.dy_dtype == TG_F16 ? back_for<TG_F16>(p.hidden_dtype, shape, whole)
                                                        : back_for<TG_BF16>(p.hidden_dtype, shape, whole);
-    const int threads = shape.rows ? 256 : shape.threads, per_block = shape.rows ? 8 : 1;
     const size_t smem = static_cast<size_t>((p.K + 7) / 8) * 32;
     int n = 0;
-    cudaError_t e = resident(kernel, threads, smem, d.id, &n);
+    cudaError_t e = resident(kernel, shape.threads, smem, d.id, &n);
     if (e != cudaSuccess) return host::cuda_fail(e, "occupancy of the norm's backward pass");
-    const int64_t cap = static_cast<int64_t>(d.sms) * n, want = (p.M + per_block - 1) / per_block;
-    const int64_t blocks = want < cap ? want : cap, units = blocks * per_block;
+    const int64_t cap = static_cast<int64_t>(d.sms) * n, want = p.M;
+    const int64_t units = want < cap ? want : cap;
     void* ws = nullptr;
     if (p.d_gain) {
         if ((s = host::workspace(static_cast<size_t>(units) * p.K * 4, st, "cudaMallocFromPoolAsync(norm's partial sums)", &ws)) != TG_OK)
             return s;
         a.part = static_cast<float*>(ws);
     }
-    kernel<<<static_cast<unsigned>(blocks), threads, smem, st>>>(a);
+    kernel<<<static_cast<unsigned>(units), shape.threads, smem, st>>>(a);
     e = cudaGetLastError();
     if (e == cudaSuccess) host::count_launches(1);
     if (e == cudaSuccess && p.d_gain) {

@@ -187,29 +187,27 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Oct<HT> (&h)
     }
 }
 
-// Rows unit, unit + units, ..., a unit being the block (NV vectors of eight values a thread) or, with ROWS, for short rows, a warp.
-// WHOLE: rows of whole vectors on 16-byte boundaries.  STAGED: the gain waits in shared memory (otherwise, with one vector a thread
-// and about one row a block, in registers).
-template <int XT, int RT, int NV, bool ROWS, bool WHOLE>
-__global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a) {
+// The block's rows are blockIdx.x, blockIdx.x + gridDim.x, ..., NV vectors of eight values a thread.  WHOLE: rows of whole vectors on
+// 16-byte boundaries.  STAGED: the gain waits in shared memory (otherwise, with one vector a thread, in registers).
+template <int XT, int RT, int NV, bool WHOLE>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int HT = RT == N_NONE ? XT : RT;
     constexpr bool STAGED = NV > 1;
     extern __shared__ __align__(16) float gain[];
-    __shared__ Pair part[ROWS ? 1 : 2][32];
-    const int tpr = ROWS ? 32 : blockDim.x;
-    const int in = ROWS ? threadIdx.x % 32 : threadIdx.x;
-    const int64_t unit = ROWS ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-    const int64_t units = ROWS ? static_cast<int64_t>(gridDim.x) * (blockDim.x / 32) : gridDim.x;
+    __shared__ Pair part[2][32];
+    const int tpr = blockDim.x, in = threadIdx.x;
+    const int64_t units = gridDim.x, unit = blockIdx.x;
     // the next row's values are on their way while a row is finished
     Oct<XT> x[NV];
     Oct<HT> h[NV], add[RT == N_NONE ? 1 : NV];
     auto fetch = [&](int64_t row) {
+        const bool wide = row < a.wide;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (in + j * tpr) * 8;
-            x[j].template load<WHOLE>(a.x + row * a.ldx + static_cast<int64_t>(col) * item_bytes(XT), a.K - col, a.vec);
+            x[j].template load<WHOLE>(a.x + row * a.ldx + static_cast<int64_t>(col) * item_bytes(XT), a.K - col, wide);
             if constexpr (RT != N_NONE)
-                add[j].template load<WHOLE>(a.residual + row * a.ldr + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
+                add[j].template load<WHOLE>(a.residual + row * a.ldr + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, wide);
         }
     };
     if (unit < a.M) fetch(unit);
@@ -225,7 +223,10 @@ __global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel
         Pair sum{0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            const int n = a.K - (in + j * tpr) * 8;
+            x[j].template cut<WHOLE>(n);
             if constexpr (RT != N_NONE) {
+                add[j].template cut<WHOLE>(n);
                 add_rows(h[j], x[j], add[j]);
             } else {
 #pragma unroll
@@ -241,8 +242,7 @@ __global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel
             }
             sum = pair_add(sum, {squares(h[j], 1.0f), 0.0f});
         }
-        Pair* parts = part[ROWS ? 0 : turn];
-        sum = ROWS ? warp_sum(sum) : block_sum(sum, parts);
+        sum = block_sum(sum, part[turn]);
         float r = row_factor(sum, a.inv_hi, a.inv_lo, a.eps);
         if (!(sum.hi < __int_as_float(0x7f800000))) {
             // a row whose squares' sum is past fp32's range (or that has an infinity or a NaN, and keeps it): once more,
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel
             Pair low{0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < NV; ++j) low = pair_add(low, {squares(h[j], DOWN), 0.0f});
-            if (!ROWS) __syncthreads();                  // the parts are read above
-            low = ROWS ? warp_sum(low) : block_sum(low, parts);
+            __syncthreads();                             // the parts are read above
+            low = block_sum(low, part[turn]);
             r = row_factor(low, a.inv_hi, a.inv_lo, 0.0f) * DOWN;
         }
         if (in == 0) a.r[row] = r;
@@ -268,15 +268,14 @@ __global__ void __launch_bounds__(ROWS ? 256 : NV == 1 ? 1024 : 512) norm_kernel
     }
 }
 
-template <int XT, int RT>
-NormKernel pick(const Spread& s, bool whole) {
-    if (!whole) {
-        if (s.rows) return &norm_kernel<XT, RT, 4, true, false>;
-        return s.nv == 1 ? &norm_kernel<XT, RT, 1, false, false> : s.nv == 4 ? &norm_kernel<XT, RT, 4, false, false> : &norm_kernel<XT, RT, 8, false, false>;
-    }
-    if (s.rows) return &norm_kernel<XT, RT, 4, true, true>;
-    return s.nv == 1 ? &norm_kernel<XT, RT, 1, false, true> : s.nv == 4 ? &norm_kernel<XT, RT, 4, false, true> : &norm_kernel<XT, RT, 8, false, true>;
+template <int XT, int RT, bool WHOLE>
+NormKernel pick(const Spread& s) {
+    return s.nv == 1 ? &norm_kernel<XT, RT, 1, WHOLE> : s.nv == 2 ? &norm_kernel<XT, RT, 2, WHOLE>
+         : s.nv == 4 ? &norm_kernel<XT, RT, 4, WHOLE> : &norm_kernel<XT, RT, 8, WHOLE>;
 }
+
+template <int XT, int RT>
+NormKernel pick(const Spread& s, bool whole) { return whole ? pick<XT, RT, true>(s) : pick<XT, RT, false>(s); }
 
 }  // namespace
 

@@ -418,7 +418,7 @@ tg_status tg_rmsnorm(const tg_rmsnorm_args *args, tg_stream_t stream);
  *   d_hidden, lddh      : the gradient that reaches h past the norm, of hidden's type; NULL: zero.
  *   dx, lddx            : of hidden's type; may be d_hidden or, of the same type, dy.
  *   d_gain              : DEVICE fp32 [K], NULL when not wanted.  M == 0 writes zeros.
- * Deterministic.  With d_gain, a workspace of 4 K bytes for each block (each warp up to 1024 columns)
+ * Deterministic.  With d_gain, a workspace of 4 K bytes for each block
  * that is resident, from the library's memory pool, released on the stream.
  */
 typedef struct tg_rmsnorm_backward_args {
