@@ -599,7 +599,7 @@ _RMSNORM = struct.Struct("@qq" + 2 * "Qq" + "Q" + 4 * "Qq" + "Q" + "f5i")       
 _RMSNORM_BACKWARD = struct.Struct("@qq" + 2 * "Qq" + "QQ" + 2 * "Qq" + "Q" + "3i4x")         # tg_rmsnorm_backward_args
 
 _ROUTER = struct.Struct("@3q" + "Qq" + "Q" + "3q" + "5Q" + "f3i")                            # tg_router_args
-_ROUTER_BACKWARD = struct.Struct("@3q" + "Qq" + "5Q" + "Qq" + "f3i")                         # tg_router_backward_args
+_ROUTER_BACKWARD = struct.Struct("@3q" + "Qq" + "4Q" + "Qq" + "f3i")                         # tg_router_backward_args
 _LORA = struct.Struct("@5q" + "Qq" + 2 * "Qqq" + "QQ" + 2 * "Qq" + "2i")                     # tg_lora_args
 SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -793,6 +793,7 @@ class Routing(NamedTuple):
     renormalize: bool
     score: str = "softmax"
     weight_scale: float = 1.0
+    plain: bool = True       # tg_moe_router's (softmax, no bias, groups or factor), whose gradient has a kernel of its own
 
 
 def _logits(logits: torch.Tensor) -> tuple[int, int, int, int]:
@@ -830,8 +831,9 @@ def moe_router(logits: torch.Tensor, top_k: int, *, renormalize: bool = False, s
     shape = (T, top_k)
     r = Routing(_empty(logits, shape, torch.int32, stream), _empty(logits, shape, torch.float32, stream),
                 _empty(logits, G, torch.int32, stream), _empty(logits, (), torch.float32, stream),
-                _empty(logits, G, torch.float32, stream), bool(renormalize), score, float(weight_scale))
-    if code == 0 and bias is None and groups == 1 and weight_scale == 1.0 and top_groups in (None, 1) and group_top == 1:
+                _empty(logits, G, torch.float32, stream), bool(renormalize), score, float(weight_scale),
+                code == 0 and bias is None and groups == 1 and weight_scale == 1.0 and top_groups in (None, 1) and group_top == 1)
+    if r.plain:
         status = load().tg_moe_router(logits.data_ptr(), dt, ld, T, G, top_k, int(renormalize), r.experts.data_ptr(),
                                       r.weights.data_ptr(), r.counts.data_ptr(), r.loss.data_ptr(), r.slope.data_ptr(),
                                       _stream_handle(stream))
@@ -875,7 +877,7 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
         ldd = _row_major_ld(out, "out", G)
     _on_one_gpu("logits routing.experts routing.weights routing.slope d_weights d_loss out", logits, experts,
                 weights, slope, d_weights, d_loss, out)
-    if code == 0 and routing.weight_scale == 1.0:
+    if routing.plain and code == 0 and routing.weight_scale == 1.0:
         status = load().tg_moe_router_backward(logits.data_ptr(), dt, ld, T, G, k, int(routing.renormalize),
                                                experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
                                                None if d_weights is None else d_weights.data_ptr(),
@@ -883,8 +885,8 @@ def moe_router_backward(logits: torch.Tensor, routing: Routing, d_weights: torch
                                                _stream_handle(stream))
     else:
         status = load().tg_moe_router_scored_backward(
-            _ROUTER_BACKWARD.pack(T, G, k, logits.data_ptr(), ld, experts.data_ptr(), weights.data_ptr(), slope.data_ptr(),
-                                  _ptr(d_weights), _ptr(d_loss), out.data_ptr(), ldd, routing.weight_scale, dt,
+            _ROUTER_BACKWARD.pack(T, G, k, logits.data_ptr(), ld, experts.data_ptr(), slope.data_ptr(), _ptr(d_weights),
+                                  _ptr(d_loss), out.data_ptr(), ldd, routing.weight_scale, dt,
                                   code, routing.renormalize), _stream_handle(stream))
     if status:
         _check(status)

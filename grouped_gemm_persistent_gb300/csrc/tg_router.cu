@@ -298,7 +298,6 @@ struct BackArgs {
     const float* d_loss;      // null: zero
     uint8_t* out;
     int64_t ldo_bytes;
-    float scale, inv_scale;   // the weights' factor
 };
 
 template <int DT, int L, int V>
@@ -331,8 +330,8 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) router_backward_ker
         e_next = -1;
         if (choice && row < a.T) {
             e_next = __ldg(a.experts + row * a.k + in);
-            w_next = __ldg(a.weights + row * a.k + in) * a.inv_scale;
-            dw_next = __ldg(a.d_weights + row * a.k + in) * a.scale;
+            w_next = __ldg(a.weights + row * a.k + in);
+            dw_next = __ldg(a.d_weights + row * a.k + in);
         }
         if (e_next < 0 || e_next >= a.G) {       // no choice (-1): nothing of it counts
             e_next = -1;
@@ -491,31 +490,6 @@ cudaError_t launch_join(const RouterArgs& a, int blocks, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, router_join_kernel, a, blocks);
 }
 
-tg_status softmax_backward(const void* logits, tg_dtype dtype, int64_t ld, int64_t T, int64_t G, int64_t k, int renormalize,
-                           float weight_scale, const int32_t* experts, const float* weights, const float* slope,
-                           const float* d_weights, const float* d_loss, void* d_logits, int64_t ldd, cudaStream_t stream) {
-    host::Device d;
-    const tg_status s = host::device(&d);
-    if (s != TG_OK) return s;
-    const RouterVariant v = variant_for(dtype, static_cast<int>(G), static_cast<int>(k));
-    const int64_t esize = dtype == TG_F32 ? 4 : 2;
-    const BackArgs a{static_cast<const uint8_t*>(logits), ld * esize, T, int(G), int(k), renormalize != 0,
-                     host::aligned(logits, 16) && ld * esize % 16 == 0,
-                     host::aligned(d_logits, 16) && ldd * esize % 16 == 0, experts, weights, slope, d_weights, d_loss,
-                     static_cast<uint8_t*>(d_logits), ldd * esize, weight_scale, 1.0f / weight_scale};
-    const int64_t block_rows = R_WARPS * (32 / v.lanes);
-    const int64_t want = (T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
-    const size_t smem = static_cast<size_t>(R_WARPS) * 32 * v.per_lane * 4;
-    cudaError_t e = allow_smem(v.backward, smem);
-    if (e == cudaSuccess) {
-        v.backward<<<static_cast<unsigned>(want < cap ? want : cap), R_THREADS, smem, stream>>>(a);
-        e = cudaGetLastError();
-    }
-    if (e != cudaSuccess) return host::cuda_fail(e, "router backward launch");
-    host::count_launches(1);
-    return TG_OK;
-}
-
 }  // namespace gate
 
 }  // namespace tg
@@ -583,6 +557,23 @@ extern "C" tg_status tg_moe_router_backward(const void* logits, tg_dtype dtype, 
     tg_status s = check_router(logits, dtype, ld, T, G, k);
     if (s != TG_OK || T == 0) return s;
     if ((s = check_backward(G, dtype, experts, weights, true, slope, d_weights, d_loss, d_logits, ldd)) != TG_OK) return s;
-    return softmax_backward(logits, dtype, ld, T, G, k, renormalize, 1.0f, experts, weights, slope, d_weights, d_loss, d_logits,
-                            ldd, reinterpret_cast<cudaStream_t>(stream));
+    host::Device d;
+    if ((s = host::device(&d)) != TG_OK) return s;
+    const RouterVariant v = variant_for(dtype, static_cast<int>(G), static_cast<int>(k));
+    const int64_t esize = dtype == TG_F32 ? 4 : 2;
+    const BackArgs a{static_cast<const uint8_t*>(logits), ld * esize, T, int(G), int(k), renormalize != 0,
+                     host::aligned(logits, 16) && ld * esize % 16 == 0,
+                     host::aligned(d_logits, 16) && ldd * esize % 16 == 0, experts, weights, slope, d_weights, d_loss,
+                     static_cast<uint8_t*>(d_logits), ldd * esize};
+    const int64_t block_rows = R_WARPS * (32 / v.lanes);
+    const int64_t want = (T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
+    const size_t smem = static_cast<size_t>(R_WARPS) * 32 * v.per_lane * 4;
+    cudaError_t e = allow_smem(v.backward, smem);
+    if (e == cudaSuccess) {
+        v.backward<<<static_cast<unsigned>(want < cap ? want : cap), R_THREADS, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return host::cuda_fail(e, "router backward launch");
+    host::count_launches(1);
+    return TG_OK;
 }

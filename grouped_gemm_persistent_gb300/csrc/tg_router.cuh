@@ -57,6 +57,21 @@ struct Logits {
             }
         }
     }
+    // the same of every STRIDE-th logit
+    template <int STRIDE>
+    __device__ __forceinline__ void load_apart(const uint8_t* p, int n) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (DT == TG_F32) {
+                w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + i * STRIDE) : NEG_INF;
+            } else {
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+                const uint32_t lo = 2 * i < n ? __ldg(h + 2 * i * STRIDE) : NEG_INF & 0xffffu;
+                const uint32_t hi = 2 * i + 1 < n ? __ldg(h + (2 * i + 1) * STRIDE) : NEG_INF & 0xffffu;
+                w[i] = lo | hi << 16;
+            }
+        }
+    }
     __device__ __forceinline__ uint32_t bits(int j) const {
         if constexpr (DT == TG_F32) return w[j];
         else return j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xffffu;
@@ -162,11 +177,7 @@ __device__ __forceinline__ double finish_expert(const RouterArgs& a, int g, floa
 // (tg_router.cu).
 cudaError_t launch_join(const RouterArgs& a, int blocks, cudaStream_t stream);
 
-// tg_moe_router_backward with the weights' factor (its arguments checked; tg_router.cu).
-tg_status softmax_backward(const void* logits, tg_dtype dtype, int64_t ld, int64_t T, int64_t G, int64_t k, int renormalize,
-                           float weight_scale, const int32_t* experts, const float* weights, const float* slope,
-                           const float* d_weights, const float* d_loss, void* d_logits, int64_t ldd, cudaStream_t stream);
-
+// The checks of the arguments that the gates share (tg_router.cu).
 tg_status check_router(const void* logits, tg_dtype dt, int64_t ld, int64_t T, int64_t G, int64_t k);
 tg_status check_backward(int64_t G, tg_dtype dt, const int32_t* experts, const float* weights, bool weights_needed,
                          const float* slope, const float* d_weights, const float* d_loss, const void* d_logits, int64_t ldd);

@@ -8,7 +8,8 @@
 //   loss        G sum_g f_g P_g as in tg_router.cu, with P_g the mean of s / sum_g s
 // and, counts being constant, with u = d_loss * slope and c' the gradient of the chosen s through w
 //   sigmoid:    d x = s (1 - s) ((u - sum s u / sum s) / sum s + c')
-// (softmax: the other gate's backward kernel, which knows the factor).
+//   softmax:    d x = s (u - sum s u + c' - sum s c')
+// where, with w' the factor's product with the gradient of w, s c' is s w' or, renormalised, w (w' - sum w w') (whose sum is 0).
 //
 // Choosing.  A choice by v is one of real numbers: with fp32 scores two experts next to each other in the order would change
 // places with the last bits of exp.  The kernel works in fp32 with a bound E on a score's error and sees where that does not decide:
@@ -76,6 +77,13 @@ __device__ __forceinline__ float ex2_flush(float x) {
 __device__ __forceinline__ float rcp_flush(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// (a subnormal score would have an infinite reciprocal)
+__device__ __forceinline__ float mul_flush(float x, float y) {
+    float r;
+    asm("mul.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 
@@ -516,7 +524,7 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
         if (in >= a.k) my_e = -1;
         if (my_e >= 0) {
             const float z = X::one(row, my_e);
-            my_s = SIGMOID ? sigmoid_approx(z) : exp_flush(z - m) * inv;
+            my_s = SIGMOID ? sigmoid_approx(z) : mul_flush(exp_flush(z - m), inv);
             atomicAdd(&s_count[my_e], 1);
         }
         const float chosen = a.renorm ? group_sum<L>(my_s) : 1.0f;
@@ -615,10 +623,10 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_kernel(const
     }
 }
 
-struct SigmoidBackArgs {
+struct ScoredBackArgs {
     const uint8_t* logits;
     int64_t ld_bytes, T;
-    int G, k, renorm, vec_in, vec_out;
+    int G, k, renorm;
     const int32_t* experts;
     const float* slope;
     const float* d_weights;   // null: zero
@@ -628,22 +636,27 @@ struct SigmoidBackArgs {
     float factor;
 };
 
-template <int DT, int L, int V>
-__global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_kernel(const SigmoidBackArgs a) {
+// CLOSE: a lane has V neighbouring experts of a row, moved in 16-byte vectors; otherwise every L-th expert, moved one by one, a line at a time
+// over the lanes, wherever the row starts.  65536 rows, us, neighbours / apart:
+//   bf16  64: 7.6 / 9.6   256: 23.8 / 24.8   512: 56 / 62   1024: 147 / 113     (neighbours up to 512, off the boundaries apart)
+//   fp32  64: 8.4 / 9.1   128: 14.8 / 13.4   256: 31.4 / 30.2   512: 72 / 63   1024: 252 / 122     (apart)
+// 255 fp32 off the boundaries: neighbours, read one by one, 46.6, apart 29.1.
+template <int DT, int L, int V, bool SIGMOID, bool CLOSE>
+__global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) scored_backward_kernel(const ScoredBackArgs a) {
     using X = Logits<DT, V>;
     constexpr int ROWS = 32 / L;
-    // per warp: the gradient of the chosen experts' scores through the weights, by expert; zero elsewhere
+    // per warp: the part of the chosen experts' gradients that comes through their weights, by expert; zero elsewhere
     extern __shared__ __align__(16) uint8_t dyn[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, in = lane % L;
     float* extra = reinterpret_cast<float*>(dyn) + warp * 32 * V + (lane / L) * L * V;
-    const int first = in * V;
-    const int n = a.G - first < 0 ? 0 : a.G - first < V ? a.G - first : V;
+    constexpr int STRIDE = CLOSE ? 1 : L;
+    const int first = CLOSE ? in * V : in, have = (a.G - first + STRIDE - 1) / STRIDE, n = have < 0 ? 0 : have < V ? have : V;
     const float dl = a.d_loss ? __ldg(a.d_loss) : 0.0f;
     float u[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        u[j] = (a.d_loss && j < n) ? dl * __ldg(a.slope + first + j) : 0.0f;
-        extra[first + j] = 0.0f;
+        u[j] = (a.d_loss && j < n) ? dl * __ldg(a.slope + first + j * STRIDE) : 0.0f;
+        extra[first + j * STRIDE] = 0.0f;
     }
     __syncwarp();
     // (T * k is below 2^31)
@@ -653,14 +666,14 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
     const int64_t ahead = step * a.ld_bytes, out_ahead = step * a.ldo_bytes;
     const uint8_t* row = a.logits + t * a.ld_bytes;
     uint8_t* out = a.out + t * a.ldo_bytes + first * X::ESIZE;
-    const bool choice = a.d_weights != nullptr && in < a.k, whole_rows = a.vec_in && a.G == L * V;
+    const bool choice = a.d_weights != nullptr && in < a.k;
     X next;
     int e_next = -1;
     float z_next = 0.0f, dw_next = 0.0f;
     auto fetch = [&](uint32_t from, const uint8_t* at) {
         const uint32_t r = from + lane / L;
-        if (whole_rows && from + ROWS <= rows_in) next.load_whole(at + first * X::ESIZE);
-        else next.load(at + first * X::ESIZE, r < rows_in ? n : 0, a.vec_in != 0);
+        if constexpr (CLOSE) next.load(at + first * X::ESIZE, r < rows_in ? n : 0, true);
+        else next.template load_apart<STRIDE>(at + first * X::ESIZE, r < rows_in ? n : 0);
         e_next = -1;
         if (choice && r < rows_in) {
             e_next = __ldg(a.experts + r * a.k + in);
@@ -679,45 +692,70 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
         const int e = e_next;
         const float z = z_next, dw = dw_next;
         if (base + step < rows_in) fetch(base + step, row + ahead);
-        // with e = e^-|x| and t = 1 / (1 + e): s is t or e t, s (1 - s) is e t^2 on either side of zero, 0 at both infinities
-        float p[V];                              // s (1 - s)
-        float whole = 0.0f, pu = 0.0f;
+        float p[V];                              // sigmoid: s (1 - s); softmax: s
+        float m = 0.0f, whole = 0.0f, pu = 0.0f;
+        if constexpr (SIGMOID) {
+            // with e = e^-|x| and t = 1 / (1 + e): s is t or e t, s (1 - s) is e t^2 on either side of zero, 0 at both infinities
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float f = ex2_flush(fabsf(x.value(j)) * -1.4426950408889634f), q = rcp_flush(1.0f + f), r = f * q;
-            const float score = x.value(j) < 0.0f ? r : q;
-            p[j] = r * q;
-            whole += score;
-            pu = fmaf(score, u[j], pu);
+            for (int j = 0; j < V; ++j) {
+                const float f = ex2_flush(fabsf(x.value(j)) * -1.4426950408889634f), q = rcp_flush(1.0f + f), r = f * q;
+                const float score = x.value(j) < 0.0f ? r : q;
+                p[j] = r * q;
+                // (past the row's end the logit is -infinity: nothing)
+                whole += score;
+                pu = fmaf(score, u[j], pu);
+            }
+        } else {
+            m = x.value(0);
+#pragma unroll
+            for (int j = 1; j < V; ++j) m = max_nan(m, x.value(j));
+            m = group_max_nan<L>(m);
+            m = m != MINUS_INF ? m : 0.0f;        // (e^(-infinity - 0) = 0)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                p[j] = exp_flush(x.value(j) - m);
+                whole += p[j];
+                pu = fmaf(p[j], u[j], pu);
+            }
         }
         whole = group_sum<L>(whole);
         const float inv = whole != 0.0f ? 1.0f / whole : 0.0f;
-        const float c = group_sum<L>(pu) * inv;
+        float c = group_sum<L>(pu) * inv;
+        float d[V];
         if (a.d_weights) {
-            const float my = e >= 0 ? 1.0f / (1.0f + __expf(-z)) : 0.0f;
+            // by the weight w = s / sum of the chosen: g / sum by itself has no room in 32 bits where the sum is small
+            float my = 0.0f, rest = 1.0f;        // s and, of a sigmoid, 1 - s
+            if (e >= 0) {
+                if constexpr (SIGMOID) {
+                    const float f = ex2_flush(fabsf(z) * -1.4426950408889634f), q = rcp_flush(1.0f + f), r = mul_flush(f, q);
+                    my = z < 0.0f ? r : q;
+                    rest = z < 0.0f ? q : r;
+                } else {
+                    my = mul_flush(exp_flush(z - m), inv);
+                }
+            }
             float g = a.factor * dw;
             if (a.renorm) {
-                const float chosen = group_sum<L>(my), per = chosen != 0.0f ? 1.0f / chosen : 0.0f;
-                g = (g - group_sum<L>(my * g) * per) * per;
+                const float chosen = group_sum<L>(my);
+                my *= chosen != 0.0f ? 1.0f / chosen : 0.0f;
+                g -= group_sum<L>(my * g);
+            } else if (!SIGMOID) {
+                c += group_sum<L>(my * g);
             }
+            g *= my * rest;
             if (e >= 0) extra[e] = g;
             __syncwarp();
-        }
-        float d[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = fmaf(u[j], inv, -c * inv);
-        if (a.d_weights) {
-#pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(extra + first + j);
-                d[j] += f.x; d[j + 1] += f.y; d[j + 2] += f.z; d[j + 3] += f.w;
-            }
+            for (int j = 0; j < V; ++j) d[j] = extra[first + j * STRIDE];
             __syncwarp();
             if (e >= 0) extra[e] = 0.0f;
             __syncwarp();
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] *= p[j];
+        for (int j = 0; j < V; ++j) d[j] = fmaf(p[j] * inv, u[j] - c, d[j]);
         if (t >= rows_in) continue;
         uint32_t o[X::WORDS];
 #pragma unroll
@@ -732,23 +770,23 @@ __global__ void __launch_bounds__(R_THREADS, V == 8 ? 2 : 1) sigmoid_backward_ke
                 o[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
         }
-        if (n == V && a.vec_out) {
+        if (CLOSE && n == V) {
 #pragma unroll
             for (int i = 0; i < X::WORDS; i += 4)
                 reinterpret_cast<uint4*>(out)[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        } else {
+            continue;
+        }
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (j >= n) continue;
-                if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(out)[j] = o[j];
-                else reinterpret_cast<uint16_t*>(out)[j] = static_cast<uint16_t>(o[j / 2] >> ((j & 1) * 16));
-            }
+        for (int j = 0; j < V; ++j) {
+            if (j >= n) continue;
+            if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(out)[j * STRIDE] = o[j];
+            else reinterpret_cast<uint16_t*>(out)[j * STRIDE] = static_cast<uint16_t>(o[j / 2] >> ((j & 1) * 16));
         }
     }
 }
 
 using ScoredKernel = void (*)(const ScoredArgs);
-using SigmoidBackKernel = void (*)(const SigmoidBackArgs);
+using ScoredBackKernel = void (*)(const ScoredBackArgs);
 
 // Positions a lane and lanes a row
 struct Shape {
@@ -788,12 +826,25 @@ ScoredKernel scored_for(tg_dtype dt, bool sigmoid, const Shape& s) {
     return dt == TG_F32 ? scored_for<TG_F32, false>(s) : dt == TG_F16 ? scored_for<TG_F16, false>(s) : scored_for<TG_BF16, false>(s);
 }
 
-template <int DT>
-SigmoidBackKernel back_for(const Shape& s) {
-    if (s.per_lane == 32) return &sigmoid_backward_kernel<DT, 32, 32>;
-    if (s.per_lane == 16) return &sigmoid_backward_kernel<DT, 32, 16>;
-    return s.lanes == 32 ? &sigmoid_backward_kernel<DT, 32, 8> : s.lanes == 16 ? &sigmoid_backward_kernel<DT, 16, 8>
-                                                                              : &sigmoid_backward_kernel<DT, 8, 8>;
+template <int DT, bool SIGMOID>
+ScoredBackKernel back_for(bool on_boundaries, const Shape& s) {
+    if constexpr (DT != TG_F32) {
+        if (on_boundaries && s.per_lane <= 16) {
+            if (s.per_lane == 16) return &scored_backward_kernel<DT, 32, 16, SIGMOID, true>;
+            if (s.lanes == 32) return &scored_backward_kernel<DT, 32, 8, SIGMOID, true>;
+            return s.lanes == 16 ? &scored_backward_kernel<DT, 16, 8, SIGMOID, true> : &scored_backward_kernel<DT, 8, 8, SIGMOID, true>;
+        }
+    }
+    if (s.per_lane == 32) return &scored_backward_kernel<DT, 32, 32, SIGMOID, false>;
+    if (s.per_lane == 16) return &scored_backward_kernel<DT, 32, 16, SIGMOID, false>;
+    if (s.lanes == 32) return &scored_backward_kernel<DT, 32, 8, SIGMOID, false>;
+    return s.lanes == 16 ? &scored_backward_kernel<DT, 16, 8, SIGMOID, false> : &scored_backward_kernel<DT, 8, 8, SIGMOID, false>;
+}
+
+template <bool SIGMOID>
+ScoredBackKernel back_for(tg_dtype dt, bool on_boundaries, const Shape& s) {
+    return dt == TG_F32 ? back_for<TG_F32, SIGMOID>(on_boundaries, s) : dt == TG_F16 ? back_for<TG_F16, SIGMOID>(on_boundaries, s)
+                                                                                     : back_for<TG_BF16, SIGMOID>(on_boundaries, s);
 }
 
 tg_status check_scores(tg_score score, float factor) {
@@ -900,24 +951,19 @@ extern "C" tg_status tg_moe_router_scored_backward(const tg_router_backward_args
     const tg_router_backward_args& p = *args;
     tg_status s = check_router(p.logits, p.dtype, p.ld, p.T, p.G, p.k);
     if (s != TG_OK || (s = check_scores(p.score, p.weight_scale)) != TG_OK || p.T == 0) return s;
-    const bool softmax = p.score == TG_SCORE_SOFTMAX;
-    s = check_backward(p.G, p.dtype, p.experts, p.weights, softmax, p.slope, p.d_weights, p.d_loss, p.d_logits, p.ldd);
-    if (s != TG_OK) return s;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (softmax)
-        return softmax_backward(p.logits, p.dtype, p.ld, p.T, p.G, p.k, p.renormalize, p.weight_scale, p.experts, p.weights, p.slope,
-                                p.d_weights, p.d_loss, p.d_logits, p.ldd, st);
+    if ((s = check_backward(p.G, p.dtype, p.experts, nullptr, false, p.slope, p.d_weights, p.d_loss, p.d_logits, p.ldd)) != TG_OK) return s;
     host::Device d;
     if ((s = host::device(&d)) != TG_OK) return s;
     Shape shape;
     shape_for(1, p.G, p.k, &shape);
     const int64_t esize = p.dtype == TG_F32 ? 4 : 2;
-    const SigmoidBackArgs a{static_cast<const uint8_t*>(p.logits), p.ld * esize, p.T, int(p.G), int(p.k), p.renormalize != 0,
-                            host::aligned(p.logits, 16) && p.ld * esize % 16 == 0,
-                            host::aligned(p.d_logits, 16) && p.ldd * esize % 16 == 0, p.experts, p.slope, p.d_weights, p.d_loss,
-                            static_cast<uint8_t*>(p.d_logits), p.ldd * esize, p.weight_scale};
-    const SigmoidBackKernel kernel = p.dtype == TG_F32 ? back_for<TG_F32>(shape) : p.dtype == TG_F16 ? back_for<TG_F16>(shape)
-                                                                                                     : back_for<TG_BF16>(shape);
+    const ScoredBackArgs a{static_cast<const uint8_t*>(p.logits), p.ld * esize, p.T, int(p.G), int(p.k), p.renormalize != 0, p.experts, p.slope,
+                           p.d_weights, p.d_loss, static_cast<uint8_t*>(p.d_logits), p.ldd * esize, p.weight_scale};
+    const bool on_boundaries = host::aligned(p.logits, 16) && p.ld * esize % 16 == 0 && host::aligned(p.d_logits, 16) &&
+                               p.ldd * esize % 16 == 0;
+    const ScoredBackKernel kernel = p.score == TG_SCORE_SIGMOID ? back_for<true>(p.dtype, on_boundaries, shape)
+                                                                : back_for<false>(p.dtype, on_boundaries, shape);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int64_t block_rows = R_WARPS * (32 / shape.lanes);
     const int64_t want = (p.T + block_rows - 1) / block_rows, cap = static_cast<int64_t>(d.sms) * R_BLOCKS_PER_SM;
     const size_t smem = static_cast<size_t>(R_WARPS) * 32 * shape.per_lane * 4;

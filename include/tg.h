@@ -528,14 +528,13 @@ tg_status tg_moe_router_scored(const tg_router_args *args, tg_stream_t stream);
 
 /*
  * tg_moe_router_scored_backward - the gradient of tg_moe_router_scored's logits; arguments as
- * tg_moe_router_backward.  The choice, and with it the groups and the bias, is constant.  weights
- * is read with TG_SCORE_SOFTMAX only.
+ * tg_moe_router_backward (without weights).  The choice, and with it the groups and the bias, is
+ * constant.
  */
 typedef struct tg_router_backward_args {
     int64_t T, G, k;
     const void *logits; int64_t ld;
     const int32_t *experts;
-    const float *weights;
     const float *slope;
     const float *d_weights;
     const float *d_loss;

@@ -26,7 +26,7 @@ def lib():
 
 FORWARD = dict(T=4, G=64, k=2, logits=PTR, ld=64, bias=2 * PTR, groups=8, top_groups=4, group_top=2, experts=PTR, weights=PTR,
                counts=PTR, loss=PTR, slope=PTR, scale=1.0, dt=1, score=1, renorm=0)
-BACKWARD = dict(T=4, G=64, k=2, logits=PTR, ld=64, experts=PTR, weights=PTR, slope=PTR, dw=PTR, dl=PTR, out=2 * PTR, ldd=64,
+BACKWARD = dict(T=4, G=64, k=2, logits=PTR, ld=64, experts=PTR, slope=PTR, dw=PTR, dl=PTR, out=2 * PTR, ldd=64,
                 scale=1.0, dt=1, score=1, renorm=0)
 
 
@@ -56,7 +56,7 @@ def test_forward_refusals(lib, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", SHARED + [
-    (dict(experts=0), BAD), (dict(weights=0, score=0), BAD), (dict(slope=0), BAD), (dict(out=0), BAD), (dict(ldd=63), BAD),
+    (dict(experts=0), BAD), (dict(slope=0), BAD), (dict(out=0), BAD), (dict(ldd=63), BAD),
     (dict(out=PTR + 2), BAD), (dict(dl=PTR + 1), BAD)])
 def test_backward_refusals(lib, kw, code):
     assert backward(lib, **kw) == code
@@ -374,6 +374,52 @@ def test_special_rows():
     assert bool(d.isfinite().all()) and bool((d[0] == 0).all()) and bool((d[1, 5:] == 0).all()) and float(d[2, 7]) == 0.0
     both = tg.moe_router_backward(x, r, dw[:, :8].contiguous(), torch.ones((), device="cuda"))
     assert bool(both[4].isnan().all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G", [48, 63, 300])
+@pytest.mark.parametrize("score,away,zero", [("sigmoid", 60.0, False), ("sigmoid", 86.0, False), ("sigmoid", 88.4, True),
+                                             ("sigmoid", 100.0, True), ("softmax", 60.0, False), ("softmax", 78.0, False),
+                                             ("softmax", 84.5, True), ("softmax", 86.5, True), ("softmax", 100.0, True)])
+def test_chosen_scores_near_the_smallest_number(G, score, away, zero):
+    """The bias takes the experts whose scores are next to nothing: their weights and gradients are those of real numbers while the
+    scores are above 2^-126, and 0 below it.
+
+    Scores: e^-(away +- 0.2), over 38 to 291 for softmax (the nine at the end have no more than the bias gives them), so on
+    either side of 2^-126 = e^-87.34 as `zero` says.  An exponential of -x is off by x 2^-24 for the logit's difference,
+    x 2^-24 for its product with log2 e and 2^-22 for itself: 2 * 88 * 2^-24 + 2^-22 < 1.2e-5.  A weight is a quotient of sums of
+    them, off by twice that (and 8 roundings): < 2.6e-5 of itself.  A gradient w (1 - s) (g - sum w g) takes 4 times the largest |g|
+    of that at most."""
+    k = 4
+    gen = torch.Generator(device="cuda").manual_seed(G)
+    x = torch.zeros(37, G, device="cuda")
+    if score == "sigmoid":
+        x -= 120.0
+    x[:, -9:] = -away + 0.4 * (torch.rand(37, 9, device="cuda", generator=gen) - 0.5)
+    bias = torch.zeros(G, device="cuda")
+    bias[-9:] = 2.0
+    dw = torch.randn(37, k, device="cuda", generator=gen)
+    r = tg.moe_router(x, k, renormalize=True, score=score, bias=bias, weight_scale=1.5)
+    assert bool((r.experts >= G - 9).all())
+    d = tg.moe_router_backward(x, r, dw)
+    if zero:
+        assert bool((r.weights == 0).all()) and bool((d == 0).all())
+        return
+    want = weigh(x, r.experts, score, True, 1.5)[0]
+    assert float((r.weights - want).abs().max()) <= 2.6e-5 * 1.5
+    grad = gradient(x, r.experts, score, True, 1.5, dw, 0.0)[0]
+    assert float((d - grad).abs().max()) <= 4 * 2.6e-5 * 1.5 * float(dw.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(), dict(score="sigmoid"), dict(weight_scale=2.0), dict(score="sigmoid", groups=4, top_groups=2)])
+def test_a_routing_put_together_by_hand(kw):
+    x, bias, dw = make(16, 50, 64, F)
+    r = tg.moe_router(x, 4, renormalize=True, **kw)
+    again = tg.Routing(r.experts, r.weights, r.counts, r.loss, r.slope, True, r.score, r.weight_scale)
+    one = torch.ones((), device="cuda")
+    dw = dw[:, :4].contiguous()
+    assert torch.equal(tg.moe_router_backward(x, r, dw, one), tg.moe_router_backward(x, again, dw, one))
 
 
 @pytest.mark.gpu
