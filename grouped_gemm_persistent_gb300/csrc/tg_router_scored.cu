@@ -33,7 +33,7 @@
 // from and none below lo; otherwise, and without a bias by the largest logit itself, by counting the groups that come before each.
 //
 // Bound by instruction issue: 594 warp instructions a row of 256 with 8 groups and k = 8, 73 % of the issue rate, 93 us for 131072
-// rows whose logits are read in 20 us; a choice more costs 2.2 us, the groups 15.  The gradient: 292 instructions a row, 55 us (40 us
+// rows whose logits are read in 20 us; a choice more costs 2.6 us, the groups 17.  The gradient: 317 instructions a row, 52 us (40 us
 // at the copy rate).
 //
 // Positions.  A row is L lanes of V positions.  Each group has a power of two of positions, V at least, so that
