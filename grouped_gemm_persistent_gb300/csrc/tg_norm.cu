@@ -35,11 +35,11 @@ namespace tg {
 namespace norm {
 
 template <>
-NormKernel norm_for<TG_BF16>(bool residual, tg_dtype rt, const Spread& s, bool whole);
+NormKernel norm_for<TG_BF16>(bool residual, tg_dtype rt, const Spread& s, Form form);
 template <>
-NormKernel norm_for<TG_F16>(bool residual, tg_dtype rt, const Spread& s, bool whole);
+NormKernel norm_for<TG_F16>(bool residual, tg_dtype rt, const Spread& s, Form form);
 template <>
-NormKernel norm_for<TG_F32>(bool residual, tg_dtype rt, const Spread& s, bool whole);
+NormKernel norm_for<TG_F32>(bool residual, tg_dtype rt, const Spread& s, Form form);
 
 namespace {
 
@@ -124,8 +124,7 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
         a.e5m2 = p.q_dtype == TG_E5M2;
         vec = vec && host::aligned(p.q, 8) && p.ldq % 8 == 0;
     }
-    const bool whole = vec && p.K % 8 == 0;
-    a.vec = vec;
+    const Form form = form_of(vec, p.K);
     a.wide = 0;
     if (vec) {
         a.wide = wide_rows(p.M, p.K, p.ldx);
@@ -139,9 +138,9 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
     a.inv_hi = static_cast<float>(inv);
     a.inv_lo = static_cast<float>(inv - a.inv_hi);
     const Spread shape = spread_for(p.K, p.M <= 2 * d.sms, ht == TG_F32, p.q != nullptr);
-    const NormKernel kernel = p.x_dtype == TG_F32 ? norm_for<TG_F32>(residual, p.residual_dtype, shape, whole)
-                            : p.x_dtype == TG_F16 ? norm_for<TG_F16>(residual, p.residual_dtype, shape, whole)
-                                                  : norm_for<TG_BF16>(residual, p.residual_dtype, shape, whole);
+    const NormKernel kernel = p.x_dtype == TG_F32 ? norm_for<TG_F32>(residual, p.residual_dtype, shape, form)
+                            : p.x_dtype == TG_F16 ? norm_for<TG_F16>(residual, p.residual_dtype, shape, form)
+                                                  : norm_for<TG_BF16>(residual, p.residual_dtype, shape, form);
     const size_t smem = shape.nv == 1 ? 0 : static_cast<size_t>((p.K + 7) / 8) * 32;
     int64_t blocks = p.M;
     cudaError_t e = cudaSuccess;

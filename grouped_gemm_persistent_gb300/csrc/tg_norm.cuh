@@ -27,7 +27,22 @@ __device__ __forceinline__ float widen16(uint32_t b) {
     else return __uint_as_float(b << 16);
 }
 
-// Eight neighbouring values of a row, as they lie in memory
+// How the lanes hold a row.  WHOLE, ODD: eight neighbouring values each, rows on 16-byte boundaries, of whole vectors or not.  APART: rows
+// that start elsewhere; the sixteen lanes of a block of 128 values hold every sixteenth value of it, so that a load or a store of a
+// warp is two runs of neighbours.  (40970 x 4095 bf16 without padding, bf16 residual: into e4m3 600 us with eight neighbours read
+// one by one, 359 apart; gradients 570 and 343.  A row of whole blocks read without checks instead: 543 and 435, the 16-bit
+// values being put together, and waited for, inside the branch.)
+enum Form : int { ODD, WHOLE, APART };
+
+// The first value of the v-th lane, and how many values it has (eight or more: eight)
+template <int FORM>
+__device__ __forceinline__ int first_of(int v) { return FORM == APART ? (v & ~15) * 8 + (v & 15) : v * 8; }
+template <int FORM>
+__device__ __forceinline__ int count_of(int first, int K) { return FORM == APART ? (K - first + 15) >> 4 : K - first; }
+template <int FORM>
+constexpr int STRIDE = FORM == APART ? 16 : 1;
+
+// Eight values of a row, as they lie in memory
 template <int DT>
 struct Oct {
     static constexpr int WORDS = DT == TG_F32 ? 8 : 4;
@@ -45,30 +60,32 @@ struct Oct {
             w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
         }
     }
-    // n of the eight are inside the row; WHOLE: eight or none, 16-byte loads; otherwise wide: the same, with values past the row's end
+    // n of the eight are inside the row; WHOLE: eight or none, 16-byte loads; ODD, wide: the same, with values past the row's end
     // that cut() takes away (one by one they would have to be waited for here)
-    template <bool WHOLE>
+    template <int FORM>
     __device__ __forceinline__ void load(const uint8_t* p, int n, bool wide) {
         zero();
-        if (WHOLE || wide) {
+        if (FORM == WHOLE || (FORM == ODD && wide)) {
             if (n > 0) load_whole(p);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (i >= n) continue;
-                if constexpr (DT == TG_F32) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-                else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (i % 2 * 16);
+                if constexpr (DT == TG_F32) w[i] = reinterpret_cast<const uint32_t*>(p)[i * STRIDE<FORM>];
+                else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i * STRIDE<FORM>]) << (i % 2 * 16);
             }
         }
     }
     // the values from n on become zero
-    template <bool WHOLE>
+    template <int FORM>
     __device__ __forceinline__ void cut(int n) {
-        if (WHOLE || n >= 8 || n <= 0) return;
+        if constexpr (FORM == ODD) {
+            if (n >= 8 || n <= 0) return;
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i) {
-            if constexpr (DT == TG_F32) w[i] = i < n ? w[i] : 0u;
-            else w[i] &= 2 * i + 1 < n ? 0xffffffffu : 2 * i < n ? 0xffffu : 0u;
+            for (int i = 0; i < WORDS; ++i) {
+                if constexpr (DT == TG_F32) w[i] = i < n ? w[i] : 0u;
+                else w[i] &= 2 * i + 1 < n ? 0xffffffffu : 2 * i < n ? 0xffffu : 0u;
+            }
         }
     }
     __device__ __forceinline__ float value(int i) const {
@@ -91,29 +108,29 @@ struct Oct {
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
-    template <bool WHOLE>
-    __device__ __forceinline__ void store(uint8_t* p, int n, bool vec) const {
-        if (WHOLE ? n > 0 : vec && n >= 8) {
+    template <int FORM>
+    __device__ __forceinline__ void store(uint8_t* p, int n) const {
+        if (FORM == WHOLE ? n > 0 : FORM == ODD && n >= 8) {
 #pragma unroll
             for (int i = 0; i < WORDS; i += 4)
                 reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-        } else if constexpr (!WHOLE) {
+        } else if constexpr (FORM != WHOLE) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (i >= n) continue;
-                if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(p)[i] = w[i];
-                else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+                if constexpr (DT == TG_F32) reinterpret_cast<uint32_t*>(p)[i * STRIDE<FORM>] = w[i];
+                else reinterpret_cast<uint16_t*>(p)[i * STRIDE<FORM>] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
             }
         }
     }
 };
 
-template <int DT, bool WHOLE>
-__device__ __forceinline__ void store8(uint8_t* p, const float (&f)[8], int n, bool vec) {
+template <int DT, int FORM>
+__device__ __forceinline__ void store8(uint8_t* p, const float (&f)[8], int n) {
     Oct<DT> o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.set2(i, f[2 * i], f[2 * i + 1]);
-    o.template store<WHOLE>(p, n, vec);
+    o.template store<FORM>(p, n);
 }
 
 // One value of the gain, or 1
@@ -135,7 +152,7 @@ __device__ __forceinline__ void stage_values(float* to, const uint8_t* gain, int
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int v = base + i * blockDim.x, n = v < vectors ? K - v * 8 : 0;
-            o[i].template load<false>(gain + static_cast<int64_t>(v) * 8 * item_bytes(DT), n, vec && n >= 8);
+            o[i].template load<ODD>(gain + static_cast<int64_t>(v) * 8 * item_bytes(DT), n, vec && n >= 8);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
@@ -161,10 +178,17 @@ __device__ __forceinline__ void stage_gain(float* to, const uint8_t* gain, int d
     __syncthreads();
 }
 
-__device__ __forceinline__ void read_gain(float (&g)[8], const float* from) {
-    const float4 a = *reinterpret_cast<const float4*>(from), b = *(reinterpret_cast<const float4*>(from) + 1);
-    g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
-    g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+// The gain of a lane's values, n of them inside the row
+template <int FORM>
+__device__ __forceinline__ void read_gain(float (&g)[8], const float* from, int n) {
+    if constexpr (FORM == APART) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = i < n ? from[i * STRIDE<FORM>] : 0.0f;
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(from), b = *(reinterpret_cast<const float4*>(from) + 1);
+        g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
+        g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+    }
 }
 
 struct NormArgs {
@@ -185,8 +209,7 @@ struct NormArgs {
     int64_t M;
     int K;
     int gain_dtype, y_dtype, e5m2;
-    int vec;                     // rows on 16-byte boundaries (of 8-bit values 8-byte)
-    int64_t wide;                // rows before this one may be read in whole vectors
+    int64_t wide;                // rows before this one may be read in whole vectors (ODD)
     float eps, inv_hi, inv_lo;
 };
 
@@ -204,10 +227,9 @@ inline Spread spread(int64_t K, int nv) {
     return {static_cast<int>((vectors + 32 * nv - 1) / (32 * nv) * 32), nv};
 }
 
-// The kernel for x of type XT and a residual (none, or of x's type or fp32); whole: rows of whole vectors on 16-byte boundaries.  Defined
-// in tg_norm_inst.cu, compiled once for each XT.
+// The kernel for x of type XT and a residual (none, or of x's type or fp32).  Defined in tg_norm_inst.cu, compiled once for each XT.
 template <int XT>
-NormKernel norm_for(bool residual, tg_dtype rt, const Spread& s, bool whole);
+NormKernel norm_for(bool residual, tg_dtype rt, const Spread& s, Form form);
 
 // How many blocks of a kernel an SM holds, asked of the driver once for each kernel, block size and device.
 template <class K>
@@ -261,6 +283,8 @@ inline int64_t wide_rows(int64_t M, int64_t K, int64_t ld) {
     const int64_t past = (K + 7) / 8 * 8 - K, last = (past + ld - 1) / ld;
     return M > last ? M - last : 0;
 }
+
+inline Form form_of(bool on_boundaries, int64_t K) { return !on_boundaries ? APART : K % 8 ? ODD : WHOLE; }
 
 inline bool vectors_of(const void* p, int64_t ld_bytes) { return host::aligned(p, 16) && ld_bytes % 16 == 0; }
 

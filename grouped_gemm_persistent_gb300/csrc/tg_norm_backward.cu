@@ -35,17 +35,18 @@ struct NormBackArgs {
     int64_t M;
     int K;
     int gain_dtype;
-    int vec;                     // rows on 16-byte boundaries
-    int64_t wide;                // rows before this one may be read in whole vectors
+    int64_t wide;                // rows before this one may be read in whole vectors (ODD)
     float inv_k;
 };
 
-// Rows as in norm_kernel; the gain waits in shared memory, its gradient is summed in registers over a block's rows.
-template <int DT, int HT, int NV, bool WHOLE>
-__global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constant__ NormBackArgs a) {
+// Rows as in norm_kernel; the gain waits in shared memory, its gradient is summed in registers over a block's rows.  APART with two
+// vectors: held to 64 registers, 32 warps an SM, although fp32 streams spill a few (40970 x 4095: 501 us instead of 594 with 82).
+template <int DT, int HT, int NV, int FORM>
+__global__ void __launch_bounds__(512, FORM == APART && NV == 2 ? 2 : 0) norm_backward_kernel(const __grid_constant__ NormBackArgs a) {
     ptx::grid_launch_dependents();
     extern __shared__ __align__(16) float gain[];
     __shared__ float part[2][16];
+    constexpr int HELD = NV < 8 ? NV : 1;        // vectors of a row that stay in registers
     const int tpr = blockDim.x, in = threadIdx.x;
     const int64_t units = gridDim.x, unit = blockIdx.x;
     stage_gain(gain, a.gain, a.gain_dtype, a.K);
@@ -57,40 +58,41 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
     int turn = 0;
     for (int64_t row = unit; row < a.M; row += units, turn ^= 1) {
         const bool wide = row < a.wide;
-        Oct<DT> dy[NV];
-        Oct<HT> h[NV], dh[NV];
+        Oct<DT> dy[HELD];
+        Oct<HT> h[HELD], dh[HELD];
+        auto fetch = [&](int to, int j) {
+            const int col = first_of<FORM>(in + j * tpr), n = count_of<FORM>(col, a.K);
+            dy[to].template load<FORM>(a.dy + row * a.lddy + static_cast<int64_t>(col) * item_bytes(DT), n, wide);
+            h[to].template load<FORM>(a.h + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), n, wide);
+        };
+        auto fetch_other = [&](int to, int j) {
+            const int col = first_of<FORM>(in + j * tpr), n = count_of<FORM>(col, a.K);
+            if (a.d_hidden) dh[to].template load<FORM>(a.d_hidden + row * a.lddh + static_cast<int64_t>(col) * item_bytes(HT), n, wide);
+            else dh[to].zero();
+        };
+        if constexpr (HELD == NV) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (in + j * tpr) * 8;
-            dy[j].template load<WHOLE>(a.dy + row * a.lddy + static_cast<int64_t>(col) * item_bytes(DT), a.K - col, wide);
-            h[j].template load<WHOLE>(a.h + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, wide);
-        }
-        if (a.d_hidden) {
+            for (int j = 0; j < NV; ++j) fetch(j, j);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (in + j * tpr) * 8;
-                dh[j].template load<WHOLE>(a.d_hidden + row * a.lddh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, wide);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) dh[j].zero();
+            for (int j = 0; j < NV; ++j) fetch_other(j, j);
         }
         const float r = a.r[row];
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (in + j * tpr) * 8;
+            const int col = first_of<FORM>(in + j * tpr), at = j % HELD;
             if (col >= a.K) continue;
-            dy[j].template cut<WHOLE>(a.K - col);
-            h[j].template cut<WHOLE>(a.K - col);
+            if constexpr (HELD < NV) fetch(at, j);
+            dy[at].template cut<FORM>(a.K - col);
+            h[at].template cut<FORM>(a.K - col);
             float g[8];
-            read_gain(g, gain + col);
+            read_gain<FORM>(g, gain + col, count_of<FORM>(col, a.K));
             float t = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float n = h[j].value(i) * r;
-                t = fmaf(dy[j].value(i) * g[i], n, t);
-                acc[j][i] = fmaf(dy[j].value(i), n, acc[j][i]);
+                const float n = h[at].value(i) * r;
+                t = fmaf(dy[at].value(i) * g[i], n, t);
+                acc[j][i] = fmaf(dy[at].value(i), n, acc[j][i]);
             }
             s += t;
         }
@@ -106,22 +108,26 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const __grid_constan
         const float c = s * (r * a.inv_k);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (in + j * tpr) * 8;
+            const int col = first_of<FORM>(in + j * tpr), at = j % HELD;
             if (col >= a.K) continue;
+            if constexpr (HELD < NV) {
+                fetch(at, j);
+                fetch_other(at, j);
+            }
             float g[8], o[8];
-            read_gain(g, gain + col);
+            read_gain<FORM>(g, gain + col, count_of<FORM>(col, a.K));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = fmaf(dy[j].value(i) * g[i], r, fmaf(-(h[j].value(i) * r), c, dh[j].value(i)));
-            store8<HT, WHOLE>(a.dx + row * a.lddx + static_cast<int64_t>(col) * item_bytes(HT), o, a.K - col, a.vec);
+            for (int i = 0; i < 8; ++i) o[i] = fmaf(dy[at].value(i) * g[i], r, fmaf(-(h[at].value(i) * r), c, dh[at].value(i)));
+            store8<HT, FORM>(a.dx + row * a.lddx + static_cast<int64_t>(col) * item_bytes(HT), o, count_of<FORM>(col, a.K));
         }
     }
     if (a.part) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (in + j * tpr) * 8;
+            const int col = first_of<FORM>(in + j * tpr);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (col + i < a.K) a.part[unit * a.K + col + i] = acc[j][i];
+                if (col + i * STRIDE<FORM> < a.K) a.part[unit * a.K + col + i * STRIDE<FORM>] = acc[j][i];
         }
     }
 }
@@ -147,18 +153,24 @@ __global__ void __launch_bounds__(1024) norm_gain_kernel(const float* part, int6
 
 using NormBackKernel = void (*)(const NormBackArgs);
 
-// Two vectors a thread up to 8192 values, eight above.  40960 x 4096 bf16 with d_hidden: two 206 us, four 211, one 264.
-Spread spread_for(int64_t K) { return spread(K, K <= 8192 ? 2 : 8); }
+// Two vectors a thread up to 8192 values, four up to 16384, eight above, which are not held between the row's sum and dx but read again.
+// 40960 x 4096 bf16 with d_hidden: two 206 us, four 211, one 264.  10000 x 16383 without padding, fp32 stream: four 604, eight held
+// (and spilled) 1738.  5000 x 32768, fp32 stream: read again 504, held 1385 (339 at the copy rate); bf16 424 and 468.
+Spread spread_for(int64_t K) { return spread(K, K <= 8192 ? 2 : K <= 16384 ? 4 : 8); }
+
+template <int DT, int HT, int FORM>
+NormBackKernel back_for(const Spread& s) {
+    return s.nv == 2 ? &norm_backward_kernel<DT, HT, 2, FORM> : s.nv == 4 ? &norm_backward_kernel<DT, HT, 4, FORM> : &norm_backward_kernel<DT, HT, 8, FORM>;
+}
 
 template <int DT, int HT>
-NormBackKernel back_for(const Spread& s, bool whole) {
-    if (s.nv == 2) return whole ? &norm_backward_kernel<DT, HT, 2, true> : &norm_backward_kernel<DT, HT, 2, false>;
-    return whole ? &norm_backward_kernel<DT, HT, 8, true> : &norm_backward_kernel<DT, HT, 8, false>;
+NormBackKernel back_for(const Spread& s, Form form) {
+    return form == WHOLE ? back_for<DT, HT, WHOLE>(s) : form == ODD ? back_for<DT, HT, ODD>(s) : back_for<DT, HT, APART>(s);
 }
 
 template <int DT>
-NormBackKernel back_for(tg_dtype h, const Spread& s, bool whole) {
-    return h == TG_F32 ? back_for<DT, TG_F32>(s, whole) : h == TG_F16 ? back_for<DT, TG_F16>(s, whole) : back_for<DT, TG_BF16>(s, whole);
+NormBackKernel back_for(tg_dtype h, const Spread& s, Form form) {
+    return h == TG_F32 ? back_for<DT, TG_F32>(s, form) : h == TG_F16 ? back_for<DT, TG_F16>(s, form) : back_for<DT, TG_BF16>(s, form);
 }
 
 }  // namespace
@@ -215,8 +227,7 @@ extern "C" tg_status tg_rmsnorm_backward(const tg_rmsnorm_backward_args* args, t
     a.K = static_cast<int>(p.K);
     const bool vec = vectors_of(p.dy, a.lddy) && vectors_of(p.hidden, a.ldh) &&
                        (!p.d_hidden || vectors_of(p.d_hidden, a.lddh)) && vectors_of(p.dx, a.lddx);
-    const bool whole = vec && p.K % 8 == 0;
-    a.vec = vec;
+    const Form form = form_of(vec, p.K);
     a.wide = 0;
     if (vec) {
         a.wide = wide_rows(p.M, p.K, p.lddy);
@@ -225,9 +236,9 @@ extern "C" tg_status tg_rmsnorm_backward(const tg_rmsnorm_backward_args* args, t
     }
     a.inv_k = 1.0f / static_cast<float>(p.K);
     const Spread shape = spread_for(p.K);
-    const NormBackKernel kernel = p.dy_dtype == TG_F32 ? back_for<TG_F32>(p.hidden_dtype, shape, whole)
-                                : p.dy_dtype == TG_F16 ? back_for<TG_F16>(p.hidden_dtype, shape, whole)
-                                                       : back_for<TG_BF16>(p.hidden_dtype, shape, whole);
+    const NormBackKernel kernel = p.dy_dtype == TG_F32 ? back_for<TG_F32>(p.hidden_dtype, shape, form)
+                                : p.dy_dtype == TG_F16 ? back_for<TG_F16>(p.hidden_dtype, shape, form)
+                                                       : back_for<TG_BF16>(p.hidden_dtype, shape, form);
     const size_t smem = static_cast<size_t>((p.K + 7) / 8) * 32;
     int n = 0;
     cudaError_t e = resident(kernel, shape.threads, smem, d.id, &n);

@@ -107,17 +107,17 @@ __device__ __forceinline__ Pair block_sum(Pair v, Pair* part) {
 // What a row's thread writes: y in 16 or 32 bits or not at all, and the 8-bit copy
 enum : int { Y_NONE = 0, Y_HALF = 1, Y_FLOAT = 2 };
 
-template <int HT, int NV, bool WHOLE, bool STAGED, int Y, bool Q>
+template <int HT, int NV, int FORM, bool STAGED, int Y, bool Q>
 __device__ __forceinline__ void finish_row(const NormArgs& a, const Oct<HT> (&h)[NV], float r, int64_t row, int in, int tpr,
                                            const float* gain, const float (&g0)[8]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int v = in + j * tpr, col = v * 8;
+        const int v = in + j * tpr, col = first_of<FORM>(v);
         if ((v & ~31) * 8 >= a.K) return;                // (a whole warp: the shuffles below stay together)
-        const int n = a.K - col;                         // below 1: nothing here
+        const int n = count_of<FORM>(col, a.K);          // below 1: nothing here
         float y[8], g[8];
         if constexpr (STAGED) {
-            if (n > 0) read_gain(g, gain + col);
+            if (n > 0) read_gain<FORM>(g, gain + col, n);
             else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) g[i] = 0.0f;
@@ -142,14 +142,14 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Oct<HT> (&h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o.w[i] = f.w[i];
             }
-            o.template store<WHOLE>(a.y + row * a.ldy + col * 2, n, a.vec);
+            o.template store<FORM>(a.y + row * a.ldy + col * 2, n);
         } else if constexpr (Y == Y_FLOAT) {
-            store8<TG_F32, WHOLE>(a.y + row * a.ldy + static_cast<int64_t>(col) * 4, y, n, a.vec);
+            store8<TG_F32, FORM>(a.y + row * a.ldy + static_cast<int64_t>(col) * 4, y, n);
         }
         if constexpr (Q) {
             // 16 lanes hold a block.  Values past the row's end count as zero (0 times r may be NaN).
             float top = 0.0f;
-            if constexpr (WHOLE) {
+            if constexpr (FORM == WHOLE) {
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) top = max_magnitude(top, y[i], y[i + 1]);
                 if (n <= 0) top = 0.0f;
@@ -176,20 +176,19 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Oct<HT> (&h)
             }
             if (inv == 0.0f) w[0] = w[1] = 0u;           // a block that is not finite: zeros
             uint8_t* dst = a.q + row * a.ldq + col;
-            if (WHOLE ? n > 0 : a.vec && n >= 8) {
+            if (FORM == WHOLE ? n > 0 : FORM == ODD && n >= 8) {
                 *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-            } else if constexpr (!WHOLE) {
+            } else if constexpr (FORM != WHOLE) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i < n) dst[i] = static_cast<uint8_t>(w[i / 4] >> (i % 4 * 8));
+                    if (i < n) dst[i * STRIDE<FORM>] = static_cast<uint8_t>(w[i / 4] >> (i % 4 * 8));
             }
         }
     }
 }
 
-// The block's rows are blockIdx.x, blockIdx.x + gridDim.x, ..., NV vectors of eight values a thread.  WHOLE: rows of whole vectors on
-// 16-byte boundaries.  STAGED: the gain waits in shared memory (otherwise, with one vector a thread, in registers).
-template <int XT, int RT, int NV, bool WHOLE>
+// The block's rows are blockIdx.x, blockIdx.x + gridDim.x, ..., NV times eight values a thread.  STAGED: the gain waits in shared memory (otherwise, with one vector a thread, in registers).
+template <int XT, int RT, int NV, int FORM>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int HT = RT == N_NONE ? XT : RT;
     constexpr bool STAGED = NV > 1;
@@ -204,10 +203,10 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
         const bool wide = row < a.wide;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (in + j * tpr) * 8;
-            x[j].template load<WHOLE>(a.x + row * a.ldx + static_cast<int64_t>(col) * item_bytes(XT), a.K - col, wide);
+            const int col = first_of<FORM>(in + j * tpr), n = count_of<FORM>(col, a.K);
+            x[j].template load<FORM>(a.x + row * a.ldx + static_cast<int64_t>(col) * item_bytes(XT), n, wide);
             if constexpr (RT != N_NONE)
-                add[j].template load<WHOLE>(a.residual + row * a.ldr + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, wide);
+                add[j].template load<FORM>(a.residual + row * a.ldr + static_cast<int64_t>(col) * item_bytes(HT), n, wide);
         }
     };
     if (unit < a.M) fetch(unit);
@@ -216,17 +215,20 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
         stage_gain(gain, a.gain, a.gain_dtype, a.K);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g0[i] = in * 8 + i < a.K ? gain_value(a.gain, a.gain_dtype, in * 8 + i) : 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            const int col = first_of<FORM>(in) + i * STRIDE<FORM>;
+            g0[i] = col < a.K ? gain_value(a.gain, a.gain_dtype, col) : 0.0f;
+        }
     }
     int turn = 0;
     for (int64_t row = unit; row < a.M; row += units, turn ^= 1) {
         Pair sum{0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int n = a.K - (in + j * tpr) * 8;
-            x[j].template cut<WHOLE>(n);
+            const int n = a.K - (in + j * tpr) * 8;          // (ODD)
+            x[j].template cut<FORM>(n);
             if constexpr (RT != N_NONE) {
-                add[j].template cut<WHOLE>(n);
+                add[j].template cut<FORM>(n);
                 add_rows(h[j], x[j], add[j]);
             } else {
 #pragma unroll
@@ -237,8 +239,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if constexpr (RT != N_NONE) {
-                const int col = (in + j * tpr) * 8;
-                h[j].template store<WHOLE>(a.hidden + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), a.K - col, a.vec);
+                const int col = first_of<FORM>(in + j * tpr);
+                h[j].template store<FORM>(a.hidden + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), count_of<FORM>(col, a.K));
             }
             sum = pair_add(sum, {squares(h[j], 1.0f), 0.0f});
         }
@@ -257,33 +259,35 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
         }
         if (in == 0) a.r[row] = r;
         if (!a.y) {
-            finish_row<HT, NV, WHOLE, STAGED, Y_NONE, true>(a, h, r, row, in, tpr, gain, g0);
+            finish_row<HT, NV, FORM, STAGED, Y_NONE, true>(a, h, r, row, in, tpr, gain, g0);
         } else if (a.y_dtype == TG_F32) {
-            if (a.q) finish_row<HT, NV, WHOLE, STAGED, Y_FLOAT, true>(a, h, r, row, in, tpr, gain, g0);
-            else finish_row<HT, NV, WHOLE, STAGED, Y_FLOAT, false>(a, h, r, row, in, tpr, gain, g0);
+            if (a.q) finish_row<HT, NV, FORM, STAGED, Y_FLOAT, true>(a, h, r, row, in, tpr, gain, g0);
+            else finish_row<HT, NV, FORM, STAGED, Y_FLOAT, false>(a, h, r, row, in, tpr, gain, g0);
         } else {
-            if (a.q) finish_row<HT, NV, WHOLE, STAGED, Y_HALF, true>(a, h, r, row, in, tpr, gain, g0);
-            else finish_row<HT, NV, WHOLE, STAGED, Y_HALF, false>(a, h, r, row, in, tpr, gain, g0);
+            if (a.q) finish_row<HT, NV, FORM, STAGED, Y_HALF, true>(a, h, r, row, in, tpr, gain, g0);
+            else finish_row<HT, NV, FORM, STAGED, Y_HALF, false>(a, h, r, row, in, tpr, gain, g0);
         }
     }
 }
 
-template <int XT, int RT, bool WHOLE>
+template <int XT, int RT, int FORM>
 NormKernel pick(const Spread& s) {
-    return s.nv == 1 ? &norm_kernel<XT, RT, 1, WHOLE> : s.nv == 2 ? &norm_kernel<XT, RT, 2, WHOLE>
-         : s.nv == 4 ? &norm_kernel<XT, RT, 4, WHOLE> : &norm_kernel<XT, RT, 8, WHOLE>;
+    return s.nv == 1 ? &norm_kernel<XT, RT, 1, FORM> : s.nv == 2 ? &norm_kernel<XT, RT, 2, FORM>
+         : s.nv == 4 ? &norm_kernel<XT, RT, 4, FORM> : &norm_kernel<XT, RT, 8, FORM>;
 }
 
 template <int XT, int RT>
-NormKernel pick(const Spread& s, bool whole) { return whole ? pick<XT, RT, true>(s) : pick<XT, RT, false>(s); }
+NormKernel pick(const Spread& s, Form form) {
+    return form == WHOLE ? pick<XT, RT, WHOLE>(s) : form == ODD ? pick<XT, RT, ODD>(s) : pick<XT, RT, APART>(s);
+}
 
 }  // namespace
 
 template <>
-NormKernel norm_for<TG_NORM_X>(bool residual, tg_dtype rt, const Spread& s, bool whole) {
-    if (!residual) return pick<TG_NORM_X, N_NONE>(s, whole);
-    if (TG_NORM_X == TG_F32 || rt == TG_F32) return pick<TG_NORM_X, TG_F32>(s, whole);
-    return pick<TG_NORM_X, TG_NORM_X>(s, whole);
+NormKernel norm_for<TG_NORM_X>(bool residual, tg_dtype rt, const Spread& s, Form form) {
+    if (!residual) return pick<TG_NORM_X, N_NONE>(s, form);
+    if (TG_NORM_X == TG_F32 || rt == TG_F32) return pick<TG_NORM_X, TG_F32>(s, form);
+    return pick<TG_NORM_X, TG_NORM_X>(s, form);
 }
 
 }  // namespace norm

@@ -278,6 +278,34 @@ def test_rows_off_the_16_byte_boundaries(K, xt, rt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K", [1, 7, 15, 17, 127, 129, 255, 257, 1001, 2049, 4095, 8193, 16383, 16391, 32767])
+@pytest.mark.parametrize("xt,rt,gt", [(BF, BF, F), (HF, F, HF), (F, F, F)])
+def test_rows_without_padding(K, xt, rt, gt):
+    """Rows one behind the other, of odd length: each starts elsewhere, the last ends where the memory does."""
+    M = 35
+
+    def dense(seed, t):
+        return make(seed, M, K, t)[0].contiguous()
+
+    x, residual, dy, dh = dense(20, xt), dense(21, rt), dense(22, xt), dense(23, rt)
+    gain = make(24, 1, K, F, None, gt)[2]
+    rows = {name: torch.full((M * K + 64,), 7.0, dtype=rt, device="cuda") for name in ("hidden", "dx")}
+    view = {name: t[32:32 + M * K].view(M, K) for name, t in rows.items()}
+    n = tg.rmsnorm(x, gain, EPS, residual=residual, hidden=view["hidden"], out_dtype=F, fp8_dtype=E4)
+    check_forward(x, residual, gain, n)
+    q, scale = tg.quantize_fp8(n.y, (1, 128))
+    assert torch.equal(n.q.view(torch.uint8), q.view(torch.uint8)) and torch.equal(n.scale, scale)
+    half = tg.rmsnorm(x, gain, EPS, residual=residual, out_dtype=BF)
+    check_forward(x, residual, gain, half)
+    for past in (dh, None):
+        dx, d_gain = tg.rmsnorm_backward(n, dy, gain, past, view["dx"])
+        check_backward(n, gain, dy, past, dx, d_gain)
+    for t in rows.values():
+        assert bool((t[:32] == 7.0).all()) and bool((t[32 + M * K:] == 7.0).all())
+    tg.device_status()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [5, 400])
 @pytest.mark.parametrize("K", [200, 4096])
 def test_in_place_and_nothing_beside_the_rows(M, K):
