@@ -247,7 +247,8 @@ cudaError_t resident(K kernel, int threads, size_t smem, int device, int* out) {
             return cudaSuccess;
         }
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // the limit of the longest rows, whatever these are: a lower one would take it from rows that were asked for before
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, N_MAX_K * 4);
         if (e != cudaSuccess) return e;
     }
     int n = 0;

@@ -336,6 +336,37 @@ def test_in_place_and_nothing_beside_the_rows(M, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("offset", [0, 1])
+def test_long_and_longer_rows_in_turn(offset):
+    """The same kernels with more, less and again more shared memory."""
+    for K in (32768, 16400, 32768, 24000, 16640, 32768):
+        x, residual, gain = make(32, 3, K, BF, BF, F, offset=offset)
+        n = tg.rmsnorm(x, gain, EPS, residual=residual)
+        check_forward(x, residual, gain, n)
+        dx, d_gain = tg.rmsnorm_backward(n, x, gain, residual)
+        check_backward(n, gain, x, residual, dx, d_gain)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [4097, 12000, 16391, 16400, 32768])
+@pytest.mark.parametrize("dt", [BF, F])
+def test_long_gradients_in_place(K, dt):
+    """The gradient written over d_hidden or over dy: what a row still reads of them is not lost."""
+    for pad in (0, 3):                               # rows on 16-byte boundaries, and off them
+        x, residual, gain = make(30, 9, K, dt, dt, F, offset=pad)
+        dy, dh, _ = make(31, 9, K, dt, dt, None, offset=pad)
+        n = tg.rmsnorm(x, gain, EPS, residual=residual)
+        dx, d_gain = tg.rmsnorm_backward(n, dy, gain, dh)
+        check_backward(n, gain, dy, dh, dx, d_gain)
+        for which in (dh, dy):
+            a, b = make(31, 9, K, dt, dt, None, offset=pad)[:2]
+            over = a if which is dy else b
+            got, got_gain = tg.rmsnorm_backward(n, a, gain, b, over)
+            assert got is over or got.data_ptr() == over.data_ptr()
+            assert torch.equal(over, dx) and torch.equal(got_gain, d_gain)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("K", [384, 2048])
 def test_special_rows(K):
     x, residual, gain = make(9, 6, K, F, F, F)
