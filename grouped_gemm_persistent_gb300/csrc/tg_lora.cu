@@ -978,7 +978,9 @@ extern "C" tg_status tg_lora_add(const tg_lora_args* args, tg_stream_t stream) {
     int ctas = 1;
     while (ctas < MAX_CTAS && likely * ctas * 2 <= 2 * d.sms && a.K >= ctas * 512) ctas *= 2;
     const int plan_bytes = PLAN_WARPS * int(buckets + 1) * 4;
-    e = plan_bytes > 48 * 1024 ? cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_bytes) : cudaSuccess;
+    // (the limit of the most buckets, whatever these are: another thread's call may be between here and its launch)
+    constexpr int MOST_PLAN_BYTES = PLAN_WARPS * (MAX_BUCKETS + 1) * 4;
+    e = plan_bytes > 48 * 1024 ? cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_PLAN_BYTES) : cudaSuccess;
     if (e == cudaSuccess && v.bytes > 48 * 1024)
         e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.bytes);
     if (e == cudaSuccess) {
