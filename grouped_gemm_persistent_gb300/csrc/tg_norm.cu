@@ -144,7 +144,7 @@ extern "C" tg_status tg_rmsnorm(const tg_rmsnorm_args* args, tg_stream_t stream)
     const size_t smem = shape.nv == 1 ? 0 : static_cast<size_t>((p.K + 7) / 8) * 32;
     int64_t blocks = p.M;
     cudaError_t e = cudaSuccess;
-    if (blocks > 2 * d.sms || smem > 48 * 1024) {       // (it also lets the kernel have that much)
+    if (blocks > 2 * d.sms || smem > FREE_SMEM) {       // (it also lets the kernel have that much)
         int n = 0;
         if ((e = resident(kernel, shape.threads, smem, d.id, &n)) != cudaSuccess) return host::cuda_fail(e, "occupancy of the norm");
         if (blocks > static_cast<int64_t>(n) * d.sms) blocks = static_cast<int64_t>(n) * d.sms;

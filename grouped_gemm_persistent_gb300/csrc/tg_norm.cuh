@@ -18,6 +18,7 @@ namespace norm {
 
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr int N_MAX_K = TG_RMSNORM_MAX_COLUMNS;
+constexpr size_t FREE_SMEM = 40 * 1024;       // dynamic shared memory that is there without asking: 48 KB with the kernels' own
 
 constexpr int item_bytes(int dt) { return dt == TG_F32 ? 4 : 2; }
 
@@ -246,7 +247,7 @@ cudaError_t resident(K kernel, int threads, size_t smem, int device, int* out) {
             *out = known[i].blocks;
             return cudaSuccess;
         }
-    if (smem > 48 * 1024) {
+    if (smem > FREE_SMEM) {
         // the limit of the longest rows, whatever these are: a lower one would take it from rows that were asked for before
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, N_MAX_K * 4);
         if (e != cudaSuccess) return e;

@@ -336,6 +336,18 @@ def test_in_place_and_nothing_beside_the_rows(M, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K", [8192, 10240, 12096, 12160, 12161, 12200, 12264, 12280, 12287, 12288, 12289, 12296])
+@pytest.mark.parametrize("M", [3, 400])
+def test_a_gain_that_just_fits(M, K):
+    """The gain takes about as much shared memory as a kernel has without asking (48 KB, of which the row's sums take some)."""
+    x, residual, gain = make(33, M, K, BF, BF, F)
+    n = tg.rmsnorm(x, gain, EPS, residual=residual)
+    check_forward(x, residual, gain, n)
+    dx, d_gain = tg.rmsnorm_backward(n, x, gain, residual)
+    check_backward(n, gain, x, residual, dx, d_gain)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("offset", [0, 1])
 def test_long_and_longer_rows_in_turn(offset):
     """The same kernels with more, less and again more shared memory."""
