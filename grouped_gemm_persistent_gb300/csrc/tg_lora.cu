@@ -46,6 +46,7 @@ constexpr uint32_t FULL = 0xffffffffu;
 constexpr int L_WARPS = 8;
 constexpr int L_THREADS = 32 * L_WARPS;
 constexpr int ROW_CUT = 512;        // k of a block of the rows form
+constexpr int FREE_SMEM = 40 * 1024;       // dynamic shared memory that is there without asking: 48 KB with the kernels' own
 
 // Eight neighbouring 16-bit values
 struct Half8 {
@@ -980,8 +981,8 @@ extern "C" tg_status tg_lora_add(const tg_lora_args* args, tg_stream_t stream) {
     const int plan_bytes = PLAN_WARPS * int(buckets + 1) * 4;
     // (the limit of the most buckets, whatever these are: another thread's call may be between here and its launch)
     constexpr int MOST_PLAN_BYTES = PLAN_WARPS * (MAX_BUCKETS + 1) * 4;
-    e = plan_bytes > 48 * 1024 ? cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_PLAN_BYTES) : cudaSuccess;
-    if (e == cudaSuccess && v.bytes > 48 * 1024)
+    e = plan_bytes > FREE_SMEM ? cudaFuncSetAttribute(lora_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_PLAN_BYTES) : cudaSuccess;
+    if (e == cudaSuccess && v.bytes > FREE_SMEM)
         e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.bytes);
     if (e == cudaSuccess) {
         lora_plan_kernel<<<PLAN_CTAS, 32 * PLAN_WARPS, plan_bytes, st>>>(p.adapters, p.T, a.G, plan);

@@ -179,6 +179,14 @@ def test_tiles(T, K, N, r, G, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G", [255, 256, 350, 370, 375, 379, 380, 381, 382, 383, 384, 385, 511, 512, 513, 700])
+def test_numbers_of_adapters(G):
+    """The order of the rows counts by adapter in shared memory: about as much as a kernel has without asking, and more."""
+    base, x, a, b, ids, scale = make(40, 5000, 64, 40, 8, G, BF, BF, "rows")
+    check(base, x, a, b, ids, scale, tg.lora_add(base, x, a, b, ids, scale))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,r", [(20, 16), (90, 64), (300, 100), (5000, 32)])
 @pytest.mark.parametrize("pad", [2, 8, 6])
 def test_strides_and_in_place(T, r, pad):
