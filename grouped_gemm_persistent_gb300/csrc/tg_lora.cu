@@ -711,7 +711,8 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            u[i] *= scale;
+            // (the ranks that fill up to RT are zeros of A: with an infinity in x they would be NaN)
+            u[i] = lane * PER + i < p.r ? u[i] * scale : 0.0f;
             top = fmaxf(top, fabsf(u[i]));
         }
         float down = 1.0f, up = 1.0f;

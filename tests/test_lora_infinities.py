@@ -1,0 +1,36 @@
+"""Infinities in the adapters' products: the same in both forms as in 64 bits, infinities and NaN told apart (GPU)."""
+import pytest
+import torch
+
+import grouped_gemm_persistent_gb300 as tg
+from test_lora import BF, F, HF, lib, make  # noqa: F401
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("lib")]
+
+
+def same_kind(got, want):
+    """NaN where NaN is wanted, the same infinities, numbers elsewhere."""
+    assert torch.equal(got.isnan(), want.isnan())
+    for sign in (1.0, -1.0):
+        assert torch.equal(got == sign * float("inf"), want == sign * float("inf"))
+
+
+@pytest.mark.parametrize("T,K,N,G", [(20, 320, 200, 5), (600, 4096, 200, 5), (5000, 320, 200, 5), (5000, 136, 100, 400)])
+@pytest.mark.parametrize("r", [1, 8, 24, 40, 100])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_an_infinity_in_x_at_ranks_that_are_filled_up(T, K, N, G, r, dt):
+    """The few rows' form has no ranks past r; the tiles fill them up, with nothing that an infinity may meet."""
+    base, x, a, b, ids, scale = make(50, T, K, N, r, G, dt, F, "rows")
+    ids[3] = 1
+    x[3, 7] = float("inf")
+    # u = +-inf by the sign of A's column 7; even columns of B go with those signs, so that their sums are infinite
+    sign = a[1, :, 7].float().sign()
+    b[1, ::2] = (b[1, ::2].float().abs() * sign).to(dt)
+    b[1, 2::4] = -b[1, 2::4]
+    got = tg.lora_add(base, x, a, b, ids, scale)
+    u = float(scale[1]) * (x[3].double() * a[1].double()).sum(1)
+    want = base[3].double() + (u * b[1].double()).sum(1)
+    assert bool(want[::2].isinf().all())
+    same_kind(got[3], want)
+    others = torch.arange(T, device="cuda") != 3
+    assert bool(got[others].isfinite().all())
