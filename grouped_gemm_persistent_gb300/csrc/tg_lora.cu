@@ -713,11 +713,12 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
         for (int i = 0; i < PER; ++i) {
             // (the ranks that fill up to RT are zeros of A: with an infinity in x they would be NaN)
             u[i] = lane * PER + i < p.r ? u[i] * scale : 0.0f;
-            top = fmaxf(top, fabsf(u[i]));
+            if (fabsf(u[i]) < __int_as_float(0x7f800000)) top = fmaxf(top, fabsf(u[i]));
         }
         float down = 1.0f, up = 1.0f;
         if constexpr (DT == TG_F16) {
-            // 2^-e with the largest |u| in [2^e, 2^(e + 1)); left alone where it is zero, tiny or not finite
+            // 2^-e with the largest finite |u| in [2^e, 2^(e + 1)) (beside an infinity the others stay numbers); left alone where
+            // it is zero, tiny or next to fp32's range
             const uint32_t e = __reduce_max_sync(FULL, __float_as_uint(top)) >> 23;
             if (e > 10u && e < 245u) {
                 down = __uint_as_float((254u - e) << 23);

@@ -34,3 +34,20 @@ def test_an_infinity_in_x_at_ranks_that_are_filled_up(T, K, N, G, r, dt):
     same_kind(got[3], want)
     others = torch.arange(T, device="cuda") != 3
     assert bool(got[others].isfinite().all())
+
+
+@pytest.mark.parametrize("T", [20, 5000])
+def test_numbers_past_fp16_beside_an_infinity(T):
+    """An adapter with an infinite weight of one rank, whose other ranks give numbers that fp16 does not hold."""
+    K, N, r = 256, 72, 16
+    base, x, a, b, ids, scale = make(51, T, K, N, r, 3, HF, F, "rows")
+    x, a = (x.float() * 100).to(HF), (a.float() * 200 * K ** 0.5).to(HF)
+    a[1, 2, 7] = float("inf")
+    ids[3] = 1
+    got = tg.lora_add(base, x, a, b, ids, scale)
+    rows = torch.nonzero(ids == 1)[:, 0]
+    u = float(scale[1]) * (x[rows].double()[:, None] * a[1].double()[None]).sum(2)
+    assert bool((u.abs() > 65504).any(1).all())
+    want = base[rows].double() + (u[:, None] * b[1].double()[None]).sum(2)
+    assert bool(want.isinf().all())
+    same_kind(got[rows], want)
