@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import grouped_gemm_persistent_gb300 as tg
-from test_lora import BF, F, HF, lib, make  # noqa: F401
+from test_lora import BF, F, HF, check, lib, make  # noqa: F401
 
 pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("lib")]
 
@@ -51,3 +51,17 @@ def test_numbers_past_fp16_beside_an_infinity(T):
     want = base[rows].double() + (u[:, None] * b[1].double()[None]).sum(2)
     assert bool(want.isinf().all())
     same_kind(got[rows], want)
+
+
+@pytest.mark.parametrize("T", [20, 5000])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("size,weight", [(3.4e38, 1e-3), (1e37, 1e-2), (1e-36, 100.0), (3e-38, 300.0)])
+def test_numbers_at_the_ends_of_fp32_between_the_products(T, dt, size, weight):
+    """A factor that takes what is between the two products next to fp32's largest or smallest numbers; the result is well inside."""
+    base, x, a, b, ids, _ = make(52, T, 8, 72, 16, 3, dt, F, "rows")
+    x = torch.zeros_like(x)
+    x[:, 0] = 1.0
+    a = torch.where(a < 0, -1.0, 1.0).to(dt)
+    b, base = (b.float() * weight).to(dt), torch.zeros_like(base)
+    scale = torch.full((3,), size, device="cuda")
+    check(base, x, a, b, ids, scale, tg.lora_add(base, x, a, b, ids, scale))
