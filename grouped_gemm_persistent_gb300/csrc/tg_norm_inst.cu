@@ -53,7 +53,7 @@ __device__ __forceinline__ float row_factor(Pair sum, float inv_hi, float inv_lo
     return __fmaf_rn(0.5f * r, e, r);
 }
 
-// The sum of eight values' squares, the values times f (1, or 2^-70): a product's, a fused and two additions' roundings
+// The sum of eight values' squares, the values times f (1, or 2^-80): a product's, a fused and two additions' roundings
 template <int DT>
 __device__ __forceinline__ float squares(const Oct<DT>& o, float f) {
     const uint64_t ff = ptx::f32x2_pack(f, f);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
         if (!(sum.hi < __int_as_float(0x7f800000))) {
             // a row whose squares' sum is past fp32's range (or that has an infinity or a NaN, and keeps it): once more,
             // scaled down; eps is nothing beside it
-            constexpr float DOWN = 8.470329473e-22f;      // 2^-70
+            constexpr float DOWN = 8.271806126e-25f;      // 2^-80: the squares of 32768 values of 2^128 sum to 2^111
             Pair low{0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < NV; ++j) low = pair_add(low, {squares(h[j], DOWN), 0.0f});
