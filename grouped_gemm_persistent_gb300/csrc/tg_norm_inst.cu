@@ -245,18 +245,19 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
             sum = pair_add(sum, {squares(h[j], 1.0f), 0.0f});
         }
         sum = block_sum(sum, part[turn]);
-        float r = row_factor(sum, a.inv_hi, a.inv_lo, a.eps);
-        if (!(sum.hi < __int_as_float(0x7f800000))) {
-            // a row whose squares' sum is past fp32's range (or that has an infinity or a NaN, and keeps it): once more,
-            // scaled down; eps is nothing beside it
-            constexpr float DOWN = 8.271806126e-25f;      // 2^-80: the squares of 32768 values of 2^128 sum to 2^111
-            Pair low{0.0f, 0.0f};
+        float scaled = 1.0f, eps = a.eps;
+        if (!(sum.hi * a.inv_hi + eps < 1.267650600e30f)) {       // 2^100
+            // a row whose squares or eps take its factor's square near fp32's ends (or that has an infinity or a NaN, and keeps
+            // it): once more, scaled down by 2^-80, with which the squares of 32768 values of 2^128 sum to 2^111
+            scaled = 8.271806126e-25f;
+            eps = eps * scaled * scaled;
+            Pair again{0.0f, 0.0f};
 #pragma unroll
-            for (int j = 0; j < NV; ++j) low = pair_add(low, {squares(h[j], DOWN), 0.0f});
+            for (int j = 0; j < NV; ++j) again = pair_add(again, {squares(h[j], scaled), 0.0f});
             __syncthreads();                             // the parts are read above
-            low = block_sum(low, part[turn]);
-            r = row_factor(low, a.inv_hi, a.inv_lo, 0.0f) * DOWN;
+            sum = block_sum(again, part[turn]);
         }
+        const float r = row_factor(sum, a.inv_hi, a.inv_lo, eps) * scaled;
         if (in == 0) a.r[row] = r;
         if (!a.y) {
             finish_row<HT, NV, FORM, STAGED, Y_NONE, true>(a, h, r, row, in, tpr, gain, g0);

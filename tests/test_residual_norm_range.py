@@ -55,3 +55,11 @@ def test_squares_past_fp32(K, dt):
     one = torch.zeros_like(x)
     one[:, K // 2] = x[:, 0]                       # a single value is all of a row
     norm(one, 1e-6)
+
+
+@pytest.mark.parametrize("K", [1, 384, 1001, 8192, 32768])
+@pytest.mark.parametrize("eps", [1e30, 2e33, 2e38, 2.9e38])
+def test_an_eps_as_large_as_the_squares(K, eps):
+    """Any finite eps counts, beside squares that fp32 holds and beside those that it does not."""
+    root = eps ** 0.5
+    norm(rows_of((1.0, root * 1e-9, root * 1e-3, root * 0.5, root, root * 1.5, root * 30, 1e25), K, F), eps)
