@@ -46,14 +46,14 @@ __device__ __forceinline__ float row_factor(Pair sum, float inv_hi, float inv_lo
     const Pair m0 = pair_add({p, pe}, {eps, 0.0f});
     const float m = __fadd_rn(m0.hi, m0.lo), ml = __fsub_rn(m0.lo, __fsub_rn(m, m0.hi));
     const float r = rsqrtf(m);
-    if (!(m >= 1.17549435e-38f)) return r;            // below fp32's normal numbers r^2 would overflow
+    if (m == 0.0f) return r;
     const float t = __fmul_rn(r, r), tl = __fmaf_rn(r, r, -t);
     const float q = __fmul_rn(m, t), ql = __fmaf_rn(m, t, -q) + (m * tl + ml * t);
     const float e = __fsub_rn(1.0f, q) - ql;          // 1 - m r^2
     return __fmaf_rn(0.5f * r, e, r);
 }
 
-// The sum of eight values' squares, the values times f (1, or 2^-80): a product's, a fused and two additions' roundings
+// The sum of eight values' squares, the values times f (1, 2^-80 or 2^100): a product's, a fused and two additions' roundings
 template <int DT>
 __device__ __forceinline__ float squares(const Oct<DT>& o, float f) {
     const uint64_t ff = ptx::f32x2_pack(f, f);
@@ -246,10 +246,12 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
         }
         sum = block_sum(sum, part[turn]);
         float scaled = 1.0f, eps = a.eps;
-        if (!(sum.hi * a.inv_hi + eps < 1.267650600e30f)) {       // 2^100
-            // a row whose squares or eps take its factor's square near fp32's ends (or that has an infinity or a NaN, and keeps
-            // it): once more, scaled down by 2^-80, with which the squares of 32768 values of 2^128 sum to 2^111
-            scaled = 8.271806126e-25f;
+        const float mean = sum.hi * a.inv_hi + eps;
+        if (!(mean < 1.267650600e30f) || mean < 7.888609052e-31f) {       // 2^100, 2^-100
+            // a row whose squares or factor's square come near an end of fp32 (or that has an infinity or a NaN, and keeps it): once
+            // more, scaled down by 2^-80, with which the squares of 32768 values of 2^128 sum to 2^111, or up by 2^100, with
+            // which those of 32768 values sum to 2^115 and that of the smallest number is 2^-98
+            scaled = mean < 1.0f ? 1.267650600e30f : 8.271806126e-25f;
             eps = eps * scaled * scaled;
             Pair again{0.0f, 0.0f};
 #pragma unroll

@@ -369,8 +369,8 @@ tg_status tg_moe_gemm_scaled(const tg_scaled_operand *A, int64_t T, int64_t K, c
  *
  *   h         = x + residual, added in fp32 and rounded to the residual's type; x itself
  *               without a residual
- *   row_scale = 1 / sqrt(mean over the row of h^2 + eps), rounded to fp32 once (squares below
- *               fp32's normal numbers may be lost beside eps)
+ *   row_scale = 1 / sqrt(mean over the row of h^2 + eps), rounded to fp32 once (to infinity
+ *               where it passes fp32: without eps, rows of zeros or below 2^-128)
  *   y         = (h * row_scale) * gain, each product rounded to fp32, then to y's type
  *   q, scale  = tg_quantize_blocks of the fp32 y in 1 x 128 blocks
  *

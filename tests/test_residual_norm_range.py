@@ -63,3 +63,26 @@ def test_an_eps_as_large_as_the_squares(K, eps):
     """Any finite eps counts, beside squares that fp32 holds and beside those that it does not."""
     root = eps ** 0.5
     norm(rows_of((1.0, root * 1e-9, root * 1e-3, root * 0.5, root, root * 1.5, root * 30, 1e25), K, F), eps)
+
+
+@pytest.mark.parametrize("K", [1, 384, 1001, 8192, 32768])
+@pytest.mark.parametrize("dt", [F, BF])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-38, 1e-31, 1e-29])
+def test_squares_below_fp32(K, dt, eps):
+    """Without an eps, or with one of their own size, rows of small numbers have a factor as others have."""
+    x = rows_of((1e-12, 1e-15, 1e-17, 1e-19, 1e-20, 1e-22, 3e-23, 1e-25, 1e-30, 1e-35, 1e-37), K, dt)
+    if K > 1:                                      # (a single value may happen to be next to nothing)
+        norm(x, eps)
+        norm(torch.zeros_like(x), eps, residual=x)
+    norm(x[::2].contiguous(), eps)
+
+
+@pytest.mark.parametrize("K", [8, 1001])
+def test_factors_past_fp32(K):
+    """Without an eps a row below 2^-128 has a factor that fp32 does not hold: infinity, as for a row of zeros."""
+    x = torch.full((3, K), 2.0 ** -140, device="cuda")
+    x[1] = 0.0
+    x[2] = 2.0 ** -127
+    n = tg.rmsnorm(x, None, 0.0, out_dtype=F)
+    assert bool(n.row_scale[:2].isinf().all()) and float(n.row_scale[2]) == 2.0 ** 127
+    assert bool(n.y[0].isinf().all()) and bool(n.y[1].isnan().all()) and bool((n.y[2] == 1.0).all())
