@@ -13,15 +13,17 @@
 // (as many as are resident), keep the gain in shared memory and load the next row while they finish one.  65536 x 4096 bf16 with a
 // bf16 residual into e4m3 (279 us at the copy rate): a block a row 341 us, 38 instructions a value, with loads and outputs
 // chosen inside the loop; persistent, the next row on its way, 326; packed arithmetic (two values an instruction) 296; the gain
-// staged by wide loads 285, 6.6 TB/s.
+// staged by wide loads 285; squares added as pairs 295, 6.4 TB/s.
 //
 // The row factor.  An 8-bit value next to a rounding border, and a scale next to a power of two, fall on one side or
 // the other with the last bit of r, so r is worked out to well below fp32's half step and rounded once: every
 // implementation of the definition then gives the same bytes (up to one row in some thousands whose r lies that near a
-// border itself).  Eight neighbours' squares are added in fp32; their sums, independent and many, go into a pair of
-// fp32 numbers (value and what its rounding lost) through the lanes and warps; 1 / sqrt is the hardware's
-// approximation and one Newton step whose residual is worked out in such pairs.  Double precision would take 15
-// cycles a warp instruction on this GPU, about 700 a row, against 1200 that a 4096-wide row's bytes take.
+// border itself).  A thread's squares, and then the lanes' and warps' sums, are added as a pair of fp32 numbers (value and
+// what its rounding lost); 1 / sqrt is the hardware's approximation and one Newton step whose residual is worked out in
+// such pairs.  Eight neighbours' squares added in plain fp32 in front of the pairs would be 10 us less of 295, but put r a step off in
+// 4 % of the rows, 20 % where one column outweighs the others; with Knuth's two-sum of any two numbers instead of an order of
+// them it is 316.  Double precision would take 15 cycles a warp instruction on this GPU, about 700 a row, against 1200 that a
+// 4096-wide row's bytes take.
 #include <cuda_runtime.h>
 
 #include <cstdint>

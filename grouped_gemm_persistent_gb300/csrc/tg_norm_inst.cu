@@ -22,6 +22,7 @@ struct Pair {
     float hi, lo;
 };
 
+// (the error of a rounded sum by Knuth's two-sum, which needs no order of the two)
 __device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
     const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
     const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
@@ -53,18 +54,52 @@ __device__ __forceinline__ float row_factor(Pair sum, float inv_hi, float inv_lo
     return __fmaf_rn(0.5f * r, e, r);
 }
 
-// The sum of eight values' squares, the values times f (1, 2^-80 or 2^100): a product's, a fused and two additions' roundings
-template <int DT>
-__device__ __forceinline__ float squares(const Oct<DT>& o, float f) {
-    const uint64_t ff = ptx::f32x2_pack(f, f);
-    uint64_t v[4];
+// The largest magnitude of a thread's values (NaN is passed over)
+template <int DT, int NV>
+__device__ __forceinline__ float largest(const Oct<DT> (&h)[NV]) {
+    uint32_t w = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f == 1.0f ? o.pair(i) : ptx::f32x2_mul(o.pair(i), ff);
-    const uint64_t s = ptx::f32x2_add(ptx::f32x2_fma(v[1], v[1], ptx::f32x2_mul(v[0], v[0])),
-                                      ptx::f32x2_fma(v[3], v[3], ptx::f32x2_mul(v[2], v[2])));
-    float lo, hi;
-    ptx::f32x2_unpack(s, lo, hi);
-    return lo + hi;
+    for (int j = 0; j < NV; ++j) {
+        if constexpr (DT == TG_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+                asm("max.f32 %0, %0, %1, %2;" : "+r"(w) : "r"(h[j].w[i] & 0x7fffffffu), "r"(h[j].w[i + 1] & 0x7fffffffu));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DT == TG_BF16) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(h[j].w[i]));
+                else asm("max.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(w) : "r"(h[j].w[i]));
+            }
+        }
+    }
+    if constexpr (DT == TG_F32) return __uint_as_float(w);
+    else return fmaxf(fabsf(widen16<DT>(w & 0xffffu)), fabsf(widen16<DT>(w >> 16)));
+}
+
+// The sum of a thread's squares, the values times f (1, 2^-80 or 2^100), as a pair.  Two sums run side by side from a power of two above
+// the largest square, so that in each addition the sum is the larger number: what the addition adds to it is then an fp32 number,
+// and what it leaves of the square is added up by itself (Dekker's fast two-sum, the square being the fused operation's).
+template <int DT, int NV>
+__device__ __forceinline__ Pair sum_of_squares(const Oct<DT> (&h)[NV], float f) {
+    const float top = largest(h) * f;
+    // (2^-126 for zeros; where it would pass fp32, -0 or infinity: the sum is infinite or NaN and is not used)
+    const float from = __uint_as_float((__float_as_uint(top * top) & 0x7f800000u) + 0x800000u);
+    const uint64_t ff = ptx::f32x2_pack(f, f), minus = ptx::f32x2_pack(-1.0f, -1.0f);
+    uint64_t hi = ptx::f32x2_pack(from, from), lo = 0ull;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t v = f == 1.0f ? h[j].pair(i) : ptx::f32x2_mul(h[j].pair(i), ff);
+            const uint64_t s = ptx::f32x2_fma(v, v, hi), less = ptx::f32x2_fma(s, minus, hi);
+            lo = ptx::f32x2_add(lo, ptx::f32x2_fma(v, v, less));
+            hi = s;
+        }
+    hi = ptx::f32x2_add(hi, ptx::f32x2_pack(-from, -from));       // (exact: a power of two not above the sum)
+    Pair a, b;
+    ptx::f32x2_unpack(hi, a.hi, b.hi);
+    ptx::f32x2_unpack(lo, a.lo, b.lo);
+    return pair_add(a, b);
 }
 
 // x + residual in the residual's type.  Two 16-bit numbers are added with one rounding, which is the rounding of their fp32 sum: where
@@ -222,7 +257,6 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
     }
     int turn = 0;
     for (int64_t row = unit; row < a.M; row += units, turn ^= 1) {
-        Pair sum{0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int n = a.K - (in + j * tpr) * 8;          // (ODD)
@@ -242,9 +276,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
                 const int col = first_of<FORM>(in + j * tpr);
                 h[j].template store<FORM>(a.hidden + row * a.ldh + static_cast<int64_t>(col) * item_bytes(HT), count_of<FORM>(col, a.K));
             }
-            sum = pair_add(sum, {squares(h[j], 1.0f), 0.0f});
         }
-        sum = block_sum(sum, part[turn]);
+        Pair sum = block_sum(sum_of_squares(h, 1.0f), part[turn]);
         float scaled = 1.0f, eps = a.eps;
         const float mean = sum.hi * a.inv_hi + eps;
         if (!(mean < 1.267650600e30f) || mean < 7.888609052e-31f) {       // 2^100, 2^-100
@@ -253,9 +286,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(const __grid
             // which those of 32768 values sum to 2^115 and that of the smallest number is 2^-98
             scaled = mean < 1.0f ? 1.267650600e30f : 8.271806126e-25f;
             eps = eps * scaled * scaled;
-            Pair again{0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < NV; ++j) again = pair_add(again, {squares(h[j], scaled), 0.0f});
+            const Pair again = sum_of_squares(h, scaled);
             __syncthreads();                             // the parts are read above
             sum = block_sum(again, part[turn]);
         }
