@@ -161,7 +161,8 @@ __device__ __noinline__ int choose_in_64(const ScoredArgs& a, const uint8_t* row
         key[j] = 0ull;
         if (j >= n) continue;
         const double x = Logits<DT, V>::one(row, e0 + j);
-        if (x == -__builtin_huge_val()) continue;
+        // (a bias of -infinity forbids an expert whose score is NaN too)
+        if (x == -__builtin_huge_val() || (a.bias && __ldg(a.bias + e0 + j) == MINUS_INF)) continue;
         const unsigned long long by_v = order64(value_of<SIGMOID>(x, of, a.bias, e0 + j)), by_x = order64(x);
         key[j] = by_logit ? by_x : by_v;
         const unsigned long long o = by_logit && a.group_top == 1 ? by_x : by_v;
