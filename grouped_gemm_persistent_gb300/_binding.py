@@ -783,17 +783,52 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     return out
 
 
-class Routing(NamedTuple):
-    """What moe_router returns, and moe_router_backward needs again."""
+class _Routing(NamedTuple):
     experts: torch.Tensor    # int32 [T, k], -1 where a row has no further expert
     weights: torch.Tensor    # fp32 [T, k]
     counts: torch.Tensor     # int32 [G]
     loss: torch.Tensor       # fp32, balance loss
     slope: torch.Tensor      # fp32 [G], d loss / d probability
     renormalize: bool
-    score: str = "softmax"
-    weight_scale: float = 1.0
-    plain: bool = True       # tg_moe_router's (softmax, no bias, groups or factor), whose gradient has a kernel of its own
+
+
+class Routing(_Routing):
+    """What moe_router returns, and moe_router_backward needs again.
+
+    A tuple of experts, weights, counts, loss, slope and renormalize.  With other scores, a bias, groups or a factor it has
+    three more: ``score``, ``weight_scale`` and ``plain`` (false), so that one put together again from its entries does not
+    lose them; the gate without those has the same three as attributes.
+    """
+    __slots__ = ()
+    _fields = _Routing._fields + ("score", "weight_scale", "plain")
+
+    def __new__(cls, experts, weights, counts, loss, slope, renormalize, score="softmax", weight_scale=1.0, plain=True):
+        entries = (experts, weights, counts, loss, slope, renormalize)
+        if not plain or score != "softmax" or weight_scale != 1.0:
+            entries += (score, weight_scale, plain)
+        return tuple.__new__(cls, entries)
+
+    @property
+    def score(self) -> str:
+        return self[6] if len(self) > 6 else "softmax"
+
+    @property
+    def weight_scale(self) -> float:
+        return self[7] if len(self) > 6 else 1.0
+
+    @property
+    def plain(self) -> bool:     # tg_moe_router's (softmax, no bias, groups or factor), whose gradient has a kernel of its own
+        return len(self) == 6 or self[8]
+
+    @classmethod
+    def _make(cls, entries):
+        return cls(*entries)
+
+    def _replace(self, **fields):
+        return type(self)(**{**self._asdict(), **fields})
+
+    def __repr__(self) -> str:
+        return f"Routing({', '.join(f'{k}={v!r}' for k, v in self._asdict().items())})"
 
 
 def _logits(logits: torch.Tensor) -> tuple[int, int, int, int]:
@@ -829,11 +864,11 @@ def moe_router(logits: torch.Tensor, top_k: int, *, renormalize: bool = False, s
         raise ValueError(f"bias must be a contiguous fp32 tensor {[G]}")
     _on_one_gpu("logits bias", logits, bias)
     shape = (T, top_k)
+    plain = (code == 0 and bias is None and groups == 1 and weight_scale == 1.0 and top_groups in (None, 1) and group_top == 1)
     r = Routing(_empty(logits, shape, torch.int32, stream), _empty(logits, shape, torch.float32, stream),
                 _empty(logits, G, torch.int32, stream), _empty(logits, (), torch.float32, stream),
-                _empty(logits, G, torch.float32, stream), bool(renormalize), score, float(weight_scale),
-                code == 0 and bias is None and groups == 1 and weight_scale == 1.0 and top_groups in (None, 1) and group_top == 1)
-    if r.plain:
+                _empty(logits, G, torch.float32, stream), bool(renormalize), score, float(weight_scale), plain)
+    if plain:
         status = load().tg_moe_router(logits.data_ptr(), dt, ld, T, G, top_k, int(renormalize), r.experts.data_ptr(),
                                       r.weights.data_ptr(), r.counts.data_ptr(), r.loss.data_ptr(), r.slope.data_ptr(),
                                       _stream_handle(stream))
