@@ -745,6 +745,8 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     ``b`` [G, N, r] are all bf16 or all fp16, their last dimension contiguous, r at most 128; ``adapters`` is an int32 CUDA
     tensor [T] in any order (rows of one request side by side are fastest), -1 (or any value outside [0, G)) for a row
     without; ``scale`` is fp32 [G].  ``out`` (allocated if not given) has base's shape and type and may be ``base``.
+    Other rows never enter a row's result, but its last bits may be others in a batch of another size or with another
+    number of adapters: the order of the sums goes by the sizes.
     """
     xt, bt = _DTYPE_CODE.get(x.dtype), _DTYPE_CODE.get(base.dtype)
     if xt is None or xt == F32 or a.dtype != x.dtype or b.dtype != x.dtype:

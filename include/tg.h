@@ -566,10 +566,12 @@ tg_status tg_moe_router_scored_backward(const tg_router_backward_args *args, tg_
  *   scale            : DEVICE fp32 [G], or NULL for ones.
  *   base, out        : T x N row-major, base_dtype (bf16, fp16 or fp32), any alignment, as the
  *                      other matrices (16-byte aligned rows are moved with wide accesses); out may
- *                      be base.
+ *                      be base and overlaps no other input.
  * Both products are summed in fp32; the one between them is held to 2^-17 (bf16) or better, and
- * the sum with base is rounded once.  A row's result depends on its own values and adapter alone.
- * Deterministic.  T == 0 or N == 0 is a no-op; without K, r or G out is base.  A workspace of some
+ * the sum with base is rounded once.  Other rows' values and adapters never enter a row's result.
+ * The sizes (T and G among them) and the GPU choose the order of the sums along K and whether the
+ * number between the products is held to fp32 or to the bits above, so a row's last bits may be
+ * others in a batch of another size.  Deterministic.  T == 0 or N == 0 is a no-op; without K, r or G out is base.  A workspace of some
  * bytes a row from the library's memory pool, released on the stream.
  */
 typedef struct tg_lora_args {
