@@ -840,8 +840,10 @@ template <int DT, int BT, int RT, int ROWS>
 TileVariant variant() { return {&lora_tile_kernel<DT, BT, RT, ROWS>, ROWS, Tile<RT, ROWS, BT == TG_F32 ? 4 : 2>::BYTES}; }
 
 // Tiles of 64 rows (32 above 64 ranks, for their sums' room) read an adapter less often; tiles of 16 where an adapter has fewer than 32
-// rows on average, if all of them are in use.  8191 rows of one adapter: 64-row tiles 49 us, 16-row tiles 56; spread over 200 adapters
-// 75 (64 rows), over 300 88 (16 rows).
+// rows on average, if all of them are in use.  8191 rows, K 4096, N 1536, rank 64, 64-row against 16-row tiles, us: one adapter
+// 43 / 56, 16 adapters 44 / 57, 64 66 / 57, 128 78 / 59, 200 73 / 72, 300 80 / 87, 512 144 / 99.  (Between a few adapters and the border
+// neither is better throughout: 16384 rows at rank 128 over 600 adapters take 108 us in 32-row tiles and 160 in 16-row ones.  It goes by
+// the adapters there are, the host not knowing which are in use: 512 of them, of which the rows name 10, 51 / 57.)
 template <int DT, int BT>
 TileVariant variant_for(int64_t T, int G, int r) {
     const bool tall = T >= 32 * static_cast<int64_t>(G);
@@ -857,8 +859,11 @@ TileVariant variant_for(tg_dtype base, int64_t T, int G, int r) {
                                                                               : variant_for<DT, TG_BF16>(T, G, r);
 }
 
-// The rows form reads T r (K + N) 16-bit values through L2, whoever shares an adapter; the tile form takes about 14 us for K = N =
-// 4096 however few the rows are.  At that size, rank 16: 128 rows 10.2 us against 14, 256 rows 17.5 against 14.
+// The rows form reads T r (K + N) 16-bit values through L2, whoever shares an adapter; the tile form takes 10 to 14 us however few the
+// rows are.  Rows / tiles, us, at the nearest measured sizes below and above the border (T r (K + N) in millions of 2^20):
+//   K = N = 4096, r 16  16 M: 10.6 / 12.0   24 M: 14.2 / 12.1      K = N = 4096, r 64  16 M: 11.7 / 12.8   32 M: 17.9 / 13.7
+//   K = N = 1024, r 16  16 M: 10.0 / 12.2   32 M: 17.2 / 13.3      K = N = 512, r 64   16 M: 10.7 / 10.4   24 M: 13.4 / 10.5
+//   K 8192, N 1024, r 8 18 M: 11.9 / 11.9   27 M: 15.0 / 12.2      K 1024, N 8192, r 32 18 M: 14.0 / 14.4  36 M: 23.0 / 14.7
 constexpr int64_t ROWS_FORM = 21 << 20, ROWS_FORM_T = 4096;      // largest T r (K + N), and T
 
 tg_status check_operand(const char* name, const void* p, int64_t ld, int64_t cols, int64_t esize) {

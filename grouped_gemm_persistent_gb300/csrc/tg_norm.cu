@@ -45,10 +45,12 @@ NormKernel norm_for<TG_F32>(bool residual, tg_dtype rt, const Spread& s, Form fo
 
 namespace {
 
-// One vector a thread up to 256 values, two up to 1024 (65536 x 512 into e4m3 40 us, 48 with four).  Longer rows: four of 16-bit streams
+// One vector a thread up to 256 values, two up to 1024 (65536 x 512 into e4m3 41 us, 52 with four).  Longer rows: four of 16-bit streams
 // (eight above 16384: a block has 512 threads then); one of 32-bit streams that are not quantised, up to 8192 values, and of few
-// rows, so that a row takes one round of loads.  40960 x 4096, x bf16: into e4m3 with a bf16 residual 181 us with four a thread, 198
-// with two, 243 with one; into bf16 with an fp32 residual 344, 351 and 324.
+// rows, so that a row takes one round of loads.  40960 x 4096, x bf16: into e4m3 with a bf16 residual 186 us with four a thread, 205
+// with two, 262 with one; into bf16 with an fp32 residual 348, 361 and 318.  Eight spill: up to 232 bytes a thread with 16-bit
+// streams, 350 to 1200 with an fp32 x or stream, 3828 with both in odd rows (5000 x 32768 bf16 into e4m3 290 us, 169 at the copy
+// rate).
 Spread spread_for(int64_t K, bool few, bool wide, bool q) {
     const int64_t vectors = (K + 7) / 8;
     if (vectors <= 32 || (vectors <= 1024 && (few || (wide && !q && vectors > 128)))) return spread(K, 1);

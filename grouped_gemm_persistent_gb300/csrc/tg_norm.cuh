@@ -31,7 +31,7 @@ __device__ __forceinline__ float widen16(uint32_t b) {
 // How the lanes hold a row.  WHOLE, ODD: eight neighbouring values each, rows on 16-byte boundaries, of whole vectors or not.  APART: rows
 // that start elsewhere; the sixteen lanes of a block of 128 values hold every sixteenth value of it, so that a load or a store of a
 // warp is two runs of neighbours.  (40970 x 4095 bf16 without padding, bf16 residual: into e4m3 600 us with eight neighbours read
-// one by one, 359 apart; gradients 570 and 343.  A row of whole blocks read without checks instead: 543 and 435, the 16-bit
+// one by one, 366 apart; gradients 570 and 343.  A row of whole blocks read without checks instead: 543 and 435, the 16-bit
 // values being put together, and waited for, inside the branch.)
 enum Form : int { ODD, WHOLE, APART };
 

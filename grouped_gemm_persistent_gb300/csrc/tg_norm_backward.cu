@@ -156,6 +156,7 @@ using NormBackKernel = void (*)(const NormBackArgs);
 // Two vectors a thread up to 8192 values, four up to 16384, eight above, which are not held between the row's sum and dx but read again.
 // 40960 x 4096 bf16 with d_hidden: two 206 us, four 211, one 264.  10000 x 16383 without padding, fp32 stream: four 604, eight held
 // (and spilled) 1738.  5000 x 32768, fp32 stream: read again 504, held 1385 (339 at the copy rate); bf16 424 and 468.
+// (Four vectors of fp32 dy and stream spill 144 to 184 bytes a thread, other types none on 16-byte boundaries.)
 Spread spread_for(int64_t K) { return spread(K, K <= 8192 ? 2 : K <= 16384 ? 4 : 8); }
 
 template <int DT, int HT, int FORM>

@@ -16,7 +16,7 @@
 // two neighbours among the first k + 1 whose keys are within the bound, or two groups at the border of the kept ones.  Then the k + 1
 // candidates, or the groups' largest experts, are worked out in 64 bits, each by a lane, and put in order; a row whose next
 // candidate is within the bound too is done again as a whole (choose_in_64).  Double precision is slow here (a row of 256 takes the
-// SM some 5 us): with the whole row always, 131072 x 256 fp32 took 118 us instead of 105, and 8191 rows 43 instead of 24.
+// SM some 5 us): with the whole row always, sigmoid scores of 131072 x 256 fp32 take 109 us instead of 95, of 8191 rows 28 instead of 18.
 // Neighbours whose logit and bias are both the same are a true tie, which the index decides: with 16-bit logits and a bias of zeros
 // they are common.
 //   sigmoid  e^-x: 2^-22 of itself and |x| 2^-24 for its argument, which s (1 - s) <= 1/4 takes down to 7.3e-8; 1 + e^-x and the
@@ -32,12 +32,18 @@
 // The groups are chosen the same way, by their scores' bits and their indices, while each has its group_top experts to choose
 // from and none below lo; otherwise, and without a bias by the largest logit itself, by counting the groups that come before each.
 //
-// Bound by instruction issue: 594 warp instructions a row of 256 with 8 groups and k = 8, 73 % of the issue rate, 93 us for 131072
+// Bound by instruction issue: 594 warp instructions a row of 256 with 8 groups and k = 8, 73 % of the issue rate, 95 us for 131072
 // rows whose logits are read in 20 us; a choice more costs 2.6 us, the groups 17.  The gradient: 317 instructions a row, 52 us (40 us
 // at the copy rate).
 //
 // Positions.  A row is L lanes of V positions.  Each group has a power of two of positions, V at least, so that
 // a group is whole lanes and its sums are a few exchanges; the positions past its experts hold -infinity.
+//
+// Registers.  Eight positions a lane are held to 64 for two blocks an SM (softmax spills 112 to 164 bytes a thread, sigmoid at most
+// 68); 16 and 32 positions take 126 and 128, one block an SM, so that a grid cut for two runs in two waves; 32 spill 136 to 564.
+//
+// Weights come from the hardware's 2^x and 1 / x: next to 1e-7 of themselves around logits of zero, about 1e-5 at 88 from it (softmax:
+// from the row's largest), where the rounding of the exponent's argument is that large.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -502,7 +502,8 @@ typedef enum {
  * Scores are compared as the real numbers they are, to 64 bits (without a bias, where v rises
  * with the logit, logits are compared); fp32 rounding decides no choice.  An expert with a
  * logit or a bias of -infinity is not chosen; v that is NaN counts as above every number.
- * Scores below 2^-126 may count as 0.  The rest as tg_moe_router.
+ * Scores below 2^-126 may count as 0.  Weights are held to about 1e-7 of themselves, growing to
+ * 1e-5 with logits 88 away from zero (softmax: from the row's largest).  The rest as tg_moe_router.
  *
  *   groups divides G; top_groups * (G / groups) >= k; the groups, each rounded up to a power of
  *   two of 8 experts or more (above 256 of them in all 16, above 512 32), hold at most
