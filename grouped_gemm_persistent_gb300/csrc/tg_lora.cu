@@ -26,8 +26,8 @@
 // and 14 into the second.
 //
 // Precision.  u is summed in fp32, times scale, and enters the second product as hi + lo of the operands' type (bf16: 16
-// bits, 2^-17; fp16, and bf16 next to the ends of fp32's range, of the row's power-of-two multiple that brings its largest value to
-// 1..2: 22 bits in fp16): a single 16-bit u would add half a step of its own type to the adapters' part, as much as rounding the result does.
+// bits, 2^-17, of a multiple next to the ends of its range; fp16, of the row's power-of-two multiple that brings its largest value to
+// 1..2: 22 bits): a single 16-bit u would add half a step of its own type to the adapters' part, as much as rounding the result does.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -716,14 +716,10 @@ __global__ void __launch_bounds__(L_THREADS, 2) lora_tile_kernel(const __grid_co
             if (fabsf(u[i]) < __int_as_float(0x7f800000)) top = fmaxf(top, fabsf(u[i]));
         }
         // fp16: 2^-e with the largest finite |u| in [2^e, 2^(e + 1)) (beside an infinity the others stay numbers).  bf16 has fp32's range:
-        // only where u or what is left of it would pass an end of that.
-        float down = 1.0f, up = 1.0f;
+        // 2^64 or 2^-64 where u or what is left of it would pass an end of that, which keeps the products with any B inside.
         const uint32_t e = __reduce_max_sync(FULL, __float_as_uint(top)) >> 23;
-        if (DT == TG_F16 || e < 32u || e > 252u) {
-            const uint32_t to = e < 1u ? 1u : e > 253u ? 253u : e;        // (2^e and 2^-e are normal numbers)
-            down = __uint_as_float((254u - to) << 23);
-            up = __uint_as_float(to << 23);
-        }
+        const uint32_t to = DT == TG_F16 ? (e < 1u ? 1u : e > 253u ? 253u : e) : e < 32u ? 63u : e > 252u ? 191u : 127u;
+        const float down = __uint_as_float((254u - to) << 23), up = __uint_as_float(to << 23);      // (both normal numbers)
         uint32_t hi[PER / 2], lo[PER / 2];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {

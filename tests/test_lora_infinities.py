@@ -65,3 +65,16 @@ def test_numbers_at_the_ends_of_fp32_between_the_products(T, dt, size, weight):
     b, base = (b.float() * weight).to(dt), torch.zeros_like(base)
     scale = torch.full((3,), size, device="cuda")
     check(base, x, a, b, ids, scale, tg.lora_add(base, x, a, b, ids, scale))
+
+
+@pytest.mark.parametrize("T", [20, 5000])
+@pytest.mark.parametrize("size,weight", [(1e-36, 1e38), (3.4e38, 1e-38), (1e-37, 3e37), (1.5e38, 1e-36)])
+def test_opposite_ends_of_fp32_in_one_product(T, size, weight):
+    """A number at one end of the range times weights at the other: the products are ordinary, in bf16 alone."""
+    base, x, a, b, ids, _ = make(53, T, 8, 72, 16, 3, BF, F, "rows")
+    x = torch.zeros_like(x)
+    x[:, 0] = 1.0
+    a = torch.where(a < 0, -1.0, 1.0).to(BF)
+    b = (b.float() * weight).to(BF)
+    scale = torch.full((3,), size, device="cuda")
+    check(base, x, a, b, ids, scale, tg.lora_add(base, x, a, b, ids, scale))
